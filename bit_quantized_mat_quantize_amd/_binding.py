@@ -19,6 +19,7 @@ Q8_0, Q8_K = 0, 1
 Q4_0, Q4_K, Q6_K, Q2_K = 0, 1, 2, 3
 CANONICAL, REPACKED = 0, 1
 ALGO_AUTO, ALGO_GEMV, ALGO_MFMA, ALGO_SKINNY = 0, 1, 2, 3
+F32, F16, BF16 = 0, 1, 2
 STATUS = {0: "QMM_OK", 1: "QMM_EINVAL", 2: "QMM_EALIGN", 3: "QMM_EUNSUPPORTED", 4: "QMM_EDEVICE"}
 
 _ACT = {"q8_0": Q8_0, "q8_K": Q8_K}
@@ -68,6 +69,13 @@ def load() -> ctypes.CDLL:
         "qmm_mul_mat_id_noalloc": (I, [I, P, SZ, I64, I, P, SZ, I, P, I64, I64, P, SZ, I64, I64, I, P]),
         "qmm_mul_mat_q2_K_ex": (I, [P, SZ, I, P, SZ, P, SZ, I64, I64, I64, I, P]),
         "qmm_quantize_mul_mat": (I, [I, P, SZ, I, P, P, SZ, P, SZ, I64, I64, I64, P]),
+        "qmm_embed_rows": (I, [I, P, SZ, I, P, I64, ctypes.c_float, P, SZ, I64, I64, P]),
+        "qmm_lora_workspace_bytes": (SZ, [I64, I64, I64, I64]),
+        "qmm_lora_add": (I, [I, P, SZ, P, SZ, I64, I64, P, P, P, SZ, P, P, SZ, I64, P, SZ, I64, I64, I64, I64,
+                             P, SZ, P]),
+        "qmm_logprobs_workspace_bytes": (SZ, [I64, I64, I64]),
+        "qmm_logprobs": (I, [I, P, SZ, I64, I64, I64, ctypes.c_float, P, SZ, I64, P, I64, P, P, I64, P, P,
+                             P, SZ, P]),
         "qmm_debug_block_sums": (I, [I, P, SZ, I, P, SZ, P, SZ, I64, I64, I64, P]),
         "qmm_status_string": (ctypes.c_char_p, [I]),
         "qmm_last_error": (ctypes.c_char_p, []),
@@ -308,6 +316,163 @@ def debug_block_sums(wfmt: str, w, y, M: int, N: int, K: int, layout: str = "can
     _check(load().qmm_debug_block_sums(_WEIGHT[wfmt], pw, nw, _LAYOUT[layout], py, ny, po, no,
                                        M, N, K, _stream(stream)), "qmm_debug_block_sums")
     return out
+
+
+# ---- the operators beside the projections.  They run on the device of their
+# tensors (whichever is current) and on `stream`, by default that device's
+# current one; what they allocate belongs to that stream.
+
+def _on(stream, **tensors):
+    """The context to allocate and launch in; every tensor has to be on one GPU."""
+    import torch
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _float_type(t, name: str) -> int:
+    import torch
+    types = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    if t.dtype not in types:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16 (got {t.dtype})")
+    return types[t.dtype]
+
+
+def _is(t, name: str, dtype, shape) -> None:
+    """A contiguous tensor of this type and shape (None: not given, fine)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name: str):
+    """(pointer, bytes from it to the last row's end, row stride) of a 2-D tensor with unit column stride."""
+    M, N = t.shape
+    if N > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    ld = t.stride(0) if M > 1 else N
+    return t.data_ptr(), ((M - 1) * ld + N) * t.element_size() if M and N else 0, ld
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def embed_rows(wfmt: str, w, ids, N: int, K: int, layout: str = "canonical", scale: float = 1.0,
+               out=None, stream=None):
+    """out [T, K] fp32 = scale * the rows ids (int32 [T]) of the packed table w [N, K], decoded.
+
+    An id outside [0, N) gives a row of NaN."""
+    import torch
+    (T,) = ids.shape
+    _is(ids, "ids", torch.int32, (T,))
+    with _on(stream, ids=ids, w=w, out=out):
+        if out is None:
+            out = torch.empty((T, K), dtype=torch.float32, device=ids.device)
+        _is(out, "out", torch.float32, (T, K))
+        pw, nw = _dev(w, "w")
+        _check(load().qmm_embed_rows(_WEIGHT[wfmt], pw, nw, _LAYOUT[layout], ids.data_ptr(), T, scale,
+                                     out.data_ptr(), T * K * 4, N, K, _stream(stream)), "qmm_embed_rows")
+    return out
+
+
+def lora_workspace_bytes(M: int, R: int, K: int, E: int) -> int:
+    return int(load().qmm_lora_workspace_bytes(M, R, K, E))
+
+
+def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=None, stream=None):
+    """out [M, N] fp32 = base + scales[e] * (x A_e^T) B_e^T with e = ids[m] (int32 [M]; -1: base alone).
+
+    x: fp32 [M, K], the projection's input; A [E, R, K], B [E, N, R]: float32, float16 or bfloat16; scales
+    fp32 [E]; ranks int32 [E], each adapter's own rank (at most R).  base and out may be column ranges of
+    wider matrices; out=base adds in place.  Without `out` a new tensor is returned.  An id outside
+    [-1, E) gives a row of NaN."""
+    import torch
+    (M, N), (E, R, K) = base.shape, A.shape
+    _is(x, "x", torch.float32, (M, K))
+    _is(A, "A", A.dtype, (E, R, K))
+    _is(B, "B", A.dtype, (E, N, R))
+    _is(ids, "ids", torch.int32, (M,))
+    _is(scales, "scales", torch.float32, (E,))
+    _is(ranks, "ranks", torch.int32, (E,))
+    if base.dtype != torch.float32:
+        raise ValueError(f"base must be float32 (got {base.dtype})")
+    with _on(stream, base=base, x=x, A=A, B=B, ids=ids, scales=scales, ranks=ranks, out=out, workspace=workspace):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.float32, device=base.device)
+        elif out.dtype != torch.float32 or tuple(out.shape) != (M, N):
+            raise ValueError(f"out must be float32 of shape {(M, N)} (got {out.dtype}, {tuple(out.shape)})")
+        if workspace is None:
+            workspace = torch.empty(max(lora_workspace_bytes(M, R, K, E), 16), dtype=torch.uint8, device=base.device)
+        pb, nb, ldb = _rows(base, "base")
+        po, no, ldo = _rows(out, "out")
+        pw, nw = _dev(workspace, "workspace")
+        _check(load().qmm_lora_add(_float_type(A, "A"), A.data_ptr(), A.nbytes, B.data_ptr(), B.nbytes, E, R,
+                                   _ptr(scales), _ptr(ranks), x.data_ptr(), x.nbytes, ids.data_ptr(), pb, nb, ldb,
+                                   po, no, ldo, M, N, K, pw, nw, _stream(stream)), "qmm_lora_add")
+    return out
+
+
+def logprobs_workspace_bytes(M: int, V: int, k: int) -> int:
+    return int(load().qmm_logprobs_workspace_bytes(M, V, k))
+
+
+def logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, mask=None, entropy: bool = True,
+             workspace=None, stream=None):
+    """(token_logprobs, entropy, top_ids, top_logprobs) of logits [M, V] (float32, float16 or bfloat16).
+
+    tokens: int32 [M] or [M, G], the tokens whose log probability is asked for (first result, fp32 of the
+    same shape); entropy: fp32 [M]; k: that many most likely tokens (int32 and fp32 [M, k], -1 and -inf where
+    there are fewer).  mask: int32 words [W], [1, W] or [M, W], W >= ceil(V / 32); bit i % 32 of word i // 32
+    allows token i.  scale multiplies the logits (one over the temperature).  What is not asked for is None."""
+    import torch
+    M, V = logits.shape
+    G = 0
+    if tokens is not None:
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != M:
+            raise ValueError(f"tokens must have shape ({M},) or ({M}, G) (got {tuple(tokens.shape)})")
+        G = tokens.shape[1] if tokens.dim() == 2 else 1
+        _is(tokens, "tokens", torch.int32, tokens.shape)
+    mask_ld, mask_bytes = 0, 0
+    if mask is not None:
+        rows, words = (1, mask.shape[0]) if mask.dim() == 1 else mask.shape
+        if rows not in (1, M) or words < (V + 31) // 32:
+            raise ValueError(f"mask must have 1 or {M} rows of at least {(V + 31) // 32} words (got {tuple(mask.shape)})")
+        _is(mask, "mask", torch.int32, mask.shape)
+        mask_ld, mask_bytes = words if rows > 1 else 0, mask.nbytes
+    with _on(stream, logits=logits, tokens=tokens, mask=mask, workspace=workspace):
+        def new(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=logits.device)
+
+        lp = None if tokens is None else new(*tokens.shape)
+        ent = new(M) if entropy else None
+        top_ids, top_lp = (new(M, k, dtype=torch.int32), new(M, k)) if k > 0 else (None, None)
+        need = logprobs_workspace_bytes(M, V, k)
+        if workspace is None and need:
+            workspace = new(need, dtype=torch.uint8)
+        px, nx, ld = _rows(logits, "logits")
+        _check(load().qmm_logprobs(_float_type(logits, "logits"), px, nx, ld, M, V, scale, _ptr(mask), mask_bytes,
+                                   mask_ld, _ptr(tokens), G, _ptr(lp), _ptr(ent), k, _ptr(top_ids), _ptr(top_lp),
+                                   _ptr(workspace), 0 if workspace is None else workspace.nbytes, _stream(stream)),
+               "qmm_logprobs")
+    return lp, ent, top_ids, top_lp
 
 
 def version() -> str:

@@ -4,7 +4,8 @@
 // HIP runtime, so a bad call returns an error code, enqueues nothing and needs
 // no GPU to be tested.  Valid calls dispatch to the kernel families in
 // quantize.hip, repack.hip, gemv.hip, skinny.hip, gemm.hip, q6k.hip,
-// q6k_gemm.hip, q2k.hip, q2k_gemm.hip, q40_gemm.hip and moe.hip.
+// q6k_gemm.hip, q2k.hip, q2k_gemm.hip, q40_gemm.hip, moe.hip, embed.hip,
+// lora.hip and logprobs.hip.
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -740,6 +741,189 @@ qmm_status qmm_debug_block_sums(qmm_weight_type t, const void *w, size_t w_bytes
                          : t == QMM_Q2_K ? qmm::launch_group_sums_q2_K(wb, rep, yb, P, M, N, K, s)
                                          : qmm::launch_block_sums_q4_0(wb, rep, yb, P, M, N, K, s),
                          "debug_block_sums launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+size_t float_size(qmm_float_type t) { return t == QMM_F32 ? 4 : ((t == QMM_F16 || t == QMM_BF16) ? 2 : 0); }
+
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return a_bytes && b_bytes && p < q + b_bytes && q < p + a_bytes;
+}
+
+// bytes from the first element to the end of the last of `rows` rows of n elements
+size_t strided_bytes(int64_t rows, int64_t ld, int64_t n, size_t size) {
+    return (size_t)((rows - 1) * ld + n) * size;
+}
+
+constexpr int64_t kMaxLd = int64_t(1) << 32;  // with 2^24 rows and 4-byte elements below 2^62 bytes
+
+qmm_status check_ld(const char *name, int64_t ld, int64_t n) {
+    if (ld < n) return fail(QMM_EINVAL, "%s = %lld is below the row length %lld", name, (long long)ld, (long long)n);
+    if (ld > kMaxLd) return fail(QMM_EUNSUPPORTED, "%s = %lld exceeds the limit %lld", name, (long long)ld, (long long)kMaxLd);
+    return QMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qmm_status qmm_embed_rows(qmm_weight_type t, const void *w, size_t w_bytes, qmm_layout l, const int32_t *ids,
+                          int64_t T, float scale, float *out, size_t out_bytes, int64_t N, int64_t K, void *stream) {
+    if (!w_qk(t)) return fail(QMM_EUNSUPPORTED, "unknown weight type %d", (int)t);
+    if (l != QMM_LAYOUT_CANONICAL && l != QMM_LAYOUT_REPACKED)
+        return fail(QMM_EUNSUPPORTED, "unknown layout %d", (int)l);
+    QMM_TRY(check_rows("T", T));
+    QMM_TRY(check_rows("N", N));
+    QMM_TRY(check_k(K, w_qk(t)));
+    if (T == 0) return QMM_OK;
+    if (N == 0) return fail(QMM_EINVAL, "an empty table (N = 0) has no rows for T = %lld ids", (long long)T);
+    const size_t need = qmm_weight_bytes(t, l, N, K), out_need = (size_t)(T * K) * sizeof(float);
+    QMM_TRY(check_ptr("w", w));
+    QMM_TRY(check_ptr("ids", ids));
+    QMM_TRY(check_ptr("out", out));
+    QMM_TRY(check_size("w", w_bytes, need));
+    QMM_TRY(check_size("out", out_bytes, out_need));
+    if (overlap(out, out_need, w, need) || overlap(out, out_need, ids, (size_t)T * sizeof(int32_t)))
+        return fail(QMM_EINVAL, "out overlaps w or ids");
+    return device_status(qmm::launch_embed_rows((int)t, static_cast<const uint8_t *>(w), l == QMM_LAYOUT_REPACKED, ids,
+                                                T, scale, out, N, K, static_cast<hipStream_t>(stream)),
+                         "embed_rows launch");
+}
+
+// the pool's sizes are bounded as mul_mat_id's: E by the same limit, R so that a
+// tile's v (16 rows) stays in 17 KiB of LDS
+constexpr int64_t kLoraMaxRank = 256;
+
+size_t qmm_lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E) {
+    if (M < 1 || M > kMaxRows || R < 1 || R > kLoraMaxRank || K < 32 || K % 32 || K > kMaxK || E < 1 ||
+        E > qmm::kMoeMaxExperts)
+        return 0;
+    return (size_t)qmm::lora_workspace_bytes(M, R, K, E);
+}
+
+qmm_status qmm_lora_add(qmm_float_type t, const void *A, size_t a_bytes, const void *B, size_t b_bytes, int64_t E,
+                        int64_t R, const float *scales, const int32_t *ranks, const float *x, size_t x_bytes,
+                        const int32_t *ids, const float *base, size_t base_bytes, int64_t ld_base, float *out,
+                        size_t out_bytes, int64_t ld_out, int64_t M, int64_t N, int64_t K, void *workspace,
+                        size_t ws_bytes, void *stream) {
+    const size_t size = float_size(t);
+    if (!size) return fail(QMM_EUNSUPPORTED, "unknown adapter type %d", (int)t);
+    if (E < 1 || E > qmm::kMoeMaxExperts)
+        return fail(QMM_EUNSUPPORTED, "E = %lld adapters; 1 <= E <= %d", (long long)E, qmm::kMoeMaxExperts);
+    if (R < 1 || R > kLoraMaxRank)
+        return fail(QMM_EUNSUPPORTED, "R = %lld; 1 <= R <= %lld", (long long)R, (long long)kLoraMaxRank);
+    QMM_TRY(check_rows("M", M));
+    QMM_TRY(check_rows("N", N));
+    QMM_TRY(check_k(K, 32));
+    if (M == 0 || N == 0) return QMM_OK;
+    QMM_TRY(check_ld("ld_base", ld_base, N));
+    QMM_TRY(check_ld("ld_out", ld_out, N));
+    QMM_TRY(check_ptr("A", A));
+    QMM_TRY(check_ptr("B", B));
+    if (scales != nullptr) QMM_TRY(check_ptr("scales", scales));
+    if (ranks != nullptr) QMM_TRY(check_ptr("ranks", ranks));
+    QMM_TRY(check_ptr("x", x));
+    QMM_TRY(check_ptr("ids", ids));
+    QMM_TRY(check_ptr("base", base));
+    QMM_TRY(check_ptr("out", out));
+    QMM_TRY(check_ptr("workspace", workspace));
+    const size_t a_need = (size_t)(E * R * K) * size, b_need = (size_t)(E * R * N) * size;
+    const size_t x_need = (size_t)(M * K) * sizeof(float);
+    const size_t base_need = strided_bytes(M, ld_base, N, sizeof(float));
+    const size_t out_need = strided_bytes(M, ld_out, N, sizeof(float));
+    const size_t ws_need = qmm_lora_workspace_bytes(M, R, K, E);
+    QMM_TRY(check_size("A", a_bytes, a_need));
+    QMM_TRY(check_size("B", b_bytes, b_need));
+    QMM_TRY(check_size("x", x_bytes, x_need));
+    QMM_TRY(check_size("base", base_bytes, base_need));
+    QMM_TRY(check_size("out", out_bytes, out_need));
+    QMM_TRY(check_size("workspace", ws_bytes, ws_need));
+    const bool in_place = out == base && ld_out == ld_base;
+    if (!in_place && overlap(out, out_need, base, base_need))
+        return fail(QMM_EINVAL, "out overlaps base without being base (same pointer and row stride)");
+    if (overlap(out, out_need, x, x_need) || overlap(out, out_need, A, a_need) || overlap(out, out_need, B, b_need) ||
+        overlap(out, out_need, workspace, ws_need))
+        return fail(QMM_EINVAL, "out overlaps x, A, B or the workspace");
+    if (!qmm::lora_grid_ok(M, N, R, K, E))
+        return fail(QMM_EUNSUPPORTED, "M = %lld, N = %lld needs more than 2^32 threads", (long long)M, (long long)N);
+    const qmm::LoraArgs a{A, B, scales, ranks, x, ids, base, out, static_cast<float *>(workspace),
+                          M, N, K, R, E, ld_base, ld_out};
+    return device_status(qmm::launch_lora_add((int)t, a, static_cast<hipStream_t>(stream)), "lora_add launch");
+}
+
+size_t qmm_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k) {
+    if (M < 1 || M > qmm::logprobs_max_rows() || V < 1 || V > kMaxRows || k < 0 || k > qmm::logprobs_max_k()) return 0;
+    return (size_t)qmm::logprobs_workspace_bytes(M, V, k);
+}
+
+qmm_status qmm_logprobs(qmm_float_type t, const void *logits, size_t logits_bytes, int64_t ld, int64_t M, int64_t V,
+                        float scale, const uint32_t *mask, size_t mask_bytes, int64_t mask_ld, const int32_t *tokens,
+                        int64_t G, float *token_logprobs, float *entropy, int64_t k, int32_t *top_ids,
+                        float *top_logprobs, void *workspace, size_t ws_bytes, void *stream) {
+    const size_t size = float_size(t);
+    if (!size) return fail(QMM_EUNSUPPORTED, "unknown logit type %d", (int)t);
+    QMM_TRY(check_rows("M", M));
+    QMM_TRY(check_rows("V", V));
+    if (M > qmm::logprobs_max_rows())
+        return fail(QMM_EUNSUPPORTED, "M = %lld exceeds the limit %lld", (long long)M, (long long)qmm::logprobs_max_rows());
+    if (!(scale > 0.0f && scale <= 1e30f)) return fail(QMM_EINVAL, "scale = %g; 0 < scale <= 1e30", (double)scale);
+    if (k < 0 || k > qmm::logprobs_max_k())
+        return fail(QMM_EUNSUPPORTED, "k = %lld; 0 <= k <= %lld", (long long)k, (long long)qmm::logprobs_max_k());
+    if (G < 0) return fail(QMM_EINVAL, "G = %lld is negative", (long long)G);
+    if (M == 0) return QMM_OK;
+    if (V == 0) return fail(QMM_EINVAL, "rows without logits (V = 0)");
+    if (G > ((int64_t(1) << 31) - 1) / M)
+        return fail(QMM_EUNSUPPORTED, "M*G = %lld*%lld tokens exceeds 2^31 - 1", (long long)M, (long long)G);
+    QMM_TRY(check_ld("ld", ld, V));
+    QMM_TRY(check_ptr("logits", logits));
+    QMM_TRY(check_size("logits", logits_bytes, strided_bytes(M, ld, V, size)));
+    if (mask != nullptr) {
+        const int64_t words = (V + 31) / 32;
+        QMM_TRY(check_ptr("mask", mask));
+        if (mask_ld != 0) QMM_TRY(check_ld("mask_ld", mask_ld, words));
+        QMM_TRY(check_size("mask", mask_bytes, strided_bytes(M, mask_ld, words, sizeof(uint32_t))));
+    }
+    if (G > 0) {
+        QMM_TRY(check_ptr("tokens", tokens));
+        QMM_TRY(check_ptr("token_logprobs", token_logprobs));
+    }
+    if (entropy != nullptr) QMM_TRY(check_ptr("entropy", entropy));
+    if (k > 0) {
+        QMM_TRY(check_ptr("top_ids", top_ids));
+        QMM_TRY(check_ptr("top_logprobs", top_logprobs));
+    }
+    const size_t ws_need = qmm_logprobs_workspace_bytes(M, V, k);
+    if (ws_need != 0) {
+        QMM_TRY(check_ptr("workspace", workspace));
+        QMM_TRY(check_size("workspace", ws_bytes, ws_need));
+    }
+    const size_t x_need = strided_bytes(M, ld, V, size), top = (size_t)(M * k) * sizeof(float);
+    if (overlap(token_logprobs, (size_t)(M * G) * sizeof(float), logits, x_need) ||
+        overlap(entropy, entropy != nullptr ? (size_t)M * sizeof(float) : 0, logits, x_need) ||
+        overlap(top_ids, top, logits, x_need) || overlap(top_logprobs, top, logits, x_need) ||
+        overlap(workspace, ws_need, logits, x_need))
+        return fail(QMM_EINVAL, "an output or the workspace overlaps the logits");
+    qmm::LogprobArgs a{};
+    a.logits = logits;
+    a.mask = mask;
+    a.tokens = tokens;
+    a.token_logprobs = token_logprobs;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.M = M;
+    a.V = V;
+    a.ld = ld;
+    a.mask_ld = mask_ld;
+    a.G = G;
+    a.k = k;
+    a.scale = scale;
+    return device_status(qmm::launch_logprobs((int)t, a, workspace, static_cast<hipStream_t>(stream)),
+                         "logprobs launch");
 }
 
 const char *qmm_status_string(qmm_status s) {

@@ -201,4 +201,44 @@ hipError_t launch_gemm_id_q4_K(const uint8_t *w, bool repacked, int64_t w_stride
                                int64_t y_rows, int y_per_slot, int64_t U, const int32_t *group_ws,
                                int64_t E, int64_t P, float *out, int64_t N, int64_t K, hipStream_t s);
 
+// ---- rows of a packed table by id, decoded and scaled (embed.hip); fmt is a qmm_weight_type
+hipError_t launch_embed_rows(int fmt, const uint8_t *w, bool repacked, const int32_t *ids, int64_t T, float scale,
+                             float *out, int64_t N, int64_t K, hipStream_t s);
+
+// ---- low-rank adapters per row (lora.hip); type is a qmm_float_type (of A and B).
+// Workspace: fp32 partial sums of v[m][r], one set per split of K.
+struct LoraArgs {
+    const void *A, *B;      // [E][R][K], [E][N][R]
+    const float *scales;    // [E] or null (1)
+    const int32_t *ranks;   // [E] or null (R)
+    const float *x;         // [M][K]
+    const int32_t *ids;     // [M]
+    const float *base;      // row stride ld_base; may be out
+    float *out;             // row stride ld_out
+    float *ws;
+    int64_t M, N, K, R, E, ld_base, ld_out;
+};
+int64_t lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E);
+bool lora_grid_ok(int64_t M, int64_t N, int64_t R, int64_t K, int64_t E);  // both launches fit a grid
+hipError_t launch_lora_add(int type, const LoraArgs &a, hipStream_t s);
+
+// ---- log probabilities of rows of logits (logprobs.hip); type is a qmm_float_type (of the logits).
+struct LogprobArgs {
+    const void *logits;     // row stride ld (elements)
+    const uint32_t *mask;   // bit i of a row: token i is allowed; row stride mask_ld words (0: one row for all); or null
+    const int32_t *tokens;  // [M][G]
+    float *token_logprobs;  // [M][G]
+    float *entropy;         // [M] or null
+    int32_t *top_ids;       // [M][k]
+    float *top_logprobs;    // [M][k]
+    float4 *ws_stats;       // [M][splits], set by launch_logprobs
+    uint64_t *ws_keys;      // [M][splits][k], set by launch_logprobs
+    int64_t M, V, ld, mask_ld, G, k;
+    float scale;
+};
+int64_t logprobs_max_k();
+int64_t logprobs_max_rows();  // rows of one launch
+int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);  // 0: not used
+hipError_t launch_logprobs(int type, LogprobArgs a, void *ws, hipStream_t s);
+
 }  // namespace qmm

@@ -89,6 +89,8 @@ typedef enum {
 typedef enum { QMM_Q8_0 = 0, QMM_Q8_K = 1 } qmm_act_type;
 typedef enum { QMM_Q4_0 = 0, QMM_Q4_K = 1, QMM_Q6_K = 2, QMM_Q2_K = 3 } qmm_weight_type;
 typedef enum { QMM_LAYOUT_CANONICAL = 0, QMM_LAYOUT_REPACKED = 1 } qmm_layout;
+/* plain number formats (adapters, logits) */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_float_type;
 
 /* Kernel family for a mul_mat call:
  *   GEMV    vector int8 dot products, one wavefront per output row (Q4_0 and
@@ -352,6 +354,87 @@ qmm_status qmm_debug_block_sums(qmm_weight_type t, const void *w, size_t w_bytes
                                 qmm_layout l, const void *y, size_t y_bytes,
                                 int32_t *P, size_t p_bytes,
                                 int64_t M, int64_t N, int64_t K, void *stream);
+
+/* ---- The operators beside the projections: the rows a token id selects from a
+ * packed table, low-rank adapters on top of a projection, and what a row of
+ * logits says.  The pages do not cover them; the formulas below define them. */
+
+/* out[t*K + k] = scale * deq(W)[ids[t], k]: rows of a packed table W [N, K] in
+ * format t and layout l (a token embedding; the same matrix may serve as the
+ * head through mul_mat), decoded to fp32 as the formulas at the top of this
+ * header define.  ids: device int32 [T], any order, any repeats; an id outside
+ * [0, N) cannot be checked on the host: its row is NaN and nothing is read out
+ * of bounds.  out: device fp32 [T, K], overwritten, must not overlap w or ids.
+ * The table may exceed 4 GiB.  scale is any fp32 number. */
+qmm_status qmm_embed_rows(qmm_weight_type t, const void *w, size_t w_bytes, qmm_layout l,
+                          const int32_t *ids, int64_t T, float scale,
+                          float *out, size_t out_bytes, int64_t N, int64_t K, void *stream);
+
+/* Bytes of the workspace qmm_lora_add needs (fp32 partial sums of the first
+ * product).  Returns 0 for invalid arguments and for M = 0. */
+size_t qmm_lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E);
+
+/* Low-rank adapters of many requests on top of a shared projection's output:
+ * with e = ids[m],
+ *     out[m, n] = base[m, n] + scales[e] * sum_{r < ranks[e]} B[e, n, r] * v[m, r],
+ *     v[m, r]   = sum_k A[e, r, k] * x[m, k]
+ * for 0 <= e < E.  ids[m] = -1 is a row without an adapter: its out is base, bit
+ * for bit.  Any other id cannot be checked on the host: that row is NaN and
+ * nothing is read out of bounds.  Rows may name their adapters in any order;
+ * rows of one request beside one another are the fast case.
+ * A [E, R, K] and B [E, N, R]: device, format t, contiguous.  R is the pool's
+ * common rank; `ranks` (device int32 [E], or NULL: R for all) gives each
+ * adapter's own, clamped to [0, R]: what lies behind it is not used, whatever
+ * it holds.  `scales` (device fp32 [E], or NULL: 1).  x [M, K]: the fp32
+ * activations that the projection quantized.  base [M, N] fp32 with row stride
+ * ld_base >= N elements (mul_mat's output, or a column range of it); out
+ * likewise with ld_out.  out may be base itself (then ld_out = ld_base: the
+ * update in place), otherwise out must not overlap any input (QMM_EINVAL).
+ * Both products are computed in fp32 (x is not rounded); K is split over
+ * workgroups and the parts are added in a fixed order: results do not depend
+ * on timing.  workspace: device, at least qmm_lora_workspace_bytes(M, R, K, E),
+ * overwritten; calls that may overlap need one each.
+ * Requires K a multiple of 32, 1 <= R <= 256, 1 <= E <= 4096.  x_bytes, base_bytes
+ * and out_bytes count from the given pointers; the last row needs N elements. */
+qmm_status qmm_lora_add(qmm_float_type t, const void *A, size_t a_bytes, const void *B, size_t b_bytes,
+                        int64_t E, int64_t R, const float *scales, const int32_t *ranks,
+                        const float *x, size_t x_bytes, const int32_t *ids,
+                        const float *base, size_t base_bytes, int64_t ld_base,
+                        float *out, size_t out_bytes, int64_t ld_out,
+                        int64_t M, int64_t N, int64_t K,
+                        void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of the workspace qmm_logprobs needs; 0 where it needs none (many rows),
+ * and for invalid arguments. */
+size_t qmm_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);
+
+/* Log probabilities of rows of logits x [M, V] (format t, row stride ld >= V
+ * elements; mul_mat's output with t = QMM_F32).  With z = scale * x over the
+ * allowed tokens of a row:
+ *     log p_i = z_i - log sum_j e^{z_j},   entropy = -sum_i p_i log p_i   (natural log)
+ * token_logprobs[m, g] = log p of tokens[m, g] (device int32 [M, G]; G = 0: both
+ * NULL).  An id outside [0, V) gives NaN and reads nothing.
+ * entropy: [M], or NULL.
+ * top_ids, top_logprobs [M, k]: the k largest logits, largest first, the lowest
+ * index first among equals (0 and -0 are equal); k = 0: both NULL.  Places that
+ * no token takes (fewer than k are allowed and above -inf) hold -1 and -inf.
+ * mask: bit i % 32 of word i / 32 of a row allows token i; words from mask row
+ * stride mask_ld (words; 0: one row of mask for all rows), or NULL: all allowed.
+ * What a masked place holds does not matter.  A masked token has log p = -inf.
+ * A row in which nothing is allowed or all is -inf: log p = -inf, entropy 0.
+ * A NaN or +inf among the allowed logits makes the row's log p and entropy NaN;
+ * NaN never enters the top list.
+ * Statistics are fp32; x is read once.  scale (one over the temperature): above
+ * 0, at most 1e30.  Requires V <= 2^24, k <= 64, M < 2^24, M*G < 2^31.
+ * Outputs must not overlap inputs or one another.
+ * workspace: device, qmm_logprobs_workspace_bytes(M, V, k) bytes (NULL where
+ * that is 0), overwritten; calls that may overlap need one each. */
+qmm_status qmm_logprobs(qmm_float_type t, const void *logits, size_t logits_bytes, int64_t ld,
+                        int64_t M, int64_t V, float scale,
+                        const uint32_t *mask, size_t mask_bytes, int64_t mask_ld,
+                        const int32_t *tokens, int64_t G, float *token_logprobs, float *entropy,
+                        int64_t k, int32_t *top_ids, float *top_logprobs,
+                        void *workspace, size_t ws_bytes, void *stream);
 
 /* Static description of a status code. */
 const char *qmm_status_string(qmm_status s);
