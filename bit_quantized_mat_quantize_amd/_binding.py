@@ -8,6 +8,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -320,26 +321,43 @@ def debug_block_sums(wfmt: str, w, y, M: int, N: int, K: int, layout: str = "can
 
 # ---- the operators beside the projections.  They run on the device of their
 # tensors (whichever is current) and on `stream`, by default that device's
-# current one; what they allocate belongs to that stream.
+# current one; what they allocate belongs to that stream.  A small call costs
+# the host more than the GPU (one launch 3 us, one tensor 1.7 us), so the checks
+# are cheap where nothing is wrong.
 
-def _on(stream, **tensors):
-    """The context to allocate and launch in; every tensor has to be on one GPU."""
-    import torch
-    device = None
+_HERE = contextlib.nullcontext()
+
+
+def _gpu(**tensors) -> int:
+    """The index of the one GPU that every tensor is on (None: not given)."""
+    index = None
     for name, t in tensors.items():
         if t is None:
             continue
-        if not t.is_cuda:
+        i = t.get_device()
+        if i < 0:
             raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if index is None:
+            index = i
+        elif i != index:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    return index
+
+
+def _on(index: int, stream):
+    """The context to allocate and launch in."""
+    import torch
     if stream is None:
-        return torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     return torch.cuda.stream(stream)
+
+
+def _current(index: int) -> int:
+    """The device's current stream as a hipStream_t (torch.cuda.current_stream builds an object first: 2 us)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _float_type(t, name: str) -> int:
@@ -350,24 +368,21 @@ def _float_type(t, name: str) -> int:
     return types[t.dtype]
 
 
-def _is(t, name: str, dtype, shape) -> None:
-    """A contiguous tensor of this type and shape (None: not given, fine)."""
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _is(t, name: str, dtype, *shape) -> None:
+    """A contiguous tensor of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, {dtype} and of shape {shape} (got {t.dtype}, {tuple(t.shape)}, "
+                         f"strides {t.stride()})")
 
 
-def _rows(t, name: str):
-    """(pointer, bytes from it to the last row's end, row stride) of a 2-D tensor with unit column stride."""
-    M, N = t.shape
-    if N > 1 and t.stride(1) != 1:
+def _rows(t, name: str, dtype, M: int, N: int):
+    """(pointer, bytes from it to the last row's end, row stride) of a matrix with unit column stride."""
+    if t.dtype is not dtype or t.shape != (M, N):
+        raise ValueError(f"{name} must be {dtype} of shape {(M, N)} (got {t.dtype}, {tuple(t.shape)})")
+    step, column = t.stride()
+    if N > 1 and column != 1:
         raise ValueError(f"{name} must have unit stride along its rows")
-    ld = t.stride(0) if M > 1 else N
+    ld = step if M > 1 else N
     return t.data_ptr(), ((M - 1) * ld + N) * t.element_size() if M and N else 0, ld
 
 
@@ -382,14 +397,17 @@ def embed_rows(wfmt: str, w, ids, N: int, K: int, layout: str = "canonical", sca
     An id outside [0, N) gives a row of NaN."""
     import torch
     (T,) = ids.shape
-    _is(ids, "ids", torch.int32, (T,))
-    with _on(stream, ids=ids, w=w, out=out):
+    _is(ids, "ids", torch.int32, T)
+    if not w.is_contiguous():
+        raise ValueError("w must be contiguous")
+    index = _gpu(ids=ids, w=w, out=out)
+    with _on(index, stream):
         if out is None:
             out = torch.empty((T, K), dtype=torch.float32, device=ids.device)
-        _is(out, "out", torch.float32, (T, K))
-        pw, nw = _dev(w, "w")
-        _check(load().qmm_embed_rows(_WEIGHT[wfmt], pw, nw, _LAYOUT[layout], ids.data_ptr(), T, scale,
-                                     out.data_ptr(), T * K * 4, N, K, _stream(stream)), "qmm_embed_rows")
+        else:
+            _is(out, "out", torch.float32, T, K)
+        _check(load().qmm_embed_rows(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], ids.data_ptr(), T, scale,
+                                     out.data_ptr(), T * K * 4, N, K, _current(index)), "qmm_embed_rows")
     return out
 
 
@@ -406,27 +424,29 @@ def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=No
     [-1, E) gives a row of NaN."""
     import torch
     (M, N), (E, R, K) = base.shape, A.shape
-    _is(x, "x", torch.float32, (M, K))
-    _is(A, "A", A.dtype, (E, R, K))
-    _is(B, "B", A.dtype, (E, N, R))
-    _is(ids, "ids", torch.int32, (M,))
-    _is(scales, "scales", torch.float32, (E,))
-    _is(ranks, "ranks", torch.int32, (E,))
-    if base.dtype != torch.float32:
-        raise ValueError(f"base must be float32 (got {base.dtype})")
-    with _on(stream, base=base, x=x, A=A, B=B, ids=ids, scales=scales, ranks=ranks, out=out, workspace=workspace):
+    f32, i32 = torch.float32, torch.int32
+    _is(x, "x", f32, M, K)
+    _is(A, "A", A.dtype, E, R, K)
+    _is(B, "B", A.dtype, E, N, R)
+    _is(ids, "ids", i32, M)
+    if scales is not None:
+        _is(scales, "scales", f32, E)
+    if ranks is not None:
+        _is(ranks, "ranks", i32, E)
+    pb, nb, ldb = _rows(base, "base", f32, M, N)
+    index = _gpu(base=base, x=x, A=A, B=B, ids=ids, scales=scales, ranks=ranks, out=out, workspace=workspace)
+    with _on(index, stream):
         if out is None:
-            out = torch.empty((M, N), dtype=torch.float32, device=base.device)
-        elif out.dtype != torch.float32 or tuple(out.shape) != (M, N):
-            raise ValueError(f"out must be float32 of shape {(M, N)} (got {out.dtype}, {tuple(out.shape)})")
+            out = torch.empty((M, N), dtype=f32, device=base.device)
+        po, no, ldo = _rows(out, "out", f32, M, N)
         if workspace is None:
             workspace = torch.empty(max(lora_workspace_bytes(M, R, K, E), 16), dtype=torch.uint8, device=base.device)
-        pb, nb, ldb = _rows(base, "base")
-        po, no, ldo = _rows(out, "out")
-        pw, nw = _dev(workspace, "workspace")
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         _check(load().qmm_lora_add(_float_type(A, "A"), A.data_ptr(), A.nbytes, B.data_ptr(), B.nbytes, E, R,
                                    _ptr(scales), _ptr(ranks), x.data_ptr(), x.nbytes, ids.data_ptr(), pb, nb, ldb,
-                                   po, no, ldo, M, N, K, pw, nw, _stream(stream)), "qmm_lora_add")
+                                   po, no, ldo, M, N, K, workspace.data_ptr(), workspace.nbytes, _current(index)),
+               "qmm_lora_add")
     return out
 
 
@@ -444,33 +464,39 @@ def logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, mask=None, ent
     allows token i.  scale multiplies the logits (one over the temperature).  What is not asked for is None."""
     import torch
     M, V = logits.shape
+    f32, i32 = torch.float32, torch.int32
     G = 0
     if tokens is not None:
-        if tokens.dim() not in (1, 2) or tokens.shape[0] != M:
-            raise ValueError(f"tokens must have shape ({M},) or ({M}, G) (got {tuple(tokens.shape)})")
-        G = tokens.shape[1] if tokens.dim() == 2 else 1
-        _is(tokens, "tokens", torch.int32, tokens.shape)
+        shape = tokens.shape
+        if len(shape) not in (1, 2) or shape[0] != M:
+            raise ValueError(f"tokens must have shape ({M},) or ({M}, G) (got {tuple(shape)})")
+        G = shape[1] if len(shape) == 2 else 1
+        _is(tokens, "tokens", i32, *shape)
     mask_ld, mask_bytes = 0, 0
     if mask is not None:
         rows, words = (1, mask.shape[0]) if mask.dim() == 1 else mask.shape
         if rows not in (1, M) or words < (V + 31) // 32:
             raise ValueError(f"mask must have 1 or {M} rows of at least {(V + 31) // 32} words (got {tuple(mask.shape)})")
-        _is(mask, "mask", torch.int32, mask.shape)
+        _is(mask, "mask", i32, *mask.shape)
         mask_ld, mask_bytes = words if rows > 1 else 0, mask.nbytes
-    with _on(stream, logits=logits, tokens=tokens, mask=mask, workspace=workspace):
-        def new(*shape, dtype=torch.float32):
-            return torch.empty(shape, dtype=dtype, device=logits.device)
-
-        lp = None if tokens is None else new(*tokens.shape)
-        ent = new(M) if entropy else None
-        top_ids, top_lp = (new(M, k, dtype=torch.int32), new(M, k)) if k > 0 else (None, None)
-        need = logprobs_workspace_bytes(M, V, k)
-        if workspace is None and need:
-            workspace = new(need, dtype=torch.uint8)
-        px, nx, ld = _rows(logits, "logits")
+    px, nx, ld = _rows(logits, "logits", logits.dtype, M, V)
+    index = _gpu(logits=logits, tokens=tokens, mask=mask, workspace=workspace)
+    device = logits.device
+    with _on(index, stream):
+        lp = None if tokens is None else torch.empty(shape, dtype=f32, device=device)
+        ent = torch.empty((M,), dtype=f32, device=device) if entropy else None
+        top_ids = top_lp = None
+        if k > 0:
+            top_ids = torch.empty((M, k), dtype=i32, device=device)
+            top_lp = torch.empty((M, k), dtype=f32, device=device)
+        if workspace is None:
+            need = logprobs_workspace_bytes(M, V, k)
+            workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         _check(load().qmm_logprobs(_float_type(logits, "logits"), px, nx, ld, M, V, scale, _ptr(mask), mask_bytes,
                                    mask_ld, _ptr(tokens), G, _ptr(lp), _ptr(ent), k, _ptr(top_ids), _ptr(top_lp),
-                                   _ptr(workspace), 0 if workspace is None else workspace.nbytes, _stream(stream)),
+                                   _ptr(workspace), 0 if workspace is None else workspace.nbytes, _current(index)),
                "qmm_logprobs")
     return lp, ent, top_ids, top_lp
 

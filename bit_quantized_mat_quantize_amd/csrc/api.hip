@@ -794,12 +794,8 @@ qmm_status qmm_embed_rows(qmm_weight_type t, const void *w, size_t w_bytes, qmm_
                          "embed_rows launch");
 }
 
-// the pool's sizes are bounded as mul_mat_id's: E by the same limit, R so that a
-// tile's v (16 rows) stays in 17 KiB of LDS
-constexpr int64_t kLoraMaxRank = 256;
-
 size_t qmm_lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E) {
-    if (M < 1 || M > kMaxRows || R < 1 || R > kLoraMaxRank || K < 32 || K % 32 || K > kMaxK || E < 1 ||
+    if (M < 1 || M > kMaxRows || R < 1 || R > qmm::lora_max_rank() || K < 32 || K % 32 || K > kMaxK || E < 1 ||
         E > qmm::kMoeMaxExperts)
         return 0;
     return (size_t)qmm::lora_workspace_bytes(M, R, K, E);
@@ -814,8 +810,8 @@ qmm_status qmm_lora_add(qmm_float_type t, const void *A, size_t a_bytes, const v
     if (!size) return fail(QMM_EUNSUPPORTED, "unknown adapter type %d", (int)t);
     if (E < 1 || E > qmm::kMoeMaxExperts)
         return fail(QMM_EUNSUPPORTED, "E = %lld adapters; 1 <= E <= %d", (long long)E, qmm::kMoeMaxExperts);
-    if (R < 1 || R > kLoraMaxRank)
-        return fail(QMM_EUNSUPPORTED, "R = %lld; 1 <= R <= %lld", (long long)R, (long long)kLoraMaxRank);
+    if (R < 1 || R > qmm::lora_max_rank())
+        return fail(QMM_EUNSUPPORTED, "R = %lld; 1 <= R <= %lld", (long long)R, (long long)qmm::lora_max_rank());
     QMM_TRY(check_rows("M", M));
     QMM_TRY(check_rows("N", N));
     QMM_TRY(check_k(K, 32));

@@ -135,6 +135,14 @@ hipError_t launch_layout(const uint8_t *w, bool repacked, int64_t NB, int64_t ds
                     : launch<FMT, false, QPT>(w, NB, dsec, ids, T, scale, out, N, K, s);
 }
 
+template <int FMT>
+hipError_t launch_quads(const uint8_t *w, bool repacked, int64_t NB, int64_t dsec, const int32_t *ids, int64_t T,
+                        float scale, float *out, int64_t N, int64_t K, hipStream_t s) {
+    if (T * (K / 4) >= 4 * 2048 * kThreads && K >= 16 * kThreads)
+        return launch_layout<FMT, 4>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
+    return launch_layout<FMT, 1>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
+}
+
 }  // namespace
 
 hipError_t launch_embed_rows(int fmt, const uint8_t *w, bool repacked, const int32_t *ids, int64_t T, float scale,
@@ -142,10 +150,10 @@ hipError_t launch_embed_rows(int fmt, const uint8_t *w, bool repacked, const int
     const int64_t NB = N * (K / (fmt == F_Q4_0 ? QK4_0 : QK_K));
     const int64_t dsec = ((fmt == F_Q2_K ? 4 : 2) * NB + 255) / 256 * 256;  // not used by Q4_K
     switch (fmt) {
-        case F_Q4_0: return launch_layout<F_Q4_0, 1>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
-        case F_Q4_K: return launch_layout<F_Q4_K, 1>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
-        case F_Q6_K: return launch_layout<F_Q6_K, 1>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
-        default: return launch_layout<F_Q2_K, 1>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
+        case F_Q4_0: return launch_quads<F_Q4_0>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
+        case F_Q4_K: return launch_quads<F_Q4_K>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
+        case F_Q6_K: return launch_quads<F_Q6_K>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
+        default: return launch_quads<F_Q2_K>(w, repacked, NB, dsec, ids, T, scale, out, N, K, s);
     }
 }
 

@@ -29,8 +29,9 @@
 namespace qmm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kBatch = 16;     // logits per thread and batch
 constexpr int kList = 256;     // keys a wavefront's list holds
 constexpr int kMaxK = 64;      // a cut leaves at most kMaxK, and 64 may be appended at once
 constexpr int kMaxSplits = 64;
@@ -44,6 +45,22 @@ struct BF16 {
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(_Float16 v) { return (float)v; }
 __device__ __forceinline__ float to_f32(BF16 v) { return __uint_as_float((uint32_t)v.b << 16); }
+
+// the logits of a 16-byte piece
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 p, float (&y)[16 / sizeof(T)]) {
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            y[i] = __uint_as_float(w[i]);
+        } else {
+            const uint16_t h[2] = {(uint16_t)w[i], (uint16_t)(w[i] >> 16)};
+            y[2 * i] = to_f32(__builtin_bit_cast(T, h[0]));
+            y[2 * i + 1] = to_f32(__builtin_bit_cast(T, h[1]));
+        }
+    }
+}
 
 // ---- keys.  order(x) is monotone in x, and order(lowest finite) > 0; a key of 0 is no token.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -76,6 +93,7 @@ __device__ __forceinline__ void wave_lds_fence() {
 template <typename U, int n>
 __device__ __forceinline__ U kth_bound(const U (&v)[n], int k) {
     U bound = 0;
+#pragma unroll 1
     for (int bit = (int)sizeof(U) * 8 - 1; bit >= 0; --bit) {
         const U next = bound | (U(1) << bit);
         int c = 0;
@@ -149,13 +167,6 @@ struct Stats {
         s = f * s;
         m = to;
     }
-    __device__ __forceinline__ void join(Stats o, float c) {
-        const float to = fmaxf(m, o.m);
-        rescale(to, c);
-        o.rescale(to, c);
-        s += o.s;
-        t += o.t;
-    }
     __device__ __forceinline__ void join_wave(float c) {
         rescale(wave_max(m), c);
         s = wave_sum(s);
@@ -175,72 +186,80 @@ struct Stats {
 
 __device__ __forceinline__ bool allowed(const uint32_t *mask, int i) { return mask[i >> 5] >> (i & 31) & 1; }
 
-// ---- the workgroup's lists, ranked: f(rank, key) for the k best, in any order.
-// Every thread calls it; lists hold at most k keys each (k <= 64).
+// ---- keys of the workgroup, at most one per thread, ranked: f(rank, key) for the
+// k best, in any order.  Every thread calls it; returns the number of keys.
 template <typename F>
-__device__ __forceinline__ int rank_lists(const List &l, uint64_t *all, int *counts, F f) {
+__device__ __forceinline__ int rank_keys(uint64_t key, bool has, int k, uint64_t *all, int *counts, F f) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (lane == 0) counts[wave] = l.count;
-    const uint64_t key = lane < l.count ? l.keys[lane] : 0;
+    const uint64_t who = __ballot(has);
+    if (lane == 0) counts[wave] = __popcll(who);
     __syncthreads();
-    int off = 0, n = 0;
+    int at = lanes_below(who), n = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        off += w < wave ? counts[w] : 0;
+        at += w < wave ? counts[w] : 0;
         n += counts[w];
     }
-    if (lane < l.count) all[off + lane] = key;
+    if (has) all[at] = key;
     __syncthreads();
     int rank = 0;
+#pragma unroll 8
     for (int i = 0; i < n; ++i) rank += all[i] > key;
-    if (lane < l.count && rank < l.k) f(rank, key);
+    if (has && rank < k) f(rank, key);
     return n;
 }
 
-// ---- results of one row
-__device__ __forceinline__ void finish_row(const LogprobArgs &a, const Stats &st, int64_t row, const List &l,
-                                           uint64_t *all, int *counts) {
-    const bool any = !(st.m == -kInf && st.s == 0.f);
+// ---- results of one row.  A thread's first given token and its logit are
+// fetched before the statistics are known.
+struct Given {
+    float x;
+    bool valid;
+};
+template <typename T>
+__device__ __forceinline__ Given given_token(const LogprobArgs &a, int64_t row, int64_t i) {
+    Given g{-kInf, false};
+    if (i < a.G) {
+        const int tok = a.tokens[row * a.G + i];
+        g.valid = tok >= 0 && tok < a.V;
+        if (g.valid && (a.mask == nullptr || allowed(a.mask + row * a.mask_ld, tok)))
+            g.x = to_f32(static_cast<const T *>(a.logits)[row * a.ld + tok]);
+    }
+    return g;
+}
+template <typename T>
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, const Stats &st, int64_t row, Given g, uint64_t key,
+                                           bool has, uint64_t *all, int *counts) {
     if (a.entropy != nullptr && threadIdx.x == 0) a.entropy[row] = st.entropy();
+    for (int64_t i = threadIdx.x; i < a.G; i += kThreads) {
+        if (i >= kThreads) g = given_token<T>(a, row, i);
+        a.token_logprobs[row * a.G + i] = g.valid ? st.logprob(g.x, a.scale) : __builtin_nanf("");
+    }
     if (a.k > 0) {
         int32_t *ids = a.top_ids + row * a.k;
         float *lps = a.top_logprobs + row * a.k;
-        const int n = rank_lists(l, all, counts, [&](int rank, uint64_t key) {
-            ids[rank] = (int32_t)~(uint32_t)key;
-            lps[rank] = st.logprob(of_order((uint32_t)(key >> 32)), a.scale);
+        const int n = rank_keys(key, has, (int)a.k, all, counts, [&](int rank, uint64_t best) {
+            ids[rank] = (int32_t)~(uint32_t)best;
+            lps[rank] = st.logprob(of_order((uint32_t)(best >> 32)), a.scale);
         });
         for (int i = n + (int)threadIdx.x; i < a.k; i += kThreads) {  // fewer than k tokens have a probability
             ids[i] = -1;
-            lps[i] = any && st.s != st.s ? st.s : -kInf;
+            lps[i] = st.s != st.s ? st.s : -kInf;
         }
     }
 }
-template <typename T>
-__device__ __forceinline__ void given_tokens(const LogprobArgs &a, const Stats &st, int64_t row) {
-    const T *x = static_cast<const T *>(a.logits) + row * a.ld;
-    const uint32_t *mask = a.mask != nullptr ? a.mask + row * a.mask_ld : nullptr;
-    for (int64_t i = threadIdx.x; i < a.G; i += kThreads) {
-        const int tok = a.tokens[row * a.G + i];
-        float lp = __builtin_nanf("");
-        if (tok >= 0 && tok < a.V)
-            lp = st.logprob(mask == nullptr || allowed(mask, tok) ? to_f32(x[tok]) : -kInf, a.scale);
-        a.token_logprobs[row * a.G + i] = lp;
-    }
-}
 
-// ---- the pass.  Workgroup = (row, split); a split is a range of 16-byte pieces
-// of the row, counted from the 16-byte boundary at or below the row's start.
-template <typename T>
+// ---- the pass.  Workgroup = (row, split).  A row's whole 16-byte pieces,
+// counted from the 16-byte boundary at or below its start, are divided among the
+// splits; the up to 14 logits before the first and behind the last (rows need
+// not start or end on a boundary) are a batch of their own in split 0.
+template <typename T, bool MASK>
 __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int splits) {
     constexpr int VEC = 16 / sizeof(T);
-    constexpr int U = 16 / VEC;  // pieces per thread and batch: 16 logits
+    constexpr int U = kBatch / VEC;  // pieces per thread and batch
     __shared__ uint64_t lists[kWaves][kList];
-    __shared__ uint64_t all[kWaves * kMaxK];
+    __shared__ uint64_t all[kThreads];
     __shared__ int counts[kWaves];
     __shared__ Stats wave_stats[kWaves];
-    struct alignas(16) Pack {
-        T e[VEC];
-    };
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x / (uint32_t)splits;
@@ -250,42 +269,60 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
     const int64_t first = row * a.ld;
     const int lead = (int)(first % VEC);  // elements between the boundary and the row's start
     const T *x = static_cast<const T *>(a.logits) + (first - lead);
-    const uint32_t *mask = a.mask != nullptr ? a.mask + row * a.mask_ld : nullptr;
-    const int pieces = (lead + V + VEC - 1) / VEC;
-    const int per = (pieces + splits - 1) / splits;
-    const int j0 = split * per, j1 = j0 + per < pieces ? j0 + per : pieces;
+    const uint32_t *mask = MASK ? a.mask + row * a.mask_ld : nullptr;
+    Given given{-kInf, false};
+    if (splits == 1) given = given_token<T>(a, row, threadIdx.x);
+
+    const int f0 = lead > 0 ? 1 : 0, f1 = (lead + V) / VEC;  // the whole pieces
+    const int whole = f1 > f0 ? f1 - f0 : 0;
+    const int per = (whole + splits - 1) / splits;
+    const int j0 = f0 + split * per, j1 = j0 + per < f0 + whole ? j0 + per : f0 + whole;
+    const int head = whole > 0 ? f0 * VEC - lead : V;  // logits [0, head) and [tail, V) are in no whole piece
+    const int tail = whole > 0 ? f1 * VEC - lead : V;
+    const bool edges = split == 0 && head + V - tail > 0;
 
     Stats st{-kInf, 0.f, 0.f};
     List l{lists[wave], 0, (int)a.k, 0, -__FLT_MAX__};
-    for (int jb = j0; jb < j1; jb += kThreads * U) {
-        float v[U * VEC];
+    const int batches = (j1 - j0 + kThreads * U - 1) / (kThreads * U);
+    for (int it = 0; it < batches + (edges ? 1 : 0); ++it) {
+        float v[kBatch];
+        int index0;      // of v[0]; v[u * VEC + q] follows at u * kThreads * VEC + q
+        int filled = 1;  // pieces per thread with anything in them: a split's last batch is seldom full
+        if (it < batches) {
+            const int jt = j0 + it * kThreads * U + (int)threadIdx.x;
+            index0 = jt * VEC - lead;
+            filled = (j1 - (jt - (int)threadIdx.x) + kThreads - 1) / kThreads;
+            uint4 p[U];
+            uint32_t bits[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = jb + u * kThreads + threadIdx.x;
-            const int i0 = j * VEC - lead;  // index of the piece's first logit
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) v[u * VEC + q] = -kInf;
-            if (j < j1) {
-                if (i0 >= 0 && i0 + VEC <= V) {
-                    const Pack p = *reinterpret_cast<const Pack *>(x + (int64_t)j * VEC);
-                    uint32_t bits = ~0u;
-                    if (mask != nullptr) {
-                        const uint32_t w0 = mask[i0 >> 5], w1 = mask[(i0 + VEC - 1) >> 5];
-                        bits = (uint32_t)((((uint64_t)w1 << 32) | w0) >> (i0 & 31));
-                    }
-#pragma unroll
-                    for (int q = 0; q < VEC; ++q) v[u * VEC + q] = bits >> q & 1 ? to_f32(p.e[q]) : -kInf;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < VEC; ++q)
-                        if (i0 + q >= 0 && i0 + q < V && (mask == nullptr || allowed(mask, i0 + q)))
-                            v[u * VEC + q] = to_f32(x[(int64_t)j * VEC + q]);
+            for (int u = 0; u < U; ++u) {  // pieces past the split's end read its last one
+                const int at = jt + u * kThreads < j1 ? jt + u * kThreads : j1 - 1;
+                p[u] = ld16(x + (int64_t)at * VEC);
+                if (MASK) {
+                    const int i = at * VEC - lead;
+                    const uint32_t w0 = mask[i >> 5], w1 = mask[(i + VEC - 1) >> 5];
+                    bits[u] = (uint32_t)((((uint64_t)w1 << 32) | w0) >> (i & 31));
                 }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool in = jt + u * kThreads < j1;
+                float y[VEC];
+                unpack<T>(p[u], y);
+#pragma unroll
+                for (int q = 0; q < VEC; ++q)
+                    v[u * VEC + q] = in && (!MASK || (bits[u] >> q & 1)) ? y[q] : -kInf;
+            }
+        } else {
+            index0 = (int)threadIdx.x < head ? (int)threadIdx.x : tail + (int)threadIdx.x - head;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) v[i] = -kInf;
+            if (index0 < V && (!MASK || allowed(mask, index0))) v[0] = to_f32(x[lead + index0]);
         }
+
         float top = -kInf;
 #pragma unroll
-        for (int i = 0; i < U * VEC; ++i) top = fmaxf(top, v[i]);
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, v[i]);
         if (top > st.m) st.rescale(top, c);
         // all of them -inf so far: any finite number in the maximum's place gives e = 0
         const float m = st.m == -kInf ? 0.f : st.m;
@@ -293,50 +330,55 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
         // small one would be rounded at its size
         float bs = 0.f, bt = 0.f;
 #pragma unroll
-        for (int i = 0; i < U * VEC; ++i) {
-            const float d = (v[i] - m) * c;
-            const float e = __builtin_amdgcn_exp2f(d);
-            bs += e;
-            bt += fmaxf(d, -1.0e4f) * e;  // e is 0 there: keeps -inf * 0 out
+        for (int u = 0; u < U; ++u) {
+            if (u > 0 && u >= filled) break;
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) {
+                const float d = (v[u * VEC + q] - m) * c;
+                const float e = __builtin_amdgcn_exp2f(d);
+                bs += e;
+                bt = __builtin_fmaf(fmaxf(d, -1.0e4f), e, bt);  // e is 0 there: keeps -inf * 0 out
+            }
         }
         st.s += bs;
         st.t += bt;
-        if (a.k > 0) {
-            if (jb == j0) {
+
+        if (a.k > 0 && __ballot(top >= l.least) != 0) {
+            if (l.bound == 0) {
                 const uint32_t o[1] = {top > -kInf ? order_of(top) : 0};
                 l.raise((uint64_t)kth_bound(o, l.k) << 32);
             }
-            if (__ballot(top >= l.least) != 0) {
+            uint32_t left = 0;  // which of this lane's logits may enter
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+            for (int i = 0; i < kBatch; ++i) left |= v[i] >= l.least ? 1u << i : 0;
+            while (__ballot(left != 0) != 0) {
+                const int i = left != 0 ? __builtin_ctz(left) : 0;
+                float y = v[0];
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) {
-                        const float y = v[u * VEC + q];
-                        if (__ballot(y >= l.least) != 0)
-                            l.add(key_of(y, (uint32_t)((jb + u * kThreads + (int)threadIdx.x) * VEC - lead + q)),
-                                  y >= l.least);
-                    }
+                for (int q = 1; q < kBatch; ++q) y = i == q ? v[q] : y;
+                l.add(key_of(y, (uint32_t)(index0 + i / VEC * (kThreads * VEC) + i % VEC)), left != 0);
+                left &= left - 1;
             }
         }
     }
-    if (a.k > 0) l.cut();
+    if (l.count > kWave) l.cut();
     st.join_wave(c);
     if (lane == 0) wave_stats[wave] = st;
     __syncthreads();
-    st = wave_stats[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) st.join(wave_stats[w], c);
+    st = lane < kWaves ? wave_stats[lane] : Stats{-kInf, 0.f, 0.f};
+    st.join_wave(c);
 
+    const bool has = lane < l.count;
+    const uint64_t key = has ? l.keys[lane] : 0;
     if (splits == 1) {
-        finish_row(a, st, row, l, all, counts);
-        given_tokens<T>(a, st, row);
+        finish_row<T>(a, st, row, given, key, has, all, counts);
         return;
     }
     const int64_t part = row * splits + split;
     if (threadIdx.x == 0) a.ws_stats[part] = make_float4(st.m, st.s, st.t, 0.f);
     if (a.k > 0) {
         uint64_t *out = a.ws_keys + part * a.k;
-        const int n = rank_lists(l, all, counts, [&](int rank, uint64_t key) { out[rank] = key; });
+        const int n = rank_keys(key, has, (int)a.k, all, counts, [&](int rank, uint64_t best) { out[rank] = best; });
         for (int i = n + (int)threadIdx.x; i < a.k; i += kThreads) out[i] = 0;
     }
 }
@@ -345,43 +387,54 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_logprobs_merge(const LogprobArgs a, int splits) {
     __shared__ uint64_t lists[kWaves][kList];
-    __shared__ uint64_t all[kWaves * kMaxK];
+    __shared__ uint64_t all[kThreads];
     __shared__ int counts[kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x;
     const float c = a.scale * kLog2e;
+    const Given given = given_token<T>(a, row, threadIdx.x);
+    const int total = splits * (int)a.k;
+    const uint64_t *in = a.ws_keys + row * total;
+    uint64_t key = (int)threadIdx.x < total ? in[threadIdx.x] : 0;
     Stats st{-kInf, 0.f, 0.f};
     if (lane < splits) {
         const float4 p = a.ws_stats[row * splits + lane];
         st = Stats{p.x, p.y, p.z};
     }
     st.join_wave(c);
-    List l{lists[wave], 0, (int)a.k, 0, -__FLT_MAX__};
-    if (a.k > 0) {
+    bool has = key != 0;
+    if (total > kThreads) {  // more keys than threads: each wavefront's k best of its share
         constexpr int n = kMaxSplits * kMaxK / kThreads;
-        const int total = splits * (int)a.k;
-        const uint64_t *in = a.ws_keys + row * total;
-        uint64_t v[n], top[1] = {0};
+        List l{lists[wave], 0, (int)a.k, 0, -__FLT_MAX__};
+        uint64_t v[n], best = key;
+        v[0] = key;
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const int at = i * kThreads + threadIdx.x;
+        for (int i = 1; i < n; ++i) {
+            const int at = i * kThreads + (int)threadIdx.x;
             v[i] = at < total ? in[at] : 0;
-            top[0] = v[i] > top[0] ? v[i] : top[0];
+            best = v[i] > best ? v[i] : best;
         }
-        l.raise(kth_bound(top, l.k));
+        const uint32_t o[1] = {(uint32_t)(best >> 32)};
+        l.raise((uint64_t)kth_bound(o, l.k) << 32);
+        for (int i = 0; i * kThreads < total; ++i) {
+            uint64_t y = v[0];
 #pragma unroll
-        for (int i = 0; i < n; ++i)
-            if (i * kThreads < total) l.add(v[i], v[i] != 0);
-        l.cut();
+            for (int q = 1; q < n; ++q) y = i == q ? v[q] : y;
+            l.add(y, y != 0);
+        }
+        if (l.count > kWave) l.cut();
+        has = lane < l.count;
+        key = has ? l.keys[lane] : 0;
     }
-    finish_row(a, st, row, l, all, counts);
-    given_tokens<T>(a, st, row);
+    finish_row<T>(a, st, row, given, key, has, all, counts);
 }
 
-// enough workgroups to fill the chip (four per CU), each with at least 2048 logits
+// as many workgroups as run at once (four of eight wavefronts per CU) and no more,
+// each with at least one batch: 513 rows of 50257 in two splits, 1026 workgroups,
+// took 37 us for the two that had to wait, in one 
 int splits_of(int64_t M, int64_t V) {
-    int64_t s = (1024 + M - 1) / M;
-    const int64_t most = (V + 2047) / 2048;
+    int64_t s = M < 1024 ? 1024 / M : 1;
+    const int64_t most = (V + kThreads * kBatch - 1) / (kThreads * kBatch);
     s = s > most ? most : s;
     return (int)(s > kMaxSplits ? kMaxSplits : s);
 }
@@ -389,7 +442,9 @@ int splits_of(int64_t M, int64_t V) {
 template <typename T>
 hipError_t both(const LogprobArgs &a, hipStream_t s) {
     const int splits = splits_of(a.M, a.V);
-    hipLaunchKernelGGL(k_logprobs<T>, dim3((unsigned)(a.M * splits)), dim3(kThreads), 0, s, a, splits);
+    const dim3 grid((unsigned)(a.M * splits));
+    if (a.mask != nullptr) hipLaunchKernelGGL((k_logprobs<T, true>), grid, dim3(kThreads), 0, s, a, splits);
+    else hipLaunchKernelGGL((k_logprobs<T, false>), grid, dim3(kThreads), 0, s, a, splits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || splits == 1) return e;
     hipLaunchKernelGGL(k_logprobs_merge<T>, dim3((unsigned)a.M), dim3(kThreads), 0, s, a, splits);

@@ -14,8 +14,8 @@
 // lanes, takes the distinct ones one after another (ballot), and stores the rows
 // that match.  Rows of one request are neighbours in a prefill batch, so most
 // tiles have one adapter and nothing is sorted; in a decode batch each row may
-// have its own, and `zsplit` workgroups per tile take the distinct adapters
-// z, z + zsplit, ... so that they run beside one another.
+// have its own, and `zsplit` workgroups share a tile so that its adapters run
+// beside one another.
 //
 // The products run on the fp32 matrix instruction (v_mfma_f32_16x16x4_f32): x
 // is fp32 and the result is, so x is not rounded to 16 bits, and A and B in
@@ -34,9 +34,12 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+constexpr int kShrinkThreads = 512;
 constexpr int kTileRows = 16;
 constexpr int kStep = 32;  // k per wavefront step of the shrink
+constexpr int kMaxRank = 256;
+constexpr int kNT = 4;     // 16-column tiles of a wavefront's group in the expand
+constexpr int kGroupCols = kThreads / kWave * 16 * kNT;  // columns of a workgroup's group
 
 // ---- element types: T is the storage type of A and B
 struct BF16 {
@@ -48,13 +51,12 @@ __device__ __forceinline__ float to_f32(BF16 v) { return __uint_as_float((uint32
 
 // n consecutive elements at an address aligned to the whole load
 template <typename T, int n>
-__device__ __forceinline__ void load_n(const T *p, float (&v)[n]) {
-    struct alignas(sizeof(T) * n < 16 ? sizeof(T) * n : 16) Pack {
-        T e[n];
-    };
-    const Pack q = *reinterpret_cast<const Pack *>(p);
-#pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = to_f32(q.e[i]);
+struct alignas(sizeof(T) * n < 16 ? sizeof(T) * n : 16) Pack {
+    T e[n];
+};
+template <typename T, int n>
+__device__ __forceinline__ Pack<T, n> load_pack(const T *p) {
+    return *reinterpret_cast<const Pack<T, n> *>(p);
 }
 
 __device__ __forceinline__ int rank_of(const int32_t *ranks, int e, int R) {
@@ -64,32 +66,45 @@ __device__ __forceinline__ int rank_of(const int32_t *ranks, int e, int R) {
 }
 
 // The distinct adapters of a tile, one call of f(e, match) each; match has a bit
-// for every row that asks for e.  Every wavefront of a workgroup sees the same
-// ids, so f may hold barriers.
+// for every row that asks for e.  Lane l < 16 holds row l's id.  A tile that is
+// shared by zsplit workgroups gives the adapter to the one that the first row
+// asking for it falls to (one ballot per row of its own); otherwise the adapters
+// are taken as they come, which for one adapter is one ballot.  Every wavefront of
+// a workgroup sees the same ids, so f may hold barriers.
 template <typename F>
 __device__ __forceinline__ void for_each_adapter(int id, bool valid, int z, int zsplit, F f) {
-    uint64_t rem = __ballot(valid);
-    for (int n = 0; rem != 0; ++n) {
-        const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
-        const uint64_t match = __ballot(valid && id == e);
-        rem &= ~match;
-        if (n % zsplit == z) f(e, (uint32_t)match);
+    if (zsplit == 1) {
+        uint64_t rem = __ballot(valid);
+        while (rem != 0) {
+            const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
+            const uint64_t match = __ballot(valid && id == e);
+            rem &= ~match;
+            f(e, (uint32_t)match);
+        }
+    } else {
+        for (int r = z; r < kTileRows; r += zsplit) {
+            const int e = __builtin_amdgcn_readlane(id, r);
+            const uint32_t match = (uint32_t)__ballot(valid && id == e);
+            if (match != 0 && __builtin_ctz(match) == r) f(e, match);
+        }
     }
 }
 
 // ---- v: partial sums P[s][m][r] over the k steps of split s.
-// Workgroup = (tile, z, block of RT * 16 ranks, split); its wavefronts take the
-// steps in turn and add their tiles in LDS.  Rows that do not match read the
-// first matching row's x (same cache lines), ranks past the adapter's own read
-// its last one; neither is used.
+// Workgroup = (tile, z, block of RT * 16 ranks, split) of eight wavefronts, which
+// take pairs of the split's steps in turn and add their tiles in LDS: the partials that
+// the second kernel reads again stay few.  Rows that do not match read the first
+// matching row's x (same cache lines), ranks past the pool's read its last one;
+// neither is used.
 template <typename T, int RT>
-__global__ __launch_bounds__(kThreads) void k_lora_shrink(const T *__restrict__ A, int64_t E, int R,
-                                                          const int32_t *__restrict__ ranks,
-                                                          const float *__restrict__ x,
-                                                          const int32_t *__restrict__ ids, int64_t M, int K,
-                                                          int splits, int rank_blocks, int zsplit, int Rp,
-                                                          float *__restrict__ P) {
-    __shared__ v4f red[kWaves][RT][kWave];
+__global__ __launch_bounds__(kShrinkThreads, 4) void k_lora_shrink(const T *__restrict__ A, int64_t E, int R,
+                                                                const int32_t *__restrict__ ranks,
+                                                                const float *__restrict__ x,
+                                                                const int32_t *__restrict__ ids, int64_t M, int K,
+                                                                int splits, int rank_blocks, int zsplit, int Rp,
+                                                                float *__restrict__ P) {
+    constexpr int W = kShrinkThreads / kWave;
+    __shared__ v4f red[W][RT][kWave];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = lane & 15, g = lane >> 4;
     uint32_t b = blockIdx.x;
@@ -104,8 +119,10 @@ __global__ __launch_bounds__(kThreads) void k_lora_shrink(const T *__restrict__ 
     const int st0 = s * per, st1 = st0 + per < steps ? st0 + per : steps;
 
     for_each_adapter(id, id >= 0 && id < E, z, zsplit, [&](int e, uint32_t match) {
-        const int rank = rank_of(ranks, e, R);
-        if (rank <= r0) return;
+        // rank tiles of this block that the adapter has; with one tile the rank is not
+        // waited for: whatever lies past it is not used
+        const int tiles = RT == 1 ? 1 : (rank_of(ranks, e, R) - r0 + 15) >> 4;
+        if (RT > 1 && tiles <= 0) return;
         const int xr = match >> row & 1 ? row : __builtin_ctz(match);
         const float *xp = x + (m0 + xr) * K + 8 * g;
         const T *ap[RT];
@@ -113,157 +130,364 @@ __global__ __launch_bounds__(kThreads) void k_lora_shrink(const T *__restrict__ 
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const int r = r0 + t * 16 + row;
-            ap[t] = A + ((int64_t)e * R + (r < rank ? r : rank - 1)) * K + 8 * g;
+            ap[t] = A + ((int64_t)e * R + (r < R ? r : R - 1)) * K + 8 * g;
             acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
         }
-#pragma unroll 2
-        for (int st = st0 + wave; st < st1; st += kWaves) {
-            float xv[8];
-            load_n<float, 8>(xp + st * kStep, xv);
+        constexpr int H = 2;  // the loads of two steps are in flight before the first one's products
+        for (int st = st0 + H * wave; st < st1; st += H * W) {
+            const bool two = st + 1 < st1;
+            Pack<float, 8> xv[H];
+            Pack<T, 8> av[H][RT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                float av[8];
-                load_n<T, 8>(ap[t] + st * kStep, av);
+            for (int h = 0; h < H; ++h) {
+                if (h == 1 && !two) break;
+                xv[h] = load_pack<float, 8>(xp + (st + h) * kStep);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv[i], av[i], acc[t], 0, 0, 0);
+                for (int t = 0; t < RT; ++t)
+                    if (t < tiles) av[h][t] = load_pack<T, 8>(ap[t] + (st + h) * kStep);
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                if (h == 1 && !two) break;
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    if (t < tiles) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv[h].e[i], to_f32(av[h][t].e[i]), acc[t], 0,
+                                                                          0, 0);
+                    }
             }
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) red[wave][t][lane] = acc[t];
         __syncthreads();
-        for (int i = threadIdx.x; i < RT * kWave; i += kThreads) {
-            const int t = i >> 6, l = i & 63;
-            v4f v = red[0][t][l];
+        // element i of the tiles: float i % 4 of lane i / 4 % 64 of tile i / 256
+        for (int i = threadIdx.x; i < RT * kWave * 4; i += kShrinkThreads) {
+            const int t = i >> 8, l = i >> 2 & 63, q = i & 3;
+            const float *p = reinterpret_cast<const float *>(&red[0][0][0]) + i;
+            float v = 0.f;
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) v += red[w][t][l];
-            const int r = r0 + t * 16 + (l & 15);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int mr = 4 * (l >> 4) + q;
-                if (match >> mr & 1) P[((int64_t)s * M + m0 + mr) * Rp + r] = v[q];
-            }
+            for (int w = 0; w < W; ++w) v += p[w * RT * kWave * 4];
+            const int r = r0 + t * 16 + (l & 15), mr = 4 * (l >> 4) + q;
+            if (match >> mr & 1) P[((int64_t)s * M + m0 + mr) * Rp + r] = v;
         }
         __syncthreads();
     });
 }
 
-// ---- out = base + v B^T.  Workgroup = (tile, z, strip of columns): the tile's v
-// (partials added in order, scaled) goes to LDS once per adapter, then each
-// wavefront multiplies 16 columns of B at a time: B's rows are the matrix
-// instruction's rows, so a lane ends with four consecutive columns of one output
-// row.  VEC: base and out rows are 16-byte aligned (16-byte accesses); BV: R is a
-// multiple of 4 (B in loads of four elements).
-template <typename T, bool VEC, bool BV, int NT>
+// ---- the second product's operands.  fp32 B: C = 4 consecutive ranks per lane
+// feed four v_mfma_f32_16x16x4_f32.  16-bit B goes to the 16-bit instruction as it
+// is (C = 8 ranks per lane, v_mfma_f32_16x16x32), and v as three 16-bit numbers
+// that add up to it: bf16 pieces cut off eight bits each, which is exact; fp16
+// pieces round to 11 bits each of v times a power of two that puts the row's
+// largest |v| below 2^15 (fp16's range is narrow), what is left is below 2^-33 of
+// that.  Three products of 32 ranks take 48 cycles; eight fp32 instructions would
+// take 256, and B would have to be converted.
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+template <typename T>
+struct Operand;
+template <>
+struct Operand<float> {
+    static constexpr int C = 4, pieces = 1;
+    typedef float Stored;  // v in LDS
+    static __device__ __forceinline__ int exponent(float) { return 0; }
+    static __device__ __forceinline__ void split(float v, Stored (&p)[1]) { p[0] = v; }
+    static __device__ __forceinline__ v4f mul(uint4 w, uint4 v, v4f acc) {
+        const v4f a = __builtin_bit_cast(v4f, w), b = __builtin_bit_cast(v4f, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], acc, 0, 0, 0);
+        return acc;
+    }
+};
+template <>
+struct Operand<BF16> {
+    static constexpr int C = 8, pieces = 3;
+    typedef uint16_t Stored;
+    static __device__ __forceinline__ int exponent(float) { return 0; }
+    static __device__ __forceinline__ void split(float v, Stored (&p)[3]) {
+        const bool finite = fabsf(v) < __builtin_inff();
+        const uint32_t quiet = v != v ? 0x400000u : 0;  // cutting bits off a NaN must not leave an infinity
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            p[i] = (uint16_t)((__float_as_uint(v) | quiet) >> 16);
+            v = finite ? v - __uint_as_float((uint32_t)p[i] << 16) : 0.f;
+        }
+        if (!finite) p[1] = p[2] = 0;
+    }
+    static __device__ __forceinline__ v4f mul(uint4 w, uint4 v, v4f acc) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, w), __builtin_bit_cast(v8b, v), acc, 0, 0, 0);
+    }
+};
+template <>
+struct Operand<_Float16> {
+    static constexpr int C = 8, pieces = 3;
+    typedef uint16_t Stored;
+    // of the power of two for a row whose largest |v| is top
+    static __device__ __forceinline__ int exponent(float top) {
+        const int e = (int)(__float_as_uint(top) >> 23) - 127;  // top in [2^e, 2^(e+1))
+        return e == 128 ? 0 : (14 - e < 126 ? 14 - e : 126);
+    }
+    static __device__ __forceinline__ void split(float v, Stored (&p)[3]) {
+        const bool finite = fabsf(v) < __builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            p[i] = (uint16_t)f32_to_f16_bits(v);
+            v = finite ? v - f16_bits_to_f32(p[i]) : 0.f;
+        }
+    }
+    static __device__ __forceinline__ v4f mul(uint4 w, uint4 v, v4f acc) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, v), acc, 0, 0, 0);
+    }
+};
+
+// elements of a row of v in LDS: whole chunks of 4 * C ranks, and 16 bytes more so
+// that the rows start on different banks
+template <typename T>
+__host__ __device__ constexpr int v_row(int Rp) {
+    return (Rp + 4 * Operand<T>::C - 1) / (4 * Operand<T>::C) * (4 * Operand<T>::C) +
+           16 / (int)sizeof(typename Operand<T>::Stored);
+}
+
+// ---- out = base + v B^T.  Workgroup = (tile, z, strip of columns).  The tile's v
+// (partials added in order, scaled, each row with its own adapter's rank) goes to
+// LDS once.  Per group of 256 columns each wavefront multiplies four times 16
+// columns of B, adapter by adapter: B's rows are the matrix instruction's rows, so
+// a lane ends with four consecutive columns of one output row, and the rows that
+// match go to a tile in LDS.  From there base and out are read and written by
+// whole rows, 1 KiB per wavefront and instruction.  The first group's base and B
+// are on their way while v is added up.  VEC: rows of base and out are 16-byte
+// aligned and N is a multiple of 4 (16-byte accesses); BV: R is a multiple of C (B
+// in loads of C elements); H: 64 * H ranks at most; SHARED: zsplit > 1.
+template <typename T, bool VEC, bool BV, int H, bool SHARED>
 __global__ __launch_bounds__(kThreads) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
                                                           const float *__restrict__ scales,
                                                           const int32_t *__restrict__ ranks,
                                                           const int32_t *__restrict__ ids, int64_t M,
                                                           const float *__restrict__ P, int splits, int Rp,
                                                           const float *base, int64_t ld_base, float *out,
-                                                          int64_t ld_out, int64_t N, int strips, int zsplit) {
-    extern __shared__ float vs[];  // [kTileRows][Rp + 4]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+                                                          int64_t ld_out, int64_t N, int strips, int groups,
+                                                          int zsplit) {
+    typedef Operand<T> Op;
+    typedef typename Op::Stored Stored;
+    constexpr int C = Op::C;
+    constexpr int kTileLd = kGroupCols + 4;
+    constexpr int kRows = kTileRows / (kThreads / kWave);  // output rows of a wavefront
+    __shared__ __align__(16) float tile[kTileRows * kTileLd];
+    __shared__ int exponents[kTileRows];
+    extern __shared__ __align__(16) uint8_t v_lds[];  // Stored [pieces][kTileRows][vld]
+    Stored *vs = reinterpret_cast<Stored *>(v_lds);
+    const int vld = v_row<T>(Rp);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, g = lane >> 4;
-    const int vld = Rp + 4;
     uint32_t b = blockIdx.x;
-    const int64_t n_wave = (int64_t)(b % strips * kWaves + wave) * (16 * NT);
+    const int64_t strip0 = (int64_t)(b % strips) * groups * kGroupCols;
     b /= strips;
-    const int z = (int)(b % (uint32_t)zsplit);
-    const int64_t m0 = (int64_t)(b / zsplit) * kTileRows;
-    const int64_t m = m0 + row;
-    const int id = m < M ? ids[m] : -1;
-    const bool valid = id >= 0 && id < E;
+    const int z = SHARED ? (int)(b % (uint32_t)zsplit) : 0;
+    const int64_t m0 = (int64_t)(SHARED ? b / zsplit : b) * kTileRows;
+    const int tile_rows = M - m0 < kTileRows ? (int)(M - m0) : kTileRows;
+    // Loads below take the nearest valid address where theirs is past an end, and
+    // what they bring there is not used: no branch stands between them, so a wait
+    // for one does not become a wait for all.
+    // lane l holds what row l % 16 asks for
+    int id = ids[m0 + (row < tile_rows ? row : tile_rows - 1)];
 
-    // rows without an adapter: the base as it is; an id that names none: NaN
-    if (z == 0 && m < M && !valid && !(id == -1 && base == out)) {
+    // this wavefront's rows of base: four consecutive columns per lane, or columns
+    // lane, lane + 64, ...
+    v4f o[kRows];
+    auto column = [&](int64_t n0, int q) { return n0 + (VEC ? 4 * lane + q : lane + 64 * q); };
+    auto load_base = [&](int64_t n0, uint32_t rows) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int64_t n = n_wave + 16 * t + 4 * g;
+        for (int i = 0; i < kRows; ++i) {
+            const int mr = wave * kRows + i;
+            if (SHARED && !(rows >> mr & 1)) continue;  // other workgroups' rows
+            const float *p = base + (m0 + (mr < tile_rows ? mr : tile_rows - 1)) * ld_base;
+            if (VEC) {
+                const int64_t n = column(n0, 0);
+                o[i] = *reinterpret_cast<const v4f *>(p + (n < N ? n : N - 4));
+            } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (n + q < N)
-                    out[m * ld_out + n + q] = id == -1 ? base[m * ld_base + n + q] : __builtin_nanf("");
+                for (int q = 0; q < 4; ++q) {
+                    const int64_t n = column(n0, q);
+                    o[i][q] = p[n < N ? n : N - 1];
+                }
+            }
+        }
+    };
+    // a tile that is not shared is read before it is known who wants what
+    if (!SHARED) load_base(strip0, ~0u);
+
+    id = row < tile_rows ? id : -1;
+    const bool valid = id >= 0 && id < E;
+    // the rows this workgroup writes: those of its adapters, and for z = 0 the ones
+    // without (in place these stay as they are)
+    uint32_t here = 0;
+    const int of = SHARED ? zsplit : 1;
+    for_each_adapter(id, valid && lane < kTileRows, z, of, [&](int, uint32_t match) { here |= match; });
+    const uint32_t adapters = here;
+    if (z == 0)
+        here |= (uint32_t)__ballot(lane < tile_rows && !valid && !(id == -1 && base == out));
+    if (here == 0) return;
+    const int own = valid ? id : 0;
+    int rank = R;
+    float scale = 1.0f;
+    if (ranks != nullptr) rank = ranks[own];
+    if (scales != nullptr) scale = scales[own];
+
+    // C ranks from r on (16 bytes) of this lane's rows of B in the wavefront's columns
+    uint4 w[kNT];
+    auto load_b = [&](int e, int64_t n0, int r) {
+        const T *Be = B + ((int64_t)e * N + n0) * R;
+        const int cols = N - n0 < kGroupCols ? (int)(N - n0) : kGroupCols;
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            const int nb = (wave * kNT + t) * 16 + row;
+            const T *p = Be + (uint32_t)((nb < cols ? nb : cols - 1) * R);
+            if (BV) {
+                w[t] = ld16(p + (r < R ? r : 0));
+            } else {
+                Pack<T, C> q;
+#pragma unroll
+                for (int i = 0; i < C; ++i) q.e[i] = p[r + i < R ? r + i : 0];
+                w[t] = __builtin_bit_cast(uint4, q);
+            }
+        }
+    };
+
+    // v's partials: sixteen lanes per row, four consecutive ranks each and 64 at a
+    // time; a row without an adapter has none, what is read there is not used
+    const int vrow = wave * kRows + g;  // kRows is 4: the wavefront's rows by 16 lanes each
+    v4f v[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const int r = 64 * h + 4 * row;
+        const float *p = P + (m0 + (vrow < tile_rows ? vrow : tile_rows - 1)) * Rp + (r < Rp ? r : 0);
+        v[h] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (64 * h >= Rp) break;
+        for (int s = 0; s < splits; s += 8) {
+            v4f part[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                part[i] = *reinterpret_cast<const v4f *>(p + (int64_t)(s + i < splits ? s + i : s) * M * Rp);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[h] += s + i < splits ? part[i] : v4f{0.f, 0.f, 0.f, 0.f};
         }
     }
+    // the first group's B and base are on their way while v is made up
+    const int first = adapters != 0 ? __builtin_ctz(adapters) : 0;  // a row of the first adapter
+    load_b(__builtin_amdgcn_readlane(own, first), strip0, C * g);
+    if (SHARED) load_base(strip0, here);
+    rank = !valid || rank < 0 ? 0 : (rank > R ? R : rank);
+    {
+        int rk = __shfl(rank, vrow);  // every lane takes part: the source lane has to be active
+        const float sc = __shfl(scale, vrow);
+        rk = adapters >> vrow & 1 ? rk : 0;
+        float top = 0.f;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[h][q] = 64 * h + 4 * row + q < rk ? v[h][q] * sc : 0.f;
+                top = fmaxf(top, fabsf(v[h][q]));
+            }
+        top = fmaxf(top, dpp_f32<0xB1>(top));  // over the row's sixteen lanes
+        top = fmaxf(top, dpp_f32<0x4E>(top));
+        top = fmaxf(top, dpp_f32<0x141>(top));
+        top = fmaxf(top, dpp_f32<0x140>(top));
+        const int ex = Op::exponent(top);
+        if (row == 0) exponents[vrow] = -ex;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int r = 64 * h + 4 * row;
+            if (r >= vld) continue;  // past what the chunks of 4 * C ranks read
+            Stored p4[4][Op::pieces];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) Op::split(Op::pieces > 1 ? ldexpf(v[h][q], ex) : v[h][q], p4[q]);
+#pragma unroll
+            for (int i = 0; i < Op::pieces; ++i) {
+                const Pack<Stored, 4> four{{p4[0][i], p4[1][i], p4[2][i], p4[3][i]}};
+                *reinterpret_cast<Pack<Stored, 4> *>(vs + (i * kTileRows + vrow) * vld + r) = four;
+            }
+        }
+    }
+    __syncthreads();
 
-    for_each_adapter(id, valid && lane < kTileRows, z, zsplit, [&](int e, uint32_t match) {
-        const int rank = rank_of(ranks, e, R);
-        const float scale = scales != nullptr ? scales[e] : 1.0f;
-        for (int i = threadIdx.x; i < kTileRows * Rp; i += kThreads) {
-            const int mr = i / Rp, r = i - mr * Rp;
-            float v = 0.f;
-            if ((match >> mr & 1) && r < rank) {
-                const float *p = P + (m0 + mr) * Rp + r;
-                for (int s = 0; s < splits; ++s) v += p[(int64_t)s * M * Rp];
-                v *= scale;
+    for (int j = 0; j < groups; ++j) {
+        const int64_t n0 = strip0 + (int64_t)j * kGroupCols;
+        for_each_adapter(id, valid && lane < kTileRows, z, of, [&](int e, uint32_t match) {
+            const int er = __builtin_amdgcn_readlane(rank, __builtin_ctz(match));
+            v4f acc[kNT];
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+            for (int c = 0; c < er; c += 4 * C) {
+                const int r = c + C * g;
+                if (j > 0 || c > 0 || !(match >> first & 1)) load_b(e, n0, r);
+                if (c + 4 * C > er) {  // what B holds behind the rank is not used
+                    uint32_t keep[4];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int left = er - r - d * (C / 4);
+                        keep[d] = left >= C / 4 ? ~0u : (left == 1 ? 0xffffu : 0u);
+                    }
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t)
+                        w[t] = make_uint4(w[t].x & keep[0], w[t].y & keep[1], w[t].z & keep[2], w[t].w & keep[3]);
+                }
+                uint4 vp[Op::pieces];
+#pragma unroll
+                for (int i = 0; i < Op::pieces; ++i) vp[i] = ld16(vs + (i * kTileRows + row) * vld + r);
+#pragma unroll
+                for (int i = Op::pieces - 1; i >= 0; --i)  // the small pieces first
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) acc[t] = Op::mul(w[t], vp[i], acc[t]);
             }
-            vs[mr * vld + r] = v;
-        }
+            if (match >> row & 1) {
+                const int ex = exponents[row];
+#pragma unroll
+                for (int t = 0; t < kNT; ++t) {
+                    if (Op::pieces > 1)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[t][q] = ldexpf(acc[t][q], ex);
+                    *reinterpret_cast<v4f *>(&tile[row * kTileLd + (wave * kNT + t) * 16 + 4 * g]) = acc[t];
+                }
+            }
+        });
         __syncthreads();
-        const bool mine = match >> row & 1;
-        v4f acc[NT], bv[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-            const int64_t n = n_wave + 16 * t + 4 * g;
-            bv[t] = v4f{0.f, 0.f, 0.f, 0.f};
-            if (mine) {
-                if (VEC && n + 3 < N) {
-                    bv[t] = *reinterpret_cast<const v4f *>(base + m * ld_base + n);
+        for (int i = 0; i < kRows; ++i) {
+            const int mr = wave * kRows + i;
+            if (!(here >> mr & 1)) continue;
+            const int e = __builtin_amdgcn_readlane(id, mr);
+            const float *d = &tile[mr * kTileLd];
+            float *p = out + (m0 + mr) * ld_out;
+            if (e >= 0 && e < E) {
+                if (VEC) {
+                    o[i] += *reinterpret_cast<const v4f *>(d + 4 * lane);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (n + q < N) bv[t][q] = base[m * ld_base + n + q];
+                    for (int q = 0; q < 4; ++q) o[i][q] += d[lane + 64 * q];
                 }
+            } else if (e != -1) {
+                const float nan = __builtin_nanf("");
+                o[i] = v4f{nan, nan, nan, nan};
+            }
+            if (VEC) {
+                if (column(n0, 0) < N) *reinterpret_cast<v4f *>(p + column(n0, 0)) = o[i];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (column(n0, q) < N) p[column(n0, q)] = o[i][q];
             }
         }
-        for (int c = 0; c < rank; c += 16) {
-            const int r = c + 4 * g;
-            const v4f v = *reinterpret_cast<const v4f *>(vs + row * vld + r);
-            float w[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int64_t n = n_wave + 16 * t + row;
-                const T *p = B + ((int64_t)e * N + (n < N ? n : N - 1)) * R + r;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[t][i] = 0.f;
-                if (BV) {
-                    if (r < rank) load_n<T, 4>(p, w[t]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[t][i] = r + i < rank ? w[t][i] : 0.f;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (r + i < rank) w[t][i] = to_f32(p[i]);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[t][i], v[i], acc[t], 0, 0, 0);
-        }
-        if (mine) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int64_t n = n_wave + 16 * t + 4 * g;
-                const v4f o = bv[t] + acc[t];
-                if (VEC && n + 3 < N) {
-                    *reinterpret_cast<v4f *>(out + m * ld_out + n) = o;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (n + q < N) out[m * ld_out + n + q] = o[q];
-                }
-            }
-        }
+        if (j + 1 == groups || n0 + kGroupCols >= N) break;
+        load_base(n0 + kGroupCols, here);
         __syncthreads();
-    });
+    }
 }
 
 // ---- launch shapes (host only; they need no device)
-constexpr int kTargetGroups = 1024;  // workgroups that fill the chip: four per CU
 constexpr int kMaxSplits = 32;
 
 struct Shape {
@@ -279,33 +503,44 @@ Shape shape(int64_t M, int64_t R, int64_t K, int64_t E) {
     h.zsplit = M <= 64 ? 16 : (M <= 512 ? 4 : 1);
     if (h.zsplit > E) h.zsplit = (int)E;
     if (h.zsplit > M) h.zsplit = (int)M;
+    // two workgroups of eight wavefronts per CU, two steps for each wavefront at least
     const int64_t groups = h.tiles * h.zsplit * h.rank_blocks;
-    const int64_t most = (K / kStep + 2 * kWaves - 1) / (2 * kWaves);  // two steps for each wavefront at least
-    int64_t s = (kTargetGroups + groups - 1) / groups;
+    const int64_t most = (K / kStep + 2 * (kShrinkThreads / kWave) - 1) / (2 * (kShrinkThreads / kWave));
+    int64_t s = (512 + groups - 1) / groups;
     s = s > kMaxSplits ? kMaxSplits : s;
     h.splits = (int)(s > most ? most : s);
     return h;
+}
+// column groups per workgroup of the second kernel: two where there are plenty of
+// them (2048 rows of 28672 columns: 105 us for both kernels, against 112 with one
+// and 120 with four)
+struct Strips {
+    int64_t strips;
+    int groups;
+};
+Strips strips_of(int64_t N, const Shape &h) {
+    const int64_t all = (N + kGroupCols - 1) / kGroupCols;
+    const int groups = all * h.tiles * h.zsplit >= 8192 ? 2 : 1;
+    return Strips{(all + groups - 1) / groups, groups};
 }
 
 template <typename T, int RT>
 hipError_t shrink(const LoraArgs &a, const Shape &h, hipStream_t s) {
     const int64_t grid = h.tiles * h.zsplit * h.rank_blocks * h.splits;
-    hipLaunchKernelGGL((k_lora_shrink<T, RT>), dim3((unsigned)grid), dim3(kThreads), 0, s,
+    hipLaunchKernelGGL((k_lora_shrink<T, RT>), dim3((unsigned)grid), dim3(kShrinkThreads), 0, s,
                        static_cast<const T *>(a.A), a.E, (int)a.R, a.ranks, a.x, a.ids, a.M, (int)a.K, h.splits,
                        h.rank_blocks, h.zsplit, h.Rp, a.ws);
     return hipGetLastError();
 }
 
-constexpr int kNT = 4;
-int64_t expand_strips(int64_t N) { return (N + kWaves * 16 * kNT - 1) / (kWaves * 16 * kNT); }
-
-template <typename T, bool VEC, bool BV>
+template <typename T, bool VEC, bool BV, int H>
 hipError_t expand(const LoraArgs &a, const Shape &h, hipStream_t s) {
-    const int64_t strips = expand_strips(a.N);
-    const size_t lds = sizeof(float) * kTileRows * (h.Rp + 4);
-    hipLaunchKernelGGL((k_lora_expand<T, VEC, BV, kNT>), dim3((unsigned)(strips * h.zsplit * h.tiles)), dim3(kThreads),
-                       lds, s, static_cast<const T *>(a.B), a.E, (int)a.R, a.scales, a.ranks, a.ids, a.M, a.ws,
-                       h.splits, h.Rp, a.base, a.ld_base, a.out, a.ld_out, a.N, (int)strips, h.zsplit);
+    const Strips st = strips_of(a.N, h);
+    const size_t lds = sizeof(typename Operand<T>::Stored) * Operand<T>::pieces * kTileRows * v_row<T>(h.Rp);
+    const auto kernel = h.zsplit > 1 ? k_lora_expand<T, VEC, BV, H, true> : k_lora_expand<T, VEC, BV, H, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(st.strips * h.zsplit * h.tiles)), dim3(kThreads), lds, s,
+                       static_cast<const T *>(a.B), a.E, (int)a.R, a.scales, a.ranks, a.ids, a.M, a.ws, h.splits, h.Rp,
+                       a.base, a.ld_base, a.out, a.ld_out, a.N, (int)st.strips, st.groups, h.zsplit);
     return hipGetLastError();
 }
 
@@ -314,9 +549,11 @@ hipError_t both(const LoraArgs &a, hipStream_t s) {
     const Shape h = shape(a.M, a.R, a.K, a.E);
     hipError_t e = h.rt == 1 ? shrink<T, 1>(a, h, s) : (h.rt == 2 ? shrink<T, 2>(a, h, s) : shrink<T, 4>(a, h, s));
     if (e != hipSuccess) return e;
-    const bool vec = a.ld_base % 4 == 0 && a.ld_out % 4 == 0, bv = a.R % 4 == 0;
-    return vec ? (bv ? expand<T, true, true>(a, h, s) : expand<T, true, false>(a, h, s))
-               : (bv ? expand<T, false, true>(a, h, s) : expand<T, false, false>(a, h, s));
+    constexpr int H = kMaxRank / 64;
+    const bool vec = a.ld_base % 4 == 0 && a.ld_out % 4 == 0 && a.N % 4 == 0, bv = a.R % Operand<T>::C == 0;
+    if (vec && bv) return h.Rp <= 64 ? expand<T, true, true, 1>(a, h, s) : expand<T, true, true, H>(a, h, s);
+    if (vec) return expand<T, true, false, H>(a, h, s);
+    return bv ? expand<T, false, true, H>(a, h, s) : expand<T, false, false, H>(a, h, s);
 }
 
 }  // namespace
@@ -326,10 +563,13 @@ int64_t lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E) {
     return (int64_t)sizeof(float) * h.splits * M * h.Rp;
 }
 
+int64_t lora_max_rank() { return kMaxRank; }
+
 bool lora_grid_ok(int64_t M, int64_t N, int64_t R, int64_t K, int64_t E) {
     const Shape h = shape(M, R, K, E);
-    const int64_t most = (int64_t(1) << 32) / kThreads - 1;  // threads of one launch are counted in 32 bits
-    return h.tiles * h.zsplit * h.rank_blocks * h.splits <= most && expand_strips(N) * h.zsplit * h.tiles <= most;
+    const int64_t threads = int64_t(1) << 32;  // of one launch: they are counted in 32 bits
+    return h.tiles * h.zsplit * h.rank_blocks * h.splits * kShrinkThreads < threads &&
+           strips_of(N, h).strips * h.zsplit * h.tiles * kThreads < threads;
 }
 
 hipError_t launch_lora_add(int type, const LoraArgs &a, hipStream_t s) {

@@ -219,6 +219,7 @@ struct LoraArgs {
     int64_t M, N, K, R, E, ld_base, ld_out;
 };
 int64_t lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E);
+int64_t lora_max_rank();
 bool lora_grid_ok(int64_t M, int64_t N, int64_t R, int64_t K, int64_t E);  // both launches fit a grid
 hipError_t launch_lora_add(int type, const LoraArgs &a, hipStream_t s);
 
