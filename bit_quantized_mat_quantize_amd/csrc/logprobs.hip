@@ -10,14 +10,14 @@
 //
 // The k best ride in the same pass.  A token's key is 64 bits, the order of its
 // logit above the complement of its index: keys are unique, and of equal logits
-// the lower index is the larger key.  Each wavefront keeps a lower bound of its
-// k-th best and appends what is not below it to a list in LDS.  The first bound
-// comes from the lanes' maxima of the first batch (the k-th largest of 64 values
-// that are all present); a full list is cut back to its k best, which raises the
-// bound, so after a few thousand logits hardly any pass and a batch costs one
-// comparison.  Both cuts find the k-th largest by bisection over the bits: each
-// step is a ballot and a count, no data moves.  At the end the lists of the
-// workgroup are ranked by counting.
+// the lower index is the larger key.  Each wavefront appends the keys that reach
+// a common lower bound of the k-th best to a list in LDS.  The bound is the k-th
+// largest of 64 (or 256) maxima, each over some of the threads: values that are all
+// present.  It is taken after batches 1, 3, 9, 33, ... of a workgroup, so that the
+// lists grow slowly; a list that is full all the same (equal or ascending logits)
+// is cut back to its k best.  Both find the k-th largest by bisection over the bits: each step is a ballot and
+// a count, no data moves.  At the end the lists of the workgroup are ranked by
+// counting.
 //
 // A row is split over workgroups where there are few rows (partial statistics
 // and keys go to the workspace, k_logprobs_merge joins them); otherwise one
@@ -152,6 +152,32 @@ struct List {
     }
 };
 
+// The order of the k-th largest of 64 * G maxima over the workgroup's threads, each
+// over kWaves / G threads (0: fewer than k of them have a logit): at least k logits
+// are not below it.
+template <int G>
+__device__ __forceinline__ uint32_t common_bound_of(int k, uint32_t (*lds)[kWave]) {
+    uint32_t best[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        best[g] = 0;
+#pragma unroll
+        for (int w = g; w < kWaves; w += G) {
+            const uint32_t v = lds[w][threadIdx.x & 63];
+            best[g] = v > best[g] ? v : best[g];
+        }
+    }
+    __syncthreads();
+    return kth_bound(best, k);
+}
+__device__ __forceinline__ uint32_t common_bound(uint32_t mine, int k, uint32_t (*lds)[kWave]) {
+    lds[threadIdx.x >> 6][threadIdx.x & 63] = mine;
+    __syncthreads();
+    // of 8192 logits about 64 ln(64 / (64 - k)) reach the bound of 64 maxima: 24 for
+    // k = 20, but 300 for k = 64, where four times as many maxima let 74 pass
+    return k <= 20 ? common_bound_of<1>(k, lds) : common_bound_of<4>(k, lds);
+}
+
 // ---- running statistics in base 2: c = scale * log2(e)
 struct Stats {
     float m, s, t;
@@ -259,6 +285,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
     __shared__ uint64_t lists[kWaves][kList];
     __shared__ uint64_t all[kThreads];
     __shared__ int counts[kWaves];
+    __shared__ uint32_t maxima[kWaves][kWave];
     __shared__ Stats wave_stats[kWaves];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -343,11 +370,12 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
         st.s += bs;
         st.t += bt;
 
+        // after batches 1, 3, 9, 33, ...: after 1, 2, 3, 5, 9 it cost more than it saved
+        // (513 rows of 50257, k = 8: 25.9 against 24.4 us), after 1, 5, 17 less than it
+        // let through (27.3 us)
+        if (a.k > 0 && (it == 0 || ((it & (it - 1)) == 0 && (it & 0x2aaaaaaa) != 0)))
+            l.raise((uint64_t)common_bound(st.m > -kInf ? order_of(st.m) : 0, l.k, maxima) << 32);
         if (a.k > 0 && __ballot(top >= l.least) != 0) {
-            if (l.bound == 0) {
-                const uint32_t o[1] = {top > -kInf ? order_of(top) : 0};
-                l.raise((uint64_t)kth_bound(o, l.k) << 32);
-            }
             uint32_t left = 0;  // which of this lane's logits may enter
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) left |= v[i] >= l.least ? 1u << i : 0;
@@ -389,54 +417,50 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_merge(const LogprobArgs a
     __shared__ uint64_t lists[kWaves][kList];
     __shared__ uint64_t all[kThreads];
     __shared__ int counts[kWaves];
+    __shared__ uint32_t maxima[kWaves][kWave];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x;
     const float c = a.scale * kLog2e;
     const Given given = given_token<T>(a, row, threadIdx.x);
     const int total = splits * (int)a.k;
     const uint64_t *in = a.ws_keys + row * total;
-    uint64_t key = (int)threadIdx.x < total ? in[threadIdx.x] : 0;
     Stats st{-kInf, 0.f, 0.f};
     if (lane < splits) {
         const float4 p = a.ws_stats[row * splits + lane];
         st = Stats{p.x, p.y, p.z};
     }
     st.join_wave(c);
-    bool has = key != 0;
-    if (total > kThreads) {  // more keys than threads: each wavefront's k best of its share
-        constexpr int n = kMaxSplits * kMaxK / kThreads;
-        List l{lists[wave], 0, (int)a.k, 0, -__FLT_MAX__};
-        uint64_t v[n], best = key;
-        v[0] = key;
+    constexpr int n = kMaxSplits * kMaxK / kThreads;  // keys per thread
+    List l{lists[wave], 0, (int)a.k, 0, -__FLT_MAX__};
+    if (a.k > 0) {
+        uint64_t v[n], best = 0;
 #pragma unroll
-        for (int i = 1; i < n; ++i) {
+        for (int i = 0; i < n; ++i) {
             const int at = i * kThreads + (int)threadIdx.x;
             v[i] = at < total ? in[at] : 0;
             best = v[i] > best ? v[i] : best;
         }
-        const uint32_t o[1] = {(uint32_t)(best >> 32)};
-        l.raise((uint64_t)kth_bound(o, l.k) << 32);
-        for (int i = 0; i * kThreads < total; ++i) {
-            uint64_t y = v[0];
+        l.raise((uint64_t)common_bound((uint32_t)(best >> 32), l.k, maxima) << 32);
 #pragma unroll
-            for (int q = 1; q < n; ++q) y = i == q ? v[q] : y;
-            l.add(y, y != 0);
-        }
+        for (int i = 0; i < n; ++i)
+            if (i * kThreads < total) l.add(v[i], v[i] != 0);
         if (l.count > kWave) l.cut();
-        has = lane < l.count;
-        key = has ? l.keys[lane] : 0;
     }
+    const bool has = lane < l.count;
+    const uint64_t key = has ? l.keys[lane] : 0;
     finish_row<T>(a, st, row, given, key, has, all, counts);
 }
 
-// as many workgroups as run at once (four of eight wavefronts per CU) and no more,
-// each with at least one batch: 513 rows of 50257 in two splits, 1026 workgroups,
-// took 37 us for the two that had to wait, in one 
+// A row of up to four batches is not split: one workgroup takes 9.9 us for 32000
+// logits and its call 14.9 us, where four take 9.4 us with the second launch and
+// its call 18.7 us.  Longer ones make as many workgroups as run at once (four per
+// CU) and no more: 513 rows of 50257 in two splits, 1026 workgroups, took 37 us for
+// the two that had to wait, and 34 us in one.
 int splits_of(int64_t M, int64_t V) {
-    int64_t s = M < 1024 ? 1024 / M : 1;
-    const int64_t most = (V + kThreads * kBatch - 1) / (kThreads * kBatch);
-    s = s > most ? most : s;
-    return (int)(s > kMaxSplits ? kMaxSplits : s);
+    constexpr int64_t batch = kThreads * kBatch;
+    if (M >= 1024 || V <= 4 * batch) return 1;
+    const int64_t s = 1024 / M, most = (V + batch - 1) / batch;
+    return (int)(s > most ? (most > kMaxSplits ? kMaxSplits : most) : (s > kMaxSplits ? kMaxSplits : s));
 }
 
 template <typename T>

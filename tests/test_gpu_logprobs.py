@@ -99,7 +99,7 @@ def _logits(rng, M, V):
 @pytest.mark.parametrize("type", TYPES)
 @pytest.mark.parametrize("M,V,G,k,scale", [(1, 1, 1, 1, 1.0), (1, 2, 2, 5, 0.5), (3, 63, 1, 64, 1.0),
                                            (2, 257, 3, 20, 1.25), (1, 4097, 1, 5, 1.0), (7, 5000, 1, 40, 0.7),
-                                           (1, 32000, 1, 20, 1.0), (2, 100003, 2, 64, 1.0), (40, 9001, 1, 8, 2.0),
+                                           (1, 32000, 1, 20, 1.0), (1, 40961, 1, 33, 1.0), (2, 100003, 2, 64, 1.0), (40, 9001, 1, 8, 2.0),
                                            (1030, 333, 1, 3, 1.0), (1025, 4100, 2, 1, 1.0)])
 def test_against_64_bits(M, V, G, k, scale, type):
     print(M, V, G, k, scale, type, flush=True)
@@ -128,7 +128,7 @@ def test_row_strides(pad, type):
 
 
 @pytest.mark.parametrize("type", TYPES)
-@pytest.mark.parametrize("M,V", [(1, 40), (3, 1000), (2, 20011), (1030, 97)])
+@pytest.mark.parametrize("M,V", [(1, 40), (3, 1000), (2, 20011), (2, 70003), (1030, 97)])
 @pytest.mark.parametrize("shared", [False, True])
 def test_masks(M, V, shared, type):
     """Masked places may hold anything; rows that allow one token or none; bits behind V do not matter."""
@@ -156,8 +156,8 @@ def test_masks(M, V, shared, type):
         assert (to_host(got[2])[0] == -1).all() and (to_host(got[3])[0] == -np.inf).all()
 
 
-@pytest.mark.parametrize("M", [2, 1100])
-@pytest.mark.parametrize("V", [900, 9000])
+@pytest.mark.parametrize("M", [2, 1030])
+@pytest.mark.parametrize("V", [900, 9000, 40000])
 def test_ties_and_orders(M, V):
     """Equal logits (all of them, two values, 0 and -0), ascending and descending rows: ties go to the lowest
     index, and rows on which every logit enters the list come out right."""
@@ -173,7 +173,7 @@ def test_ties_and_orders(M, V):
         Reference(x64).check(qmm.logprobs(x, tokens=to_dev(tokens), k=k), tokens, k, name)
 
 
-@pytest.mark.parametrize("V", [70, 5001])
+@pytest.mark.parametrize("V", [70, 5001, 50001])
 def test_extreme_values(V):
     """Rows of the lowest finite number, of -inf, with one finite logit, with a range that overflows a difference."""
     rng = np.random.default_rng(V)
@@ -187,7 +187,7 @@ def test_extreme_values(V):
     Reference(x64).check(qmm.logprobs(x, tokens=to_dev(tokens), k=4), tokens, 4)
 
 
-@pytest.mark.parametrize("V", [70, 5001])
+@pytest.mark.parametrize("V", [70, 5001, 50001])
 def test_nan_and_inf_poison_their_row_only(V):
     rng = np.random.default_rng(V)
     x = rng.standard_normal((4, V)).astype(np.float32)
@@ -231,7 +231,7 @@ def test_streams_and_graphs_with_a_workspace_each():
     rng = np.random.default_rng(5)
     side = torch.cuda.Stream()
     calls = []
-    for M, V, k in ((1, 30000, 20), (5, 12000, 3)):
+    for M, V, k in ((1, 60000, 20), (5, 40000, 3)):
         x, x64 = _dev_type(_logits(rng, M, V), "f32")
         tokens = rng.integers(0, V, (M, 1)).astype(np.int32)
         dt = to_dev(tokens)
