@@ -260,9 +260,15 @@ __host__ __device__ constexpr int v_row(int Rp) {
 // whole rows, 1 KiB per wavefront and instruction.  The first group's base and B
 // are on their way while v is added up.  VEC: rows of base and out are 16-byte
 // aligned and N is a multiple of 4 (16-byte accesses); BV: R is a multiple of C (B
-// in loads of C elements); H: 64 * H ranks at most; SHARED: zsplit > 1.
-template <typename T, bool VEC, bool BV, int H, bool SHARED>
-__global__ __launch_bounds__(kThreads) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
+// in loads of C elements); H: 64 * H ranks at most.
+//
+// Measured (one box, base and out not in a cache): 2048 rows, N = 28672, K = 8192,
+// rank 16: 82 us of 79 that adding two matrices of this size takes, 6 TB/s; 555
+// rows, K = 4096, rank 64: 37 us (latency: ids, then B, then the products); 32 rows
+// of 28 adapters, N = 8192: 8 us.
+enum class Tiles { Own, Shared, Long };  // Shared: zsplit > 1; Long: base and out go past the caches
+template <typename T, bool VEC, bool BV, int H, Tiles MODE>
+__global__ __launch_bounds__(kThreads, 4) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
                                                           const float *__restrict__ scales,
                                                           const int32_t *__restrict__ ranks,
                                                           const int32_t *__restrict__ ids, int64_t M,
@@ -272,6 +278,7 @@ __global__ __launch_bounds__(kThreads) void k_lora_expand(const T *__restrict__ 
                                                           int zsplit) {
     typedef Operand<T> Op;
     typedef typename Op::Stored Stored;
+    constexpr bool SHARED = MODE == Tiles::Shared;
     constexpr int C = Op::C;
     constexpr int kTileLd = kGroupCols + 4;
     constexpr int kRows = kTileRows / (kThreads / kWave);  // output rows of a wavefront
@@ -306,7 +313,8 @@ __global__ __launch_bounds__(kThreads) void k_lora_expand(const T *__restrict__ 
             const float *p = base + (m0 + (mr < tile_rows ? mr : tile_rows - 1)) * ld_base;
             if (VEC) {
                 const int64_t n = column(n0, 0);
-                o[i] = *reinterpret_cast<const v4f *>(p + (n < N ? n : N - 4));
+                const v4f *at = reinterpret_cast<const v4f *>(p + (n < N ? n : N - 4));
+                o[i] = MODE == Tiles::Long ? __builtin_nontemporal_load(at) : *at;
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -474,7 +482,9 @@ __global__ __launch_bounds__(kThreads) void k_lora_expand(const T *__restrict__ 
                 o[i] = v4f{nan, nan, nan, nan};
             }
             if (VEC) {
-                if (column(n0, 0) < N) *reinterpret_cast<v4f *>(p + column(n0, 0)) = o[i];
+                v4f *to = reinterpret_cast<v4f *>(p + column(n0, 0));
+                if (column(n0, 0) < N && MODE == Tiles::Long) __builtin_nontemporal_store(o[i], to);
+                else if (column(n0, 0) < N) *to = o[i];
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -537,7 +547,12 @@ template <typename T, bool VEC, bool BV, int H>
 hipError_t expand(const LoraArgs &a, const Shape &h, hipStream_t s) {
     const Strips st = strips_of(a.N, h);
     const size_t lds = sizeof(typename Operand<T>::Stored) * Operand<T>::pieces * kTileRows * v_row<T>(h.Rp);
-    const auto kernel = h.zsplit > 1 ? k_lora_expand<T, VEC, BV, H, true> : k_lora_expand<T, VEC, BV, H, false>;
+    // no cache holds 32 MiB of out: it goes past them, and base with it (2048 rows of
+    // 28672: 105 -> 101 us for both kernels, 555 rows at rank 64: 55 -> 50 us)
+    const auto kernel = h.zsplit > 1 ? k_lora_expand<T, VEC, BV, H, Tiles::Shared>
+                        : VEC && a.M * a.N >= (int64_t(32) << 20) / 4
+                            ? k_lora_expand<T, VEC, BV, H, VEC ? Tiles::Long : Tiles::Own>
+                            : k_lora_expand<T, VEC, BV, H, Tiles::Own>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(st.strips * h.zsplit * h.tiles)), dim3(kThreads), lds, s,
                        static_cast<const T *>(a.B), a.E, (int)a.R, a.scales, a.ranks, a.ids, a.M, a.ws, h.splits, h.Rp,
                        a.base, a.ld_base, a.out, a.ld_out, a.N, (int)st.strips, st.groups, h.zsplit);
