@@ -77,6 +77,9 @@ def load() -> ctypes.CDLL:
         "qmm_logprobs_workspace_bytes": (SZ, [I64, I64, I64]),
         "qmm_logprobs": (I, [I, P, SZ, I64, I64, I64, ctypes.c_float, P, SZ, I64, P, I64, P, P, I64, P, P,
                              P, SZ, P]),
+        "qmm_mul_mat_logprobs_workspace_bytes": (SZ, [I64, I64, I64]),
+        "qmm_mul_mat_logprobs": (I, [I, P, SZ, I, P, SZ, I64, I64, I64, ctypes.c_float, P, SZ, I64, P, I64, P, P, I64,
+                                     P, P, P, SZ, P]),
         "qmm_debug_block_sums": (I, [I, P, SZ, I, P, SZ, P, SZ, I64, I64, I64, P]),
         "qmm_status_string": (ctypes.c_char_p, [I]),
         "qmm_last_error": (ctypes.c_char_p, []),
@@ -439,19 +442,57 @@ def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=No
         if out is None:
             out = torch.empty((M, N), dtype=f32, device=base.device)
         po, no, ldo = _rows(out, "out", f32, M, N)
-        if workspace is None:
-            workspace = torch.empty(max(lora_workspace_bytes(M, R, K, E), 16), dtype=torch.uint8, device=base.device)
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        workspace = _workspace(workspace, lora_workspace_bytes(M, R, K, E), base.device)
         _check(load().qmm_lora_add(_float_type(A, "A"), A.data_ptr(), A.nbytes, B.data_ptr(), B.nbytes, E, R,
                                    _ptr(scales), _ptr(ranks), x.data_ptr(), x.nbytes, ids.data_ptr(), pb, nb, ldb,
-                                   po, no, ldo, M, N, K, workspace.data_ptr(), workspace.nbytes, _current(index)),
+                                   po, no, ldo, M, N, K, _ptr(workspace),
+                                   0 if workspace is None else workspace.nbytes, _current(index)),
                "qmm_lora_add")
     return out
 
 
 def logprobs_workspace_bytes(M: int, V: int, k: int) -> int:
     return int(load().qmm_logprobs_workspace_bytes(M, V, k))
+
+
+def _logprob_inputs(M: int, V: int, tokens, mask):
+    """(tokens per row, words from a mask row to the next, bytes of the mask), checked."""
+    import torch
+    G, mask_ld, mask_bytes = 0, 0, 0
+    if tokens is not None:
+        shape = tokens.shape
+        if len(shape) not in (1, 2) or shape[0] != M:
+            raise ValueError(f"tokens must have shape ({M},) or ({M}, G) (got {tuple(shape)})")
+        G = shape[1] if len(shape) == 2 else 1
+        _is(tokens, "tokens", torch.int32, *shape)
+    if mask is not None:
+        rows, words = (1, mask.shape[0]) if mask.dim() == 1 else mask.shape
+        if rows not in (1, M) or words < (V + 31) // 32:
+            raise ValueError(f"mask must have 1 or {M} rows of at least {(V + 31) // 32} words (got {tuple(mask.shape)})")
+        _is(mask, "mask", torch.int32, *mask.shape)
+        mask_ld, mask_bytes = words if rows > 1 else 0, mask.nbytes
+    return G, mask_ld, mask_bytes
+
+
+def _logprob_outputs(M: int, k: int, tokens, entropy: bool, device):
+    import torch
+    f32 = torch.float32
+    lp = None if tokens is None else torch.empty(tokens.shape, dtype=f32, device=device)
+    ent = torch.empty((M,), dtype=f32, device=device) if entropy else None
+    if k <= 0:
+        return lp, ent, None, None
+    return (lp, ent, torch.empty((M, k), dtype=torch.int32, device=device),
+            torch.empty((M, k), dtype=f32, device=device))
+
+
+def _workspace(given, need: int, device):
+    """The caller's workspace, or a new one (None where nothing is needed)."""
+    import torch
+    if given is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if not given.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return given
 
 
 def logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, mask=None, entropy: bool = True,
@@ -462,43 +503,46 @@ def logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, mask=None, ent
     same shape); entropy: fp32 [M]; k: that many most likely tokens (int32 and fp32 [M, k], -1 and -inf where
     there are fewer).  mask: int32 words [W], [1, W] or [M, W], W >= ceil(V / 32); bit i % 32 of word i // 32
     allows token i.  scale multiplies the logits (one over the temperature).  What is not asked for is None."""
-    import torch
     M, V = logits.shape
-    f32, i32 = torch.float32, torch.int32
-    G = 0
-    if tokens is not None:
-        shape = tokens.shape
-        if len(shape) not in (1, 2) or shape[0] != M:
-            raise ValueError(f"tokens must have shape ({M},) or ({M}, G) (got {tuple(shape)})")
-        G = shape[1] if len(shape) == 2 else 1
-        _is(tokens, "tokens", i32, *shape)
-    mask_ld, mask_bytes = 0, 0
-    if mask is not None:
-        rows, words = (1, mask.shape[0]) if mask.dim() == 1 else mask.shape
-        if rows not in (1, M) or words < (V + 31) // 32:
-            raise ValueError(f"mask must have 1 or {M} rows of at least {(V + 31) // 32} words (got {tuple(mask.shape)})")
-        _is(mask, "mask", i32, *mask.shape)
-        mask_ld, mask_bytes = words if rows > 1 else 0, mask.nbytes
+    G, mask_ld, mask_bytes = _logprob_inputs(M, V, tokens, mask)
     px, nx, ld = _rows(logits, "logits", logits.dtype, M, V)
     index = _gpu(logits=logits, tokens=tokens, mask=mask, workspace=workspace)
-    device = logits.device
     with _on(index, stream):
-        lp = None if tokens is None else torch.empty(shape, dtype=f32, device=device)
-        ent = torch.empty((M,), dtype=f32, device=device) if entropy else None
-        top_ids = top_lp = None
-        if k > 0:
-            top_ids = torch.empty((M, k), dtype=i32, device=device)
-            top_lp = torch.empty((M, k), dtype=f32, device=device)
-        if workspace is None:
-            need = logprobs_workspace_bytes(M, V, k)
-            workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        lp, ent, top_ids, top_lp = out = _logprob_outputs(M, k, tokens, entropy, logits.device)
+        workspace = _workspace(workspace, logprobs_workspace_bytes(M, V, k), logits.device)
         _check(load().qmm_logprobs(_float_type(logits, "logits"), px, nx, ld, M, V, scale, _ptr(mask), mask_bytes,
                                    mask_ld, _ptr(tokens), G, _ptr(lp), _ptr(ent), k, _ptr(top_ids), _ptr(top_lp),
                                    _ptr(workspace), 0 if workspace is None else workspace.nbytes, _current(index)),
                "qmm_logprobs")
-    return lp, ent, top_ids, top_lp
+    return out
+
+
+def mul_mat_logprobs_workspace_bytes(rows: int, N: int, k: int) -> int:
+    return int(load().qmm_mul_mat_logprobs_workspace_bytes(rows, N, k))
+
+
+def mul_mat_logprobs(wfmt: str, w, y, M: int, N: int, K: int, tokens=None, k: int = 0, scale: float = 1.0,
+                     mask=None, entropy: bool = True, layout: str = "canonical", rows: int = 512, workspace=None,
+                     stream=None):
+    """logprobs of mul_mat(w, y) [M, N], `rows` rows at a time (or as many as a given workspace holds): the
+    logits of all M rows need not exist at once.  w, y, M, N, K, layout as in mul_mat, the rest and the
+    results as in logprobs."""
+    G, mask_ld, mask_bytes = _logprob_inputs(M, N, tokens, mask)
+    if not (w.is_contiguous() and y.is_contiguous()):
+        raise ValueError("w and y must be contiguous")
+    if rows < 1:
+        raise ValueError(f"rows = {rows}: at least one at a time")
+    index = _gpu(w=w, y=y, tokens=tokens, mask=mask, workspace=workspace)
+    with _on(index, stream):
+        lp, ent, top_ids, top_lp = out = _logprob_outputs(M, k, tokens, entropy, w.device)
+        at_once = min(M, max(rows, 8))
+        workspace = _workspace(workspace, mul_mat_logprobs_workspace_bytes(at_once, N, k), w.device)
+        _check(load().qmm_mul_mat_logprobs(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], y.data_ptr(), y.nbytes,
+                                           M, N, K, scale, _ptr(mask), mask_bytes, mask_ld, _ptr(tokens), G, _ptr(lp),
+                                           _ptr(ent), k, _ptr(top_ids), _ptr(top_lp), _ptr(workspace),
+                                           0 if workspace is None else workspace.nbytes, _current(index)),
+               "qmm_mul_mat_logprobs")
+    return out
 
 
 def version() -> str:

@@ -767,6 +767,76 @@ qmm_status check_ld(const char *name, int64_t ld, int64_t n) {
     return QMM_OK;
 }
 
+qmm::LogprobArgs logprob_args(const void *logits, int64_t ld, int64_t M, int64_t V, float scale, const uint32_t *mask,
+                              int64_t mask_ld, const int32_t *tokens, int64_t G, float *token_logprobs, float *entropy,
+                              int64_t k, int32_t *top_ids, float *top_logprobs) {
+    qmm::LogprobArgs a{};
+    a.logits = logits;
+    a.mask = mask;
+    a.tokens = tokens;
+    a.token_logprobs = token_logprobs;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.M = M;
+    a.V = V;
+    a.ld = ld;
+    a.mask_ld = mask_ld;
+    a.G = G;
+    a.k = k;
+    a.scale = scale;
+    return a;
+}
+
+// everything but the logits and the workspace
+qmm_status check_logprobs(const qmm::LogprobArgs &a, size_t mask_bytes) {
+    QMM_TRY(check_rows("M", a.M));
+    QMM_TRY(check_rows("V", a.V));
+    if (a.M > qmm::logprobs_max_rows())
+        return fail(QMM_EUNSUPPORTED, "M = %lld exceeds the limit %lld", (long long)a.M,
+                    (long long)qmm::logprobs_max_rows());
+    if (!(a.scale > 0.0f && a.scale <= 1e30f))
+        return fail(QMM_EINVAL, "scale = %g; 0 < scale <= 1e30", (double)a.scale);
+    if (a.k < 0 || a.k > qmm::logprobs_max_k())
+        return fail(QMM_EUNSUPPORTED, "k = %lld; 0 <= k <= %lld", (long long)a.k, (long long)qmm::logprobs_max_k());
+    if (a.G < 0) return fail(QMM_EINVAL, "G = %lld is negative", (long long)a.G);
+    if (a.M == 0) return QMM_OK;
+    if (a.V == 0) return fail(QMM_EINVAL, "rows without logits (V = 0)");
+    if (a.G > ((int64_t(1) << 31) - 1) / a.M)
+        return fail(QMM_EUNSUPPORTED, "M*G = %lld*%lld tokens exceeds 2^31 - 1", (long long)a.M, (long long)a.G);
+    if (a.mask != nullptr) {
+        const int64_t words = (a.V + 31) / 32;
+        QMM_TRY(check_ptr("mask", a.mask));
+        if (a.mask_ld != 0) QMM_TRY(check_ld("mask_ld", a.mask_ld, words));
+        QMM_TRY(check_size("mask", mask_bytes, strided_bytes(a.M, a.mask_ld, words, sizeof(uint32_t))));
+    }
+    if (a.G > 0) {
+        QMM_TRY(check_ptr("tokens", a.tokens));
+        QMM_TRY(check_ptr("token_logprobs", a.token_logprobs));
+    }
+    if (a.entropy != nullptr) QMM_TRY(check_ptr("entropy", a.entropy));
+    if (a.k > 0) {
+        QMM_TRY(check_ptr("top_ids", a.top_ids));
+        QMM_TRY(check_ptr("top_logprobs", a.top_logprobs));
+    }
+    return QMM_OK;
+}
+
+bool outputs_overlap(const qmm::LogprobArgs &a, const void *p, size_t bytes) {
+    const size_t top = (size_t)(a.M * a.k) * sizeof(float);
+    return overlap(a.token_logprobs, (size_t)(a.M * a.G) * sizeof(float), p, bytes) ||
+           overlap(a.entropy, a.entropy != nullptr ? (size_t)a.M * sizeof(float) : 0, p, bytes) ||
+           overlap(a.top_ids, top, p, bytes) || overlap(a.top_logprobs, top, p, bytes);
+}
+
+// A row's part of mul_mat_logprobs' workspace: its logits, and what its statistics
+// need if it is alone (fewer rows are cut into more pieces).
+constexpr int64_t kHeadRows = 8;
+size_t head_logit_bytes(int64_t N) { return ((size_t)N * sizeof(float) + 15) / 16 * 16; }
+size_t head_row_bytes(int64_t N, int64_t k) {
+    return head_logit_bytes(N) + ((size_t)qmm::logprobs_workspace_bytes(1, N, k) + 15) / 16 * 16;
+}
+
 }  // namespace
 
 extern "C" {
@@ -862,64 +932,78 @@ qmm_status qmm_logprobs(qmm_float_type t, const void *logits, size_t logits_byte
                         float *top_logprobs, void *workspace, size_t ws_bytes, void *stream) {
     const size_t size = float_size(t);
     if (!size) return fail(QMM_EUNSUPPORTED, "unknown logit type %d", (int)t);
-    QMM_TRY(check_rows("M", M));
-    QMM_TRY(check_rows("V", V));
-    if (M > qmm::logprobs_max_rows())
-        return fail(QMM_EUNSUPPORTED, "M = %lld exceeds the limit %lld", (long long)M, (long long)qmm::logprobs_max_rows());
-    if (!(scale > 0.0f && scale <= 1e30f)) return fail(QMM_EINVAL, "scale = %g; 0 < scale <= 1e30", (double)scale);
-    if (k < 0 || k > qmm::logprobs_max_k())
-        return fail(QMM_EUNSUPPORTED, "k = %lld; 0 <= k <= %lld", (long long)k, (long long)qmm::logprobs_max_k());
-    if (G < 0) return fail(QMM_EINVAL, "G = %lld is negative", (long long)G);
+    const qmm::LogprobArgs a = logprob_args(logits, ld, M, V, scale, mask, mask_ld, tokens, G, token_logprobs, entropy, k,
+                                            top_ids, top_logprobs);
+    QMM_TRY(check_logprobs(a, mask_bytes));
     if (M == 0) return QMM_OK;
-    if (V == 0) return fail(QMM_EINVAL, "rows without logits (V = 0)");
-    if (G > ((int64_t(1) << 31) - 1) / M)
-        return fail(QMM_EUNSUPPORTED, "M*G = %lld*%lld tokens exceeds 2^31 - 1", (long long)M, (long long)G);
     QMM_TRY(check_ld("ld", ld, V));
     QMM_TRY(check_ptr("logits", logits));
-    QMM_TRY(check_size("logits", logits_bytes, strided_bytes(M, ld, V, size)));
-    if (mask != nullptr) {
-        const int64_t words = (V + 31) / 32;
-        QMM_TRY(check_ptr("mask", mask));
-        if (mask_ld != 0) QMM_TRY(check_ld("mask_ld", mask_ld, words));
-        QMM_TRY(check_size("mask", mask_bytes, strided_bytes(M, mask_ld, words, sizeof(uint32_t))));
-    }
-    if (G > 0) {
-        QMM_TRY(check_ptr("tokens", tokens));
-        QMM_TRY(check_ptr("token_logprobs", token_logprobs));
-    }
-    if (entropy != nullptr) QMM_TRY(check_ptr("entropy", entropy));
-    if (k > 0) {
-        QMM_TRY(check_ptr("top_ids", top_ids));
-        QMM_TRY(check_ptr("top_logprobs", top_logprobs));
-    }
+    const size_t x_need = strided_bytes(M, ld, V, size);
+    QMM_TRY(check_size("logits", logits_bytes, x_need));
     const size_t ws_need = qmm_logprobs_workspace_bytes(M, V, k);
     if (ws_need != 0) {
         QMM_TRY(check_ptr("workspace", workspace));
         QMM_TRY(check_size("workspace", ws_bytes, ws_need));
     }
-    const size_t x_need = strided_bytes(M, ld, V, size), top = (size_t)(M * k) * sizeof(float);
-    if (overlap(token_logprobs, (size_t)(M * G) * sizeof(float), logits, x_need) ||
-        overlap(entropy, entropy != nullptr ? (size_t)M * sizeof(float) : 0, logits, x_need) ||
-        overlap(top_ids, top, logits, x_need) || overlap(top_logprobs, top, logits, x_need) ||
-        overlap(workspace, ws_need, logits, x_need))
+    if (outputs_overlap(a, logits, x_need) || overlap(workspace, ws_need, logits, x_need))
         return fail(QMM_EINVAL, "an output or the workspace overlaps the logits");
-    qmm::LogprobArgs a{};
-    a.logits = logits;
-    a.mask = mask;
-    a.tokens = tokens;
-    a.token_logprobs = token_logprobs;
-    a.entropy = entropy;
-    a.top_ids = top_ids;
-    a.top_logprobs = top_logprobs;
-    a.M = M;
-    a.V = V;
-    a.ld = ld;
-    a.mask_ld = mask_ld;
-    a.G = G;
-    a.k = k;
-    a.scale = scale;
     return device_status(qmm::launch_logprobs((int)t, a, workspace, static_cast<hipStream_t>(stream)),
                          "logprobs launch");
+}
+
+size_t qmm_mul_mat_logprobs_workspace_bytes(int64_t rows, int64_t N, int64_t k) {
+    if (rows < 1 || rows > qmm::logprobs_max_rows() || N < 1 || N > kMaxRows || k < 0 || k > qmm::logprobs_max_k())
+        return 0;
+    return (size_t)rows * head_row_bytes(N, k);
+}
+
+qmm_status qmm_mul_mat_logprobs(qmm_weight_type t, const void *w, size_t w_bytes, qmm_layout l, const void *y,
+                                size_t y_bytes, int64_t M, int64_t N, int64_t K, float scale, const uint32_t *mask,
+                                size_t mask_bytes, int64_t mask_ld, const int32_t *tokens, int64_t G,
+                                float *token_logprobs, float *entropy, int64_t k, int32_t *top_ids,
+                                float *top_logprobs, void *workspace, size_t ws_bytes, void *stream) {
+    if (!w_qk(t)) return fail(QMM_EUNSUPPORTED, "unknown weight type %d", (int)t);
+    float *logits = static_cast<float *>(workspace);
+    qmm::LogprobArgs a = logprob_args(logits, N, M, N, scale, mask, mask_ld, tokens, G, token_logprobs, entropy, k,
+                                      top_ids, top_logprobs);
+    QMM_TRY(check_logprobs(a, mask_bytes));
+    // the logits' room is checked as the workspace's
+    QMM_TRY(mul_mat_common(t, w, w_bytes, l, y, y_bytes, logits, ~size_t(0), M, N, K));
+    if (M == 0) return QMM_OK;
+    const size_t row = head_row_bytes(N, k);
+    const int64_t least = M < kHeadRows ? M : kHeadRows;
+    QMM_TRY(check_size("workspace", ws_bytes, (size_t)least * row));
+    // the activation rows of a part start on 16 bytes: 8 rows of any format do
+    int64_t at_once = ws_bytes / row < (size_t)M ? (int64_t)(ws_bytes / row) / kHeadRows * kHeadRows : M;
+    const qmm_act_type at = t == QMM_Q4_0 ? QMM_Q8_0 : QMM_Q8_K;
+    if (outputs_overlap(a, workspace, (size_t)at_once * row))
+        return fail(QMM_EINVAL, "an output overlaps the workspace");
+    void *rest = static_cast<uint8_t *>(workspace) + (size_t)at_once * head_logit_bytes(N);
+    for (int64_t m = 0; m < M; m += at_once) {
+        const int64_t n = M - m < at_once ? M - m : at_once;
+        const uint8_t *ym = static_cast<const uint8_t *>(y) + qmm_act_bytes(at, m, K);
+        const size_t y_part = qmm_act_bytes(at, n, K), out_part = (size_t)(n * N) * sizeof(float);
+        switch (t) {
+            case QMM_Q4_0: QMM_TRY(qmm_mul_mat_q4_0(w, w_bytes, l, ym, y_part, logits, out_part, n, N, K, stream)); break;
+            case QMM_Q4_K: QMM_TRY(qmm_mul_mat_q4_K(w, w_bytes, l, ym, y_part, logits, out_part, n, N, K, stream)); break;
+            case QMM_Q6_K: QMM_TRY(qmm_mul_mat_q6_K(w, w_bytes, l, ym, y_part, logits, out_part, n, N, K, stream)); break;
+            case QMM_Q2_K: QMM_TRY(qmm_mul_mat_q2_K(w, w_bytes, l, ym, y_part, logits, out_part, n, N, K, stream)); break;
+        }
+        a.M = n;
+        QMM_TRY(device_status(qmm::launch_logprobs((int)QMM_F32, a, rest, static_cast<hipStream_t>(stream)),
+                              "mul_mat_logprobs statistics launch"));
+        if (mask != nullptr) a.mask += n * mask_ld;
+        if (G > 0) {
+            a.tokens += n * G;
+            a.token_logprobs += n * G;
+        }
+        if (entropy != nullptr) a.entropy += n;
+        if (k > 0) {
+            a.top_ids += n * k;
+            a.top_logprobs += n * k;
+        }
+    }
+    return QMM_OK;
 }
 
 const char *qmm_status_string(qmm_status s) {

@@ -436,6 +436,28 @@ qmm_status qmm_logprobs(qmm_float_type t, const void *logits, size_t logits_byte
                         int64_t k, int32_t *top_ids, float *top_logprobs,
                         void *workspace, size_t ws_bytes, void *stream);
 
+/* Bytes of the workspace with which qmm_mul_mat_logprobs computes `rows` rows at a
+ * time (their fp32 logits and what qmm_logprobs needs for them).  Returns 0 for
+ * invalid arguments. */
+size_t qmm_mul_mat_logprobs_workspace_bytes(int64_t rows, int64_t N, int64_t k);
+
+/* The head and what its logits say, in one call: logits = mul_mat(w, y) for
+ * weight format t (kernel choice as QMM_ALGO_AUTO describes), then qmm_logprobs of
+ * them, for as many rows at a time as the workspace holds, so that the M x N
+ * logits need not exist at once (2048 rows of 128256 are 1 GiB).  scale, mask,
+ * tokens, G, k and the outputs are those of qmm_logprobs with V = N.  A row's
+ * results are those of the two calls on the rows computed with it; how many these
+ * are matters only through AUTO's kernel choice (the last bits of the logits).
+ * workspace: device, bytes for at least min(M, 8) rows, overwritten; a number
+ * between is rounded down to a multiple of 8 rows.  Calls that may overlap need
+ * one each. */
+qmm_status qmm_mul_mat_logprobs(qmm_weight_type t, const void *w, size_t w_bytes, qmm_layout l,
+                                const void *y, size_t y_bytes, int64_t M, int64_t N, int64_t K,
+                                float scale, const uint32_t *mask, size_t mask_bytes, int64_t mask_ld,
+                                const int32_t *tokens, int64_t G, float *token_logprobs, float *entropy,
+                                int64_t k, int32_t *top_ids, float *top_logprobs,
+                                void *workspace, size_t ws_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *qmm_status_string(qmm_status s);
 

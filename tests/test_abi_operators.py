@@ -109,6 +109,34 @@ def test_logprobs_refusals(lib):  # noqa: F811
     assert lib.qmm_logprobs_workspace_bytes(3, 100000, 65) == 0 and lib.qmm_logprobs_workspace_bytes(0, 100000, 1) == 0
 
 
+def test_mul_mat_logprobs_refusals(lib):  # noqa: F811
+    base = dict(t=1, w=_far(0), wb=BIG, l=1, y=_far(1), yb=BIG, M=20, N=1001, K=512, scale=1.0, mask=None, mb=0, mld=0,
+                tok=_far(2), G=1, lp=_far(3), ent=_far(4), k=4, ti=_far(5), tl=_far(6), ws=_far(7), wsb=BIG)
+
+    def call(**kw):
+        a = {**base, **kw}
+        return lib.qmm_mul_mat_logprobs(a["t"], a["w"], a["wb"], a["l"], a["y"], a["yb"], a["M"], a["N"], a["K"],
+                                        a["scale"], a["mask"], a["mb"], a["mld"], a["tok"], a["G"], a["lp"], a["ent"],
+                                        a["k"], a["ti"], a["tl"], a["ws"], a["wsb"], None)
+
+    bytes_ = lib.qmm_mul_mat_logprobs_workspace_bytes
+    assert call(t=4) == EUNSUP and call(l=2) == EUNSUP and call(K=384) == EUNSUP
+    assert call(M=-1) == EINVAL and call(N=0) == EINVAL and call(N=2**24 + 1) == EUNSUP
+    assert call(scale=0.0) == EINVAL and call(k=65) == EUNSUP and call(G=-1) == EINVAL
+    for p in ("w", "y", "tok", "lp", "ti", "tl", "ws"):
+        assert call(**{p: None}) == EINVAL, p
+        assert call(**{p: base[p] + 4}) == EALIGN, p
+    assert call(wb=1001 * 2 * 144 - 1) == EINVAL and call(yb=20 * 2 * 292 - 1) == EINVAL
+    assert call(mask=_far(8), mb=20 * 32 * 4 - 1, mld=32) == EINVAL
+    # room for eight rows at least, or for all of fewer
+    assert call(wsb=bytes_(8, 1001, 4) - 1) == EINVAL and "workspace" in _last(lib)
+    assert call(M=3, wsb=bytes_(3, 1001, 4) - 1) == EINVAL
+    assert call(lp=_far(7) + bytes_(20, 1001, 4) - 16) == EINVAL and "overlaps" in _last(lib)
+    assert call(M=0, w=None, y=None, ws=None) == OK
+    assert bytes_(8, 1001, 4) == 8 * bytes_(1, 1001, 4) >= 8 * 1001 * 4
+    assert bytes_(0, 1001, 4) == 0 and bytes_(1, 0, 4) == 0 and bytes_(1, 1001, 65) == 0
+
+
 def test_binding_refusals():
     """Shapes and types are checked before the library is called; CPU tensors are refused."""
     ids = torch.zeros(3, dtype=torch.int32)
