@@ -4,8 +4,9 @@
 //     m = max x,  S = sum_i e^{scale (x_i - m)},  T = sum_i scale (x_i - m) e^{scale (x_i - m)}
 //     log p_i = scale (x_i - m) - log S,          H = log S - T / S
 //
-// One pass over the logits: each lane keeps a running (m, S, T) in fp32 and
-// rescales it when its maximum grows; exponents are taken in base 2.  T's terms
+// One pass over the logits: each lane keeps a running (m, S, T) in fp32, S with
+// what its rounding leaves, and rescales it when its maximum grows; exponents are
+// taken in base 2; lanes, wavefronts and splits are joined in 64 bits.  T's terms
 // are all <= 0, so the entropy has no cancellation.
 //
 // The k best ride in the same pass.  A token's key is 64 bits, the order of its
@@ -179,8 +180,31 @@ __device__ __forceinline__ uint32_t common_bound(uint32_t mine, int k, uint32_t 
 }
 
 // ---- running statistics in base 2: c = scale * log2(e)
+// S is 1 plus what the other tokens have, often little: joins add in 64 bits, and
+// log S is taken of S - 1.
+template <int kCtrl>
+__device__ __forceinline__ double dpp_f64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)dpp_i32<kCtrl>((int)(uint32_t)u), hi = (uint32_t)dpp_i32<kCtrl>((int)(u >> 32));
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    v += dpp_f64<0xB1>(v);
+    v += dpp_f64<0x4E>(v);
+    v += dpp_f64<0x141>(v);
+    v += dpp_f64<0x140>(v);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWave; i += 16) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, i), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), i);
+        sum += __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+    }
+    return sum;
+}
 struct Stats {
-    float m, s, t;
+    float m, t;
+    double s;
     // the same sums against a maximum to >= m
     __device__ __forceinline__ void rescale(float to, float c) {
         if (m == -kInf) {  // s and t are 0, or NaN, and stay so
@@ -189,25 +213,44 @@ struct Stats {
         }
         const float d = (m - to) * c;
         const float f = __builtin_amdgcn_exp2f(d);
-        t = f > 0.f ? f * (t + d * s) : f * s;
-        s = f * s;
+        t = f > 0.f ? f * (t + d * (float)s) : f * t;
+        s *= f;
         m = to;
     }
     __device__ __forceinline__ void join_wave(float c) {
         rescale(wave_max(m), c);
-        s = wave_sum(s);
+        s = wave_sum_f64(s);
         t = wave_sum(t);
     }
+    __device__ __forceinline__ bool none() const { return m == -kInf && s == 0.0; }  // nothing allowed, or all -inf
+    __device__ __forceinline__ float log_s() const { return log1pf((float)(s - 1.0)); }
     // log p of logit x, in natural units throughout (the lowest finite logit times
-    // log2(e) would overflow); an empty row (nothing allowed, or all -inf) has none
+    // log2(e) would overflow)
     __device__ __forceinline__ float logprob(float x, float scale) const {
-        if (m == -kInf && s == 0.f) return -kInf;
-        return (x - m) * scale - log2f(s) * kLn2;
+        return none() ? -kInf : (x - m) * scale - log_s();
     }
-    __device__ __forceinline__ float entropy() const {
-        if (m == -kInf && s == 0.f) return 0.f;
-        return (log2f(s) - t / s) * kLn2;
+    __device__ __forceinline__ float entropy() const { return none() ? 0.f : log_s() - t / (float)s * kLn2; }
+};
+// A thread's share: s + rest is the sum, rest what rounding left.
+struct Share {
+    float m, s, rest, t;
+    __device__ __forceinline__ void rescale(float to, float c) {
+        if (m != -kInf) {
+            const float d = (m - to) * c;
+            const float f = __builtin_amdgcn_exp2f(d);
+            t = f > 0.f ? f * (t + d * s) : f * s;
+            s = f * s;
+            rest = f * rest;
+        }
+        m = to;
     }
+    __device__ __forceinline__ void add(float bs, float bt) {
+        const float sum = s + bs, b = sum - s;
+        rest += (s - (sum - b)) + (bs - b);
+        s = sum;
+        t += bt;
+    }
+    __device__ __forceinline__ Stats stats() const { return Stats{m, t, (double)s + (double)rest}; }
 };
 
 __device__ __forceinline__ bool allowed(const uint32_t *mask, int i) { return mask[i >> 5] >> (i & 31) & 1; }
@@ -269,7 +312,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, const Stats &st
         });
         for (int i = n + (int)threadIdx.x; i < a.k; i += kThreads) {  // fewer than k tokens have a probability
             ids[i] = -1;
-            lps[i] = st.s != st.s ? st.s : -kInf;
+            lps[i] = st.s != st.s ? (float)st.s : -kInf;
         }
     }
 }
@@ -308,7 +351,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
     const int tail = whole > 0 ? f1 * VEC - lead : V;
     const bool edges = split == 0 && head + V - tail > 0;
 
-    Stats st{-kInf, 0.f, 0.f};
+    Share mine{-kInf, 0.f, 0.f, 0.f};
     List l{lists[wave], 0, (int)a.k, 0, -__FLT_MAX__};
     const int batches = (j1 - j0 + kThreads * U - 1) / (kThreads * U);
     for (int it = 0; it < batches + (edges ? 1 : 0); ++it) {
@@ -350,12 +393,12 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
         float top = -kInf;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) top = fmaxf(top, v[i]);
-        if (top > st.m) st.rescale(top, c);
+        if (top > mine.m) mine.rescale(top, c);
         // all of them -inf so far: any finite number in the maximum's place gives e = 0
-        const float m = st.m == -kInf ? 0.f : st.m;
-        // the batch's terms by themselves first: next to the term of the maximum each
-        // small one would be rounded at its size
-        float bs = 0.f, bt = 0.f;
+        const float m = mine.m == -kInf ? 0.f : mine.m;
+        // the batch's terms by themselves first, in two sums: next to the term of the
+        // maximum each small one would be rounded at its size
+        float bs[2] = {0.f, 0.f}, bt[2] = {0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (u > 0 && u >= filled) break;
@@ -363,18 +406,17 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
             for (int q = 0; q < VEC; ++q) {
                 const float d = (v[u * VEC + q] - m) * c;
                 const float e = __builtin_amdgcn_exp2f(d);
-                bs += e;
-                bt = __builtin_fmaf(fmaxf(d, -1.0e4f), e, bt);  // e is 0 there: keeps -inf * 0 out
+                bs[q % 2] += e;
+                bt[q % 2] = __builtin_fmaf(fmaxf(d, -1.0e4f), e, bt[q % 2]);  // e is 0 there: keeps -inf * 0 out
             }
         }
-        st.s += bs;
-        st.t += bt;
+        mine.add(bs[0] + bs[1], bt[0] + bt[1]);
 
         // after batches 1, 3, 9, 33, ...: after 1, 2, 3, 5, 9 it cost more than it saved
         // (513 rows of 50257, k = 8: 25.9 against 24.4 us), after 1, 5, 17 less than it
         // let through (27.3 us)
         if (a.k > 0 && (it == 0 || ((it & (it - 1)) == 0 && (it & 0x2aaaaaaa) != 0)))
-            l.raise((uint64_t)common_bound(st.m > -kInf ? order_of(st.m) : 0, l.k, maxima) << 32);
+            l.raise((uint64_t)common_bound(mine.m > -kInf ? order_of(mine.m) : 0, l.k, maxima) << 32);
         if (a.k > 0 && __ballot(top >= l.least) != 0) {
             uint32_t left = 0;  // which of this lane's logits may enter
 #pragma unroll
@@ -390,10 +432,11 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
         }
     }
     if (l.count > kWave) l.cut();
+    Stats st = mine.stats();
     st.join_wave(c);
     if (lane == 0) wave_stats[wave] = st;
     __syncthreads();
-    st = lane < kWaves ? wave_stats[lane] : Stats{-kInf, 0.f, 0.f};
+    st = lane < kWaves ? wave_stats[lane] : Stats{-kInf, 0.f, 0.0};
     st.join_wave(c);
 
     const bool has = lane < l.count;
@@ -403,7 +446,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
         return;
     }
     const int64_t part = row * splits + split;
-    if (threadIdx.x == 0) a.ws_stats[part] = make_float4(st.m, st.s, st.t, 0.f);
+    if (threadIdx.x == 0) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, st.s);
+        a.ws_stats[part] = make_float4(st.m, st.t, __uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32)));
+    }
     if (a.k > 0) {
         uint64_t *out = a.ws_keys + part * a.k;
         const int n = rank_keys(key, has, (int)a.k, all, counts, [&](int rank, uint64_t best) { out[rank] = best; });
@@ -424,10 +470,11 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_merge(const LogprobArgs a
     const Given given = given_token<T>(a, row, threadIdx.x);
     const int total = splits * (int)a.k;
     const uint64_t *in = a.ws_keys + row * total;
-    Stats st{-kInf, 0.f, 0.f};
+    Stats st{-kInf, 0.f, 0.0};
     if (lane < splits) {
         const float4 p = a.ws_stats[row * splits + lane];
-        st = Stats{p.x, p.y, p.z};
+        const uint64_t u = ((uint64_t)__float_as_uint(p.w) << 32) | __float_as_uint(p.z);
+        st = Stats{p.x, p.y, __builtin_bit_cast(double, u)};
     }
     st.join_wave(c);
     constexpr int n = kMaxSplits * kMaxK / kThreads;  // keys per thread
