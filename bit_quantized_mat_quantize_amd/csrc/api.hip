@@ -747,6 +747,10 @@ qmm_status qmm_debug_block_sums(qmm_weight_type t, const void *w, size_t w_bytes
 
 namespace {
 
+const char *weight_name(qmm_weight_type t) {
+    return t == QMM_Q4_0 ? "Q4_0" : t == QMM_Q4_K ? "Q4_K" : t == QMM_Q6_K ? "Q6_K" : "Q2_K";
+}
+
 size_t float_size(qmm_float_type t) { return t == QMM_F32 ? 4 : ((t == QMM_F16 || t == QMM_BF16) ? 2 : 0); }
 
 bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
@@ -859,6 +863,10 @@ qmm_status qmm_embed_rows(qmm_weight_type t, const void *w, size_t w_bytes, qmm_
     QMM_TRY(check_size("out", out_bytes, out_need));
     if (overlap(out, out_need, w, need) || overlap(out, out_need, ids, (size_t)T * sizeof(int32_t)))
         return fail(QMM_EINVAL, "out overlaps w or ids");
+    if (log_enabled())
+        fprintf(stderr, "qmm: embed_rows %s T=%lld N=%lld K=%lld layout=%s -> %s\n", weight_name(t), (long long)T,
+                (long long)N, (long long)K, l == QMM_LAYOUT_REPACKED ? "repacked" : "canonical",
+                qmm::embed_rows_long(T, K) ? "stores past the caches" : "plain stores");
     return device_status(qmm::launch_embed_rows((int)t, static_cast<const uint8_t *>(w), l == QMM_LAYOUT_REPACKED, ids,
                                                 T, scale, out, N, K, static_cast<hipStream_t>(stream)),
                          "embed_rows launch");
@@ -918,6 +926,13 @@ qmm_status qmm_lora_add(qmm_float_type t, const void *A, size_t a_bytes, const v
         return fail(QMM_EUNSUPPORTED, "M = %lld, N = %lld needs more than 2^32 threads", (long long)M, (long long)N);
     const qmm::LoraArgs a{A, B, scales, ranks, x, ids, base, out, static_cast<float *>(workspace),
                           M, N, K, R, E, ld_base, ld_out};
+    if (log_enabled()) {
+        int splits, shared;
+        qmm::lora_shape(M, R, K, E, &splits, &shared);
+        fprintf(stderr, "qmm: lora_add M=%lld N=%lld K=%lld R=%lld E=%lld -> K in %d parts, %d workgroup(s) per 16-row "
+                "tile%s\n", (long long)M, (long long)N, (long long)K, (long long)R, (long long)E, splits, shared,
+                in_place ? ", in place" : "");
+    }
     return device_status(qmm::launch_lora_add((int)t, a, static_cast<hipStream_t>(stream)), "lora_add launch");
 }
 
@@ -947,6 +962,9 @@ qmm_status qmm_logprobs(qmm_float_type t, const void *logits, size_t logits_byte
     }
     if (outputs_overlap(a, logits, x_need) || overlap(workspace, ws_need, logits, x_need))
         return fail(QMM_EINVAL, "an output or the workspace overlaps the logits");
+    if (log_enabled())
+        fprintf(stderr, "qmm: logprobs M=%lld V=%lld G=%lld k=%lld -> %d workgroup(s) per row\n", (long long)M,
+                (long long)V, (long long)G, (long long)k, qmm::logprobs_splits(M, V));
     return device_status(qmm::launch_logprobs((int)t, a, workspace, static_cast<hipStream_t>(stream)),
                          "logprobs launch");
 }
@@ -978,6 +996,9 @@ qmm_status qmm_mul_mat_logprobs(qmm_weight_type t, const void *w, size_t w_bytes
     const qmm_act_type at = t == QMM_Q4_0 ? QMM_Q8_0 : QMM_Q8_K;
     if (outputs_overlap(a, workspace, (size_t)at_once * row))
         return fail(QMM_EINVAL, "an output overlaps the workspace");
+    if (log_enabled())
+        fprintf(stderr, "qmm: mul_mat_logprobs %s M=%lld N=%lld K=%lld -> %lld rows at a time\n", weight_name(t),
+                (long long)M, (long long)N, (long long)K, (long long)at_once);
     void *rest = static_cast<uint8_t *>(workspace) + (size_t)at_once * head_logit_bytes(N);
     for (int64_t m = 0; m < M; m += at_once) {
         const int64_t n = M - m < at_once ? M - m : at_once;

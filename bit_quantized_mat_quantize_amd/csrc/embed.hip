@@ -140,16 +140,19 @@ hipError_t launch(const uint8_t *w, int64_t NB, int64_t dsec, const int32_t *ids
 }
 
 constexpr int64_t kLongBytes = 32 << 20;  // the L2 caches hold 4 MiB for each of 8 XCDs
+bool long_output(int64_t T, int64_t K) { return T * K * (int64_t)sizeof(float) >= kLongBytes; }
 
 template <int FMT>
 hipError_t launch_for(const uint8_t *w, bool repacked, int64_t NB, int64_t dsec, const int32_t *ids, int64_t T,
                       float scale, float *out, int64_t N, int64_t K, hipStream_t s) {
-    const auto f = T * K * 4 >= kLongBytes ? (repacked ? launch<FMT, true, true> : launch<FMT, false, true>)
-                                           : (repacked ? launch<FMT, true, false> : launch<FMT, false, false>);
+    const auto f = long_output(T, K) ? (repacked ? launch<FMT, true, true> : launch<FMT, false, true>)
+                                     : (repacked ? launch<FMT, true, false> : launch<FMT, false, false>);
     return f(w, NB, dsec, ids, T, scale, out, N, K, s);
 }
 
 }  // namespace
+
+bool embed_rows_long(int64_t T, int64_t K) { return long_output(T, K); }
 
 hipError_t launch_embed_rows(int fmt, const uint8_t *w, bool repacked, const int32_t *ids, int64_t T, float scale,
                              float *out, int64_t N, int64_t K, hipStream_t s) {

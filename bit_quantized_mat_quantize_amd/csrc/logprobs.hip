@@ -525,6 +525,7 @@ hipError_t both(const LogprobArgs &a, hipStream_t s) {
 }  // namespace
 
 int64_t logprobs_max_k() { return kMaxK; }
+int logprobs_splits(int64_t M, int64_t V) { return splits_of(M, V); }
 int64_t logprobs_max_rows() { return (int64_t(1) << 32) / kThreads - 1; }
 
 int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k) {

@@ -179,13 +179,22 @@ __global__ __launch_bounds__(kShrinkThreads, 4) void k_lora_shrink(const T *__re
 // ---- the second product's operands.  fp32 B: C = 4 consecutive ranks per lane
 // feed four v_mfma_f32_16x16x4_f32.  16-bit B goes to the 16-bit instruction as it
 // is (C = 8 ranks per lane, v_mfma_f32_16x16x32), and v as three 16-bit numbers
-// that add up to it: bf16 pieces cut off eight bits each, which is exact; fp16
-// pieces round to 11 bits each of v times a power of two that puts the row's
-// largest |v| below 2^15 (fp16's range is narrow), what is left is below 2^-33 of
-// that.  Three products of 32 ranks take 48 cycles; eight fp32 instructions would
-// take 256, and B would have to be converted.
+// that add up to it, of v times a power of two that puts the row's largest |v|
+// below 2^15 (fp16's range is narrow, and small pieces must not become subnormal):
+// bf16 pieces cut off eight bits each, which is exact; fp16 pieces round to 11 bits
+// each, what is left is below 2^-33 of the largest.  Three products of 32 ranks take
+// 48 cycles; eight fp32 instructions would take 256, and B would have to be
+// converted.
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+// of the power of two that puts top, a row's largest |v|, into [2^14, 2^15) (an
+// infinity or NaN: none; top below 2^-112: as near as it goes)
+__device__ __forceinline__ int exponent_to_15(float top) {
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;  // top in [2^e, 2^(e+1))
+    return e == 128 ? 0 : (14 - e < 126 ? 14 - e : 126);
+}
 
 template <typename T>
 struct Operand;
@@ -206,7 +215,7 @@ template <>
 struct Operand<BF16> {
     static constexpr int C = 8, pieces = 3;
     typedef uint16_t Stored;
-    static __device__ __forceinline__ int exponent(float) { return 0; }
+    static __device__ __forceinline__ int exponent(float top) { return exponent_to_15(top); }
     static __device__ __forceinline__ void split(float v, Stored (&p)[3]) {
         const bool finite = fabsf(v) < __builtin_inff();
         const uint32_t quiet = v != v ? 0x400000u : 0;  // cutting bits off a NaN must not leave an infinity
@@ -225,11 +234,7 @@ template <>
 struct Operand<_Float16> {
     static constexpr int C = 8, pieces = 3;
     typedef uint16_t Stored;
-    // of the power of two for a row whose largest |v| is top
-    static __device__ __forceinline__ int exponent(float top) {
-        const int e = (int)(__float_as_uint(top) >> 23) - 127;  // top in [2^e, 2^(e+1))
-        return e == 128 ? 0 : (14 - e < 126 ? 14 - e : 126);
-    }
+    static __device__ __forceinline__ int exponent(float top) { return exponent_to_15(top); }
     static __device__ __forceinline__ void split(float v, Stored (&p)[3]) {
         const bool finite = fabsf(v) < __builtin_inff();
 #pragma unroll
@@ -242,6 +247,52 @@ struct Operand<_Float16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, v), acc, 0, 0, 0);
     }
 };
+
+// One chunk: acc[t] += w[t] * (the pieces of v), the small pieces first.
+//
+// fp16: the instruction takes subnormal numbers as they are, but a sum of nothing
+// else loses the bits that their leading zeros push out (15 of 24 were left).  Rows
+// of B without a normal number are multiplied as 2^10 of themselves, and what their
+// sums hold before and after is moved by 2^10 with them; all of it is exact.
+template <typename T>
+__device__ __forceinline__ void multiply(uint4 (&w)[kNT], const uint4 (&v)[Operand<T>::pieces], v4f (&acc)[kNT]) {
+    const int lane = threadIdx.x & 63;
+    uint32_t small[kNT], any = 0;  // a bit for each of the 16 rows
+    auto move = [&](float f) {     // the lane's sums are those of rows 4 * (lane / 16) + q
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (small[t] >> (4 * (lane >> 4) + q) & 1) acc[t][q] *= f;
+    };
+    if constexpr (__is_same(T, _Float16)) {
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            uint64_t b = __ballot(((w[t].x | w[t].y | w[t].z | w[t].w) & 0x7c007c00u) != 0);
+            b |= b >> 32;
+            small[t] = ~(uint32_t)(b | b >> 16) & 0xffffu;
+            any |= small[t];
+        }
+        if (any != 0) {
+            move(1024.0f);
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) {
+                const _Float16 f = small[t] >> (lane & 15) & 1 ? (_Float16)1024.0f : (_Float16)1.0f;
+                const auto times = [f](uint32_t two) {
+                    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, two) * v2h{f, f});
+                };
+                w[t] = make_uint4(times(w[t].x), times(w[t].y), times(w[t].z), times(w[t].w));
+            }
+        }
+    }
+#pragma unroll
+    for (int i = Operand<T>::pieces - 1; i >= 0; --i)
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) acc[t] = Operand<T>::mul(w[t], v[i], acc[t]);
+    if constexpr (__is_same(T, _Float16)) {
+        if (any != 0) move(0.0009765625f);
+    }
+}
 
 // elements of a row of v in LDS: whole chunks of 4 * C ranks, and 16 bytes more so
 // that the rows start on different banks
@@ -446,10 +497,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_lora_expand(const T *__restrict
                 uint4 vp[Op::pieces];
 #pragma unroll
                 for (int i = 0; i < Op::pieces; ++i) vp[i] = ld16(vs + (i * kTileRows + row) * vld + r);
-#pragma unroll
-                for (int i = Op::pieces - 1; i >= 0; --i)  // the small pieces first
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) acc[t] = Op::mul(w[t], vp[i], acc[t]);
+                multiply<T>(w, vp, acc);
             }
             if (match >> row & 1) {
                 const int ex = exponents[row];
@@ -579,6 +627,12 @@ int64_t lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E) {
 }
 
 int64_t lora_max_rank() { return kMaxRank; }
+
+void lora_shape(int64_t M, int64_t R, int64_t K, int64_t E, int *splits, int *shared) {
+    const Shape h = shape(M, R, K, E);
+    *splits = h.splits;
+    *shared = h.zsplit;
+}
 
 bool lora_grid_ok(int64_t M, int64_t N, int64_t R, int64_t K, int64_t E) {
     const Shape h = shape(M, R, K, E);

@@ -204,6 +204,7 @@ hipError_t launch_gemm_id_q4_K(const uint8_t *w, bool repacked, int64_t w_stride
 // ---- rows of a packed table by id, decoded and scaled (embed.hip); fmt is a qmm_weight_type
 hipError_t launch_embed_rows(int fmt, const uint8_t *w, bool repacked, const int32_t *ids, int64_t T, float scale,
                              float *out, int64_t N, int64_t K, hipStream_t s);
+bool embed_rows_long(int64_t T, int64_t K);  // the output goes past the caches
 
 // ---- low-rank adapters per row (lora.hip); type is a qmm_float_type (of A and B).
 // Workspace: fp32 partial sums of v[m][r], one set per split of K.
@@ -220,6 +221,7 @@ struct LoraArgs {
 };
 int64_t lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E);
 int64_t lora_max_rank();
+void lora_shape(int64_t M, int64_t R, int64_t K, int64_t E, int *splits, int *shared);  // of a launch
 bool lora_grid_ok(int64_t M, int64_t N, int64_t R, int64_t K, int64_t E);  // both launches fit a grid
 hipError_t launch_lora_add(int type, const LoraArgs &a, hipStream_t s);
 
@@ -238,6 +240,7 @@ struct LogprobArgs {
     float scale;
 };
 int64_t logprobs_max_k();
+int logprobs_splits(int64_t M, int64_t V);  // workgroups per row
 int64_t logprobs_max_rows();  // rows of one launch
 int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);  // 0: not used
 hipError_t launch_logprobs(int type, LogprobArgs a, void *ws, hipStream_t s);

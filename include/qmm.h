@@ -425,7 +425,7 @@ size_t qmm_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);
  * A NaN or +inf among the allowed logits makes the row's log p and entropy NaN;
  * NaN never enters the top list.
  * Statistics are fp32; x is read once.  scale (one over the temperature): above
- * 0, at most 1e30.  Requires V <= 2^24, k <= 64, M < 2^24, M*G < 2^31.
+ * 0, at most 1e30.  Requires V <= 2^24, k <= 64, M < 2^23, M*G < 2^31.
  * Outputs must not overlap inputs or one another.
  * workspace: device, qmm_logprobs_workspace_bytes(M, V, k) bytes (NULL where
  * that is 0), overwritten; calls that may overlap need one each. */

@@ -215,6 +215,24 @@ def test_bad_tokens_give_nan():
     assert (np.abs(got[m, g] - ref.lp[m, tokens[m, g]]) <= ref.tol[m, tokens[m, g]]).all()
 
 
+def test_logits_past_4_gib():
+    """Rows that lie past 2^32 bytes; every row is the same one shifted, so its results are known."""
+    import torch
+    M, V, k = 9000, 120000, 4
+    rng = np.random.default_rng(13)
+    row, row64 = _dev_type(_logits(rng, 1, V), "f32")
+    x = torch.empty(M, V, device="cuda")
+    assert x.numel() * 4 > 1 << 32
+    x.copy_(row.expand(M, V))
+    at = np.array([0, 8946, 8947, 8948, M - 1])                        # row 8947 holds byte 2^32
+    x[8947, 77], x[M - 1, V - 1] = 30.0, 31.0
+    lp, H, ids, tl = qmm.logprobs(x, tokens=torch.full((M,), 77, dtype=torch.int32, device="cuda"), k=k)
+    x64 = np.tile(row64, (len(at), 1))
+    x64[2, 77], x64[4, V - 1] = 30.0, 31.0
+    pick = torch.from_numpy(at).cuda()
+    Reference(x64).check([t[pick] for t in (lp, H, ids, tl)], np.full((len(at), 1), 77), k)
+
+
 def test_more_tokens_than_threads_and_empty():
     import torch
     rng = np.random.default_rng(4)

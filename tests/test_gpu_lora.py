@@ -174,6 +174,50 @@ def test_in_place_and_column_ranges(M, N):
     assert np.array_equal(got[:, free], whole[:, free])
 
 
+@pytest.mark.parametrize("type", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("scale_x,scale_b", [(1.0, 1e-6), (1e30, 1e-5), (1e-30, 1.0), (3e4, 100.0)])
+@pytest.mark.parametrize("M", [2, 40])
+def test_magnitudes(M, scale_x, scale_b, type):
+    """B subnormal in fp16, x far outside its range, rows of v whose elements lie far apart."""
+    print(M, scale_x, scale_b, type, flush=True)
+    rng = np.random.default_rng(11)
+    N, K, R, E = 65, 64, 20, 2
+    A, B, _, _ = _pool(rng, E, R, N, K, "f32")
+    A = (A * to_dev((10.0 ** rng.uniform(-6, 0, (E, R, 1))).astype(np.float32))).to(_torch_type(type))
+    B = B * scale_b
+    B[:, 3::5] *= 1e-4                                  # rows far below their neighbours
+    B = B.to(_torch_type(type))
+    x, _, ids = _inputs(rng, M, N, K, E=E)
+    x = (x * scale_x).astype(np.float32)
+    base = np.zeros((M, N), np.float32)
+    ids[0] = 1
+    got = to_host(qmm.lora_add(to_dev(base), to_dev(x), A, B, to_dev(ids)))
+    out, tol = _formula(base, x, to_host(A.double()), to_host(B.double()), ids)
+    # what fp16 pieces leave: below 2^-33 of the row's largest v, times sum|B|
+    for m, e in enumerate(ids):
+        if e >= 0:
+            v = np.abs(to_host(A[e].double()) @ x[m].astype(np.float64)).max()
+            tol[m] += 2.0 ** -33 * v * np.abs(to_host(B[e].double())).sum(1)
+    _check(got, out, tol)
+
+
+def test_out_past_4_gib():
+    """Rows of base and out that lie past 2^32 bytes, sampled."""
+    import torch
+    M, N, K, R, E = 40000, 28672, 32, 4, 3
+    rng = np.random.default_rng(12)
+    A, B, A64, B64 = _pool(rng, E, R, N, K, "bf16")
+    x, _, ids = _inputs(rng, M, 1, K, E=E)
+    base = torch.zeros(M, N, device="cuda")
+    base += torch.arange(M, device="cuda", dtype=torch.float32).unsqueeze(1)
+    assert base.numel() * 4 > 1 << 32
+    rows = np.array([0, 1, 17, M // 2, 37449, 37450, M - 1])          # row 37449 holds byte 2^32
+    qmm.lora_add(base, to_dev(x), A, B, to_dev(ids), out=base)
+    got = to_host(base[torch.from_numpy(rows).cuda()])
+    want, tol = _formula(np.tile(rows[:, None], (1, N)).astype(np.float32), x[rows], A64, B64, ids[rows])
+    _check(got, want, tol)
+
+
 def test_unaligned_column_range_is_refused():
     rng = np.random.default_rng(1)
     A, B, _, _ = _pool(rng, 2, 4, 8, 32, "f16")
