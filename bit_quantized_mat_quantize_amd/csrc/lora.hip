@@ -554,17 +554,29 @@ struct Shape {
 };
 Shape shape(int64_t M, int64_t R, int64_t K, int64_t E) {
     Shape h;
-    h.rt = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
+    // a second tile of ranks uses the same x; four in one workgroup are slower than two
+    // workgroups of two (512 rows, K = 14336, rank 64: 79 us for both kernels, 67 so)
+    h.rt = R <= 16 ? 1 : 2;
     h.rank_blocks = (int)((R + 16 * h.rt - 1) / (16 * h.rt));
     h.Rp = h.rank_blocks * h.rt * 16;
     h.tiles = (M + kTileRows - 1) / kTileRows;
-    h.zsplit = M <= 64 ? 16 : (M <= 512 ? 4 : 1);
+    // Adapters of a tile side by side pay where a tile has many and there are few
+    // tiles; workgroups without an adapter cost what it takes to start them, and how
+    // many adapters a tile has is not known here.  Both kernels, K = 4096, N = 4096,
+    // rank 16, parts 16 / 4 / 1 of a tile: 48 rows of 16 requests 11.5 / 12.4 / 18.6
+    // us, of one 12.3 / 10.9 / 10.9; 100 rows of 64 requests - / 16.1 / 29.5, of one
+    // - / 10.8 / 11.0; 256 rows of 64 - / 19.0 / 19.2, of one - / 14.3 / 11.1
+    h.zsplit = M <= 32 ? 16 : (M <= 128 ? 4 : 1);
     if (h.zsplit > E) h.zsplit = (int)E;
     if (h.zsplit > M) h.zsplit = (int)M;
-    // two workgroups of eight wavefronts per CU, two steps for each wavefront at least
+    // two workgroups of eight wavefronts per CU, four where some of them may find no
+    // adapter or no rank of theirs (256 rows, K = 14336, rank 128: 65 us with four, 100
+    // with two; 700 rows at rank 32: 32 with two, 36 with four), and two steps for
+    // each wavefront at least
     const int64_t groups = h.tiles * h.zsplit * h.rank_blocks;
     const int64_t most = (K / kStep + 2 * (kShrinkThreads / kWave) - 1) / (2 * (kShrinkThreads / kWave));
-    int64_t s = (512 + groups - 1) / groups;
+    const int64_t wanted = h.zsplit > 1 || h.rank_blocks > 1 ? 1024 : 512;
+    int64_t s = (wanted + groups - 1) / groups;
     s = s > kMaxSplits ? kMaxSplits : s;
     h.splits = (int)(s > most ? most : s);
     return h;
@@ -610,7 +622,7 @@ hipError_t expand(const LoraArgs &a, const Shape &h, hipStream_t s) {
 template <typename T>
 hipError_t both(const LoraArgs &a, hipStream_t s) {
     const Shape h = shape(a.M, a.R, a.K, a.E);
-    hipError_t e = h.rt == 1 ? shrink<T, 1>(a, h, s) : (h.rt == 2 ? shrink<T, 2>(a, h, s) : shrink<T, 4>(a, h, s));
+    const hipError_t e = h.rt == 1 ? shrink<T, 1>(a, h, s) : shrink<T, 2>(a, h, s);
     if (e != hipSuccess) return e;
     constexpr int H = kMaxRank / 64;
     const bool vec = a.ld_base % 4 == 0 && a.ld_out % 4 == 0 && a.N % 4 == 0, bv = a.R % Operand<T>::C == 0;
