@@ -16,9 +16,9 @@
 // largest of 64 (or 256) maxima, each over some of the threads: values that are all
 // present.  It is taken after batches 1, 3, 9, 33, ... of a workgroup, so that the
 // lists grow slowly; a list that is full all the same (equal or ascending logits)
-// is cut back to its k best.  Both find the k-th largest by bisection over the bits: each step is a ballot and
-// a count, no data moves.  At the end the lists of the workgroup are ranked by
-// counting.
+// is cut back to its k best.  Both find the k-th largest by bisection over the bits:
+// each step is a ballot and a count, no data moves.  At the end the lists of the
+// workgroup are ranked by counting.
 //
 // A row is split over workgroups where there are few rows (partial statistics
 // and keys go to the workspace, k_logprobs_merge joins them); otherwise one
@@ -498,15 +498,17 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_merge(const LogprobArgs a
     finish_row<T>(a, st, row, given, key, has, all, counts);
 }
 
-// A row of up to four batches is not split: one workgroup takes 9.9 us for 32000
-// logits and its call 14.9 us, where four take 9.4 us with the second launch and
-// its call 18.7 us.  Longer ones make as many workgroups as run at once (four per
-// CU) and no more: 513 rows of 50257 in two splits, 1026 workgroups, took 37 us for
-// the two that had to wait, and 34 us in one.
+// A row of up to four batches (eight where 128 rows or more keep the CUs busy) is
+// not split: 32000 logits, k = 5, take one workgroup 9.9 us and its call 14.9 us,
+// four of them 9.4 us with the second launch and the call 18.7 us; 128 rows of
+// 50257, k = 8: 16 us in one launch, 18 us in two.  Longer rows make two workgroups
+// per CU (64 rows of 128256, k = 20, masked: 19.9 us with eight splits, 22.5 us with
+// sixteen), and from 256 rows on one workgroup each (256 rows of 50257, k = 8: 16.3
+// us, 24.2 us in four; 400 of 128256: 44.9 us, 53.5 us in two).
 int splits_of(int64_t M, int64_t V) {
     constexpr int64_t batch = kThreads * kBatch;
-    if (M >= 1024 || V <= 4 * batch) return 1;
-    const int64_t s = 1024 / M, most = (V + batch - 1) / batch;
+    if (M >= 256 || V <= (M < 128 ? 4 : 8) * batch) return 1;
+    const int64_t s = 512 / M, most = (V + batch - 1) / batch;
     return (int)(s > most ? (most > kMaxSplits ? kMaxSplits : most) : (s > kMaxSplits ? kMaxSplits : s));
 }
 
