@@ -197,7 +197,8 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
     for (int i = 0; i < kWave; i += 16) {
         const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, i), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), i);
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, i);
+        const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), i);
         sum += __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
     }
     return sum;
@@ -321,6 +322,13 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, const Stats &st
 // counted from the 16-byte boundary at or below its start, are divided among the
 // splits; the up to 14 logits before the first and behind the last (rows need
 // not start or end on a boundary) are a batch of their own in split 0.
+//
+// Measured: 1024 rows of 128256 fp32 logits, k = 1: 94 us, 5.6 TB/s, what a copy
+// reaches; 513 rows of 50257 fp16 logits, k = 8: 24 us for 52 MB: about 46 cycles of
+// vector instructions per 64 logits (an exponential is 16 of them), two rows per CU
+// and three on one, and 6 us for the bounds and lists (18 us with k = 0); 32 rows of
+// 128256 under masks, k = 20: 10.5 us in 16 splits each; one row of 32000, k = 5: 10
+// us, of which the statistics take 6 and the bounds (twice) and the ranking the rest.
 template <typename T, bool MASK>
 __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int splits) {
     constexpr int VEC = 16 / sizeof(T);
@@ -457,7 +465,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
     }
 }
 
-// ---- the splits of a row joined: one workgroup per row
+// ---- the splits of a row joined: one workgroup per row.  32 rows of 16 splits and 20
+// keys each: 5.8 us, the latency of a launch, of one load per thread, a bound and a
+// ranking.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_logprobs_merge(const LogprobArgs a, int splits) {
     __shared__ uint64_t lists[kWaves][kList];

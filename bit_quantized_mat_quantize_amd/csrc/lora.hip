@@ -17,14 +17,15 @@
 // have its own, and `zsplit` workgroups share a tile so that its adapters run
 // beside one another.
 //
-// The products run on the fp32 matrix instruction (v_mfma_f32_16x16x4_f32): x
-// is fp32 and the result is, so x is not rounded to 16 bits, and A and B in
-// fp16 or bf16 convert exactly.  Its rate (256 flop per cycle and CU) is above
-// what these products need up to ranks of about 64, where x, base and out are
-// what has to move.  A lane feeds four or eight consecutive k (or r) to
-// consecutive instructions, with the same assignment on both operands: the sum
-// over k does not mind the order, and every load is 8 to 32 contiguous bytes
-// per lane, whole 64- or 128-byte pieces per row.
+// The first product runs on the fp32 matrix instruction (v_mfma_f32_16x16x4_f32): x
+// is fp32 and the result is, so x is not rounded to 16 bits, and A in fp16 or bf16
+// converts exactly.  Its rate (256 flop per cycle and CU) is above what the product
+// needs up to ranks of about 64, where x is what has to move.  The second product
+// has few k and many outputs: there a 16-bit B is used as it is, and v in three
+// 16-bit pieces (Operand).  A lane feeds four or eight consecutive k (or r) to
+// consecutive instructions, with the same assignment on both operands: the sum over
+// k does not mind the order, and every load is 8 to 32 contiguous bytes per lane,
+// whole 64- or 128-byte pieces per row.
 #include "qmm_device.h"
 #include "qmm_launch.h"
 
@@ -96,6 +97,13 @@ __device__ __forceinline__ void for_each_adapter(int id, bool valid, int z, int 
 // the second kernel reads again stay few.  Rows that do not match read the first
 // matching row's x (same cache lines), ranks past the pool's read its last one;
 // neither is used.
+//
+// Measured: 2048 rows, K = 8192, rank 16, two requests: 15 to 19 us for the 67 MB of
+// x (3.6 to 4.4 TB/s: bound by reading x, as the second kernel of the call before it
+// leaves the caches); 555 rows of seven requests, K = 4096, rank 64: 13 us, a chain
+// of latencies (ids, ranks, two loads of x and A, the exchange in LDS) that a tile
+// with two adapters goes through twice; 32 rows of 28 adapters, K = 8192, rank 16: 6
+// us; one row: 3.7 us.
 template <typename T, int RT>
 __global__ __launch_bounds__(kShrinkThreads, 4) void k_lora_shrink(const T *__restrict__ A, int64_t E, int R,
                                                                 const int32_t *__restrict__ ranks,
@@ -313,10 +321,12 @@ __host__ __device__ constexpr int v_row(int Rp) {
 // aligned and N is a multiple of 4 (16-byte accesses); BV: R is a multiple of C (B
 // in loads of C elements); H: 64 * H ranks at most.
 //
-// Measured (one box, base and out not in a cache): 2048 rows, N = 28672, K = 8192,
-// rank 16: 82 us of 79 that adding two matrices of this size takes, 6 TB/s; 555
-// rows, K = 4096, rank 64: 37 us (latency: ids, then B, then the products); 32 rows
-// of 28 adapters, N = 8192: 8 us.
+// Measured (base and out not in a cache): 2048 rows, N = 28672, rank 16: 81 us of the
+// 79 that adding two matrices of this size takes, 6 TB/s; 555 rows, rank 64: 37 us
+// where 127 MB of base and out would take 21: each workgroup also reads 32 KB of B and
+// 32 KB of partials out of the L2 caches, as much as base and out together, and its
+// chain of latencies is ids, partials, the products, the exchange of the tile; 32
+// rows of 28 adapters, N = 8192: 8 us; one row, N = 4096: 4.5 us.
 enum class Tiles { Own, Shared, Long };  // Shared: zsplit > 1; Long: base and out go past the caches
 template <typename T, bool VEC, bool BV, int H, Tiles MODE>
 __global__ __launch_bounds__(kThreads, 4) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
