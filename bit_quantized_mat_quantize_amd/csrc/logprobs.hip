@@ -324,9 +324,9 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, const Stats &st
 // not start or end on a boundary) are a batch of their own in split 0.
 //
 // Measured: 1024 rows of 128256 fp32 logits, k = 1: 94 us, 5.6 TB/s, what a copy
-// reaches; 513 rows of 50257 fp16 logits, k = 8: 24 us for 52 MB: about 46 cycles of
+// reaches; 513 rows of 50257 fp16 logits, k = 8: 23 us for 52 MB: about 50 cycles of
 // vector instructions per 64 logits (an exponential is 16 of them), two rows per CU
-// and three on one, and 6 us for the bounds and lists (18 us with k = 0); 32 rows of
+// and three on one, and 6 us for the bounds and lists (17 us with k = 0); 32 rows of
 // 128256 under masks, k = 20: 10.5 us in 16 splits each; one row of 32000, k = 5: 10
 // us, of which the statistics take 6 and the bounds (twice) and the ranking the rest.
 template <typename T, bool MASK>
@@ -389,7 +389,15 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
                 unpack<T>(p[u], y);
 #pragma unroll
                 for (int q = 0; q < VEC; ++q)
-                    v[u * VEC + q] = in && (!MASK || (bits[u] >> q & 1)) ? y[q] : -kInf;
+                    v[u * VEC + q] = !MASK || (in && (bits[u] >> q & 1)) ? y[q] : -kInf;
+            }
+            // behind the split's end, in its last batch (all the others do without: 700
+            // rows of 128256 bf16 logits 51.0 -> 47.2 us)
+            if (!MASK && j1 - (jt - (int)threadIdx.x) < kThreads * U) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) v[u * VEC + q] = jt + u * kThreads < j1 ? v[u * VEC + q] : -kInf;
             }
         } else {
             index0 = (int)threadIdx.x < head ? (int)threadIdx.x : tail + (int)threadIdx.x - head;
@@ -428,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
         if (a.k > 0 && __ballot(top >= l.least) != 0) {
             uint32_t left = 0;  // which of this lane's logits may enter
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) left |= v[i] >= l.least ? 1u << i : 0;
+            for (int i = kBatch - 1; i >= 0; --i) left = left + left + (v[i] >= l.least ? 1u : 0u);
             while (__ballot(left != 0) != 0) {
                 const int i = left != 0 ? __builtin_ctz(left) : 0;
                 float y = v[0];
