@@ -1,4 +1,5 @@
-"""Quantized mul_mat (Q4_0 / Q4_K / Q6_K / Q2_K weights x Q8_0 / Q8_K activations) on MI355X.
+"""Quantized mul_mat (Q4_0 / Q4_K / Q6_K / Q2_K weights x Q8_0 / Q8_K activations) on MI355X,
+and the operators around it: embedding rows, low-rank adapters, log probabilities.
 
 The computation lives in ``libqmm.so`` (hand-written HIP kernels for gfx950
 behind the C ABI of ``include/qmm.h``); this package is its thin binding.

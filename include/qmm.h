@@ -52,6 +52,11 @@
  *   (nb = blocks per row).  The payload stream is 16-byte aligned, which lets a
  *   wavefront read weights with coalesced 16-byte loads.
  *
+ * Around the product: qmm_embed_rows (rows of a packed table by id, decoded),
+ * qmm_lora_add (low-rank adapters by id per row, on top of a product's output),
+ * qmm_logprobs and qmm_mul_mat_logprobs (log probabilities, entropy and the most
+ * likely tokens of rows of logits).
+ *
  * Conventions for every entry point:
  *   - All array pointers are DEVICE pointers (hipMalloc / torch CUDA tensors)
  *     owned by the caller and 16-byte aligned; the library never allocates,
