@@ -753,6 +753,10 @@ const char *weight_name(qmm_weight_type t) {
 
 size_t float_size(qmm_float_type t) { return t == QMM_F32 ? 4 : ((t == QMM_F16 || t == QMM_BF16) ? 2 : 0); }
 
+struct Span {
+    const void *p;
+    size_t bytes;
+};
 bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
     return a_bytes && b_bytes && p < q + b_bytes && q < p + a_bytes;
@@ -826,11 +830,29 @@ qmm_status check_logprobs(const qmm::LogprobArgs &a, size_t mask_bytes) {
     return QMM_OK;
 }
 
-bool outputs_overlap(const qmm::LogprobArgs &a, const void *p, size_t bytes) {
-    const size_t top = (size_t)(a.M * a.k) * sizeof(float);
-    return overlap(a.token_logprobs, (size_t)(a.M * a.G) * sizeof(float), p, bytes) ||
-           overlap(a.entropy, a.entropy != nullptr ? (size_t)a.M * sizeof(float) : 0, p, bytes) ||
-           overlap(a.top_ids, top, p, bytes) || overlap(a.top_logprobs, top, p, bytes);
+// The outputs and the workspace against the mask, the tokens, in0 and in1 (the logits,
+// or what they are computed from) and one another.
+qmm_status check_overlaps(const qmm::LogprobArgs &a, Span workspace, Span in0, Span in1) {
+    const size_t top = (size_t)(a.M * a.k) * sizeof(float), given = (size_t)(a.M * a.G) * sizeof(float);
+    const Span out[] = {{a.token_logprobs, given},
+                        {a.entropy, a.entropy != nullptr ? (size_t)a.M * sizeof(float) : 0},
+                        {a.top_ids, top},
+                        {a.top_logprobs, top},
+                        workspace};
+    const Span in[] = {{a.mask, a.mask != nullptr ? strided_bytes(a.M, a.mask_ld, (a.V + 31) / 32, sizeof(uint32_t)) : 0},
+                       {a.tokens, given},
+                       in0,
+                       in1};
+    constexpr int outs = sizeof(out) / sizeof(out[0]);
+    for (int i = 0; i < outs; ++i) {
+        for (const Span &s : in)
+            if (overlap(out[i].p, out[i].bytes, s.p, s.bytes))
+                return fail(QMM_EINVAL, "an output or the workspace overlaps an input");
+        for (int j = i + 1; j < outs; ++j)
+            if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return fail(QMM_EINVAL, "an output overlaps another one or the workspace");
+    }
+    return QMM_OK;
 }
 
 // A row's part of mul_mat_logprobs' workspace: its logits, and what its statistics
@@ -919,9 +941,14 @@ qmm_status qmm_lora_add(qmm_float_type t, const void *A, size_t a_bytes, const v
     const bool in_place = out == base && ld_out == ld_base;
     if (!in_place && overlap(out, out_need, base, base_need))
         return fail(QMM_EINVAL, "out overlaps base without being base (same pointer and row stride)");
-    if (overlap(out, out_need, x, x_need) || overlap(out, out_need, A, a_need) || overlap(out, out_need, B, b_need) ||
-        overlap(out, out_need, workspace, ws_need))
-        return fail(QMM_EINVAL, "out overlaps x, A, B or the workspace");
+    const Span in[] = {{x, x_need}, {A, a_need}, {B, b_need}, {ids, (size_t)M * sizeof(int32_t)},
+                       {scales, scales != nullptr ? (size_t)E * sizeof(float) : 0},
+                       {ranks, ranks != nullptr ? (size_t)E * sizeof(int32_t) : 0}};
+    for (const Span &i : in)
+        if (overlap(out, out_need, i.p, i.bytes) || overlap(workspace, ws_need, i.p, i.bytes))
+            return fail(QMM_EINVAL, "out or the workspace overlaps x, A, B, ids, scales or ranks");
+    if (overlap(workspace, ws_need, out, out_need) || overlap(workspace, ws_need, base, base_need))
+        return fail(QMM_EINVAL, "the workspace overlaps base or out");
     if (!qmm::lora_grid_ok(M, N, R, K, E))
         return fail(QMM_EUNSUPPORTED, "M = %lld, N = %lld needs more than 2^32 threads", (long long)M, (long long)N);
     const qmm::LoraArgs a{A, B, scales, ranks, x, ids, base, out, static_cast<float *>(workspace),
@@ -960,8 +987,7 @@ qmm_status qmm_logprobs(qmm_float_type t, const void *logits, size_t logits_byte
         QMM_TRY(check_ptr("workspace", workspace));
         QMM_TRY(check_size("workspace", ws_bytes, ws_need));
     }
-    if (outputs_overlap(a, logits, x_need) || overlap(workspace, ws_need, logits, x_need))
-        return fail(QMM_EINVAL, "an output or the workspace overlaps the logits");
+    QMM_TRY(check_overlaps(a, Span{workspace, ws_need}, Span{logits, x_need}, Span{nullptr, 0}));
     if (log_enabled())
         fprintf(stderr, "qmm: logprobs M=%lld V=%lld G=%lld k=%lld -> %d workgroup(s) per row\n", (long long)M,
                 (long long)V, (long long)G, (long long)k, qmm::logprobs_splits(M, V));
@@ -994,8 +1020,8 @@ qmm_status qmm_mul_mat_logprobs(qmm_weight_type t, const void *w, size_t w_bytes
     // the activation rows of a part start on 16 bytes: 8 rows of any format do
     int64_t at_once = ws_bytes / row < (size_t)M ? (int64_t)(ws_bytes / row) / kHeadRows * kHeadRows : M;
     const qmm_act_type at = t == QMM_Q4_0 ? QMM_Q8_0 : QMM_Q8_K;
-    if (outputs_overlap(a, workspace, (size_t)at_once * row))
-        return fail(QMM_EINVAL, "an output overlaps the workspace");
+    QMM_TRY(check_overlaps(a, Span{workspace, (size_t)at_once * row}, Span{w, qmm_weight_bytes(t, l, N, K)},
+                           Span{y, qmm_act_bytes(at, M, K)}));
     if (log_enabled())
         fprintf(stderr, "qmm: mul_mat_logprobs %s M=%lld N=%lld K=%lld -> %lld rows at a time\n", weight_name(t),
                 (long long)M, (long long)N, (long long)K, (long long)at_once);

@@ -394,7 +394,9 @@ size_t qmm_lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E);
  * activations that the projection quantized.  base [M, N] fp32 with row stride
  * ld_base >= N elements (mul_mat's output, or a column range of it); out
  * likewise with ld_out.  out may be base itself (then ld_out = ld_base: the
- * update in place), otherwise out must not overlap any input (QMM_EINVAL).
+ * update in place), otherwise out must not overlap any input (QMM_EINVAL).  An
+ * infinity in the used part of a 16-bit B makes the results it enters NaN (v is
+ * multiplied in parts).
  * Both products are computed in fp32 (x is not rounded); K is split over
  * workgroups and the parts are added in a fixed order: results do not depend
  * on timing.  workspace: device, at least qmm_lora_workspace_bytes(M, R, K, E),
@@ -431,7 +433,7 @@ size_t qmm_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);
  * NaN never enters the top list.
  * Statistics are fp32; x is read once.  scale (one over the temperature): above
  * 0, at most 1e30.  Requires V <= 2^24, k <= 64, M < 2^23, M*G < 2^31.
- * Outputs must not overlap inputs or one another.
+ * Outputs and the workspace must not overlap inputs or one another (QMM_EINVAL).
  * workspace: device, qmm_logprobs_workspace_bytes(M, V, k) bytes (NULL where
  * that is 0), overwritten; calls that may overlap need one each. */
 qmm_status qmm_logprobs(qmm_float_type t, const void *logits, size_t logits_bytes, int64_t ld,
@@ -454,8 +456,9 @@ size_t qmm_mul_mat_logprobs_workspace_bytes(int64_t rows, int64_t N, int64_t k);
  * results are those of the two calls on the rows computed with it; how many these
  * are matters only through AUTO's kernel choice (the last bits of the logits).
  * workspace: device, bytes for at least min(M, 8) rows, overwritten; a number
- * between is rounded down to a multiple of 8 rows.  Calls that may overlap need
- * one each. */
+ * between is rounded down to a multiple of 8 rows.  It and the outputs must not
+ * overlap inputs or one another (QMM_EINVAL).  Calls that may overlap need one
+ * each. */
 qmm_status qmm_mul_mat_logprobs(qmm_weight_type t, const void *w, size_t w_bytes, qmm_layout l,
                                 const void *y, size_t y_bytes, int64_t M, int64_t N, int64_t K,
                                 float scale, const uint32_t *mask, size_t mask_bytes, int64_t mask_ld,

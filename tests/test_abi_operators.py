@@ -69,6 +69,11 @@ def test_lora_add_refusals(lib):  # noqa: F811
     assert call(o=_far(4) + 16) == EINVAL and "overlaps base" in _last(lib)
     assert call(o=_far(4), ldo=100) == EINVAL
     assert call(o=_far(2)) == EINVAL and call(o=_far(0)) == EINVAL and call(o=_far(6)) == EINVAL
+    for p in ("ids", "sc", "rk", "A", "B", "x", "b"):  # the workspace and out against each input
+        other = {"sc": _far(7), "rk": _far(8)}.get(p, base[p])
+        assert call(**{p: other, "ws": other}) == EINVAL and "overlaps" in _last(lib), p
+        if p != "b":
+            assert call(**{p: other, "o": other}) == EINVAL and "overlaps" in _last(lib), p
     assert call(M=0, A=None, x=None, ws=None) == OK and call(N=0, A=None, x=None, ws=None) == OK
     for bad in ((0, 8, 64, 4), (3, 0, 64, 4), (3, 8, 60, 4), (3, 8, 64, 0), (3, 257, 64, 4), (3, 8, 64, 4097)):
         assert lib.qmm_lora_workspace_bytes(*bad) == 0
@@ -102,6 +107,15 @@ def test_logprobs_refusals(lib):  # noqa: F811
     assert call(ent=_far(0) + 3 * 4000 - 16) == EINVAL and "overlaps" in _last(lib)
     need = lib.qmm_logprobs_workspace_bytes(3, 100000, 4)
     big = dict(V=100000, ld=100000)
+    for o in ("lp", "ent", "ti", "tl"):  # against each input and the next output
+        for i in ("x", "tok", "mask"):
+            assert call(**{"mask": _far(7), "mb": BIG, o: _far(7) if i == "mask" else base[i]}) == EINVAL, (o, i)
+            assert "overlaps an input" in _last(lib)
+        nxt = {"lp": "ent", "ent": "ti", "ti": "tl", "tl": "lp"}[o]
+        assert call(**{o: base[nxt]}) == EINVAL and "overlaps another" in _last(lib)
+        assert call(ws=base[o], **big) == EINVAL and "overlaps" in _last(lib)
+    for i in ("x", "tok"):
+        assert call(ws=base[i], **big) == EINVAL and "overlaps an input" in _last(lib)
     assert need > 0 and call(wsb=need - 1, **big) == EINVAL and call(ws=None, **big) == EINVAL
     assert call(M=0, x=None, tok=None, lp=None, ti=None, tl=None, ws=None) == OK
     # many rows or a short vocabulary are not split: no workspace
@@ -132,6 +146,8 @@ def test_mul_mat_logprobs_refusals(lib):  # noqa: F811
     assert call(wsb=bytes_(8, 1001, 4) - 1) == EINVAL and "workspace" in _last(lib)
     assert call(M=3, wsb=bytes_(3, 1001, 4) - 1) == EINVAL
     assert call(lp=_far(7) + bytes_(20, 1001, 4) - 16) == EINVAL and "overlaps" in _last(lib)
+    for p in ("w", "y", "tok"):
+        assert call(ws=base[p]) == EINVAL and call(ent=base[p]) == EINVAL, p
     assert call(M=0, w=None, y=None, ws=None) == OK
     assert bytes_(8, 1001, 4) == 8 * bytes_(1, 1001, 4) >= 8 * 1001 * 4
     assert bytes_(0, 1001, 4) == 0 and bytes_(1, 0, 4) == 0 and bytes_(1, 1001, 65) == 0
