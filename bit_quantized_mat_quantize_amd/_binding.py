@@ -8,7 +8,6 @@ raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -325,11 +324,9 @@ def debug_block_sums(wfmt: str, w, y, M: int, N: int, K: int, layout: str = "can
 # ---- the operators beside the projections.  They run on the device of their
 # tensors (whichever is current) and on `stream`, by default that device's
 # current one; what they allocate belongs to that stream.  A small call costs
-# the host more than the GPU (one launch 3 us, one tensor 1.7 us), so the checks
-# are cheap where nothing is wrong.
-
-_HERE = contextlib.nullcontext()
-
+# the host more than the GPU (one launch 3.3 us, one tensor 1.3 us by
+# empty_strided, 1.7 by empty), so the checks are one expression where nothing is
+# wrong, and say what is wrong one by one where something is.
 
 def _gpu(**tensors) -> int:
     """The index of the one GPU that every tensor is on (None: not given)."""
@@ -347,11 +344,11 @@ def _gpu(**tensors) -> int:
     return index
 
 
-def _on(index: int, stream):
-    """The context to allocate and launch in."""
+def _elsewhere(index: int, stream):
+    """The context to allocate and launch in, None where that is the present one."""
     import torch
     if stream is None:
-        return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+        return None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
     if stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     return torch.cuda.stream(stream)
@@ -363,12 +360,17 @@ def _current(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+_FLOAT_TYPES = {}
+
+
 def _float_type(t, name: str) -> int:
-    import torch
-    types = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-    if t.dtype not in types:
+    if not _FLOAT_TYPES:
+        import torch
+        _FLOAT_TYPES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    i = _FLOAT_TYPES.get(t.dtype)
+    if i is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16 (got {t.dtype})")
-    return types[t.dtype]
+    return i
 
 
 def _is(t, name: str, dtype, *shape) -> None:
@@ -393,6 +395,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _new(torch, M: int, N: int, dtype, device):
+    return torch.empty_strided((M, N), (N, 1), dtype=dtype, device=device)
+
+
 def embed_rows(wfmt: str, w, ids, N: int, K: int, layout: str = "canonical", scale: float = 1.0,
                out=None, stream=None):
     """out [T, K] fp32 = scale * the rows ids (int32 [T]) of the packed table w [N, K], decoded.
@@ -404,13 +410,16 @@ def embed_rows(wfmt: str, w, ids, N: int, K: int, layout: str = "canonical", sca
     if not w.is_contiguous():
         raise ValueError("w must be contiguous")
     index = _gpu(ids=ids, w=w, out=out)
-    with _on(index, stream):
-        if out is None:
-            out = torch.empty((T, K), dtype=torch.float32, device=ids.device)
-        else:
-            _is(out, "out", torch.float32, T, K)
-        _check(load().qmm_embed_rows(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], ids.data_ptr(), T, scale,
-                                     out.data_ptr(), T * K * 4, N, K, _current(index)), "qmm_embed_rows")
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return embed_rows(wfmt, w, ids, N, K, layout, scale, out)
+    if out is None:
+        out = _new(torch, T, K, torch.float32, ids.device)
+    else:
+        _is(out, "out", torch.float32, T, K)
+    _check(load().qmm_embed_rows(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], ids.data_ptr(), T, scale,
+                                 out.data_ptr(), T * K * 4, N, K, _current(index)), "qmm_embed_rows")
     return out
 
 
@@ -426,28 +435,34 @@ def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=No
     wider matrices; out=base adds in place.  Without `out` a new tensor is returned.  An id outside
     [-1, E) gives a row of NaN."""
     import torch
-    (M, N), (E, R, K) = base.shape, A.shape
+    (M, N), (E, R, K), t = base.shape, A.shape, A.dtype
     f32, i32 = torch.float32, torch.int32
-    _is(x, "x", f32, M, K)
-    _is(A, "A", A.dtype, E, R, K)
-    _is(B, "B", A.dtype, E, N, R)
-    _is(ids, "ids", i32, M)
+    if not (x.dtype is f32 and B.dtype is t and ids.dtype is i32 and x.shape == (M, K) and B.shape == (E, N, R) and
+            ids.shape == (M,) and x.is_contiguous() and A.is_contiguous() and B.is_contiguous() and
+            ids.is_contiguous()):
+        _is(x, "x", f32, M, K)
+        _is(A, "A", t, E, R, K)
+        _is(B, "B", t, E, N, R)
+        _is(ids, "ids", i32, M)
     if scales is not None:
         _is(scales, "scales", f32, E)
     if ranks is not None:
         _is(ranks, "ranks", i32, E)
     pb, nb, ldb = _rows(base, "base", f32, M, N)
     index = _gpu(base=base, x=x, A=A, B=B, ids=ids, scales=scales, ranks=ranks, out=out, workspace=workspace)
-    with _on(index, stream):
-        if out is None:
-            out = torch.empty((M, N), dtype=f32, device=base.device)
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return lora_add(base, x, A, B, ids, scales, ranks, out, workspace)
+    if out is None:
+        out = _new(torch, M, N, f32, base.device)
+        po, no, ldo = out.data_ptr(), M * N * 4, N
+    else:
         po, no, ldo = _rows(out, "out", f32, M, N)
-        workspace = _workspace(workspace, lora_workspace_bytes(M, R, K, E), base.device)
-        _check(load().qmm_lora_add(_float_type(A, "A"), A.data_ptr(), A.nbytes, B.data_ptr(), B.nbytes, E, R,
-                                   _ptr(scales), _ptr(ranks), x.data_ptr(), x.nbytes, ids.data_ptr(), pb, nb, ldb,
-                                   po, no, ldo, M, N, K, _ptr(workspace),
-                                   0 if workspace is None else workspace.nbytes, _current(index)),
-               "qmm_lora_add")
+    workspace, nw = _workspace(torch, workspace, load().qmm_lora_workspace_bytes(M, R, K, E), base.device)
+    _check(load().qmm_lora_add(_float_type(A, "A"), A.data_ptr(), A.nbytes, B.data_ptr(), B.nbytes, E, R,
+                               _ptr(scales), _ptr(ranks), x.data_ptr(), x.nbytes, ids.data_ptr(), pb, nb, ldb,
+                               po, no, ldo, M, N, K, _ptr(workspace), nw, _current(index)), "qmm_lora_add")
     return out
 
 
@@ -474,25 +489,26 @@ def _logprob_inputs(M: int, V: int, tokens, mask):
     return G, mask_ld, mask_bytes
 
 
-def _logprob_outputs(M: int, k: int, tokens, entropy: bool, device):
-    import torch
-    f32 = torch.float32
-    lp = None if tokens is None else torch.empty(tokens.shape, dtype=f32, device=device)
-    ent = torch.empty((M,), dtype=f32, device=device) if entropy else None
-    if k <= 0:
-        return lp, ent, None, None
-    return (lp, ent, torch.empty((M, k), dtype=torch.int32, device=device),
-            torch.empty((M, k), dtype=f32, device=device))
+def _logprob_outputs(torch, M: int, k: int, tokens, entropy: bool, device):
+    f32, new = torch.float32, torch.empty_strided
+    lp = ent = top_ids = top_lp = None
+    if tokens is not None:
+        shape = tokens.shape
+        lp = new(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype=f32, device=device)
+    if entropy:
+        ent = new((M,), (1,), dtype=f32, device=device)
+    if k > 0:
+        top_ids, top_lp = _new(torch, M, k, torch.int32, device), _new(torch, M, k, f32, device)
+    return lp, ent, top_ids, top_lp
 
 
-def _workspace(given, need: int, device):
-    """The caller's workspace, or a new one (None where nothing is needed)."""
-    import torch
+def _workspace(torch, given, need: int, device):
+    """The caller's workspace, or a new one (None where nothing is needed), and its bytes."""
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        return (torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device) if need else None), need
     if not given.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return given
+    return given, given.nbytes
 
 
 def logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, mask=None, entropy: bool = True,
@@ -503,17 +519,21 @@ def logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, mask=None, ent
     same shape); entropy: fp32 [M]; k: that many most likely tokens (int32 and fp32 [M, k], -1 and -inf where
     there are fewer).  mask: int32 words [W], [1, W] or [M, W], W >= ceil(V / 32); bit i % 32 of word i // 32
     allows token i.  scale multiplies the logits (one over the temperature).  What is not asked for is None."""
+    import torch
     M, V = logits.shape
     G, mask_ld, mask_bytes = _logprob_inputs(M, V, tokens, mask)
     px, nx, ld = _rows(logits, "logits", logits.dtype, M, V)
     index = _gpu(logits=logits, tokens=tokens, mask=mask, workspace=workspace)
-    with _on(index, stream):
-        lp, ent, top_ids, top_lp = out = _logprob_outputs(M, k, tokens, entropy, logits.device)
-        workspace = _workspace(workspace, logprobs_workspace_bytes(M, V, k), logits.device)
-        _check(load().qmm_logprobs(_float_type(logits, "logits"), px, nx, ld, M, V, scale, _ptr(mask), mask_bytes,
-                                   mask_ld, _ptr(tokens), G, _ptr(lp), _ptr(ent), k, _ptr(top_ids), _ptr(top_lp),
-                                   _ptr(workspace), 0 if workspace is None else workspace.nbytes, _current(index)),
-               "qmm_logprobs")
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return logprobs(logits, tokens, k, scale, mask, entropy, workspace)
+    device = logits.device
+    lp, ent, top_ids, top_lp = out = _logprob_outputs(torch, M, k, tokens, entropy, device)
+    workspace, nw = _workspace(torch, workspace, load().qmm_logprobs_workspace_bytes(M, V, k), device)
+    _check(load().qmm_logprobs(_float_type(logits, "logits"), px, nx, ld, M, V, scale, _ptr(mask), mask_bytes,
+                               mask_ld, _ptr(tokens), G, _ptr(lp), _ptr(ent), k, _ptr(top_ids), _ptr(top_lp),
+                               _ptr(workspace), nw, _current(index)), "qmm_logprobs")
     return out
 
 
@@ -527,21 +547,24 @@ def mul_mat_logprobs(wfmt: str, w, y, M: int, N: int, K: int, tokens=None, k: in
     """logprobs of mul_mat(w, y) [M, N], `rows` rows at a time (or as many as a given workspace holds): the
     logits of all M rows need not exist at once.  w, y, M, N, K, layout as in mul_mat, the rest and the
     results as in logprobs."""
+    import torch
     G, mask_ld, mask_bytes = _logprob_inputs(M, N, tokens, mask)
     if not (w.is_contiguous() and y.is_contiguous()):
         raise ValueError("w and y must be contiguous")
     if rows < 1:
         raise ValueError(f"rows = {rows}: at least one at a time")
     index = _gpu(w=w, y=y, tokens=tokens, mask=mask, workspace=workspace)
-    with _on(index, stream):
-        lp, ent, top_ids, top_lp = out = _logprob_outputs(M, k, tokens, entropy, w.device)
-        at_once = min(M, max(rows, 8))
-        workspace = _workspace(workspace, mul_mat_logprobs_workspace_bytes(at_once, N, k), w.device)
-        _check(load().qmm_mul_mat_logprobs(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], y.data_ptr(), y.nbytes,
-                                           M, N, K, scale, _ptr(mask), mask_bytes, mask_ld, _ptr(tokens), G, _ptr(lp),
-                                           _ptr(ent), k, _ptr(top_ids), _ptr(top_lp), _ptr(workspace),
-                                           0 if workspace is None else workspace.nbytes, _current(index)),
-               "qmm_mul_mat_logprobs")
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return mul_mat_logprobs(wfmt, w, y, M, N, K, tokens, k, scale, mask, entropy, layout, rows, workspace)
+    lp, ent, top_ids, top_lp = out = _logprob_outputs(torch, M, k, tokens, entropy, w.device)
+    at_once = min(M, max(rows, 8))
+    workspace, nw = _workspace(torch, workspace, mul_mat_logprobs_workspace_bytes(at_once, N, k), w.device)
+    _check(load().qmm_mul_mat_logprobs(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], y.data_ptr(), y.nbytes,
+                                       M, N, K, scale, _ptr(mask), mask_bytes, mask_ld, _ptr(tokens), G, _ptr(lp),
+                                       _ptr(ent), k, _ptr(top_ids), _ptr(top_lp), _ptr(workspace), nw,
+                                       _current(index)), "qmm_mul_mat_logprobs")
     return out
 
 
