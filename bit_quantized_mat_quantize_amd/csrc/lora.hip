@@ -310,6 +310,9 @@ __host__ __device__ constexpr int v_row(int Rp) {
            16 / (int)sizeof(typename Operand<T>::Stored);
 }
 
+// Groups of lanes that the sixteen of a row form to add up its Rp ranks' partials.
+__host__ __device__ constexpr int part_groups(int Rp) { return Rp <= 16 ? 4 : (Rp <= 32 ? 2 : 1); }
+
 // ---- out = base + v B^T.  Workgroup = (tile, z, strip of columns).  The tile's v
 // (partials added in order, scaled, each row with its own adapter's rank) goes to
 // LDS once.  Per group of 256 columns each wavefront multiplies four times 16
@@ -318,8 +321,8 @@ __host__ __device__ constexpr int v_row(int Rp) {
 // match go to a tile in LDS.  From there base and out are read and written by
 // whole rows, 1 KiB per wavefront and instruction.  The first group's base and B
 // are on their way while v is added up.  VEC: rows of base and out are 16-byte
-// aligned and N is a multiple of 4 (16-byte accesses); BV: R is a multiple of C (B
-// in loads of C elements); H: 64 * H ranks at most.
+// aligned and N is a multiple of 4 (16-byte accesses); GR: R is a multiple of it (B
+// in loads of GR elements: C, C / 2, C / 4 or 1); H: 64 * H ranks at most.
 //
 // Measured (base and out not in a cache): 2048 rows, N = 28672, rank 16: 81 us of the
 // 79 that adding two matrices of this size takes, 6 TB/s; 555 rows, rank 64: 37 us
@@ -327,9 +330,12 @@ __host__ __device__ constexpr int v_row(int Rp) {
 // 32 KB of partials out of the L2 caches, as much as base and out together, and its
 // chain of latencies is ids, partials, the products, the exchange of the tile; 32
 // rows of 28 adapters, N = 8192: 8 us; one row, N = 4096: 4.5 us.
+// Shared (zsplit > 1) has the registers of three workgroups per CU, not four: fp16 B
+// and ranks that are no multiple of C spill otherwise (64 rows of 16 adapters, rank
+// 64, N = 28672, fp16: 35.0 -> 31.8 us; 100 rows at rank 12: 36.8 -> 32.2 us).
 enum class Tiles { Own, Shared, Long };  // Shared: zsplit > 1; Long: base and out go past the caches
-template <typename T, bool VEC, bool BV, int H, Tiles MODE>
-__global__ __launch_bounds__(kThreads, 4) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
+template <typename T, bool VEC, int GR, int H, Tiles MODE>
+__global__ __launch_bounds__(kThreads, MODE == Tiles::Shared ? 3 : 4) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
                                                           const float *__restrict__ scales,
                                                           const int32_t *__restrict__ ranks,
                                                           const int32_t *__restrict__ ids, int64_t M,
@@ -414,8 +420,20 @@ __global__ __launch_bounds__(kThreads, 4) void k_lora_expand(const T *__restrict
         for (int t = 0; t < kNT; ++t) {
             const int nb = (wave * kNT + t) * 16 + row;
             const T *p = Be + (uint32_t)((nb < cols ? nb : cols - 1) * R);
-            if (BV) {
+            if constexpr (GR == C) {
                 w[t] = ld16(p + (r < R ? r : 0));
+            } else if constexpr (GR == C / 2) {
+                const uint2 a = *reinterpret_cast<const uint2 *>(p + (r < R ? r : 0));
+                const uint2 b = *reinterpret_cast<const uint2 *>(p + (r + GR < R ? r + GR : 0));
+                w[t] = make_uint4(a.x, a.y, b.x, b.y);
+            } else if constexpr (GR == C / 4) {
+                uint32_t q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = r + i * GR < R ? r + i * GR : 0;
+                    q[i] = *reinterpret_cast<const uint32_t *>(p + at);
+                }
+                w[t] = make_uint4(q[0], q[1], q[2], q[3]);
             } else {
                 Pack<T, C> q;
 #pragma unroll
@@ -426,22 +444,30 @@ __global__ __launch_bounds__(kThreads, 4) void k_lora_expand(const T *__restrict
     };
 
     // v's partials: sixteen lanes per row, four consecutive ranks each and 64 at a
-    // time; a row without an adapter has none, what is read there is not used
+    // time; with 16 or 32 ranks in all, four or two groups of lanes take every fourth
+    // or second part (the workspace has room for whole groups of them).  A row without
+    // an adapter has none, what is read there and past the last part is not used
     const int vrow = wave * kRows + g;  // kRows is 4: the wavefront's rows by 16 lanes each
     v4f v[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-        const int r = 64 * h + 4 * row;
-        const float *p = P + (m0 + (vrow < tile_rows ? vrow : tile_rows - 1)) * Rp + (r < Rp ? r : 0);
+        const int step = h > 0 ? 1 : part_groups(Rp), lanes = 16 / step;
+        const int r = 64 * h + 4 * (row & (lanes - 1)), mine = row / lanes;
+        const float *p = P + (mine * M + m0 + (vrow < tile_rows ? vrow : tile_rows - 1)) * Rp + (r < Rp ? r : 0);
         v[h] = v4f{0.f, 0.f, 0.f, 0.f};
         if (64 * h >= Rp) break;
-        for (int s = 0; s < splits; s += 8) {
+        for (int s = 0; s < splits; s += 8 * step) {
             v4f part[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                part[i] = *reinterpret_cast<const v4f *>(p + (int64_t)(s + i < splits ? s + i : s) * M * Rp);
+                part[i] = *reinterpret_cast<const v4f *>(p + (int64_t)(s + i * step < splits ? s + i * step : s) * M * Rp);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[h] += s + i < splits ? part[i] : v4f{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 8; ++i) v[h] += s + i * step + mine < splits ? part[i] : v4f{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // groups 8 lanes apart, then 4: every lane adds the same pairs
+            if (step > 1) v[h][q] += dpp_f32<0x128>(v[h][q]);
+            if (step > 2) v[h][q] += dpp_f32<0x124>(v[h][q]);
         }
     }
     // the first group's B and base are on their way while v is made up
@@ -613,20 +639,31 @@ hipError_t shrink(const LoraArgs &a, const Shape &h, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <typename T, bool VEC, bool BV, int H>
+template <typename T, bool VEC, int GR, int H>
 hipError_t expand(const LoraArgs &a, const Shape &h, hipStream_t s) {
     const Strips st = strips_of(a.N, h);
     const size_t lds = sizeof(typename Operand<T>::Stored) * Operand<T>::pieces * kTileRows * v_row<T>(h.Rp);
     // no cache holds 32 MiB of out: it goes past them, and base with it (2048 rows of
     // 28672: 105 -> 101 us for both kernels, 555 rows at rank 64: 55 -> 50 us)
-    const auto kernel = h.zsplit > 1 ? k_lora_expand<T, VEC, BV, H, Tiles::Shared>
+    const auto kernel = h.zsplit > 1 ? k_lora_expand<T, VEC, GR, H, Tiles::Shared>
                         : VEC && a.M * a.N >= (int64_t(32) << 20) / 4
-                            ? k_lora_expand<T, VEC, BV, H, VEC ? Tiles::Long : Tiles::Own>
-                            : k_lora_expand<T, VEC, BV, H, Tiles::Own>;
+                            ? k_lora_expand<T, VEC, GR, H, VEC ? Tiles::Long : Tiles::Own>
+                            : k_lora_expand<T, VEC, GR, H, Tiles::Own>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(st.strips * h.zsplit * h.tiles)), dim3(kThreads), lds, s,
                        static_cast<const T *>(a.B), a.E, (int)a.R, a.scales, a.ranks, a.ids, a.M, a.ws, h.splits, h.Rp,
                        a.base, a.ld_base, a.out, a.ld_out, a.N, (int)st.strips, st.groups, h.zsplit);
     return hipGetLastError();
+}
+
+template <typename T, bool VEC>
+hipError_t expand_for(const LoraArgs &a, const Shape &h, hipStream_t s) {
+    constexpr int H = kMaxRank / 64, C = Operand<T>::C;
+    if (a.R % C == 0) return h.Rp <= 64 ? expand<T, VEC, C, 1>(a, h, s) : expand<T, VEC, C, H>(a, h, s);
+    // wider pieces of a lane's 16 bytes of B than single elements (2048 rows, N = 28672:
+    // rank 60 in fp16 277 us by elements, 143 us by 8 bytes)
+    if (a.R % (C / 2) == 0) return expand<T, VEC, C / 2, H>(a, h, s);
+    if (a.R % (C / 4) == 0) return expand<T, VEC, C / 4, H>(a, h, s);
+    return expand<T, VEC, 1, H>(a, h, s);
 }
 
 template <typename T>
@@ -634,18 +671,16 @@ hipError_t both(const LoraArgs &a, hipStream_t s) {
     const Shape h = shape(a.M, a.R, a.K, a.E);
     const hipError_t e = h.rt == 1 ? shrink<T, 1>(a, h, s) : shrink<T, 2>(a, h, s);
     if (e != hipSuccess) return e;
-    constexpr int H = kMaxRank / 64;
-    const bool vec = a.ld_base % 4 == 0 && a.ld_out % 4 == 0 && a.N % 4 == 0, bv = a.R % Operand<T>::C == 0;
-    if (vec && bv) return h.Rp <= 64 ? expand<T, true, true, 1>(a, h, s) : expand<T, true, true, H>(a, h, s);
-    if (vec) return expand<T, true, false, H>(a, h, s);
-    return bv ? expand<T, false, true, H>(a, h, s) : expand<T, false, false, H>(a, h, s);
+    const bool vec = a.ld_base % 4 == 0 && a.ld_out % 4 == 0 && a.N % 4 == 0;
+    return vec ? expand_for<T, true>(a, h, s) : expand_for<T, false>(a, h, s);
 }
 
 }  // namespace
 
 int64_t lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E) {
     const Shape h = shape(M, R, K, E);
-    return (int64_t)sizeof(float) * h.splits * M * h.Rp;
+    const int g = part_groups(h.Rp);
+    return (int64_t)sizeof(float) * ((h.splits + g - 1) / g * g) * M * h.Rp;
 }
 
 int64_t lora_max_rank() { return kMaxRank; }

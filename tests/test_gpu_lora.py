@@ -70,7 +70,9 @@ def _inputs(rng, M, N, K, ids=None, E=1):
 @pytest.mark.parametrize("M,N,K,R,E", [(1, 1, 32, 1, 1), (1, 4096, 1024, 16, 3), (2, 70, 64, 3, 2), (5, 257, 96, 7, 8),
                                        (16, 512, 256, 8, 16), (17, 300, 2080, 24, 4), (33, 129, 320, 64, 64),
                                        (65, 1030, 512, 33, 5), (130, 260, 128, 100, 3), (530, 36, 4096, 12, 9),
-                                       (40, 64, 32, 256, 2)])
+                                       (40, 64, 32, 256, 2), (70, 260, 96, 4, 5), (200, 131, 64, 6, 4),
+                                       (33, 516, 160, 10, 7), (12, 300, 2048, 20, 3), (140, 68, 4096, 34, 6),
+                                       (9, 5, 64, 60, 2), (300, 1028, 64, 130, 2)])
 def test_formula(M, N, K, R, E, type):
     print(M, N, K, R, E, type, flush=True)
     rng = np.random.default_rng(M * 1000 + N + K + R)
