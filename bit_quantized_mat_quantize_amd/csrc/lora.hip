@@ -617,16 +617,18 @@ Shape shape(int64_t M, int64_t R, int64_t K, int64_t E) {
     h.splits = (int)(s > most ? most : s);
     return h;
 }
-// column groups per workgroup of the second kernel: two where there are plenty of
-// them (2048 rows of 28672 columns: 105 us for both kernels, against 112 with one
-// and 120 with four)
+// Column groups per workgroup of the second kernel: two where workgroups are plenty
+// all the same, so that each adds up the partials once for both (both kernels, K =
+// 4096, rank 16: 1024 rows of 28672 columns 53.9 -> 49.3 us, 800 rows 43.5 -> 41.5 us;
+// three: 45.5 us; from 1024 groups on 40 rows of 28672 would take 14.2 instead of 12.3
+// us)
 struct Strips {
     int64_t strips;
     int groups;
 };
 Strips strips_of(int64_t N, const Shape &h) {
     const int64_t all = (N + kGroupCols - 1) / kGroupCols;
-    const int groups = all * h.tiles * h.zsplit >= 8192 ? 2 : 1;
+    const int groups = all * h.tiles * h.zsplit >= 2048 ? 2 : 1;
     return Strips{(all + groups - 1) / groups, groups};
 }
 
