@@ -310,8 +310,9 @@ __host__ __device__ constexpr int v_row(int Rp) {
            16 / (int)sizeof(typename Operand<T>::Stored);
 }
 
-// Groups of lanes that the sixteen of a row form to add up its Rp ranks' partials.
-__host__ __device__ constexpr int part_groups(int Rp) { return Rp <= 16 ? 4 : (Rp <= 32 ? 2 : 1); }
+// The sixteen lanes of a row add up its Rp ranks' partials in groups of 4, 8 or 16: log2
+// of a group's lanes.
+__host__ __device__ constexpr int part_lanes(int Rp) { return Rp <= 16 ? 2 : (Rp <= 32 ? 3 : 4); }
 
 // ---- out = base + v B^T.  Workgroup = (tile, z, strip of columns).  The tile's v
 // (partials added in order, scaled, each row with its own adapter's rank) goes to
@@ -451,8 +452,8 @@ __global__ __launch_bounds__(kThreads, MODE == Tiles::Shared ? 3 : 4) void k_lor
     v4f v[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-        const int step = h > 0 ? 1 : part_groups(Rp), lanes = 16 / step;
-        const int r = 64 * h + 4 * (row & (lanes - 1)), mine = row / lanes;
+        const int shift = h > 0 ? 4 : part_lanes(Rp), step = 16 >> shift;
+        const int r = 64 * h + 4 * (row & ((1 << shift) - 1)), mine = row >> shift;
         const float *p = P + (mine * M + m0 + (vrow < tile_rows ? vrow : tile_rows - 1)) * Rp + (r < Rp ? r : 0);
         v[h] = v4f{0.f, 0.f, 0.f, 0.f};
         if (64 * h >= Rp) break;
@@ -681,7 +682,7 @@ hipError_t both(const LoraArgs &a, hipStream_t s) {
 
 int64_t lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E) {
     const Shape h = shape(M, R, K, E);
-    const int g = part_groups(h.Rp);
+    const int g = 16 >> part_lanes(h.Rp);
     return (int64_t)sizeof(float) * ((h.splits + g - 1) / g * g) * M * h.Rp;
 }
 
