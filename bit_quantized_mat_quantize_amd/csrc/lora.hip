@@ -326,11 +326,11 @@ __host__ __device__ constexpr int part_lanes(int Rp) { return Rp <= 16 ? 2 : (Rp
 // in loads of GR elements: C, C / 2, C / 4 or 1); H: 64 * H ranks at most.
 //
 // Measured (base and out not in a cache): 2048 rows, N = 28672, rank 16: 81 us of the
-// 79 that adding two matrices of this size takes, 6 TB/s; 555 rows, rank 64: 37 us
-// where 127 MB of base and out would take 21: each workgroup also reads 32 KB of B and
-// 32 KB of partials out of the L2 caches, as much as base and out together, and its
-// chain of latencies is ids, partials, the products, the exchange of the tile; 32
-// rows of 28 adapters, N = 8192: 8 us; one row, N = 4096: 4.5 us.
+// 79 that adding two matrices of this size takes, 6 TB/s; 555 rows, rank 64: 37 us,
+// of which the partials take 5 (32 KB of them per workgroup, out of the L2) and B 4; 127 MB of base and out alone would take 21; 32 rows of 28
+// adapters, N = 8192: 7.9 us; one row, N = 4096: 4.8 us, a chain of ids, partials, B
+// and the exchange of the tile.
+//
 // Shared (zsplit > 1) has the registers of three workgroups per CU, not four: fp16 B
 // and ranks that are no multiple of C spill otherwise (64 rows of 16 adapters, rank
 // 64, N = 28672, fp16: 35.0 -> 31.8 us; 100 rows at rank 12: 36.8 -> 32.2 us).
