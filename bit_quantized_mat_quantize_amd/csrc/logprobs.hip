@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kBatch = 16;     // logits per thread and batch
+constexpr int kBatch = 16;     // logits per thread and batch; twice as many where rows are few and whole
 constexpr int kList = 256;     // keys a wavefront's list holds
 constexpr int kMaxK = 64;      // a cut leaves at most kMaxK, and 64 may be appended at once
 constexpr int kMaxSplits = 64;
@@ -327,12 +327,12 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, const Stats &st
 // reaches; 513 rows of 50257 fp16 logits, k = 8: 23 us for 52 MB: about 50 cycles of
 // vector instructions per 64 logits (an exponential is 16 of them), two rows per CU
 // and three on one, and 6 us for the bounds and lists (17 us with k = 0); 32 rows of
-// 128256 under masks, k = 20: 10.5 us in 16 splits each; one row of 32000, k = 5: 10
-// us, of which the statistics take 6 and the bounds (twice) and the ranking the rest.
-template <typename T, bool MASK>
+// 128256 under masks, k = 20: 10.5 us in 16 splits each; one row of 32000, k = 5: 9
+// us, of which the statistics take 5.5 and the bound and the ranking the rest.
+template <typename T, bool MASK, int BATCH>
 __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int splits) {
     constexpr int VEC = 16 / sizeof(T);
-    constexpr int U = kBatch / VEC;  // pieces per thread and batch
+    constexpr int U = BATCH / VEC;  // pieces per thread and batch
     __shared__ uint64_t lists[kWaves][kList];
     __shared__ uint64_t all[kThreads];
     __shared__ int counts[kWaves];
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
     List l{lists[wave], 0, (int)a.k, 0, -__FLT_MAX__};
     const int batches = (j1 - j0 + kThreads * U - 1) / (kThreads * U);
     for (int it = 0; it < batches + (edges ? 1 : 0); ++it) {
-        float v[kBatch];
+        float v[BATCH];
         int index0;      // of v[0]; v[u * VEC + q] follows at u * kThreads * VEC + q
         int filled = 1;  // pieces per thread with anything in them: a split's last batch is seldom full
         if (it < batches) {
@@ -402,13 +402,13 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
         } else {
             index0 = (int)threadIdx.x < head ? (int)threadIdx.x : tail + (int)threadIdx.x - head;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) v[i] = -kInf;
+            for (int i = 0; i < BATCH; ++i) v[i] = -kInf;
             if (index0 < V && (!MASK || allowed(mask, index0))) v[0] = to_f32(x[lead + index0]);
         }
 
         float top = -kInf;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, v[i]);
+        for (int i = 0; i < BATCH; ++i) top = fmaxf(top, v[i]);
         if (top > mine.m) mine.rescale(top, c);
         // all of them -inf so far: any finite number in the maximum's place gives e = 0
         const float m = mine.m == -kInf ? 0.f : mine.m;
@@ -436,12 +436,12 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int 
         if (a.k > 0 && __ballot(top >= l.least) != 0) {
             uint32_t left = 0;  // which of this lane's logits may enter
 #pragma unroll
-            for (int i = kBatch - 1; i >= 0; --i) left = left + left + (v[i] >= l.least ? 1u : 0u);
+            for (int i = BATCH - 1; i >= 0; --i) left = left + left + (v[i] >= l.least ? 1u : 0u);
             while (__ballot(left != 0) != 0) {
                 const int i = left != 0 ? __builtin_ctz(left) : 0;
                 float y = v[0];
 #pragma unroll
-                for (int q = 1; q < kBatch; ++q) y = i == q ? v[q] : y;
+                for (int q = 1; q < BATCH; ++q) y = i == q ? v[q] : y;
                 l.add(key_of(y, (uint32_t)(index0 + i / VEC * (kThreads * VEC) + i % VEC)), left != 0);
                 left &= left - 1;
             }
@@ -517,12 +517,12 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_merge(const LogprobArgs a
 }
 
 // A row of up to four batches (eight where 128 rows or more keep the CUs busy) is
-// not split: 32000 logits, k = 5, take one workgroup 9.9 us and its call 14.9 us,
-// four of them 9.4 us with the second launch and the call 18.7 us; 128 rows of
-// 50257, k = 8: 16 us in one launch, 18 us in two.  Longer rows make two workgroups
-// per CU (64 rows of 128256, k = 20, masked: 19.9 us with eight splits, 22.5 us with
-// sixteen), and from 256 rows on one workgroup each (256 rows of 50257, k = 8: 16.3
-// us, 24.2 us in four; 400 of 128256: 44.9 us, 53.5 us in two).
+// not split: 32000 logits, k = 5, take one workgroup 8.9 us, four of them 9.4 us with
+// the second launch, which costs the caller another 4 us; 128 rows of 50257, k = 8:
+// 16 us in one launch, 18 us in two.  Longer rows make two workgroups per CU (64 rows
+// of 128256, k = 20, masked: 19.9 us with eight splits, 22.5 us with sixteen), and
+// from 256 rows on one workgroup each (256 rows of 50257, k = 8: 16.3 us, 24.2 us in
+// four; 400 of 128256: 44.9 us, 53.5 us in two).
 int splits_of(int64_t M, int64_t V) {
     constexpr int64_t batch = kThreads * kBatch;
     if (M >= 256 || V <= (M < 128 ? 4 : 8) * batch) return 1;
@@ -530,12 +530,26 @@ int splits_of(int64_t M, int64_t V) {
     return (int)(s > most ? (most > kMaxSplits ? kMaxSplits : most) : (s > kMaxSplits ? kMaxSplits : s));
 }
 
+// A workgroup that has a row and a CU to itself waits for its loads more than it
+// computes: it takes 32 logits per thread and batch (one row of 32000, k = 5: 10.7 ->
+// 9.4 us, 256 masked rows of 128256, k = 20: 46.0 -> 39.0 us).  Where others run
+// beside it or its part is short, 16 are faster (513 rows of 50257: 23.8 us, 25.8 us
+// with 32; 32 rows of 128256 in 16 parts: 14.6 us, 15.3 us; 32 rows of 5000, less than
+// one batch: 6.8 us, 7.3 us).
+template <typename T, bool MASK>
+void pass(const LogprobArgs &a, int splits, hipStream_t s) {
+    const dim3 grid((unsigned)(a.M * splits));
+    if (splits == 1 && a.M <= 256 && a.V > kThreads * kBatch)
+        hipLaunchKernelGGL((k_logprobs<T, MASK, 2 * kBatch>), grid, dim3(kThreads), 0, s, a, splits);
+    else
+        hipLaunchKernelGGL((k_logprobs<T, MASK, kBatch>), grid, dim3(kThreads), 0, s, a, splits);
+}
+
 template <typename T>
 hipError_t both(const LogprobArgs &a, hipStream_t s) {
     const int splits = splits_of(a.M, a.V);
-    const dim3 grid((unsigned)(a.M * splits));
-    if (a.mask != nullptr) hipLaunchKernelGGL((k_logprobs<T, true>), grid, dim3(kThreads), 0, s, a, splits);
-    else hipLaunchKernelGGL((k_logprobs<T, false>), grid, dim3(kThreads), 0, s, a, splits);
+    if (a.mask != nullptr) pass<T, true>(a, splits, s);
+    else pass<T, false>(a, splits, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || splits == 1) return e;
     hipLaunchKernelGGL(k_logprobs_merge<T>, dim3((unsigned)a.M), dim3(kThreads), 0, s, a, splits);
