@@ -326,7 +326,9 @@ def debug_block_sums(wfmt: str, w, y, M: int, N: int, K: int, layout: str = "can
 # current one; what they allocate belongs to that stream.  A small call costs
 # the host more than the GPU (one launch 3.3 us, one tensor 1.3 us by
 # empty_strided, 1.7 by empty), so the checks are one expression where nothing is
-# wrong, and say what is wrong one by one where something is.
+# wrong, and say what is wrong one by one where something is.  The current stream is
+# asked for as the hipStream_t it is (torch.cuda.current_stream builds an object
+# first: 2 us).
 
 def _gpu(**tensors) -> int:
     """The index of the one GPU that every tensor is on (None: not given)."""
@@ -344,20 +346,14 @@ def _gpu(**tensors) -> int:
     return index
 
 
-def _elsewhere(index: int, stream):
-    """The context to allocate and launch in, None where that is the present one."""
+def _on(index: int, stream):
+    """The context to allocate and launch in, where it is not the present one."""
     import torch
     if stream is None:
-        return None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+        return torch.cuda.device(index)
     if stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     return torch.cuda.stream(stream)
-
-
-def _current(index: int) -> int:
-    """The device's current stream as a hipStream_t (torch.cuda.current_stream builds an object first: 2 us)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
 
 
 _FLOAT_TYPES = {}
@@ -406,20 +402,23 @@ def embed_rows(wfmt: str, w, ids, N: int, K: int, layout: str = "canonical", sca
     An id outside [0, N) gives a row of NaN."""
     import torch
     (T,) = ids.shape
-    _is(ids, "ids", torch.int32, T)
+    if ids.dtype is not torch.int32 or not ids.is_contiguous():
+        _is(ids, "ids", torch.int32, T)
     if not w.is_contiguous():
         raise ValueError("w must be contiguous")
-    index = _gpu(ids=ids, w=w, out=out)
-    there = _elsewhere(index, stream)
-    if there is not None:
-        with there:
+    index = ids.get_device()
+    if index < 0 or w.get_device() != index or (out is not None and out.get_device() != index):
+        _gpu(ids=ids, w=w, out=out)
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
             return embed_rows(wfmt, w, ids, N, K, layout, scale, out)
     if out is None:
         out = _new(torch, T, K, torch.float32, ids.device)
     else:
         _is(out, "out", torch.float32, T, K)
     _check(load().qmm_embed_rows(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], ids.data_ptr(), T, scale,
-                                 out.data_ptr(), T * K * 4, N, K, _current(index)), "qmm_embed_rows")
+                                 out.data_ptr(), T * K * 4, N, K, torch._C._cuda_getCurrentRawStream(index)),
+           "qmm_embed_rows")
     return out
 
 
@@ -444,15 +443,18 @@ def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=No
         _is(A, "A", t, E, R, K)
         _is(B, "B", t, E, N, R)
         _is(ids, "ids", i32, M)
-    if scales is not None:
+    if scales is not None and not (scales.dtype is f32 and scales.shape == (E,) and scales.is_contiguous()):
         _is(scales, "scales", f32, E)
-    if ranks is not None:
+    if ranks is not None and not (ranks.dtype is i32 and ranks.shape == (E,) and ranks.is_contiguous()):
         _is(ranks, "ranks", i32, E)
     pb, nb, ldb = _rows(base, "base", f32, M, N)
-    index = _gpu(base=base, x=x, A=A, B=B, ids=ids, scales=scales, ranks=ranks, out=out, workspace=workspace)
-    there = _elsewhere(index, stream)
-    if there is not None:
-        with there:
+    index = base.get_device()
+    if not (0 <= index == x.get_device() == A.get_device() == B.get_device() == ids.get_device() and
+            (scales is None or scales.get_device() == index) and (ranks is None or ranks.get_device() == index) and
+            (out is None or out.get_device() == index) and (workspace is None or workspace.get_device() == index)):
+        _gpu(base=base, x=x, A=A, B=B, ids=ids, scales=scales, ranks=ranks, out=out, workspace=workspace)
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
             return lora_add(base, x, A, B, ids, scales, ranks, out, workspace)
     if out is None:
         out = _new(torch, M, N, f32, base.device)
@@ -462,7 +464,8 @@ def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=No
     workspace, nw = _workspace(torch, workspace, load().qmm_lora_workspace_bytes(M, R, K, E), base.device)
     _check(load().qmm_lora_add(_float_type(A, "A"), A.data_ptr(), A.nbytes, B.data_ptr(), B.nbytes, E, R,
                                _ptr(scales), _ptr(ranks), x.data_ptr(), x.nbytes, ids.data_ptr(), pb, nb, ldb,
-                               po, no, ldo, M, N, K, _ptr(workspace), nw, _current(index)), "qmm_lora_add")
+                               po, no, ldo, M, N, K, _ptr(workspace), nw, torch._C._cuda_getCurrentRawStream(index)),
+           "qmm_lora_add")
     return out
 
 
@@ -479,12 +482,14 @@ def _logprob_inputs(M: int, V: int, tokens, mask):
         if len(shape) not in (1, 2) or shape[0] != M:
             raise ValueError(f"tokens must have shape ({M},) or ({M}, G) (got {tuple(shape)})")
         G = shape[1] if len(shape) == 2 else 1
-        _is(tokens, "tokens", torch.int32, *shape)
+        if tokens.dtype is not torch.int32 or not tokens.is_contiguous():
+            _is(tokens, "tokens", torch.int32, *shape)
     if mask is not None:
         rows, words = (1, mask.shape[0]) if mask.dim() == 1 else mask.shape
         if rows not in (1, M) or words < (V + 31) // 32:
             raise ValueError(f"mask must have 1 or {M} rows of at least {(V + 31) // 32} words (got {tuple(mask.shape)})")
-        _is(mask, "mask", torch.int32, *mask.shape)
+        if mask.dtype is not torch.int32 or not mask.is_contiguous():
+            _is(mask, "mask", torch.int32, *mask.shape)
         mask_ld, mask_bytes = words if rows > 1 else 0, mask.nbytes
     return G, mask_ld, mask_bytes
 
@@ -523,17 +528,19 @@ def logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, mask=None, ent
     M, V = logits.shape
     G, mask_ld, mask_bytes = _logprob_inputs(M, V, tokens, mask)
     px, nx, ld = _rows(logits, "logits", logits.dtype, M, V)
-    index = _gpu(logits=logits, tokens=tokens, mask=mask, workspace=workspace)
-    there = _elsewhere(index, stream)
-    if there is not None:
-        with there:
+    index = logits.get_device()
+    if not (index >= 0 and (tokens is None or tokens.get_device() == index) and
+            (mask is None or mask.get_device() == index) and (workspace is None or workspace.get_device() == index)):
+        _gpu(logits=logits, tokens=tokens, mask=mask, workspace=workspace)
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
             return logprobs(logits, tokens, k, scale, mask, entropy, workspace)
     device = logits.device
     lp, ent, top_ids, top_lp = out = _logprob_outputs(torch, M, k, tokens, entropy, device)
     workspace, nw = _workspace(torch, workspace, load().qmm_logprobs_workspace_bytes(M, V, k), device)
     _check(load().qmm_logprobs(_float_type(logits, "logits"), px, nx, ld, M, V, scale, _ptr(mask), mask_bytes,
                                mask_ld, _ptr(tokens), G, _ptr(lp), _ptr(ent), k, _ptr(top_ids), _ptr(top_lp),
-                               _ptr(workspace), nw, _current(index)), "qmm_logprobs")
+                               _ptr(workspace), nw, torch._C._cuda_getCurrentRawStream(index)), "qmm_logprobs")
     return out
 
 
@@ -554,9 +561,8 @@ def mul_mat_logprobs(wfmt: str, w, y, M: int, N: int, K: int, tokens=None, k: in
     if rows < 1:
         raise ValueError(f"rows = {rows}: at least one at a time")
     index = _gpu(w=w, y=y, tokens=tokens, mask=mask, workspace=workspace)
-    there = _elsewhere(index, stream)
-    if there is not None:
-        with there:
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
             return mul_mat_logprobs(wfmt, w, y, M, N, K, tokens, k, scale, mask, entropy, layout, rows, workspace)
     lp, ent, top_ids, top_lp = out = _logprob_outputs(torch, M, k, tokens, entropy, w.device)
     at_once = min(M, max(rows, 8))
@@ -564,7 +570,7 @@ def mul_mat_logprobs(wfmt: str, w, y, M: int, N: int, K: int, tokens=None, k: in
     _check(load().qmm_mul_mat_logprobs(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], y.data_ptr(), y.nbytes,
                                        M, N, K, scale, _ptr(mask), mask_bytes, mask_ld, _ptr(tokens), G, _ptr(lp),
                                        _ptr(ent), k, _ptr(top_ids), _ptr(top_lp), _ptr(workspace), nw,
-                                       _current(index)), "qmm_mul_mat_logprobs")
+                                       torch._C._cuda_getCurrentRawStream(index)), "qmm_mul_mat_logprobs")
     return out
 
 
