@@ -446,13 +446,15 @@ __global__ __launch_bounds__(kThreads, MODE == Tiles::Shared ? 3 : 4) void k_lor
 
     // v's partials: sixteen lanes per row, four consecutive ranks each and 64 at a
     // time; with 16 or 32 ranks in all, four or two groups of lanes take every fourth
-    // or second part (the workspace has room for whole groups of them).  A row without
+    // or second part (the workspace has room for whole groups of them; Long has few
+    // parts and does without, 96.2 against 97.7 us at 2048 x 28672 with 4 of them, though
+    // 42.8 against 41.6 us at 700 x 28672 with 12).  A row without
     // an adapter has none, what is read there and past the last part is not used
     const int vrow = wave * kRows + g;  // kRows is 4: the wavefront's rows by 16 lanes each
     v4f v[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-        const int shift = h > 0 ? 4 : part_lanes(Rp), step = 16 >> shift;
+        const int shift = h > 0 || MODE == Tiles::Long ? 4 : part_lanes(Rp), step = 16 >> shift;
         const int r = 64 * h + 4 * (row & ((1 << shift) - 1)), mine = row >> shift;
         const float *p = P + (mine * M + m0 + (vrow < tile_rows ? vrow : tile_rows - 1)) * Rp + (r < Rp ? r : 0);
         v[h] = v4f{0.f, 0.f, 0.f, 0.f};
