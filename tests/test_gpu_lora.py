@@ -108,6 +108,29 @@ def test_integers_are_exact(M, N, R, type):
     assert np.array_equal(got.astype(np.float64), want)
 
 
+@pytest.mark.parametrize("type", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M,N,R", [(100, 19200, 12), (100, 19001, 20), (144, 60000, 16), (300, 28001, 40),
+                                   (20, 70001, 4), (520, 17000, 6)])
+def test_wide_outputs_are_exact(M, N, R, type):
+    """Several column groups per workgroup, outputs past the caches, K in five parts: integers as above.
+    |v| <= 5 * 3 * 2560 and |out| <= 100 + 3 * 40 * 38400 < 2^24, so every sum is exact in fp32."""
+    rng = np.random.default_rng(M + N + R)
+    K, E = 2560, 5
+    A = rng.integers(-3, 4, (E, R, K)).astype(np.float32)
+    B = rng.integers(-3, 4, (E, N, R)).astype(np.float32)
+    x = rng.integers(-5, 6, (M, K)).astype(np.float32)
+    base = rng.integers(-100, 101, (M, N)).astype(np.float32)
+    ids = np.repeat(rng.integers(-1, E, (M + 6) // 7), 7)[:M].astype(np.int32)  # runs of seven rows
+    dt = _torch_type(type)
+    got = to_host(qmm.lora_add(to_dev(base), to_dev(x), to_dev(A).to(dt), to_dev(B).to(dt), to_dev(ids)))
+    want = base.astype(np.float64)
+    for e in range(E):
+        rows = ids == e
+        v = x[rows].astype(np.float64) @ A[e].astype(np.float64).T
+        want[rows] += v @ B[e].astype(np.float64).T
+    assert np.array_equal(got.astype(np.float64), want)
+
+
 @pytest.mark.parametrize("M", [7, 64, 600])
 def test_routing(M):
     """All rows one adapter, each row its own, none at all, sorted and shuffled: the same rows give the same bits."""
