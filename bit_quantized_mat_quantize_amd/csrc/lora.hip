@@ -21,8 +21,8 @@
 // is fp32 and the result is, so x is not rounded to 16 bits, and A in fp16 or bf16
 // converts exactly.  Its rate (256 flop per cycle and CU) is above what the product
 // needs up to ranks of about 64, where x is what has to move.  The second product
-// has few k and many outputs: there a 16-bit B is used as it is, and v in three
-// 16-bit pieces (Operand).  A lane feeds four or eight consecutive k (or r) to
+// has few k and many outputs: there a 16-bit B goes to the bf16 instruction, fp16 in
+// two pieces, and v in three (Operand).  A lane feeds four or eight consecutive k (or r) to
 // consecutive instructions, with the same assignment on both operands: the sum over
 // k does not mind the order, and every load is 8 to 32 contiguous bytes per lane,
 // whole 64- or 128-byte pieces per row.
@@ -185,16 +185,19 @@ __global__ __launch_bounds__(kShrinkThreads, 4) void k_lora_shrink(const T *__re
 }
 
 // ---- the second product's operands.  fp32 B: C = 4 consecutive ranks per lane
-// feed four v_mfma_f32_16x16x4_f32.  16-bit B goes to the 16-bit instruction as it
-// is (C = 8 ranks per lane, v_mfma_f32_16x16x32), and v as three 16-bit numbers
-// that add up to it, of v times a power of two that puts the row's largest |v|
-// below 2^15 (fp16's range is narrow, and small pieces must not become subnormal):
-// bf16 pieces cut off eight bits each, which is exact; fp16 pieces round to 11 bits
-// each, what is left is below 2^-33 of the largest.  Three products of 32 ranks take
-// 48 cycles; eight fp32 instructions would take 256, and B would have to be
-// converted.
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+// feed four v_mfma_f32_16x16x4_f32.  16-bit B: C = 8 ranks per lane feed
+// v_mfma_f32_16x16x32_bf16.  v goes in as three bf16 numbers that add up to it: each
+// cuts off eight bits, which is exact, and bf16 has the range of fp32, so how far
+// apart the elements of a row lie does not matter (fp16 pieces under one power of
+// two per row would lose the bits of an element 2^-15 of the row's largest).  v is taken
+// times a power of two that puts the row's largest |v| below 2^15: small pieces must
+// not become subnormal.  bf16 B is used as it is.  fp16 B is the sum of a bf16 number
+// of its first eight bits and one of the other three (subnormal ones are ordinary
+// bf16 numbers), which is exact too.  Three products of 32 ranks take 48 cycles, six
+// 96; eight fp32 instructions would take 256.
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
 // of the power of two that puts top, a row's largest |v|, into [2^14, 2^15) (an
@@ -204,6 +207,22 @@ __device__ __forceinline__ int exponent_to_15(float top) {
     return e == 128 ? 0 : (14 - e < 126 ? 14 - e : 126);
 }
 
+// the three bf16 pieces of v, the largest first
+__device__ __forceinline__ void split_bf16(float v, uint16_t *p) {
+    const bool finite = fabsf(v) < __builtin_inff();
+    const uint32_t quiet = v != v ? 0x400000u : 0;  // cutting bits off a NaN must not leave an infinity
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        p[i] = (uint16_t)((__float_as_uint(v) | quiet) >> 16);
+        v = finite ? v - __uint_as_float((uint32_t)p[i] << 16) : 0.f;
+    }
+    if (!finite) p[1] = p[2] = 0;
+}
+__device__ __forceinline__ v4f mul_bf16(uint4 w, uint4 v, v4f acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, w), __builtin_bit_cast(v8b, v), acc, 0, 0, 0);
+}
+
+// multiply, one chunk: acc[t] += w[t] * v, the small pieces of v first
 template <typename T>
 struct Operand;
 template <>
@@ -212,11 +231,14 @@ struct Operand<float> {
     typedef float Stored;  // v in LDS
     static __device__ __forceinline__ int exponent(float) { return 0; }
     static __device__ __forceinline__ void split(float v, Stored (&p)[1]) { p[0] = v; }
-    static __device__ __forceinline__ v4f mul(uint4 w, uint4 v, v4f acc) {
-        const v4f a = __builtin_bit_cast(v4f, w), b = __builtin_bit_cast(v4f, v);
+    static __device__ __forceinline__ void multiply(const uint4 (&w)[kNT], const uint4 (&v)[1], v4f (&acc)[kNT]) {
+        const v4f b = __builtin_bit_cast(v4f, v[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], acc, 0, 0, 0);
-        return acc;
+        for (int t = 0; t < kNT; ++t) {
+            const v4f a = __builtin_bit_cast(v4f, w[t]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], acc[t], 0, 0, 0);
+        }
     }
 };
 template <>
@@ -224,83 +246,49 @@ struct Operand<BF16> {
     static constexpr int C = 8, pieces = 3;
     typedef uint16_t Stored;
     static __device__ __forceinline__ int exponent(float top) { return exponent_to_15(top); }
-    static __device__ __forceinline__ void split(float v, Stored (&p)[3]) {
-        const bool finite = fabsf(v) < __builtin_inff();
-        const uint32_t quiet = v != v ? 0x400000u : 0;  // cutting bits off a NaN must not leave an infinity
+    static __device__ __forceinline__ void split(float v, Stored (&p)[3]) { split_bf16(v, p); }
+    static __device__ __forceinline__ void multiply(const uint4 (&w)[kNT], const uint4 (&v)[3], v4f (&acc)[kNT]) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            p[i] = (uint16_t)((__float_as_uint(v) | quiet) >> 16);
-            v = finite ? v - __uint_as_float((uint32_t)p[i] << 16) : 0.f;
-        }
-        if (!finite) p[1] = p[2] = 0;
-    }
-    static __device__ __forceinline__ v4f mul(uint4 w, uint4 v, v4f acc) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, w), __builtin_bit_cast(v8b, v), acc, 0, 0, 0);
+        for (int i = 2; i >= 0; --i)
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) acc[t] = mul_bf16(w[t], v[i], acc[t]);
     }
 };
 template <>
 struct Operand<_Float16> {
-    static constexpr int C = 8, pieces = 3;
+    // a fourth piece: the first with 0 for what is not finite, for the low part of B.  An
+    // infinite v times the high part is the result; times the low part, which is often
+    // 0 and may have the other sign, it would make a NaN of it.
+    static constexpr int C = 8, pieces = 4;
     typedef uint16_t Stored;
     static __device__ __forceinline__ int exponent(float top) { return exponent_to_15(top); }
-    static __device__ __forceinline__ void split(float v, Stored (&p)[3]) {
-        const bool finite = fabsf(v) < __builtin_inff();
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            p[i] = (uint16_t)f32_to_f16_bits(v);
-            v = finite ? v - f16_bits_to_f32(p[i]) : 0.f;
-        }
+    static __device__ __forceinline__ void split(float v, Stored (&p)[4]) {
+        split_bf16(v, p);
+        p[3] = fabsf(v) < __builtin_inff() ? p[0] : 0;
     }
-    static __device__ __forceinline__ v4f mul(uint4 w, uint4 v, v4f acc) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, v), acc, 0, 0, 0);
+    static __device__ __forceinline__ void halves(uint32_t two, uint32_t &high, uint32_t &low) {
+        const v2h h = __builtin_bit_cast(v2h, two);
+        const float a = (float)h[0], b = (float)h[1];
+        high = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2b));
+        const float ra = a - __uint_as_float(high << 16), rb = b - __uint_as_float(high & 0xffff0000u);
+        low = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{ra, rb}, v2b));
     }
-};
-
-// One chunk: acc[t] += w[t] * (the pieces of v), the small pieces first.
-//
-// fp16: the instruction takes subnormal numbers as they are, but a sum of nothing
-// else loses the bits that their leading zeros push out (15 of 24 were left).  Rows
-// of B without a normal number are multiplied as 2^10 of themselves, and what their
-// sums hold before and after is moved by 2^10 with them; all of it is exact.
-template <typename T>
-__device__ __forceinline__ void multiply(uint4 (&w)[kNT], const uint4 (&v)[Operand<T>::pieces], v4f (&acc)[kNT]) {
-    const int lane = threadIdx.x & 63;
-    uint32_t small[kNT], any = 0;  // a bit for each of the 16 rows
-    auto move = [&](float f) {     // the lane's sums are those of rows 4 * (lane / 16) + q
-#pragma unroll
-        for (int t = 0; t < kNT; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (small[t] >> (4 * (lane >> 4) + q) & 1) acc[t][q] *= f;
-    };
-    if constexpr (__is_same(T, _Float16)) {
+    static __device__ __forceinline__ void multiply(const uint4 (&w)[kNT], const uint4 (&v)[4], v4f (&acc)[kNT]) {
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
-            uint64_t b = __ballot(((w[t].x | w[t].y | w[t].z | w[t].w) & 0x7c007c00u) != 0);
-            b |= b >> 32;
-            small[t] = ~(uint32_t)(b | b >> 16) & 0xffffu;
-            any |= small[t];
-        }
-        if (any != 0) {
-            move(1024.0f);
+            uint4 high, low;
+            halves(w[t].x, high.x, low.x);
+            halves(w[t].y, high.y, low.y);
+            halves(w[t].z, high.z, low.z);
+            halves(w[t].w, high.w, low.w);
 #pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-                const _Float16 f = small[t] >> (lane & 15) & 1 ? (_Float16)1024.0f : (_Float16)1.0f;
-                const auto times = [f](uint32_t two) {
-                    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, two) * v2h{f, f});
-                };
-                w[t] = make_uint4(times(w[t].x), times(w[t].y), times(w[t].z), times(w[t].w));
+            for (int i = 2; i >= 0; --i) {
+                acc[t] = mul_bf16(low, i == 0 ? v[3] : v[i], acc[t]);
+                acc[t] = mul_bf16(high, v[i], acc[t]);
             }
         }
     }
-#pragma unroll
-    for (int i = Operand<T>::pieces - 1; i >= 0; --i)
-#pragma unroll
-        for (int t = 0; t < kNT; ++t) acc[t] = Operand<T>::mul(w[t], v[i], acc[t]);
-    if constexpr (__is_same(T, _Float16)) {
-        if (any != 0) move(0.0009765625f);
-    }
-}
+};
 
 // elements of a row of v in LDS: whole chunks of 4 * C ranks, and 16 bytes more so
 // that the rows start on different banks
@@ -333,10 +321,12 @@ __host__ __device__ constexpr int part_lanes(int Rp) { return Rp <= 16 ? 2 : (Rp
 //
 // Shared (zsplit > 1) has the registers of three workgroups per CU, not four: fp16 B
 // and ranks that are no multiple of C spill otherwise (64 rows of 16 adapters, rank
-// 64, N = 28672, fp16: 35.0 -> 31.8 us; 100 rows at rank 12: 36.8 -> 32.2 us).
+// 64, N = 28672, fp16: 35.0 -> 31.8 us; 100 rows at rank 12: 36.8 -> 32.2 us).  So do
+// fp16 B's odd ranks, read by single elements (2048 rows of 28672 at rank 33: 228 ->
+// 220 us, of 28671 260 -> 239 us).
 enum class Tiles { Own, Shared, Long };  // Shared: zsplit > 1; Long: base and out go past the caches
 template <typename T, bool VEC, int GR, int H, Tiles MODE>
-__global__ __launch_bounds__(kThreads, MODE == Tiles::Shared ? 3 : 4) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
+__global__ __launch_bounds__(kThreads, MODE == Tiles::Shared || (GR == 1 && __is_same(T, _Float16)) ? 3 : 4) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
                                                           const float *__restrict__ scales,
                                                           const int32_t *__restrict__ ranks,
                                                           const int32_t *__restrict__ ids, int64_t M,
@@ -536,7 +526,7 @@ __global__ __launch_bounds__(kThreads, MODE == Tiles::Shared ? 3 : 4) void k_lor
                 uint4 vp[Op::pieces];
 #pragma unroll
                 for (int i = 0; i < Op::pieces; ++i) vp[i] = ld16(vs + (i * kTileRows + row) * vld + r);
-                multiply<T>(w, vp, acc);
+                Op::multiply(w, vp, acc);
             }
             if (match >> row & 1) {
                 const int ex = exponents[row];
