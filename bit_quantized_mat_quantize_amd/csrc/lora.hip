@@ -189,22 +189,24 @@ __global__ __launch_bounds__(kShrinkThreads, 4) void k_lora_shrink(const T *__re
 // v_mfma_f32_16x16x32_bf16.  v goes in as three bf16 numbers that add up to it: each
 // cuts off eight bits, which is exact, and bf16 has the range of fp32, so how far
 // apart the elements of a row lie does not matter (fp16 pieces under one power of
-// two per row would lose the bits of an element 2^-15 of the row's largest).  v is taken
-// times a power of two that puts the row's largest |v| below 2^15: small pieces must
-// not become subnormal.  bf16 B is used as it is.  fp16 B is the sum of a bf16 number
-// of its first eight bits and one of the other three (subnormal ones are ordinary
-// bf16 numbers), which is exact too.  Three products of 32 ranks take 48 cycles, six
-// 96; eight fp32 instructions would take 256.
+// two per row would lose the bits of an element 2^-15 of the row's largest).  A row
+// whose v is small is raised by a power of two, so that small pieces do not become
+// subnormal: to 2^64 for fp16 B, whose products stay below 2^89, and to 2^-64 for bf16
+// B, which may be near 2^128: a sum that is finite without it stays finite (of elements
+// of v below 2^-103 the last bits may be lost there).  bf16 B is used as it is.  fp16 B
+// is the sum of a bf16 number of its first eight bits and one of the other three
+// (subnormal ones are ordinary bf16 numbers), which is exact too.  Three products of 32
+// ranks take 48 cycles, six 96; eight fp32 instructions would take 256.
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
-// of the power of two that puts top, a row's largest |v|, into [2^14, 2^15) (an
-// infinity or NaN: none; top below 2^-112: as near as it goes)
-__device__ __forceinline__ int exponent_to_15(float top) {
-    const int e = (int)(__float_as_uint(top) >> 23) - 127;  // top in [2^e, 2^(e+1))
-    return e == 128 ? 0 : (14 - e < 126 ? 14 - e : 126);
+// of the power of two that raises top, a row's largest |v|, to [2^to, 2^(to+1)); 0
+// where it is there or above (an infinity too)
+__device__ __forceinline__ int raise(float top, int to) {
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;  // top in [2^e, 2^(e+1)), or below 2^-126
+    return e < to ? to - e : 0;
 }
 
 // the three bf16 pieces of v, the largest first
@@ -245,7 +247,7 @@ template <>
 struct Operand<BF16> {
     static constexpr int C = 8, pieces = 3;
     typedef uint16_t Stored;
-    static __device__ __forceinline__ int exponent(float top) { return exponent_to_15(top); }
+    static __device__ __forceinline__ int exponent(float top) { return raise(top, -64); }
     static __device__ __forceinline__ void split(float v, Stored (&p)[3]) { split_bf16(v, p); }
     static __device__ __forceinline__ void multiply(const uint4 (&w)[kNT], const uint4 (&v)[3], v4f (&acc)[kNT]) {
 #pragma unroll
@@ -261,7 +263,7 @@ struct Operand<_Float16> {
     // 0 and may have the other sign, it would make a NaN of it.
     static constexpr int C = 8, pieces = 4;
     typedef uint16_t Stored;
-    static __device__ __forceinline__ int exponent(float top) { return exponent_to_15(top); }
+    static __device__ __forceinline__ int exponent(float top) { return raise(top, 64); }
     static __device__ __forceinline__ void split(float v, Stored (&p)[4]) {
         split_bf16(v, p);
         p[3] = fabsf(v) < __builtin_inff() ? p[0] : 0;

@@ -1,5 +1,5 @@
 """lora_add with fp16 and bf16 adapters at the ends of their ranges: B subnormal beside normal numbers, elements of v
-far below their row's largest, v infinite.
+far below their row's largest, B large, v tiny or infinite.
 
 Tolerance of `test_single_terms`.  A holds ones at one k each, so v is x to the bit, and each row of B has one element
 that is not zero, so out = b x is one product of numbers of 24 and 11 (or 8, 24) bits.  The kernel may cut both into
@@ -83,6 +83,37 @@ def test_ranks_far_apart(type, M):
     base, ids = np.zeros((M, N), np.float32), np.zeros(M, np.int32)
     got, A64, B64 = _run(base, x, A, B, ids, type)
     _check(got, *_formula(base, x, A64, B64, ids))
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_large_finite_b(M):
+    """bf16 reaches 2^127: products with a small v that fp32 holds come out."""
+    rng = np.random.default_rng(23)
+    N, K, R = 66, 64, 8
+    A = (rng.standard_normal((1, R, K)) * 1e-6).astype(np.float32)
+    B = (rng.uniform(0.5, 3, (1, N, R)) * rng.choice([-1e38, 1e35, 1e30], (1, N, R))).astype(np.float32)
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    base, ids = np.zeros((M, N), np.float32), np.zeros(M, np.int32)
+    got, A64, B64 = _run(base, x, A, B, ids, "bf16")
+    assert np.isfinite(B64).all()
+    _check(got, *_formula(base, x, A64, B64, ids))
+
+
+@pytest.mark.parametrize("M", [1, 40])
+@pytest.mark.parametrize("type", ["f16", "bf16", "f32"])
+def test_tiny_v(type, M):
+    """Rows of v between 2^-110 and 2^-80: as in test_single_terms (no result is subnormal)."""
+    rng = np.random.default_rng(24)
+    K, R = 64, 12
+    N = 5 * R
+    x = np.zeros((M, K), np.float32)
+    x[:, :R] = rng.uniform(1, 2, (M, R)) * 2.0 ** rng.integers(-110, -80, (M, R)) * rng.choice([-1, 1], (M, R))
+    B = np.zeros((1, N, R), np.float32)
+    B[0, np.arange(N), np.arange(N) % R] = rng.uniform(1, 2, N) * 2.0 ** rng.integers(0, 10, N)
+    got, A64, B64 = _run(np.zeros((M, N), np.float32), x, _ones(R, K), B, np.zeros(M), type)
+    want = x[:, :R].astype(np.float64) @ B64[0].T
+    err = np.abs(got - want)
+    assert (err <= 12 * U * np.abs(want)).all(), (err / np.abs(want)).max() / U
 
 
 @pytest.mark.parametrize("M", [1, 40])
