@@ -311,9 +311,9 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, const Stats &st
             ids[rank] = (int32_t)~(uint32_t)best;
             lps[rank] = st.logprob(of_order((uint32_t)(best >> 32)), a.scale);
         });
-        for (int i = n + (int)threadIdx.x; i < a.k; i += kThreads) {  // fewer than k tokens have a probability
+        for (int i = n + (int)threadIdx.x; i < a.k; i += kThreads) {  // fewer than k tokens are above -inf
             ids[i] = -1;
-            lps[i] = st.s != st.s ? (float)st.s : -kInf;
+            lps[i] = -kInf;
         }
     }
 }

@@ -429,8 +429,9 @@ size_t qmm_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);
  * stride mask_ld (words; 0: one row of mask for all rows), or NULL: all allowed.
  * What a masked place holds does not matter.  A masked token has log p = -inf.
  * A row in which nothing is allowed or all is -inf: log p = -inf, entropy 0.
- * A NaN or +inf among the allowed logits makes the row's log p and entropy NaN;
- * NaN never enters the top list.
+ * A NaN or +inf among the allowed logits makes the row's log p and entropy NaN, those
+ * of its top list too (+inf is its first entry); a NaN never enters the list, and places
+ * that no token takes hold -1 and -inf there as well.
  * Statistics are fp32; x is read once.  scale (one over the temperature): above
  * 0, at most 1e30.  Requires V <= 2^24, k <= 64, M < 2^23, M*G < 2^31.
  * Outputs and the workspace must not overlap inputs or one another (QMM_EINVAL).
