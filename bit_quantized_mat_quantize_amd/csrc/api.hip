@@ -762,6 +762,15 @@ bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
     return a_bytes && b_bytes && p < q + b_bytes && q < p + a_bytes;
 }
 
+// Two matrices of rows of n floats at the same row stride: no row of one shares an
+// element with a row of the other (column ranges of one wide matrix, say), although
+// the ranges from their first to their last element may overlap.
+bool columns_apart(const float *a, const float *b, int64_t ld, int64_t n) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    const int64_t between = (int64_t)((p < q ? q - p : p - q) / sizeof(float) % (uintptr_t)ld);
+    return between >= n && between <= ld - n;
+}
+
 // bytes from the first element to the end of the last of `rows` rows of n elements
 size_t strided_bytes(int64_t rows, int64_t ld, int64_t n, size_t size) {
     return (size_t)((rows - 1) * ld + n) * size;
@@ -939,7 +948,8 @@ qmm_status qmm_lora_add(qmm_float_type t, const void *A, size_t a_bytes, const v
     QMM_TRY(check_size("out", out_bytes, out_need));
     QMM_TRY(check_size("workspace", ws_bytes, ws_need));
     const bool in_place = out == base && ld_out == ld_base;
-    if (!in_place && overlap(out, out_need, base, base_need))
+    const bool apart = ld_out == ld_base && columns_apart(base, out, ld_base, N);
+    if (!in_place && !apart && overlap(out, out_need, base, base_need))
         return fail(QMM_EINVAL, "out overlaps base without being base (same pointer and row stride)");
     const Span in[] = {{x, x_need}, {A, a_need}, {B, b_need}, {ids, (size_t)M * sizeof(int32_t)},
                        {scales, scales != nullptr ? (size_t)E * sizeof(float) : 0},

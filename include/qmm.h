@@ -394,7 +394,9 @@ size_t qmm_lora_workspace_bytes(int64_t M, int64_t R, int64_t K, int64_t E);
  * activations that the projection quantized.  base [M, N] fp32 with row stride
  * ld_base >= N elements (mul_mat's output, or a column range of it); out
  * likewise with ld_out.  out may be base itself (then ld_out = ld_base: the
- * update in place), otherwise out must not overlap any input (QMM_EINVAL).  An
+ * update in place), or, with ld_out = ld_base, a column range beside it that shares
+ * no element with it; otherwise the bytes from out's first element to its last
+ * must not overlap any input's (QMM_EINVAL).  An
  * infinity in the used part of a 16-bit B makes the results it enters NaN (v is
  * multiplied in parts).
  * Both products are computed in fp32 (x is not rounded); K is split over
