@@ -391,6 +391,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _no_backward(name: str):
+    """The operators beside the projections have no backward; a result without one must not look like torch's."""
+    return ValueError(f"{name} has no backward and one of its tensors requires a gradient: call it under "
+                      "torch.no_grad(), or give it detached tensors")
+
+
 def _new(torch, M: int, N: int, dtype, device):
     return torch.empty_strided((M, N), (N, 1), dtype=dtype, device=device)
 
@@ -401,6 +407,8 @@ def embed_rows(wfmt: str, w, ids, N: int, K: int, layout: str = "canonical", sca
 
     An id outside [0, N) gives a row of NaN."""
     import torch
+    if out is not None and out.requires_grad and torch.is_grad_enabled():
+        raise _no_backward("embed_rows")
     (T,) = ids.shape
     if ids.dtype is not torch.int32 or not ids.is_contiguous():
         _is(ids, "ids", torch.int32, T)
@@ -432,8 +440,13 @@ def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=No
     x: fp32 [M, K], the projection's input; A [E, R, K], B [E, N, R]: float32, float16 or bfloat16; scales
     fp32 [E]; ranks int32 [E], each adapter's own rank (at most R).  base and out may be column ranges of
     wider matrices; out=base adds in place.  Without `out` a new tensor is returned.  An id outside
-    [-1, E) gives a row of NaN."""
+    [-1, E) gives a row of NaN.  There is no backward: tensors that require a gradient are refused
+    where gradients are recorded."""
     import torch
+    if torch.is_grad_enabled() and (base.requires_grad or x.requires_grad or A.requires_grad or B.requires_grad or
+                                    (scales is not None and scales.requires_grad) or
+                                    (out is not None and out.requires_grad)):
+        raise _no_backward("lora_add")
     (M, N), (E, R, K), t = base.shape, A.shape, A.dtype
     f32, i32 = torch.float32, torch.int32
     if not (x.dtype is f32 and B.dtype is t and ids.dtype is i32 and x.shape == (M, K) and B.shape == (E, N, R) and
@@ -523,8 +536,11 @@ def logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, mask=None, ent
     tokens: int32 [M] or [M, G], the tokens whose log probability is asked for (first result, fp32 of the
     same shape); entropy: fp32 [M]; k: that many most likely tokens (int32 and fp32 [M, k], -1 and -inf where
     there are fewer).  mask: int32 words [W], [1, W] or [M, W], W >= ceil(V / 32); bit i % 32 of word i // 32
-    allows token i.  scale multiplies the logits (one over the temperature).  What is not asked for is None."""
+    allows token i.  scale multiplies the logits (one over the temperature).  What is not asked for is None.
+    There is no backward: logits that require a gradient are refused where gradients are recorded."""
     import torch
+    if logits.requires_grad and torch.is_grad_enabled():
+        raise _no_backward("logprobs")
     M, V = logits.shape
     G, mask_ld, mask_bytes = _logprob_inputs(M, V, tokens, mask)
     px, nx, ld = _rows(logits, "logits", logits.dtype, M, V)
