@@ -391,6 +391,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _written(torch, out) -> None:
+    """Tells autograd that a given out has new values: a backward that saved the old ones raises."""
+    torch.autograd.graph.increment_version(out)
+
+
 def _no_backward(name: str):
     """The operators beside the projections have no backward; a result without one must not look like torch's."""
     return ValueError(f"{name} has no backward and one of its tensors requires a gradient: call it under "
@@ -420,13 +425,16 @@ def embed_rows(wfmt: str, w, ids, N: int, K: int, layout: str = "canonical", sca
     if stream is not None or torch._C._cuda_getDevice() != index:
         with _on(index, stream):
             return embed_rows(wfmt, w, ids, N, K, layout, scale, out)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _new(torch, T, K, torch.float32, ids.device)
     else:
         _is(out, "out", torch.float32, T, K)
     _check(load().qmm_embed_rows(_WEIGHT[wfmt], w.data_ptr(), w.nbytes, _LAYOUT[layout], ids.data_ptr(), T, scale,
                                  out.data_ptr(), T * K * 4, N, K, torch._C._cuda_getCurrentRawStream(index)),
            "qmm_embed_rows")
+    if given:
+        _written(torch, out)
     return out
 
 
@@ -469,7 +477,8 @@ def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=No
     if stream is not None or torch._C._cuda_getDevice() != index:
         with _on(index, stream):
             return lora_add(base, x, A, B, ids, scales, ranks, out, workspace)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _new(torch, M, N, f32, base.device)
         po, no, ldo = out.data_ptr(), M * N * 4, N
     else:
@@ -479,6 +488,8 @@ def lora_add(base, x, A, B, ids, scales=None, ranks=None, out=None, workspace=No
                                _ptr(scales), _ptr(ranks), x.data_ptr(), x.nbytes, ids.data_ptr(), pb, nb, ldb,
                                po, no, ldo, M, N, K, _ptr(workspace), nw, torch._C._cuda_getCurrentRawStream(index)),
            "qmm_lora_add")
+    if given:
+        _written(torch, out)
     return out
 
 
