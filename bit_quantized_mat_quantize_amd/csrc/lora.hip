@@ -324,11 +324,15 @@ __host__ __device__ constexpr int part_lanes(int Rp) { return Rp <= 16 ? 2 : (Rp
 // Shared (zsplit > 1) has the registers of three workgroups per CU, not four: fp16 B
 // and ranks that are no multiple of C spill otherwise (64 rows of 16 adapters, rank
 // 64, N = 28672, fp16: 35.0 -> 31.8 us; 100 rows at rank 12: 36.8 -> 32.2 us).  So do
-// fp16 B's odd ranks, read by single elements (2048 rows of 28672 at rank 33: 228 ->
-// 220 us, of 28671 260 -> 239 us).
+// 16-bit B of odd ranks, read by single elements: fp16 (2048 rows of 28672 at rank 33:
+// 228 -> 220 us), and bf16 where rows are not 16-byte aligned (of 28671: 261 -> 236 us;
+// aligned ones fit, 212 us against 217).
 enum class Tiles { Own, Shared, Long };  // Shared: zsplit > 1; Long: base and out go past the caches
+template <typename T, bool VEC, int GR, Tiles MODE>
+constexpr int expand_workgroups =
+    MODE == Tiles::Shared || (GR == 1 && (__is_same(T, _Float16) || (__is_same(T, BF16) && !VEC))) ? 3 : 4;
 template <typename T, bool VEC, int GR, int H, Tiles MODE>
-__global__ __launch_bounds__(kThreads, MODE == Tiles::Shared || (GR == 1 && __is_same(T, _Float16)) ? 3 : 4) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
+__global__ __launch_bounds__(kThreads, (expand_workgroups<T, VEC, GR, MODE>)) void k_lora_expand(const T *__restrict__ B, int64_t E, int R,
                                                           const float *__restrict__ scales,
                                                           const int32_t *__restrict__ ranks,
                                                           const int32_t *__restrict__ ids, int64_t M,
