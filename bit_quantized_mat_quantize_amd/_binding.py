@@ -410,7 +410,8 @@ def embed_rows(wfmt: str, w, ids, N: int, K: int, layout: str = "canonical", sca
                out=None, stream=None):
     """out [T, K] fp32 = scale * the rows ids (int32 [T]) of the packed table w [N, K], decoded.
 
-    An id outside [0, N) gives a row of NaN."""
+    An id outside [0, N) gives a row of NaN.  A slice of ids that does not start on 16 bytes is refused; its
+    clone() is not (so for the integer arguments of lora_add and logprobs)."""
     import torch
     if out is not None and out.requires_grad and torch.is_grad_enabled():
         raise _no_backward("embed_rows")

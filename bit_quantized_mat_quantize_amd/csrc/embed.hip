@@ -85,10 +85,14 @@ __device__ __forceinline__ float4 decode_quad(const uint8_t *__restrict__ w, int
 
 // Work item = kThreads * quads<LONG> quads of one row; `chunks` items per row.  An
 // id outside [0, N) gives a row of NaN and reads nothing of the table.  LONG: an
-// output that no cache holds goes past them, two quads per thread.  4099 rows of
-// 8192 (134 MB, 4 buffers in turn) take 22.3 us so, 6.9 TB/s read and written,
-// against 36.5 us with plain stores (Q4_K; 23.4 us with four quads); 2048 rows of
-// 4096 (34 MB) 8.6 against 10.0 us.
+// output of more than the L2 caches hold goes past the caches, two quads per thread.
+// 4099 rows of 8192 (134 MB, 4 buffers in turn) take 22.3 us so, 6.9 TB/s read and
+// written, against 36.5 us with plain stores (Q4_K; 23.4 us with four quads); 2048 rows
+// of 4096 (34 MB) 8.6 against 10.0 us.  Together with the quantization that reads the
+// output (Q4_K, K = 8192, 5 buffers in turn): 34 MiB 21.5 against 21.7 us, 67 MiB 35.4
+// against 35.5, 130 MiB 60 against 71.  Into a buffer that the 256 MB cache behind the L2
+// still holds from the call before, plain stores are faster up to 145 MiB (34 MiB:
+// 27.8 against 21.4 us for both kernels).
 typedef float v4f __attribute__((ext_vector_type(4)));
 template <bool LONG>
 constexpr int quads = LONG ? 2 : 1;
@@ -139,7 +143,7 @@ hipError_t launch(const uint8_t *w, int64_t NB, int64_t dsec, const int32_t *ids
     return hipGetLastError();
 }
 
-constexpr int64_t kLongBytes = 32 << 20;  // the L2 caches hold 4 MiB for each of 8 XCDs
+constexpr int64_t kLongBytes = 32 << 20;  // the L2 caches: 4 MiB for each of 8 XCDs
 bool long_output(int64_t T, int64_t K) { return T * K * (int64_t)sizeof(float) >= kLongBytes; }
 
 template <int FMT>

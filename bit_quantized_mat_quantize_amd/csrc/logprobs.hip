@@ -327,7 +327,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, const Stats &st
 // reaches; 513 rows of 50257 fp16 logits, k = 8: 23 us for 52 MB: about 50 cycles of
 // vector instructions per 64 logits (an exponential is 16 of them), two rows per CU
 // and three on one, and 6 us for the bounds and lists (17 us with k = 0); 32 rows of
-// 128256 under masks, k = 20: 10.5 us in 16 splits each; one row of 32000, k = 5: 9
+// 128256 under masks, k = 20: 10.3 us in 16 splits each; one row of 32000, k = 5: 8.8
 // us, of which the statistics take 5.5 and the bound and the ranking the rest.
 template <typename T, bool MASK, int BATCH>
 __global__ __launch_bounds__(kThreads) void k_logprobs(const LogprobArgs a, int splits) {
@@ -531,8 +531,9 @@ int splits_of(int64_t M, int64_t V) {
 }
 
 // A workgroup that has a row and a CU to itself waits for its loads more than it
-// computes: it takes 32 logits per thread and batch (one row of 32000, k = 5: 10.7 ->
-// 9.4 us, 256 masked rows of 128256, k = 20: 46.0 -> 39.0 us).  Where others run
+// computes: it takes 32 logits per thread and batch (one row of 32000, k = 5: 10.9 -> 9.4
+// us, 256 masked rows of 128256, k = 20: 44.8 -> 39.9 us, three sets of inputs in turn;
+// 38.1 -> 35.1 us where the 256 MB cache holds the one set).  Where others run
 // beside it or its part is short, 16 are faster (513 rows of 50257: 23.8 us, 25.8 us
 // with 32; 32 rows of 128256 in 16 parts: 14.6 us, 15.3 us; 32 rows of 5000, less than
 // one batch: 6.8 us, 7.3 us).

@@ -141,7 +141,10 @@ __global__ __launch_bounds__(kShrinkThreads, 4) void k_lora_shrink(const T *__re
             ap[t] = A + ((int64_t)e * R + (r < R ? r : R - 1)) * K + 8 * g;
             acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
         }
-        constexpr int H = 2;  // the loads of two steps are in flight before the first one's products
+        // Loads of two steps at a time.  With one tile of ranks all of them are in flight
+        // before the first products; with two, the second tile's load stands behind a
+        // branch that the compiler waits in, so each step's loads come by themselves.
+        constexpr int H = 2;
         for (int st = st0 + H * wave; st < st1; st += H * W) {
             const bool two = st + 1 < st1;
             Pack<float, 8> xv[H];
@@ -310,16 +313,18 @@ __host__ __device__ constexpr int part_lanes(int Rp) { return Rp <= 16 ? 2 : (Rp
 // columns of B, adapter by adapter: B's rows are the matrix instruction's rows, so
 // a lane ends with four consecutive columns of one output row, and the rows that
 // match go to a tile in LDS.  From there base and out are read and written by
-// whole rows, 1 KiB per wavefront and instruction.  The first group's base and B
-// are on their way while v is added up.  VEC: rows of base and out are 16-byte
+// whole rows, 1 KiB per wavefront and instruction.  The first group's base is asked for
+// before the partials (by tiles that are not shared), its B behind them: it arrives
+// while v is scaled and cut.  VEC: rows of base and out are 16-byte
 // aligned and N is a multiple of 4 (16-byte accesses); GR: R is a multiple of it (B
-// in loads of GR elements: C, C / 2, C / 4 or 1); H: 64 * H ranks at most.
+// in loads of GR elements: C, C / 2, C / 4 or 1); H: 64 * H ranks at most (GR < C is
+// built with H = 4 alone: the loops over h end at the rank all the same).
 //
-// Measured (base and out not in a cache): 2048 rows, N = 28672, rank 16: 81 us of the
-// 79 that adding two matrices of this size takes, 6 TB/s; 555 rows, rank 64: 37 us,
-// of which the partials take 5 (32 KB of them per workgroup, out of the L2) and B 4; 127 MB of base and out alone would take 21; 32 rows of 28
-// adapters, N = 8192: 7.9 us; one row, N = 4096: 4.8 us, a chain of ids, partials, B
-// and the exchange of the tile.
+// Measured (base and out not in a cache): 2048 rows, N = 28672, rank 16, fp16 B: 84 us
+// of the 79 that adding two matrices of this size takes, 5.6 TB/s; 555 rows, rank 64, bf16: 37 us, of which the partials take 5 (32 KB of
+// them per workgroup, out of the L2) and B 4; 127 MB of base and out alone would take 21;
+// 32 rows of 28 adapters, N = 8192: 7.9 us; one row, N = 4096, fp16: 5.1 us, a chain of
+// ids, partials, B and the exchange of the tile.
 //
 // Shared (zsplit > 1) has the registers of three workgroups per CU, not four: fp16 B
 // and ranks that are no multiple of C spill otherwise (64 rows of 16 adapters, rank
@@ -469,7 +474,7 @@ __global__ __launch_bounds__(kThreads, (expand_workgroups<T, VEC, GR, MODE>)) vo
             if (step > 2) v[h][q] += dpp_f32<0x124>(v[h][q]);
         }
     }
-    // the first group's B and base are on their way while v is made up
+    // the first group's B, and base of a shared tile, arrive while v is scaled and cut
     const int first = adapters != 0 ? __builtin_ctz(adapters) : 0;  // a row of the first adapter
     load_b(__builtin_amdgcn_readlane(own, first), strip0, C * g);
     if (SHARED) load_base(strip0, here);
@@ -644,8 +649,12 @@ template <typename T, bool VEC, int GR, int H>
 hipError_t expand(const LoraArgs &a, const Shape &h, hipStream_t s) {
     const Strips st = strips_of(a.N, h);
     const size_t lds = sizeof(typename Operand<T>::Stored) * Operand<T>::pieces * kTileRows * v_row<T>(h.Rp);
-    // no cache holds 32 MiB of out: it goes past them, and base with it (2048 rows of
-    // 28672: 105 -> 101 us for both kernels, 555 rows at rank 64: 55 -> 50 us)
+    // 32 MiB of out are more than the L2 caches hold: it goes past them, and base with it
+    // (2048 rows of 28672: 105 -> 101 us for both kernels, 555 rows at rank 64: 55 -> 50
+    // us, inputs in turn).  In place on what a kernel before it wrote and read by a
+    // quantization after it, plain accesses are 1 to 2% faster up to 128 MiB, which the
+    // 256 MB cache behind the L2 holds (1100 rows of 8192: 45.2 us for the three kernels
+    // against 45.7), past the caches 2 to 5% from 224 MiB on (8192 rows: 263 against 277).
     const auto kernel = h.zsplit > 1 ? k_lora_expand<T, VEC, GR, H, Tiles::Shared>
                         : VEC && a.M * a.N >= (int64_t(32) << 20) / 4
                             ? k_lora_expand<T, VEC, GR, H, VEC ? Tiles::Long : Tiles::Own>

@@ -21,4 +21,4 @@ LD_PRELOAD="$GCC_ASAN" python -m pytest -q -p no:cacheprovider -m "not gpu" test
     tests/test_oracle_q2k.py tests/test_oracle_moe.py
 echo "== libqmm host code under $CLANG_ASAN"
 LD_PRELOAD="$CLANG_ASAN" python -m pytest -q -p no:cacheprovider -m "not gpu" tests/test_abi.py tests/test_dispatch_log.py \
-    tests/test_abi_operators.py tests/test_dispatch_log_operators.py
+    tests/test_abi_operators.py tests/test_abi_lora_ranges.py tests/test_dispatch_log_operators.py
