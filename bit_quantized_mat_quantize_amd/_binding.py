@@ -28,6 +28,14 @@ _LAYOUT = {"canonical": CANONICAL, "repacked": REPACKED}
 _ALGO = {"auto": ALGO_AUTO, "gemv": ALGO_GEMV, "mfma": ALGO_MFMA, "skinny": ALGO_SKINNY}
 
 
+class _Cache(ctypes.Structure):
+    """qmm_cache of include/qmm.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("bytes", ctypes.c_size_t), ("pages", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("heads", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("seqs", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("rows", ctypes.c_int64)]
+
+
 class QmmError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         self.status = status
@@ -50,6 +58,7 @@ def load() -> ctypes.CDLL:
     import torch  # noqa: F401
     lib = ctypes.CDLL(LIB_PATH)
     P, I64, SZ, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    C, D = ctypes.POINTER(_Cache), ctypes.c_double
     sigs = {
         "qmm_act_bytes": (SZ, [I, I64, I64]),
         "qmm_weight_bytes": (SZ, [I, I, I64, I64]),
@@ -79,6 +88,13 @@ def load() -> ctypes.CDLL:
         "qmm_mul_mat_logprobs_workspace_bytes": (SZ, [I64, I64, I64]),
         "qmm_mul_mat_logprobs": (I, [I, P, SZ, I, P, SZ, I64, I64, I64, ctypes.c_float, P, SZ, I64, P, I64, P, P, I64,
                                      P, P, P, SZ, P]),
+        "qmm_rope": (I, [I, P, SZ, I64, I64, P, P, P, SZ, I64, I64, I64, I64, I64, I64, I, D, D, D, D, D, P]),
+        "qmm_cache_bytes": (SZ, [I64, I64, I64, I64]),
+        "qmm_cache_write": (I, [C, I, P, SZ, I64, P, SZ, I64, P]),
+        "qmm_cache_read": (I, [C, I, P, SZ, P, SZ, P]),
+        "qmm_cache_attention_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I64, I64, I, I]),
+        "qmm_cache_attention": (I, [C, I, P, SZ, I64, I64, P, SZ, I64, ctypes.c_float, I, I64, P, P, I64, P, SZ, P]),
+        "qmm_cache_evict": (I, [C, P, I64, I64, I64, P, I64, P, P, I64, P, P]),
         "qmm_debug_block_sums": (I, [I, P, SZ, I, P, SZ, P, SZ, I64, I64, I64, P]),
         "qmm_status_string": (ctypes.c_char_p, [I]),
         "qmm_last_error": (ctypes.c_char_p, []),
@@ -600,6 +616,271 @@ def mul_mat_logprobs(wfmt: str, w, y, M: int, N: int, K: int, tokens=None, k: in
                                        _ptr(ent), k, _ptr(top_ids), _ptr(top_lp), _ptr(workspace), nw,
                                        torch._C._cuda_getCurrentRawStream(index)), "qmm_mul_mat_logprobs")
     return out
+
+
+# ---- between the projections: rotary positions, the 4-bit cache of keys and values, attention over it, eviction.
+
+def rope_ramp(rot: int, base: float, length: int, factor: float, fast: float = 32.0, slow: float = 1.0):
+    """rope's scaling arguments for a model trained on `length` positions and used on `factor` times as many: pairs that
+    turn more than `fast` times within `length` keep their angles, those of fewer than `slow` turns are slowed by
+    `factor`, those between in part, and magnitude = 0.1 ln(factor) + 1."""
+    import math
+
+    def pair(turns):  # the pair that turns so often within the length
+        return rot * math.log(length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+    low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
+    return {"freq_scale": 1.0 / factor, "ramp": (float(low), float(max(high, low + 1))),
+            "magnitude": 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0}
+
+
+def _heads(t, name: str, T: int, H: int, D: int):
+    """(bytes from the pointer to the last head's end, elements from a row to the next) of [T, H, D], heads side by side."""
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must have shape {(T, H, D)} (got {tuple(t.shape)})")
+    ld, head, one = t.stride()
+    if one != 1 or (H > 1 and head != D):
+        raise ValueError(f"{name} must have its heads side by side (strides {t.stride()})")
+    if T < 2:
+        ld = H * D
+    return ((T - 1) * ld + H * D) * t.element_size() if T else 0, ld
+
+
+def rope(x, positions, rot=None, layout: str = "half", base: float = 10000.0, freq_scale: float = 1.0, ramp=None,
+         magnitude: float = 1.0, factors=None, out=None, stream=None):
+    """Rotary positions of x [T, H, D] (float32, float16 or bfloat16; any strides but along D): out of the same shape.
+
+    positions: int32 [T].  rot: how many elements of a head turn (all).  layout: "half" pairs element i with i + rot/2,
+    "interleaved" 2i with 2i + 1.  theta_i = position * base^(-2i/rot), over factors[i] (fp32 [rot/2]) where given, times
+    freq_scale for all pairs, or, with ramp = (low, high), from pair `low` to `high` more and more of it (rope_ramp).
+    magnitude multiplies what turns.  out may be x.  There is no backward: an x that requires a gradient is refused
+    where gradients are recorded."""
+    import torch
+    if (x.requires_grad or (out is not None and out.requires_grad) or
+            (factors is not None and factors.requires_grad)) and torch.is_grad_enabled():
+        raise _no_backward("rope")
+    T, H, D = x.shape
+    rot = D if rot is None else rot
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout = {layout!r}: half or interleaved")
+    low, high = (0.0, 0.0) if ramp is None else ramp
+    if ramp is not None and not high > low:
+        raise ValueError(f"ramp = {ramp}: low below high")
+    if positions.dtype is not torch.int32 or positions.shape != (T,) or not positions.is_contiguous():
+        _is(positions, "positions", torch.int32, T)
+    if factors is not None:
+        _is(factors, "factors", torch.float32, rot // 2)
+    ld_x, head_x, one = x.stride()
+    if D > 1 and one != 1:
+        raise ValueError("x must have unit stride along its heads")
+    index = x.get_device()
+    if not (0 <= index == positions.get_device() and (factors is None or factors.get_device() == index) and
+            (out is None or out.get_device() == index)):
+        _gpu(x=x, positions=positions, factors=factors, out=out)
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
+            return rope(x, positions, rot, layout, base, freq_scale, ramp, magnitude, factors, out)
+    given = out is not None
+    size = x.element_size()
+    if not given:
+        out = torch.empty_strided((T, H, D), (H * D, D, 1), dtype=x.dtype, device=x.device)
+        ld_o, head_o = H * D, D
+    else:
+        if out.dtype is not x.dtype or out.shape != x.shape or (D > 1 and out.stride(2) != 1):
+            raise ValueError(f"out must be {x.dtype} of shape {(T, H, D)} with unit stride along its heads (got "
+                             f"{out.dtype}, {tuple(out.shape)}, strides {out.stride()})")
+        ld_o, head_o, _ = out.stride()
+    if T and H:
+        nx, no = ((T - 1) * ld_x + (H - 1) * head_x + D) * size, ((T - 1) * ld_o + (H - 1) * head_o + D) * size
+    else:
+        nx = no = 0
+    _check(load().qmm_rope(_float_type(x, "x"), x.data_ptr(), nx, ld_x, head_x, positions.data_ptr(), _ptr(factors),
+                           out.data_ptr(), no, ld_o, head_o, T, H, D, rot, layout == "interleaved", base, freq_scale,
+                           low, high, magnitude, torch._C._cuda_getCurrentRawStream(index)), "qmm_rope")
+    if given:
+        _written(torch, out)
+    return out
+
+
+def cache_bytes(pages: int, heads: int, dim: int, page: int = 64) -> int:
+    return int(load().qmm_cache_bytes(pages, page, heads, dim))
+
+
+def cache_new(pages: int, heads: int, dim: int, page: int = 64, device="cuda"):
+    """A cache for keys and values: uint8 [pages, 2, heads, page, dim * 9 // 16] (the order of the bytes within a page is
+    that of include/qmm.h).  It holds anything until rows are written."""
+    import torch
+    if not cache_bytes(pages, heads, dim, page):
+        raise ValueError(f"no cache of {pages} pages of {page} entries, {heads} heads of {dim}: pages of 16, 32, .. 1024, "
+                         "heads of 64, 96, 128, 192 or 256")
+    return torch.empty((pages, 2, heads, page, dim * 9 // 16), dtype=torch.uint8, device=device)
+
+
+def _cache(torch, cache, table, lens, starts, T):
+    """(struct, heads, dim, sequences, pages of a table, entries of a page) of a cache and its batch, checked."""
+    i32 = torch.int32
+    if cache.dtype is not torch.uint8 or cache.dim() != 5 or not cache.is_contiguous() or cache.shape[1] != 2:
+        raise ValueError(f"cache must be contiguous uint8 [pages, 2, heads, page, dim * 9 // 16] (got {cache.dtype}, "
+                         f"{tuple(cache.shape)})")
+    pages, _, heads, page, row = cache.shape
+    if row % 18:
+        raise ValueError(f"cache: {row} bytes an entry are no blocks of 18")
+    dim = row * 16 // 9
+    if table.dim() != 2 or table.dtype is not i32 or not table.is_contiguous():
+        raise ValueError(f"table must be contiguous int32 [sequences, pages] (got {table.dtype}, {tuple(table.shape)})")
+    B, W = table.shape
+    if lens.dtype is not i32 or lens.shape != (B,) or not lens.is_contiguous():
+        _is(lens, "lens", i32, B)
+    if starts is not None and (starts.dtype is not i32 or starts.shape != (B + 1,) or not starts.is_contiguous()):
+        _is(starts, "starts", i32, B + 1)
+    return (_Cache(cache.data_ptr(), cache.nbytes, pages, page, heads, dim, table.data_ptr(), B, W, lens.data_ptr(),
+                   None if starts is None else starts.data_ptr(), T), heads, dim, B, W, page)
+
+
+def cache_write(cache, k, v, table, lens, starts=None, stream=None):
+    """Writes rows of keys and values, k and v [T, heads, dim] (float32, float16 or bfloat16; heads side by side), into
+    the cache as 4-bit blocks.
+
+    table: int32 [B, pages], the pages of each sequence; lens: int32 [B], its entries with the new rows; starts: int32
+    [B + 1], sequence b has the rows starts[b] .. starts[b + 1] - 1 (None: row b is sequence b's).  The last of a
+    sequence's rows becomes its entry lens[b] - 1.  Rows of no sequence, and those whose page is not in the cache, are
+    left out.  There is no backward: k and v that require a gradient are refused where gradients are recorded."""
+    import torch
+    if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+        raise _no_backward("cache_write")
+    T = k.shape[0]
+    c, heads, dim, _, _, _ = _cache(torch, cache, table, lens, starts, T)
+    nk, ldk = _heads(k, "k", T, heads, dim)
+    nv, ldv = _heads(v, "v", T, heads, dim)
+    if v.dtype is not k.dtype:
+        raise ValueError(f"k is {k.dtype}, v {v.dtype}")
+    index = cache.get_device()
+    if not (0 <= index == k.get_device() == v.get_device() == table.get_device() == lens.get_device() and
+            (starts is None or starts.get_device() == index)):
+        _gpu(cache=cache, k=k, v=v, table=table, lens=lens, starts=starts)
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
+            return cache_write(cache, k, v, table, lens, starts)
+    _check(load().qmm_cache_write(c, _float_type(k, "k"), k.data_ptr(), nk, ldk, v.data_ptr(), nv, ldv,
+                                  torch._C._cuda_getCurrentRawStream(index)), "qmm_cache_write")
+    _written(torch, cache)
+
+
+def cache_read(cache, rows: int, table, lens, starts=None, dtype=None, stream=None):
+    """(k, v) [rows, heads, dim] of `dtype` (float32): the entries that rows of the same table, lens and starts would be
+    written to, as numbers.  An entry whose page is not in the cache is NaN; rows of no sequence hold anything."""
+    import torch
+    c, heads, dim, _, _, _ = _cache(torch, cache, table, lens, starts, rows)
+    index = cache.get_device()
+    if not (0 <= index == table.get_device() == lens.get_device() and (starts is None or starts.get_device() == index)):
+        _gpu(cache=cache, table=table, lens=lens, starts=starts)
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
+            return cache_read(cache, rows, table, lens, starts, dtype)
+    k, v = (torch.empty_strided((rows, heads, dim), (heads * dim, dim, 1), dtype=dtype or torch.float32,
+                                device=cache.device) for _ in range(2))
+    _check(load().qmm_cache_read(c, _float_type(k, "dtype"), k.data_ptr(), k.nbytes, v.data_ptr(), v.nbytes,
+                                 torch._C._cuda_getCurrentRawStream(index)), "qmm_cache_read")
+    return k, v
+
+
+def cache_attention_workspace_bytes(rows: int, q_heads: int, heads: int, dim: int, seqs: int, width: int, page: int,
+                                    ragged: bool, mass: bool = False) -> int:
+    return int(load().qmm_cache_attention_workspace_bytes(rows, q_heads, heads, dim, seqs, width, page, ragged, mass))
+
+
+def cache_attention(q, cache, table, lens, starts=None, scale=None, causal: bool = True, window: int = 0, mass=None,
+                    lse: bool = False, out=None, workspace=None, stream=None):
+    """Attention of q [T, q_heads, dim] (float32, float16 or bfloat16; heads side by side) over the cache: out of the
+    same shape and type, or (out, lse) with lse fp32 [T, q_heads].
+
+    table, lens and starts as in cache_write: lens counts the rows of this call, whose keys and values are in the cache.
+    Query heads h * q_heads / heads .. share cache head h.  scale: of the scores (1 / sqrt(dim)).  causal: a row sees
+    the entries up to its own position; window > 0: of these the last `window`.  mass: fp32 [B, heads, n] with room for
+    a whole table's entries, n >= pages * page: the weights that each entry gets, summed over rows and heads, are added
+    to it.  A row that sees nothing gives 0 and lse -inf; one that sees an entry with a NaN, or whose page is not in the
+    cache, gives NaN.  Rows of no sequence are left as they are (in a new out: they hold anything).  There is no
+    backward: a q that requires a gradient is refused where gradients are recorded."""
+    import torch
+    if (q.requires_grad or (out is not None and out.requires_grad) or
+            (mass is not None and mass.requires_grad)) and torch.is_grad_enabled():
+        raise _no_backward("cache_attention")
+    T, HQ, dim = q.shape
+    c, heads, d, B, W, page = _cache(torch, cache, table, lens, starts, T)
+    nq, ldq = _heads(q, "q", T, HQ, d)
+    index = cache.get_device()
+    if not (0 <= index == q.get_device() == table.get_device() == lens.get_device() and
+            (starts is None or starts.get_device() == index) and (mass is None or mass.get_device() == index) and
+            (out is None or out.get_device() == index) and (workspace is None or workspace.get_device() == index)):
+        _gpu(cache=cache, q=q, table=table, lens=lens, starts=starts, mass=mass, out=out, workspace=workspace)
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
+            return cache_attention(q, cache, table, lens, starts, scale, causal, window, mass, lse, out, workspace)
+    device, given, ld_mass = cache.device, out is not None, 0
+    if mass is not None:
+        if (mass.dtype is not torch.float32 or mass.dim() != 3 or mass.shape[:2] != (B, heads) or
+                mass.shape[2] < W * page or not mass.is_contiguous()):
+            raise ValueError(f"mass must be contiguous float32 [{B}, {heads}, {W * page} or more] (got {mass.dtype}, "
+                             f"{tuple(mass.shape)}, strides {mass.stride()})")
+        ld_mass = mass.shape[2]
+    if not given:
+        out = torch.empty_strided((T, HQ, dim), (HQ * dim, dim, 1), dtype=q.dtype, device=device)
+        no, ldo = T * HQ * dim * q.element_size(), HQ * dim
+    else:
+        if out.dtype is not q.dtype:
+            raise ValueError(f"out must be {q.dtype} (got {out.dtype})")
+        no, ldo = _heads(out, "out", T, HQ, dim)
+    stats = _new(torch, T, HQ, torch.float32, device) if lse else None
+    lib = load()
+    workspace, nw = _workspace(torch, workspace, lib.qmm_cache_attention_workspace_bytes(
+        T, HQ, heads, dim, B, W, page, starts is not None, mass is not None), device)
+    _check(lib.qmm_cache_attention(c, _float_type(q, "q"), q.data_ptr(), nq, ldq, HQ, out.data_ptr(), no, ldo,
+                                   dim ** -0.5 if scale is None else scale, causal, window, _ptr(stats), _ptr(mass),
+                                   ld_mass, _ptr(workspace), nw, torch._C._cuda_getCurrentRawStream(index)),
+           "qmm_cache_attention")
+    if given:
+        _written(torch, out)
+    if mass is not None:
+        _written(torch, mass)
+    return (out, stats) if lse else out
+
+
+def cache_evict(cache, table, lens, mass, budget: int, recent: int = 0, to=None, stream=None):
+    """(lens, mass, ids) after at most `budget` entries of each sequence and head stay: the newest `recent` and, of the
+    others, those of the largest mass (fp32 [B, heads, n] as in cache_attention), ties to the lower position.
+
+    They move in their order into the pages of `to` (int32 [B, pages]), which are the sequences' own (None, or a table
+    with the same pages in the same places) or others that no sequence uses.  ids: int32 [B, heads, budget], where they
+    were, -1 behind; mass: fp32 [B, heads, pages of `to` * page], 0 behind; lens: int32 [B]."""
+    import torch
+    if mass.requires_grad and torch.is_grad_enabled():
+        raise _no_backward("cache_evict")
+    c, heads, _, B, W, page = _cache(torch, cache, table, lens, None, 0)
+    f32, i32 = torch.float32, torch.int32
+    if (mass.dtype is not f32 or mass.dim() != 3 or mass.shape[:2] != (B, heads) or mass.shape[2] < W * page or
+            not mass.is_contiguous()):
+        raise ValueError(f"mass must be contiguous float32 [{B}, {heads}, {W * page} or more] (got {mass.dtype}, "
+                         f"{tuple(mass.shape)}, strides {mass.stride()})")
+    if to is None:
+        to = table
+    if to.dim() != 2 or to.shape[0] != B or to.dtype is not i32 or not to.is_contiguous():
+        raise ValueError(f"to must be contiguous int32 [{B}, pages] (got {to.dtype}, {tuple(to.shape)})")
+    if to.shape[1] * page < budget or not 0 <= recent <= budget or budget < 1:
+        raise ValueError(f"budget = {budget}, recent = {recent}: recent <= budget <= the {to.shape[1] * page} entries of `to`")
+    index = cache.get_device()
+    if not 0 <= index == table.get_device() == lens.get_device() == mass.get_device() == to.get_device():
+        _gpu(cache=cache, table=table, lens=lens, mass=mass, to=to)
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        with _on(index, stream):
+            return cache_evict(cache, table, lens, mass, budget, recent, to)
+    new, device, wide = torch.empty_strided, cache.device, to.shape[1] * page
+    lens_out = new((B,), (1,), dtype=i32, device=device)
+    mass_out = new((B, heads, wide), (heads * wide, wide, 1), dtype=f32, device=device)
+    ids = new((B, heads, budget), (heads * budget, budget, 1), dtype=i32, device=device)
+    _check(load().qmm_cache_evict(c, mass.data_ptr(), mass.shape[2], budget, recent, to.data_ptr(), to.shape[1],
+                                  lens_out.data_ptr(), mass_out.data_ptr(), wide, ids.data_ptr(),
+                                  torch._C._cuda_getCurrentRawStream(index)), "qmm_cache_evict")
+    _written(torch, cache)
+    return lens_out, mass_out, ids
 
 
 def version() -> str:

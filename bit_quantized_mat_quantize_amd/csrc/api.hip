@@ -5,7 +5,8 @@
 // no GPU to be tested.  Valid calls dispatch to the kernel families in
 // quantize.hip, repack.hip, gemv.hip, skinny.hip, gemm.hip, q6k.hip,
 // q6k_gemm.hip, q2k.hip, q2k_gemm.hip, q40_gemm.hip, moe.hip, embed.hip,
-// lora.hip and logprobs.hip.
+// lora.hip, logprobs.hip, rope.hip, kv_cache.hip, attention.hip and evict.hip.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -872,6 +873,101 @@ size_t head_row_bytes(int64_t N, int64_t k) {
     return head_logit_bytes(N) + ((size_t)qmm::logprobs_workspace_bytes(1, N, k) + 15) / 16 * 16;
 }
 
+// ---- between the projections
+constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxSeqs = 65536, kMaxHeads = 1024, kMaxPositions = int64_t(1) << 30;
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // workgroups of 256 threads of one launch
+
+// Two sets of rows of n elements, `ld` elements apart, that share no element although their ranges overlap: column
+// ranges of one matrix.
+bool rows_apart(const void *a, int64_t ld_a, int64_t n_a, const void *b, int64_t ld_b, int64_t n_b, size_t size) {
+    if (ld_a != ld_b) return false;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    const bool a_first = p < q;
+    const uintptr_t by = a_first ? q - p : p - q;
+    if (by % size) return false;
+    const int64_t at = (int64_t)(by / size % (uintptr_t)ld_a);
+    return at >= (a_first ? n_a : n_b) && at <= ld_a - (a_first ? n_b : n_a);
+}
+
+int log2_of(int64_t v) {
+    int n = 0;
+    while ((int64_t(1) << n) < v) ++n;
+    return n;
+}
+bool cache_page_ok(int64_t page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
+bool cache_dim_ok(int64_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
+
+// everything of a cache but its rows and starts; `view` is what the kernels get
+qmm_status check_cache(const qmm_cache *c, qmm::KvCache &view) {
+    if (c == nullptr) return fail(QMM_EINVAL, "the cache is NULL");
+    if (!cache_page_ok(c->page))
+        return fail(QMM_EUNSUPPORTED, "pages of %lld entries; 16, 32, .. 1024", (long long)c->page);
+    if (!cache_dim_ok(c->dim))
+        return fail(QMM_EUNSUPPORTED, "heads of %lld elements; 64, 96, 128, 192 or 256", (long long)c->dim);
+    if (c->heads < 1 || c->heads > kMaxHeads)
+        return fail(QMM_EUNSUPPORTED, "%lld heads; 1 to %lld", (long long)c->heads, (long long)kMaxHeads);
+    if (c->pages < 1 || c->pages >= int64_t(1) << 31)
+        return fail(QMM_EUNSUPPORTED, "%lld pages; 1 to 2^31 - 1", (long long)c->pages);
+    if (c->seqs < 0) return fail(QMM_EINVAL, "seqs = %lld is negative", (long long)c->seqs);
+    if (c->seqs > kMaxSeqs)
+        return fail(QMM_EUNSUPPORTED, "seqs = %lld exceeds the limit %lld", (long long)c->seqs, (long long)kMaxSeqs);
+    if (c->width < 1 || c->width > kMaxPositions / c->page)
+        return fail(QMM_EUNSUPPORTED, "tables of %lld pages of %lld entries; 1 page to 2^30 entries", (long long)c->width,
+                    (long long)c->page);
+    if (c->seqs == 0) return QMM_OK;
+    QMM_TRY(check_ptr("the cache", c->data));
+    QMM_TRY(check_ptr("table", c->table));
+    QMM_TRY(check_ptr("lens", c->lens));
+    QMM_TRY(check_size("the cache", c->bytes, qmm_cache_bytes(c->pages, c->page, c->heads, c->dim)));
+    view.data = static_cast<uint8_t *>(c->data);
+    view.table = c->table;
+    view.lens = c->lens;
+    view.starts = nullptr;
+    view.pages = (int)c->pages;
+    view.page_log2 = log2_of(c->page);
+    view.heads = (int)c->heads;
+    view.D = (int)c->dim;
+    view.B = (int)c->seqs;
+    view.width = (int)c->width;
+    view.T = 0;
+    return QMM_OK;
+}
+
+qmm_status check_cache_rows(const qmm_cache *c, qmm::KvCache &view) {
+    QMM_TRY(check_cache(c, view));
+    if (c->rows < 0) return fail(QMM_EINVAL, "rows = %lld is negative", (long long)c->rows);
+    if (c->rows > kMaxTokens)
+        return fail(QMM_EUNSUPPORTED, "rows = %lld exceeds the limit %lld", (long long)c->rows, (long long)kMaxTokens);
+    if (c->starts == nullptr && c->rows != c->seqs)
+        return fail(QMM_EINVAL, "without starts every sequence has one row: rows = %lld, seqs = %lld", (long long)c->rows,
+                    (long long)c->seqs);
+    if (c->rows == 0 || c->seqs == 0) return QMM_OK;
+    if (c->starts != nullptr) QMM_TRY(check_ptr("starts", c->starts));
+    view.starts = c->starts;
+    view.T = (int)c->rows;
+    return QMM_OK;
+}
+
+// the arrays of a cache against an output (the cache itself where it is not what is written)
+bool overlaps_cache(const qmm_cache *c, const void *p, size_t bytes, bool data, bool rows) {
+    return (data && overlap(p, bytes, c->data, qmm_cache_bytes(c->pages, c->page, c->heads, c->dim))) ||
+           overlap(p, bytes, c->table, (size_t)(c->seqs * c->width) * sizeof(int32_t)) ||
+           overlap(p, bytes, c->lens, (size_t)c->seqs * sizeof(int32_t)) ||
+           (rows && c->starts != nullptr && overlap(p, bytes, c->starts, (size_t)(c->seqs + 1) * sizeof(int32_t)));
+}
+
+// rows of n elements that start on 16 bytes
+qmm_status check_strided(const char *name, const void *p, size_t bytes, int64_t rows, int64_t ld, int64_t n, size_t size) {
+    if (ld < n) return fail(QMM_EINVAL, "%s: %lld elements from a row to the next, rows of %lld", name, (long long)ld, (long long)n);
+    if (ld > kMaxLd) return fail(QMM_EUNSUPPORTED, "%s: %lld elements from a row to the next", name, (long long)ld);
+    QMM_TRY(check_ptr(name, p));
+    if ((size_t)ld * size % 16 != 0)
+        return fail(QMM_EALIGN, "%s: rows %lld elements apart do not start on 16 bytes", name, (long long)ld);
+    return check_size(name, bytes, strided_bytes(rows, ld, n, size));
+}
+
+const char *float_name(qmm_float_type t) { return t == QMM_F32 ? "fp32" : t == QMM_F16 ? "fp16" : "bf16"; }
+
 }  // namespace
 
 extern "C" {
@@ -1061,6 +1157,250 @@ qmm_status qmm_mul_mat_logprobs(qmm_weight_type t, const void *w, size_t w_bytes
         }
     }
     return QMM_OK;
+}
+
+qmm_status qmm_rope(qmm_float_type t, const void *x, size_t x_bytes, int64_t ld_x, int64_t head_x,
+                    const int32_t *positions, const float *factors, void *out, size_t out_bytes, int64_t ld_out,
+                    int64_t head_out, int64_t T, int64_t H, int64_t D, int64_t rot, int interleaved, double base,
+                    double freq_scale, double ramp_low, double ramp_high, double magnitude, void *stream) {
+    const size_t size = float_size(t);
+    if (!size) return fail(QMM_EUNSUPPORTED, "unknown type %d", (int)t);
+    if (T < 0) return fail(QMM_EINVAL, "T = %lld is negative", (long long)T);
+    if (T > kMaxTokens) return fail(QMM_EUNSUPPORTED, "T = %lld exceeds the limit %lld", (long long)T, (long long)kMaxTokens);
+    if (H < 1 || H > 65536) return fail(QMM_EUNSUPPORTED, "H = %lld heads; 1 to 65536", (long long)H);
+    if (D < 2 || D > qmm::rope_max_dim())
+        return fail(QMM_EUNSUPPORTED, "D = %lld; 2 to %lld", (long long)D, (long long)qmm::rope_max_dim());
+    if (rot < 2 || rot > D || rot % 2) return fail(QMM_EUNSUPPORTED, "rot = %lld; even, 2 to D", (long long)rot);
+    if (!(base > 0.0 && base <= 1e30)) return fail(QMM_EINVAL, "base = %g; 0 < base <= 1e30", base);
+    if (!(freq_scale >= 0.0 && freq_scale <= 1e30)) return fail(QMM_EINVAL, "freq_scale = %g; 0 <= freq_scale <= 1e30", freq_scale);
+    if (!(ramp_low > -1e30 && ramp_low < 1e30 && ramp_high > -1e30 && ramp_high < 1e30))
+        return fail(QMM_EINVAL, "ramp %g to %g", ramp_low, ramp_high);
+    if (!(magnitude >= -1e30 && magnitude <= 1e30)) return fail(QMM_EINVAL, "magnitude = %g", magnitude);
+    if (T == 0) return QMM_OK;
+    if (head_x < 0 || ld_x < 0) return fail(QMM_EINVAL, "strides of x below 0");
+    if (head_x > kMaxLd || ld_x > kMaxLd || head_out > kMaxLd || ld_out > kMaxLd)
+        return fail(QMM_EUNSUPPORTED, "a stride exceeds the limit %lld", (long long)kMaxLd);
+    const int64_t token = (H - 1) * head_out + D, head = (T - 1) * ld_out + D;  // spans of a token's heads, a head's tokens
+    if (head_out < 0 || ld_out < 0 || (H > 1 && head_out < D) || (T > 1 && ld_out < D) || (H > 1 && T > 1 && ld_out < token && head_out < head))
+        return fail(QMM_EINVAL, "out's rows overlap: %lld elements from a token to the next, %lld from a head to the next",
+                    (long long)ld_out, (long long)head_out);
+    QMM_TRY(check_ptr("x", x));
+    QMM_TRY(check_ptr("positions", positions));
+    if (factors != nullptr) QMM_TRY(check_ptr("factors", factors));
+    QMM_TRY(check_ptr("out", out));
+    const size_t x_need = (size_t)((T - 1) * ld_x + (H - 1) * head_x + D) * size;
+    const size_t out_need = (size_t)((T - 1) * ld_out + token) * size;
+    QMM_TRY(check_size("x", x_bytes, x_need));
+    QMM_TRY(check_size("out", out_bytes, out_need));
+    const bool in_place = out == x && ld_out == ld_x && head_out == head_x;
+    const int64_t x_token = (H - 1) * head_x + D;
+    const bool apart = ld_x >= x_token && ld_out >= token && rows_apart(x, ld_x, x_token, out, ld_out, token, size);
+    if (!in_place && !apart && overlap(out, out_need, x, x_need))
+        return fail(QMM_EINVAL, "out overlaps x without being x (same pointer and strides)");
+    if (overlap(out, out_need, positions, (size_t)T * sizeof(int32_t)) ||
+        (factors != nullptr && overlap(out, out_need, factors, (size_t)(rot / 2) * sizeof(float))))
+        return fail(QMM_EINVAL, "out overlaps positions or factors");
+    qmm::RopeArgs a{};
+    a.x = x;
+    a.out = out;
+    a.positions = positions;
+    a.factors = factors;
+    a.ld_x = ld_x;
+    a.ld_out = ld_out;
+    a.head_x = head_x;
+    a.head_out = head_out;
+    a.T = (int)T;
+    a.H = (int)H;
+    a.D = (int)D;
+    a.rot = (int)rot;
+    a.log2_base = log2(base);
+    a.freq_scale = freq_scale;
+    a.low = ramp_low;
+    a.high = ramp_high;
+    a.magnitude = magnitude;
+    if (log_enabled())
+        fprintf(stderr, "qmm: rope %s T=%lld H=%lld D=%lld rot=%lld %s%s\n", float_name(t), (long long)T, (long long)H,
+                (long long)D, (long long)rot, interleaved ? "interleaved" : "halves", in_place ? ", in place" : "");
+    return device_status(qmm::launch_rope((int)t, interleaved != 0, a, static_cast<hipStream_t>(stream)), "rope launch");
+}
+
+size_t qmm_cache_bytes(int64_t pages, int64_t page, int64_t heads, int64_t dim) {
+    if (pages < 1 || pages >= int64_t(1) << 31 || !cache_page_ok(page) || heads < 1 || heads > kMaxHeads || !cache_dim_ok(dim))
+        return 0;
+    return (size_t)(pages * 2 * heads) * (size_t)(page * (dim * 9 / 16));
+}
+
+qmm_status qmm_cache_write(const qmm_cache *c, qmm_float_type t, const void *k, size_t k_bytes, int64_t ld_k,
+                           const void *v, size_t v_bytes, int64_t ld_v, void *stream) {
+    const size_t size = float_size(t);
+    if (!size) return fail(QMM_EUNSUPPORTED, "unknown type %d", (int)t);
+    qmm::KvCache view{};
+    QMM_TRY(check_cache_rows(c, view));
+    if (c->rows == 0 || c->seqs == 0) return QMM_OK;
+    const int64_t n = c->heads * c->dim;
+    QMM_TRY(check_strided("k", k, k_bytes, c->rows, ld_k, n, size));
+    QMM_TRY(check_strided("v", v, v_bytes, c->rows, ld_v, n, size));
+    const size_t need = qmm_cache_bytes(c->pages, c->page, c->heads, c->dim);
+    if (overlap(c->data, need, k, strided_bytes(c->rows, ld_k, n, size)) ||
+        overlap(c->data, need, v, strided_bytes(c->rows, ld_v, n, size)) || overlaps_cache(c, c->data, need, false, true))
+        return fail(QMM_EINVAL, "the cache overlaps k, v, table, lens or starts");
+    if (log_enabled())
+        fprintf(stderr, "qmm: cache_write %s rows=%lld seqs=%lld heads=%lld dim=%lld page=%lld\n", float_name(t),
+                (long long)c->rows, (long long)c->seqs, (long long)c->heads, (long long)c->dim, (long long)c->page);
+    return device_status(qmm::launch_cache_write((int)t, view, k, ld_k, v, ld_v, static_cast<hipStream_t>(stream)),
+                         "cache_write launch");
+}
+
+qmm_status qmm_cache_read(const qmm_cache *c, qmm_float_type t, void *k, size_t k_bytes, void *v, size_t v_bytes,
+                          void *stream) {
+    const size_t size = float_size(t);
+    if (!size) return fail(QMM_EUNSUPPORTED, "unknown type %d", (int)t);
+    qmm::KvCache view{};
+    QMM_TRY(check_cache_rows(c, view));
+    if (c->rows == 0 || c->seqs == 0) return QMM_OK;
+    const size_t need = (size_t)(c->rows * c->heads * c->dim) * size;
+    QMM_TRY(check_ptr("k", k));
+    QMM_TRY(check_ptr("v", v));
+    QMM_TRY(check_size("k", k_bytes, need));
+    QMM_TRY(check_size("v", v_bytes, need));
+    if (overlap(k, need, v, need) || overlaps_cache(c, k, need, true, true) || overlaps_cache(c, v, need, true, true))
+        return fail(QMM_EINVAL, "k or v overlaps the other one, the cache, table, lens or starts");
+    if (log_enabled())
+        fprintf(stderr, "qmm: cache_read %s rows=%lld seqs=%lld heads=%lld dim=%lld page=%lld\n", float_name(t),
+                (long long)c->rows, (long long)c->seqs, (long long)c->heads, (long long)c->dim, (long long)c->page);
+    return device_status(qmm::launch_cache_read((int)t, view, k, v, static_cast<hipStream_t>(stream)), "cache_read launch");
+}
+
+size_t qmm_cache_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t dim, int64_t seqs,
+                                           int64_t width, int64_t page, int ragged, int mass) {
+    if (rows < 1 || rows > kMaxTokens || heads < 1 || heads > kMaxHeads || q_heads < heads || q_heads > kMaxHeads ||
+        q_heads % heads || !cache_dim_ok(dim) || !cache_page_ok(page) || seqs < 1 || seqs > kMaxSeqs || width < 1 ||
+        width > kMaxPositions / page)
+        return 0;
+    return (size_t)qmm::attend_workspace_bytes(rows, seqs, width * page, heads, q_heads / heads, dim, ragged != 0, mass != 0);
+}
+
+qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void *q, size_t q_bytes, int64_t ld_q,
+                               int64_t q_heads, void *out, size_t out_bytes, int64_t ld_out, float scale, int causal,
+                               int64_t window, float *lse, float *mass, int64_t ld_mass, void *workspace,
+                               size_t ws_bytes, void *stream) {
+    const size_t size = float_size(t);
+    if (!size) return fail(QMM_EUNSUPPORTED, "unknown type %d", (int)t);
+    qmm::AttendArgs a{};
+    QMM_TRY(check_cache_rows(c, a.c));
+    if (q_heads < c->heads || q_heads > kMaxHeads || q_heads % c->heads)
+        return fail(QMM_EUNSUPPORTED, "%lld query heads over %lld cache heads: a multiple of these, at most %lld",
+                    (long long)q_heads, (long long)c->heads, (long long)kMaxHeads);
+    if (!(scale >= -1e30f && scale <= 1e30f)) return fail(QMM_EINVAL, "scale = %g", (double)scale);
+    if (window < 0) return fail(QMM_EINVAL, "window = %lld is negative", (long long)window);
+    if (window > 0 && !causal) return fail(QMM_EUNSUPPORTED, "a window of what is not causal");
+    if (c->rows == 0 || c->seqs == 0) return QMM_OK;
+    const int64_t n = q_heads * c->dim, capacity = c->width * c->page;
+    QMM_TRY(check_strided("q", q, q_bytes, c->rows, ld_q, n, size));
+    QMM_TRY(check_strided("out", out, out_bytes, c->rows, ld_out, n, size));
+    if (lse != nullptr) QMM_TRY(check_ptr("lse", lse));
+    if (mass != nullptr) {
+        QMM_TRY(check_ptr("mass", mass));
+        QMM_TRY(check_ld("ld_mass", ld_mass, capacity));
+    }
+    const size_t ws_need = qmm_cache_attention_workspace_bytes(c->rows, q_heads, c->heads, c->dim, c->seqs, c->width,
+                                                               c->page, c->starts != nullptr, mass != nullptr);
+    if (ws_need != 0) {
+        QMM_TRY(check_ptr("workspace", workspace));
+        QMM_TRY(check_size("workspace", ws_bytes, ws_need));
+    }
+    const Span outs[] = {{out, strided_bytes(c->rows, ld_out, n, size)},
+                         {lse, lse != nullptr ? (size_t)(c->rows * q_heads) * sizeof(float) : 0},
+                         {mass, mass != nullptr ? strided_bytes(c->seqs * c->heads, ld_mass, capacity, sizeof(float)) : 0},
+                         {workspace, ws_need}};
+    const size_t q_need = strided_bytes(c->rows, ld_q, n, size);
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps_cache(c, outs[i].p, outs[i].bytes, true, true))
+            return fail(QMM_EINVAL, "an output or the workspace overlaps the cache, table, lens or starts");
+        if (overlap(outs[i].p, outs[i].bytes, q, q_need) && !(i == 0 && rows_apart(q, ld_q, n, out, ld_out, n, size)))
+            return fail(QMM_EINVAL, "an output or the workspace overlaps q");
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return fail(QMM_EINVAL, "an output overlaps another one or the workspace");
+    }
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.mass = mass;
+    a.ws = static_cast<float *>(workspace);
+    a.ld_q = ld_q;
+    a.ld_out = ld_out;
+    a.ld_mass = ld_mass;
+    a.scale = (float)((double)scale * 1.4426950408889634074);  // log2 e
+    a.group = (int)(q_heads / c->heads);
+    a.window = (int)(window > kMaxPositions ? 0 : window);
+    a.causal = causal != 0;
+    if (!qmm::attend_grid_ok(a))
+        return fail(QMM_EUNSUPPORTED, "rows = %lld, seqs = %lld, heads = %lld need more than %lld workgroups",
+                    (long long)c->rows, (long long)c->seqs, (long long)c->heads, (long long)kMaxBlocks);
+    if (log_enabled()) {
+        int splits;
+        qmm::attend_shape(a, &splits);
+        fprintf(stderr, "qmm: cache_attention %s rows=%lld seqs=%lld heads=%lld/%lld dim=%lld page=%lld -> %d split(s)%s\n",
+                float_name(t), (long long)c->rows, (long long)c->seqs, (long long)q_heads, (long long)c->heads,
+                (long long)c->dim, (long long)c->page, splits, mass != nullptr ? ", mass" : "");
+    }
+    return device_status(qmm::launch_attend((int)t, a, static_cast<hipStream_t>(stream)), "cache_attention launch");
+}
+
+qmm_status qmm_cache_evict(const qmm_cache *c, const float *mass, int64_t ld_mass, int64_t budget, int64_t recent,
+                           const int32_t *to, int64_t to_width, int32_t *lens_out, float *mass_out, int64_t ld_out,
+                           int32_t *ids, void *stream) {
+    qmm::EvictArgs a{};
+    QMM_TRY(check_cache(c, a.c));
+    if (budget < 1 || budget > kMaxPositions)
+        return fail(QMM_EUNSUPPORTED, "budget = %lld; 1 to 2^30", (long long)budget);
+    if (recent < 0 || recent > budget) return fail(QMM_EINVAL, "recent = %lld; 0 to the budget", (long long)recent);
+    if (to_width < 1 || to_width > kMaxPositions / c->page || to_width * c->page < budget)
+        return fail(QMM_EINVAL, "to has room for %lld pages; at least %lld entries are needed", (long long)to_width,
+                    (long long)budget);
+    if (c->seqs == 0) return QMM_OK;
+    if (c->seqs * c->heads >= int64_t(1) << 21)
+        return fail(QMM_EUNSUPPORTED, "seqs * heads = %lld; below 2^21", (long long)(c->seqs * c->heads));
+    QMM_TRY(check_ld("ld_mass", ld_mass, c->width * c->page));
+    QMM_TRY(check_ld("ld_out", ld_out, budget));
+    QMM_TRY(check_ptr("mass", mass));
+    QMM_TRY(check_ptr("to", to));
+    QMM_TRY(check_ptr("lens_out", lens_out));
+    QMM_TRY(check_ptr("mass_out", mass_out));
+    QMM_TRY(check_ptr("ids", ids));
+    const int64_t rows = c->seqs * c->heads;
+    const Span in[] = {{mass, strided_bytes(rows, ld_mass, c->width * c->page, sizeof(float))},
+                       {to, (size_t)(c->seqs * to_width) * sizeof(int32_t)}};
+    const Span outs[] = {{c->data, qmm_cache_bytes(c->pages, c->page, c->heads, c->dim)},
+                         {lens_out, (size_t)c->seqs * sizeof(int32_t)},
+                         {mass_out, (size_t)(rows * ld_out) * sizeof(float)},
+                         {ids, (size_t)(rows * budget) * sizeof(int32_t)}};
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps_cache(c, outs[i].p, outs[i].bytes, false, false))
+            return fail(QMM_EINVAL, "an output or the cache overlaps table or lens");
+        for (const Span &s : in)
+            if (overlap(outs[i].p, outs[i].bytes, s.p, s.bytes))
+                return fail(QMM_EINVAL, "an output or the cache overlaps mass or to");
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return fail(QMM_EINVAL, "an output overlaps another one or the cache");
+    }
+    a.mass = mass;
+    a.to = to;
+    a.lens_out = lens_out;
+    a.mass_out = mass_out;
+    a.ids = ids;
+    a.ld_mass = ld_mass;
+    a.ld_out = ld_out;
+    a.to_width = (int)to_width;
+    a.budget = (int)budget;
+    a.recent = (int)recent;
+    if (log_enabled())
+        fprintf(stderr, "qmm: cache_evict seqs=%lld heads=%lld dim=%lld page=%lld budget=%lld recent=%lld%s\n",
+                (long long)c->seqs, (long long)c->heads, (long long)c->dim, (long long)c->page, (long long)budget,
+                (long long)recent, to == c->table ? ", in place" : "");
+    return device_status(qmm::launch_cache_evict(a, static_cast<hipStream_t>(stream)), "cache_evict launch");
 }
 
 const char *qmm_status_string(qmm_status s) {

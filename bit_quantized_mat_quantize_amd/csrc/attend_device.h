@@ -1,0 +1,87 @@
+// attend_device.h -- what the attention kernels share: the rows of a tile, query
+// fragments, the running normalisation of values, partial results.
+//
+// Scores are kept in units of log 2: x = log2(e) * scale * q.k.  A tile's weights are
+// p = 2^(x - r + 8) with r a row's reference, at most 6 below its largest score so far:
+// r moves (and what is summed is rescaled) only when a score passes r + 6, which
+// after the first tiles is seldom, and p stays within fp16 (2^14) with 2^-24 of
+// the largest left at its end.
+#pragma once
+
+#include "kv_device.h"
+
+namespace qmm {
+
+constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kBias = 8.0f, kSlack = 6.0f;
+
+// log2 of 0 and of sums in fp32
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
+
+// positions [lo, hi) of the keys that row i (of count, length len) sees
+__device__ __forceinline__ void attend_span(const AttendArgs &a, const KvRows &rows, int i, int &lo, int &hi) {
+    const int pos = rows.len - rows.count + i;
+    hi = a.causal ? pos + 1 : rows.len;
+    hi = hi > rows.len ? rows.len : hi;
+    lo = a.window > 0 && pos + 1 > a.window ? pos + 1 - a.window : 0;
+}
+
+// 2^e as a float, |e| <= 126
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// A query row's power of two: its largest magnitude's exponent becomes 12, so that fp16
+// pieces of it keep what fp32 holds (two) or the type itself (one), down to 2^-24 of
+// the row's largest.  `top`: the largest |q| bits of the row (an infinity or NaN: 255).
+__device__ __forceinline__ int query_shift(uint32_t top) {
+    const int e = (int)(top >> 23) - 127;  // zero and subnormals: -127
+    return e < -114 ? 126 : 12 - e;
+}
+
+// elements of a word as the cache's pairs hold them: 0 4 1 5 2 6 3 7
+template <int PIECES>
+__device__ __forceinline__ void query_pieces(const float *x, float by, h8 &hi, h8 &lo) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float v = x[(i >> 1) + 4 * (i & 1)] * by;
+        hi[i] = (_Float16)v;
+        if constexpr (PIECES == 2) lo[i] = (_Float16)(v - (float)hi[i]);
+    }
+}
+
+// eight codes of a word, exact
+__device__ __forceinline__ h8 key_codes(uint32_t w) {
+    const h2 a = kv_pair(w), b = kv_pair(w >> 4), c = kv_pair(w >> 8), d = kv_pair(w >> 12);
+    return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// max over the wavefront of two 16-bit values per lane
+__device__ __forceinline__ uint32_t wave_max_u16x2(uint32_t v) {
+    uint32_t m = (v & 0xffffu) > (v >> 16) ? v & 0xffffu : v >> 16;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        const uint32_t u = __shfl_xor(m, o, 64);
+        m = u > m ? u : m;
+    }
+    return m;
+}
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
+// The power of two that value scales are multiplied by, from the largest scale's bits:
+// its exponent becomes 11 (products with codes stay within fp16, two pieces of them keep
+// everything down to 2^-40 of the largest); at most 2^15.
+__device__ __forceinline__ int value_shift(uint32_t top) {
+    const int e = (int)(top >> 10);
+    return e < 11 ? 15 : 26 - e;
+}
+
+// ---- partial results of a split: [split][row][D] sums, [split][row] (reference, sum)
+struct AttendPartial {
+    float *sums;
+    float2 *stats;
+};
+
+}  // namespace qmm

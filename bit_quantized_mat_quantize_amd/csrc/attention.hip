@@ -1,0 +1,619 @@
+// attention.hip -- attention over the paged 4-bit cache, few rows per sequence
+// (gfx950): one token, or a few, of each sequence against all its entries.
+//
+// A workgroup takes one tile of 16 query rows (row = token * group + head of the
+// group, so that one read of an entry serves the whole group), one cache head and
+// one split of the entries; its four wavefronts take 32 entries each in turn, straight
+// from memory into registers, and are joined at the end.  Per 32 entries:
+//
+//   S^T = K Q^T     16 entries x 16 rows per matrix instruction, one per block of 32
+//                   elements: the codes are exact in fp16, the block's scale multiplies
+//                   the fp32 result.  fp32 queries are two fp16 pieces (22 bits).
+//   O^T += V^T P^T  a lane holds eight entries' words of the same eight elements, so the
+//                   codes are transposed by byte permutes within the lane; code * scale
+//                   is rounded to fp16 for 16-bit queries, and cut in two exact pieces for
+//                   fp32 ones, as p is.
+//
+// In both products the entries lie along the registers of a lane and the rows along
+// the lanes, so softmax needs no exchange between lanes, and P goes from one product
+// to the next as it is.
+//
+// An entry whose page is not in the pool, or that has a NaN scale, makes the rows that
+// see it NaN: its score becomes NaN and its values 0, so that rows that do not see it
+// are not touched.
+#include "attend_device.h"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 256, kWaves = 4;
+constexpr int kRows = 16;  // query rows of a tile
+constexpr int kKeys = 32;  // entries of a wavefront's step
+
+__device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// What a lane reads of 32 entries.  Lane (n, g), n = lane & 15, g = lane >> 4:
+//   k[s]  words (b, g) of all blocks b of entry 16 s + n
+//   v[s]  words n (and 16 + n for D > 128) of the entries 16 s + 4 g .. + 3
+//   ks[s] the key scales of these four entries, block by block; vs[s] the value scales of
+//         the blocks that hold word n (and 16 + n)
+template <int D>
+struct Step {
+    static constexpr int NB = D / 32, ROUNDS = D > 128 ? 2 : 1;
+    uint32_t k[2][NB];
+    uint4 v[2][ROUNDS];
+    uint2 ks[2][NB], vs[2][ROUNDS];
+    int bad;  // bit s: entries 16 s .. 16 s + 15 have no page
+};
+
+template <int D>
+__device__ __forceinline__ void read_step(const KvCache &c, int b, int head, int k0, int last, Step<D> &t) {
+    constexpr int NB = Step<D>::NB, ROUNDS = Step<D>::ROUNDS, WORDS = D / 8;
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    t.bad = 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        int at = k0 + 16 * s;
+        at = at > last ? last : at;  // the last 16 entries that hold anything
+        int page = kv_page(c, b, at);
+        if (page < 0) t.bad |= 1 << s;
+        page = page < 0 ? 0 : page;
+        const uint8_t *kc = kv_chunk(c, page, 0, head), *vc = kv_chunk(c, page, 1, head);
+        const int e0 = at & ((1 << c.page_log2) - 1);
+        const uint32_t *kw = reinterpret_cast<const uint32_t *>(kc) + (e0 + n) * WORDS + g * NB;
+        if constexpr (NB % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < NB / 4; ++i) {
+                const uint4 u = ld16(kw + 4 * i);
+                t.k[s][4 * i] = u.x, t.k[s][4 * i + 1] = u.y, t.k[s][4 * i + 2] = u.z, t.k[s][4 * i + 3] = u.w;
+            }
+        } else if constexpr (NB % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(kw + 2 * i);
+                t.k[s][2 * i] = u.x, t.k[s][2 * i + 1] = u.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) t.k[s][i] = kw[i];
+        }
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int w = (16 * r + n) % WORDS;
+            t.v[s][r] = ld16(reinterpret_cast<const uint32_t *>(vc) + kv_value_word(D, e0 + 4 * g, w));
+            t.vs[s][r] = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(vc) + kv_scale_at(c, e0 + 4 * g, w >> 2));
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            t.ks[s][i] = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(kc) + kv_scale_at(c, e0 + 4 * g, i));
+    }
+}
+
+// scores of 32 entries: x[4 s + r] is entry 16 s + 4 g + r against row n
+template <int PIECES, int D>
+__device__ __forceinline__ void scores(const Step<D> &t, const h8 (&qh)[D / 32], const h8 (&ql)[D / 32], float factor,
+                                       float *x) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        f4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            const h8 codes = key_codes(t.k[s][b]);
+            f4 dot = mfma16(codes, qh[b], f4{0, 0, 0, 0});
+            if constexpr (PIECES == 2) dot = mfma16(codes, ql[b], dot);
+            const h2 d0 = as_h2(t.ks[s][b].x), d1 = as_h2(t.ks[s][b].y);
+            acc[0] = fmaf((float)d0.x, dot[0], acc[0]);
+            acc[1] = fmaf((float)d0.y, dot[1], acc[1]);
+            acc[2] = fmaf((float)d1.x, dot[2], acc[2]);
+            acc[3] = fmaf((float)d1.y, dot[3], acc[3]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * s + r] = (t.bad >> s) & 1 ? __builtin_nanf("") : acc[r] * factor;
+    }
+}
+
+// A tile's rows and the queries of this lane's row
+template <int PIECES, int D>
+struct Tile {
+    KvRows rows;
+    int b, row;        // sequence; this lane's row of it, token * group + head
+    bool live;         // the row exists
+    int lo, hi;        // entries that it sees
+    int first, last;   // entries that any row of the tile sees: [first, last)
+    int all_lo, all_hi;  // entries that every row sees
+    float factor;      // of the dot products of codes, to log2 units
+    int64_t out_row;   // row * heads of the batch
+    h8 qh[D / 32], ql[D / 32];
+
+    __device__ __forceinline__ bool open(const AttendArgs &a, int seq, int tile, int head) {
+        b = seq;
+        rows = kv_rows(a.c, b);
+        const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, total = rows.count * a.group;
+        const int r0 = tile * kRows;
+        if (r0 >= total) return false;
+        const int r1 = r0 + kRows - 1 < total ? r0 + kRows - 1 : total - 1;
+        row = r0 + n;
+        live = row < total;
+        const int use = live ? row : r1, token = use / a.group, h = use - token * a.group;
+        attend_span(a, rows, token, lo, hi);
+        attend_span(a, rows, r0 / a.group, first, all_hi);
+        attend_span(a, rows, r1 / a.group, all_lo, last);
+        const int qh_head = head * a.group + h;
+        out_row = (int64_t)(rows.first + token) * (a.c.heads * a.group) + qh_head;
+        const int64_t at = (int64_t)(rows.first + token) * a.ld_q + (int64_t)qh_head * D + 8 * g;
+        float x[D / 32][8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            kv_load8(type, a.q, at + 32 * i, x[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t u = __float_as_uint(x[i][j]) & 0x7fffffffu;
+                top = u > top ? u : top;
+            }
+        }
+        for (int o = 16; o < 64; o <<= 1) {
+            const uint32_t u = __shfl_xor(top, o, 64);
+            top = u > top ? u : top;
+        }
+        const int shift = query_shift(top);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) query_pieces<PIECES>(x[i], pow2i(shift), qh[i], ql[i]);
+        factor = (top >> 23) == 255 ? __builtin_nanf("") : a.scale * pow2i(-shift);
+        return true;
+    }
+    int type;
+};
+
+// One wavefront's running result: row n, elements 8 w + j at sums[r][w's round][j] ...
+template <int D>
+struct Running {
+    static constexpr int ROUNDS = Step<D>::ROUNDS;
+    f4 o[ROUNDS][8];   // o[round][j][r]: element 8 * (16 * round + 4 g + r) + j
+    float ref, sum;    // the row's reference; this lane's part of the sum of p
+    uint32_t bound;    // value scales up to these bits need no other power of two
+    int shift;         // o holds sums times 2^shift
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[r][j] = f4{0, 0, 0, 0};
+        ref = -INFINITY;
+        sum = 0.0f;
+        bound = 0;
+        shift = 15;
+    }
+    __device__ __forceinline__ void scale(float by) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[r][j] *= by;
+    }
+};
+
+// MASKED: some row does not see some entry of the step
+template <int PIECES, int D>
+__device__ __forceinline__ void step(Step<D> &t, const Tile<PIECES, D> &q, int k0, bool masked, Running<D> &run) {
+    constexpr int ROUNDS = Step<D>::ROUNDS;
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    float x[8];
+    scores<PIECES, D>(t, q.qh, q.ql, q.factor, x);
+    if (masked) {  // entries that no row sees hold anything
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = k0 + 16 * s + 4 * g + 2 * i;
+                const uint32_t keep = (at >= q.first && at < q.last ? 0xffffu : 0u) |
+                                      (at + 1 >= q.first && at + 1 < q.last ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int r = 0; r < ROUNDS; ++r) (i ? t.vs[s][r].y : t.vs[s][r].x) &= keep;
+            }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+            top = max_u16x2(top, max_u16x2(t.vs[s][r].x & 0x7fff7fffu, t.vs[s][r].y & 0x7fff7fffu));
+    if (__any((top & 0xffffu) >= run.bound || (top >> 16) >= run.bound)) {
+        // a scale beyond all so far, or one that is not finite
+        if (wave_max_u16x2(top) >= 0x7c00u) {
+            uint32_t bad = 0;  // bit 4 s + r: entry 16 s + 4 g + r
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int r = 0; r < ROUNDS; ++r) {
+                    uint32_t *u[2] = {&t.vs[s][r].x, &t.vs[s][r].y};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if ((*u[i] & 0x7c00u) == 0x7c00u) bad |= 1u << (4 * s + 2 * i), *u[i] &= 0xffff0000u;
+                        if ((*u[i] & 0x7c000000u) == 0x7c000000u) bad |= 2u << (4 * s + 2 * i), *u[i] &= 0xffffu;
+                    }
+                }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) bad |= __shfl_xor(bad, o, 64);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((bad >> i) & 1) x[i] = __builtin_nanf("");
+            top = 0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int r = 0; r < ROUNDS; ++r)
+                    top = max_u16x2(top, max_u16x2(t.vs[s][r].x & 0x7fff7fffu, t.vs[s][r].y & 0x7fff7fffu));
+        }
+        const uint32_t most = wave_max_u16x2(top);
+        if (most >= run.bound) {
+            const int shift = value_shift(most);
+            run.scale(pow2i(shift - run.shift));
+            run.shift = shift;
+            run.bound = ((most >> 10) + 1) << 10;
+        }
+    }
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
+            if (at < q.lo || at >= q.hi) x[i] = -INFINITY;
+        }
+    }
+    float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    if (__any(most > run.ref + kSlack)) {
+        for (int o = 16; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+        const float ref = fmaxf(run.ref, most), by = ref == -INFINITY ? 1.0f : exp2_fast(run.ref - ref);
+        run.scale(by);
+        run.sum *= by;
+        run.ref = ref;
+    }
+    const float from = run.ref == -INFINITY ? 0.0f : run.ref - kBias;
+    h8 ph, pl;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float p = exp2_fast(x[i] - from);
+        run.sum += p;
+        ph[i] = (_Float16)p;
+        if constexpr (PIECES == 2) pl[i] = (_Float16)(p - (float)ph[i]);
+    }
+    const _Float16 unit = (_Float16)pow2i(run.shift);
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const uint32_t w[8] = {t.v[0][r].x, t.v[0][r].y, t.v[0][r].z, t.v[0][r].w,
+                               t.v[1][r].x, t.v[1][r].y, t.v[1][r].z, t.v[1][r].w};
+        const uint32_t su[4] = {t.vs[0][r].x, t.vs[0][r].y, t.vs[1][r].x, t.vs[1][r].y};
+        h2 d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = as_h2(su[i]) * h2{unit, unit};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            h2 even[4], odd[4];  // elements 2y and 2y + 1 of the word, entries in pairs
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t both = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x0c040c00u + 0x00010001u * y);
+                even[i] = kv_pair(both);
+                odd[i] = kv_pair(both >> 4);
+            }
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                h8 vh, vl;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const h2 code = o ? odd[i] : even[i], h = code * d[i];
+                    vh[2 * i] = h.x, vh[2 * i + 1] = h.y;
+                    if constexpr (PIECES == 2) {
+                        const h2 l = __builtin_elementwise_fma(code, d[i], -h);
+                        vl[2 * i] = l.x, vl[2 * i + 1] = l.y;
+                    }
+                }
+                f4 &acc = run.o[r][2 * y + o];
+                acc = mfma16(vh, ph, acc);
+                if constexpr (PIECES == 2) {
+                    acc = mfma16(vh, pl, acc);
+                    acc = mfma16(vl, ph, acc);
+                }
+            }
+        }
+    }
+}
+
+// ---- which tile.  DIRECT: sequence x / per_seq, tile x % per_seq; else tiles of all
+// sequences in turn, sequence b's from floor(starts[b] * group / kRows) + b on (one slot a
+// sequence is at most unused).
+__device__ __forceinline__ bool find_tile(const AttendArgs &a, int x, int &b, int &tile) {
+    if (a.c.starts == nullptr) {
+        const int per = (a.group + kRows - 1) / kRows;
+        b = x / per;
+        tile = x - b * per;
+        return true;
+    }
+    auto slot = [&](int i) {
+        const int t = a.c.starts[i];
+        return (int64_t)(t < 0 ? 0 : (t > a.c.T ? a.c.T : t)) * a.group / kRows + i;
+    };
+    b = kv_last_not_above(a.c.B, x, slot);
+    if (b < 0) return false;
+    tile = x - (int)slot(b);
+    return true;
+}
+
+struct Splits {
+    int n;            // per tile
+    float *sums;      // [n][T * heads][D]
+    float2 *stats;    // [n][T * heads]: (reference - bias, sum)
+    float *lse2;      // [T * heads] in log2 units, or null
+    int64_t rows;     // T * heads
+};
+
+template <int PIECES, int D>
+__global__ __launch_bounds__(kThreads) void k_attend(AttendArgs a, Splits sp, int type) {
+    constexpr int ROUNDS = Step<D>::ROUNDS, PITCH = D + 4;
+    __shared__ float buf[2][kRows][PITCH];
+    __shared__ float2 stats[kWaves][kRows];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+    const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, split = x % sp.n;
+    int b, tile;
+    if (!find_tile(a, x / sp.n, b, tile)) return;
+    b = __builtin_amdgcn_readfirstlane(b);
+    tile = __builtin_amdgcn_readfirstlane(tile);
+    Tile<PIECES, D> q;
+    q.type = type;
+    if (!q.open(a, b, tile, head)) return;
+    Running<D> run;
+    run.clear();
+    // this split's steps of 32 entries: whole rounds of the four wavefronts
+    const int s0 = (q.first < 0 ? 0 : q.first) / kKeys, s1 = q.last > 0 ? (q.last + kKeys - 1) / kKeys : 0;
+    const int rounds = s1 > s0 ? (s1 - s0 + kWaves - 1) / kWaves : 0;
+    const int from = s0 + (int)((int64_t)rounds * split / sp.n) * kWaves, to0 = s0 + (int)((int64_t)rounds * (split + 1) / sp.n) * kWaves;
+    const int to = to0 < s1 ? to0 : s1, last16 = q.last > 0 ? (q.last - 1) & ~15 : 0;
+    int at = from + wave;
+    if (at < to) {
+        Step<D> cur, next;
+        read_step<D>(a.c, b, head, at * kKeys, last16, cur);
+        for (; at < to; at += kWaves) {
+            if (at + kWaves < to) read_step<D>(a.c, b, head, (at + kWaves) * kKeys, last16, next);
+            const int k0 = at * kKeys;
+            step<PIECES, D>(cur, q, k0, k0 < q.all_lo || k0 + kKeys > q.all_hi, run);
+            cur = next;
+        }
+    }
+    for (int o = 16; o < 64; o <<= 1) run.sum += __shfl_xor(run.sum, o, 64);
+    // the wavefronts' parts, to the largest reference
+    if (g == 0) stats[wave][n] = make_float2(run.ref, run.sum);
+    __syncthreads();
+    float ref = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) ref = fmaxf(ref, stats[w][n].x);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const float2 s = stats[w][n];
+        sum += s.x == -INFINITY ? s.y : s.y * exp2_fast(s.x - ref);  // a NaN stands in sums without a reference too
+    }
+    const float by = (run.ref == -INFINITY ? 1.0f : exp2_fast(run.ref - ref)) * pow2i(-run.shift);
+    for (int half = 2; half >= 1; half >>= 1) {  // wavefronts half .. 2 half - 1 into 0 .. half - 1
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int r = 0; r < ROUNDS; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int w = 16 * r + 4 * g + i;
+                    if (w < D / 8) {
+                        float4 *o = reinterpret_cast<float4 *>(&buf[wave - half][n][8 * w]);
+                        const float f = half == 2 || wave != 1 ? by : 1.0f;
+                        o[0] = make_float4(run.o[r][0][i] * f, run.o[r][1][i] * f, run.o[r][2][i] * f, run.o[r][3][i] * f);
+                        o[1] = make_float4(run.o[r][4][i] * f, run.o[r][5][i] * f, run.o[r][6][i] * f, run.o[r][7][i] * f);
+                    }
+                }
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int r = 0; r < ROUNDS; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int w = 16 * r + 4 * g + i;
+                    if (w < D / 8) {
+                        const float *o = &buf[wave][n][8 * w];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) run.o[r][j][i] = run.o[r][j][i] * (half == 2 ? by : 1.0f) + o[j];
+                    }
+                }
+        }
+        __syncthreads();
+    }
+    if (wave != 0 || !q.live) return;
+    const bool none = !(sum != 0.0f);  // NaN is a sum
+    if (sp.n == 1) {
+        const float inv = none ? 0.0f : 1.0f / sum, l2 = none ? -INFINITY : ref - kBias + log2_fast(sum);
+        const int64_t token = q.out_row / (a.c.heads * a.group);
+        const int64_t to_row = token * a.ld_out + (q.out_row - token * a.c.heads * a.group) * D;
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int w = 16 * r + 4 * g + i;
+                if (w < D / 8) {
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = run.o[r][j][i] * inv;
+                    kv_store8(type, a.out, to_row + 8 * w, v);
+                }
+            }
+        if (g == 0) {
+            if (a.lse != nullptr) a.lse[q.out_row] = l2 * kLn2;
+            if (sp.lse2 != nullptr) sp.lse2[q.out_row] = l2;
+        }
+    } else {
+        const int64_t row = split * sp.rows + q.out_row;
+        if (g == 0) sp.stats[row] = make_float2(ref == -INFINITY ? ref : ref - kBias, sum);
+        if (none) return;
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int w = 16 * r + 4 * g + i;
+                if (w < D / 8) {
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = run.o[r][j][i];
+                    kv_store8<0>(sp.sums, row * D + 8 * w, v);
+                }
+            }
+    }
+}
+
+// the splits of a row joined: one wavefront per row, eight elements per lane
+__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits sp, int type) {
+    const int lane = threadIdx.x & 63, D = a.c.D;
+    const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    if (row >= sp.rows) return;
+    const int heads = a.c.heads * a.group;
+    const int64_t token = row / heads;
+    const int b = kv_sequence(a.c, (int)token);
+    if (b < 0) return;  // a row of no sequence
+    float ref = -INFINITY, sum = 0.0f;
+    for (int s = lane; s < sp.n; s += 64) ref = fmaxf(ref, sp.stats[s * sp.rows + row].x);
+    for (int o = 32; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor(ref, o, 64));
+    float v[8] = {};
+    for (int s = 0; s < sp.n; ++s) {
+        const float2 st = sp.stats[s * sp.rows + row];
+        if (st.y == 0.0f) continue;  // nothing seen
+        const float by = st.x == -INFINITY ? 1.0f : exp2_fast(st.x - ref);
+        sum += st.y * by;
+        if (8 * lane < D) {
+            float u[8];
+            kv_load8<0>(sp.sums, (s * sp.rows + row) * D + 8 * lane, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = fmaf(u[j], by, v[j]);
+        }
+    }
+    const bool none = !(sum != 0.0f);
+    const float inv = none ? 0.0f : 1.0f / sum, l2 = none ? -INFINITY : ref + log2_fast(sum);
+    if (8 * lane < D) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= inv;
+        kv_store8(type, a.out, token * a.ld_out + (row - token * heads) * D + 8 * lane, v);
+    }
+    if (lane == 0) {
+        if (a.lse != nullptr) a.lse[row] = l2 * kLn2;
+        if (sp.lse2 != nullptr) sp.lse2[row] = l2;
+    }
+}
+
+// The weight that each entry got: mass[j] += sum over rows and heads of the group of
+// 2^(x - lse2).  A wavefront owns 32 entries of a head and goes over all rows that can
+// see them, 16 at a time, so every place is added to by one lane, in a fixed order.
+template <int PIECES, int D>
+__global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits sp, int type, int tiles) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+    const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, b = x / tiles;
+    const int k0 = ((x - b * tiles) * kWaves + wave) * kKeys;
+    const KvRows rows = kv_rows(a.c, b);
+    if (k0 >= rows.len || rows.count == 0) return;
+    Step<D> t;
+    read_step<D>(a.c, b, head, k0, (rows.len - 1) & ~15, t);
+    // rows that see any of these entries
+    const int shift = rows.len - rows.count;
+    int i0 = a.causal ? k0 - shift : 0, i1 = a.window > 0 ? k0 + kKeys - 1 + a.window - shift : rows.count;
+    i0 = i0 < 0 ? 0 : i0;
+    i1 = i1 > rows.count ? rows.count : i1;
+    float got[8] = {};
+    for (int tile = i0 * a.group / kRows; tile * kRows < i1 * a.group; ++tile) {
+        Tile<PIECES, D> q;
+        q.type = type;
+        if (!q.open(a, b, tile, head)) break;
+        float p[8];
+        scores<PIECES, D>(t, q.qh, q.ql, q.factor, p);
+        const float lse = sp.lse2[q.out_row];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
+            if (q.live && lse != -INFINITY && at >= q.lo && at < q.hi) got[i] += exp2_fast(p[i] - lse);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) got[i] += __shfl_xor(got[i], o, 64);
+        const int at = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
+        if (n == 0 && at < rows.len) a.mass[((int64_t)b * a.c.heads + head) * a.ld_mass + at] += got[i];
+    }
+}
+
+int64_t tiles_of(int64_t T, int64_t B, int64_t group, bool ragged) {
+    return ragged ? T * group / kRows + B : B * ((group + kRows - 1) / kRows);
+}
+
+// Workgroups per tile: two for each CU, but no split below two steps of its wavefronts
+int64_t splits_of(int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, bool ragged) {
+    const int64_t tiles = tiles_of(T, B, group, ragged) * heads;
+    const int64_t rounds = (capacity + kKeys * kWaves - 1) / (kKeys * kWaves);
+    int64_t n = (1024 + tiles - 1) / tiles;
+    n = n > rounds ? rounds : n;
+    n = n > 256 ? 256 : n;
+    return n < 1 ? 1 : n;
+}
+
+int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+template <int PIECES, int D>
+hipError_t launch(int type, const AttendArgs &a, const Splits &sp, hipStream_t s) {
+    const int64_t tiles = tiles_of(a.c.T, a.c.B, a.group, a.c.starts != nullptr);
+    hipLaunchKernelGGL((k_attend<PIECES, D>), dim3((unsigned)(tiles * sp.n * a.c.heads)), dim3(kThreads), 0, s, a, sp, type);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (sp.n > 1) {
+        hipLaunchKernelGGL(k_attend_join, dim3((unsigned)((sp.rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, s, a, sp, type);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (a.mass == nullptr) return e;
+    const int per = ((a.c.width << a.c.page_log2) + kKeys * kWaves - 1) / (kKeys * kWaves);
+    hipLaunchKernelGGL((k_attend_mass<PIECES, D>), dim3((unsigned)((int64_t)a.c.B * per * a.c.heads)), dim3(kThreads), 0, s, a,
+                       sp, type, per);
+    return hipGetLastError();
+}
+
+template <int PIECES>
+hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, hipStream_t s) {
+    switch (a.c.D) {
+        case 64: return launch<PIECES, 64>(type, a, sp, s);
+        case 96: return launch<PIECES, 96>(type, a, sp, s);
+        case 128: return launch<PIECES, 128>(type, a, sp, s);
+        case 192: return launch<PIECES, 192>(type, a, sp, s);
+        default: return launch<PIECES, 256>(type, a, sp, s);
+    }
+}
+
+}  // namespace
+
+int64_t attend_workspace_bytes(int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
+                               bool ragged, bool mass) {
+    const int64_t n = splits_of(T, B, capacity, heads, group, ragged), rows = T * heads * group;
+    return (n > 1 ? n * rows * (D * 4 + 8) : 0) + (mass ? up16(rows * 4) : 0);
+}
+
+void attend_shape(const AttendArgs &a, int *splits) {
+    *splits = (int)splits_of(a.c.T, a.c.B, (int64_t)a.c.width << a.c.page_log2, a.c.heads, a.group, a.c.starts != nullptr);
+}
+
+bool attend_grid_ok(const AttendArgs &a) {
+    constexpr int64_t most = (int64_t(1) << 24) - 1;  // workgroups of 256 threads
+    const int64_t capacity = (int64_t)a.c.width << a.c.page_log2, rows = (int64_t)a.c.T * a.c.heads * a.group;
+    const bool ragged = a.c.starts != nullptr;
+    const int64_t n = splits_of(a.c.T, a.c.B, capacity, a.c.heads, a.group, ragged);
+    return tiles_of(a.c.T, a.c.B, a.group, ragged) * n * a.c.heads <= most && (rows + kWaves - 1) / kWaves <= most &&
+           (a.mass == nullptr || a.c.B * ((capacity + kKeys * kWaves - 1) / (kKeys * kWaves)) * a.c.heads <= most);
+}
+
+hipError_t launch_attend(int type, const AttendArgs &a, hipStream_t s) {
+    Splits sp{};
+    sp.n = (int)splits_of(a.c.T, a.c.B, (int64_t)a.c.width << a.c.page_log2, a.c.heads, a.group, a.c.starts != nullptr);
+    sp.rows = (int64_t)a.c.T * a.c.heads * a.group;
+    sp.sums = a.ws;
+    sp.stats = reinterpret_cast<float2 *>(a.ws + (sp.n > 1 ? sp.n * sp.rows * a.c.D : 0));
+    sp.lse2 = a.mass != nullptr ? a.ws + (sp.n > 1 ? sp.n * sp.rows * (a.c.D + 2) : 0) : nullptr;
+    return type == 0 ? launch_for<2>(type, a, sp, s) : launch_for<1>(type, a, sp, s);
+}
+
+}  // namespace qmm

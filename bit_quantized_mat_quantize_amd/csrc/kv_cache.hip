@@ -1,0 +1,135 @@
+// kv_cache.hip -- rows of keys and values into the paged 4-bit cache, and entries
+// back as numbers (gfx950).
+//
+// A block is 32 consecutive elements of a head under the rule of the Q4_0 encoder:
+// d = -x/8 with x the element of largest magnitude (the first of equals), q =
+// clamp(rint(x * (1/d)) + 8, 0, 15), values f16(d) * (q - 8).  A block that holds an
+// infinity or NaN, or whose d passes fp16's range, gets d = NaN; where f16(d) is 0 all
+// codes are 8.
+//
+// One thread holds eight elements, which are one 32-bit word of the cache; the four
+// lanes of a block exchange their largest elements by DPP.  Keys and values of a row
+// are one run of words, so the row's reads are whole and both sides run in one
+// launch.  HBM bounds long prompts (4 or 2 bytes read per 9/16 written), the launch
+// a decode step.
+#include "kv_device.h"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// (|x|, x) of the block's element of largest magnitude, the first of equals; `bad`: any not finite
+__device__ __forceinline__ void block_top(float &a, float &x, int &bad) {
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+        const float pa = step ? dpp_f32<0x4E>(a) : dpp_f32<0xB1>(a), px = step ? dpp_f32<0x4E>(x) : dpp_f32<0xB1>(x);
+        bad |= step ? dpp_i32<0x4E>(bad) : dpp_i32<0xB1>(bad);
+        const bool mine_first = ((threadIdx.x >> step) & 1) == 0;
+        if (pa > a || (pa == a && !mine_first)) a = pa, x = px;
+    }
+}
+
+// ROWS consecutive rows of the batch per workgroup: their words of one group of four
+// values come together, so that the cache lines they share are filled at once
+template <int TYPE, int ROWS>
+__global__ __launch_bounds__(kThreads) void k_cache_write(KvCache c, const void *__restrict__ k, int64_t ld_k,
+                                                          const void *__restrict__ v, int64_t ld_v) {
+    const int words = c.heads * (c.D / 8);  // of a row's keys
+    const int u = blockIdx.y * kThreads + threadIdx.x;
+    const bool active = u < 2 * words;
+    const int part = u >= words, e = (part ? u - words : u) % (active ? words : 1);
+    const int head = e / (c.D / 8), w = e - head * (c.D / 8);
+    const void *src = part ? v : k;
+    const int64_t ld = part ? ld_v : ld_k;
+#pragma unroll 1
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = blockIdx.x * ROWS + i;
+        if (r >= c.T) return;
+        const int b = kv_sequence(c, r);
+        if (b < 0) continue;  // the whole workgroup: b depends on the row alone
+        const KvRows rows = kv_rows(c, b);
+        const int pos = rows.len - rows.count + (r - rows.first);
+        const int page = pos >= 0 ? kv_page(c, b, pos) : -1;
+        if (page < 0) continue;
+        float x[8] = {};
+        if (active) kv_load8<TYPE>(src, r * ld + (int64_t)e * 8, x);
+        float top = -1.0f, a = 0.0f;
+        int bad = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float m = fabsf(x[j]);
+            if (m > top) top = m, a = x[j];
+            bad |= !(m <= 3.402823466e38f);
+        }
+        block_top(top, a, bad);
+        const float d = 0.0f - a / 8.0f;
+        uint32_t h = f32_to_f16_bits(d);
+        if (bad || (h & 0x7c00u) == 0x7c00u) h = 0x7e00u;
+        const float id = (h & 0x7fffu) == 0 || h == 0x7e00u ? 0.0f : 1.0f / d;
+        uint32_t word = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float q = fminf(fmaxf(rintf((bad ? 0.0f : x[j]) * id) + 8.0f, 0.0f), 15.0f);
+            word |= (uint32_t)q << (4 * j);
+        }
+        if (!active) continue;
+        uint8_t *to = kv_chunk(c, page, part, head);
+        const int t = pos & ((1 << c.page_log2) - 1);
+        reinterpret_cast<uint32_t *>(to)[part ? kv_value_word(c.D, t, w) : kv_key_word(c.D, t, w)] = word;
+        if ((w & 3) == 0) reinterpret_cast<uint16_t *>(to)[kv_scale_at(c, t, w >> 2)] = (uint16_t)h;
+    }
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void k_cache_read(KvCache c, void *__restrict__ k, void *__restrict__ v) {
+    const int words = c.heads * (c.D / 8);
+    const int u = blockIdx.y * kThreads + threadIdx.x, r = blockIdx.x;
+    const int b = kv_sequence(c, r);
+    if (b < 0 || u >= 2 * words) return;
+    const KvRows rows = kv_rows(c, b);
+    const int pos = rows.len - rows.count + (r - rows.first);
+    const int page = pos >= 0 ? kv_page(c, b, pos) : -1;
+    const int part = u >= words, e = part ? u - words : u, head = e / (c.D / 8), w = e - head * (c.D / 8);
+    float x[8];
+    if (page < 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __builtin_nanf("");
+    } else {
+        const uint8_t *from = kv_chunk(c, page, part, head);
+        const int t = pos & ((1 << c.page_log2) - 1);
+        const uint32_t q = reinterpret_cast<const uint32_t *>(from)[part ? kv_value_word(c.D, t, w) : kv_key_word(c.D, t, w)];
+        const float d = f16_bits_to_f32(reinterpret_cast<const uint16_t *>(from)[kv_scale_at(c, t, w >> 2)]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = d * (float)((int)((q >> (4 * j)) & 15u) - 8);
+    }
+    kv_store8<TYPE>(part ? v : k, ((int64_t)r * words + e) * 8, x);
+}
+
+template <int TYPE>
+hipError_t launch_write(const KvCache &c, const void *k, int64_t ld_k, const void *v, int64_t ld_v, hipStream_t s) {
+    const unsigned y = (unsigned)((2 * c.heads * (c.D / 8) + kThreads - 1) / kThreads);
+    hipLaunchKernelGGL((k_cache_write<TYPE, 1>), dim3((unsigned)c.T, y), dim3(kThreads), 0, s, c, k, ld_k, v, ld_v);
+    return hipGetLastError();
+}
+template <int TYPE>
+hipError_t launch_read(const KvCache &c, void *k, void *v, hipStream_t s) {
+    const unsigned y = (unsigned)((2 * c.heads * (c.D / 8) + kThreads - 1) / kThreads);
+    hipLaunchKernelGGL((k_cache_read<TYPE>), dim3((unsigned)c.T, y), dim3(kThreads), 0, s, c, k, v);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_cache_write(int type, const KvCache &c, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                              hipStream_t s) {
+    if (type == 0) return launch_write<0>(c, k, ld_k, v, ld_v, s);
+    return type == 1 ? launch_write<1>(c, k, ld_k, v, ld_v, s) : launch_write<2>(c, k, ld_k, v, ld_v, s);
+}
+
+hipError_t launch_cache_read(int type, const KvCache &c, void *k, void *v, hipStream_t s) {
+    if (type == 0) return launch_read<0>(c, k, v, s);
+    return type == 1 ? launch_read<1>(c, k, v, s) : launch_read<2>(c, k, v, s);
+}
+
+}  // namespace qmm

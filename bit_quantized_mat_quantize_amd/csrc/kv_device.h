@@ -1,0 +1,146 @@
+// kv_device.h -- what the kernels of the 4-bit key/value cache share (gfx950):
+// the cache's layout (include/qmm.h), the rows of ragged batches and the codes.
+#pragma once
+
+#include "qmm_device.h"
+#include "qmm_launch.h"
+
+namespace qmm {
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ h2 as_h2(uint32_t u) { return __builtin_bit_cast(h2, u); }
+__device__ __forceinline__ uint32_t as_u32(h2 h) { return __builtin_bit_cast(uint32_t, h); }
+
+// ---- addresses.  A (page, keys or values, head) chunk holds the codes of `page`
+// entries, D/2 bytes each, then their block scales as fp16 [D/32][page].
+__device__ __forceinline__ int64_t kv_chunk_bytes(const KvCache &c) { return ((int64_t)c.D * 9 / 16) << c.page_log2; }
+__device__ __forceinline__ uint8_t *kv_chunk(const KvCache &c, int64_t page, int part, int head) {
+    return c.data + ((page * 2 + part) * c.heads + head) * kv_chunk_bytes(c);
+}
+// the 32-bit word of an entry t (within its page) that holds elements 8w .. 8w + 7
+__device__ __forceinline__ int kv_key_word(int D, int t, int w) { return t * (D / 8) + (w & 3) * (D / 32) + (w >> 2); }
+__device__ __forceinline__ int kv_value_word(int D, int t, int w) { return ((t >> 2) * (D / 8) + w) * 4 + (t & 3); }
+// the fp16 scale of block b of entry t, counted from the chunk's start
+__device__ __forceinline__ int kv_scale_at(const KvCache &c, int t, int b) {
+    return ((c.D / 4) << c.page_log2) + (b << c.page_log2) + t;
+}
+
+// ---- rows.  Sequence b has the rows first .. first + count of the batch; its length
+// counts them: row i stands at position len - count + i.  What the device arrays
+// say is held within the batch and the table, whatever they hold.
+struct KvRows {
+    int first, count, len;
+};
+__device__ __forceinline__ KvRows kv_rows(const KvCache &c, int b) {
+    KvRows r;
+    if (c.starts == nullptr) {
+        r.first = b;
+        r.count = 1;
+    } else {
+        const int t0 = c.starts[b], t1 = c.starts[b + 1];
+        r.first = t0 < 0 ? 0 : (t0 > c.T ? c.T : t0);
+        const int end = t1 < r.first ? r.first : (t1 > c.T ? c.T : t1);
+        r.count = end - r.first;
+    }
+    const int most = c.width << c.page_log2, len = c.lens[b];
+    r.len = len < 0 ? 0 : (len > most ? most : len);
+    return r;
+}
+
+// The last b < B with key(b) <= x for an ascending key, or -1; by the whole wavefront, 64
+// candidates at a time (one dependent load for up to 64 sequences, two for 4096).
+template <typename Key>
+__device__ __forceinline__ int kv_last_not_above(int B, int64_t x, Key key) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = B;
+    for (;;) {
+        const int step = (n + 63) >> 6, at = lo + lane * step;
+        const bool le = lane * step < n && key(at) <= x;
+        const int c = __popcll(__ballot(le));
+        if (c == 0) return -1;
+        const int past = (c - 1) * step;
+        lo += past;
+        n = n - past < step ? n - past : step;
+        if (step == 1) return lo;
+    }
+}
+
+// the sequence of batch row r, or -1 (a row of none)
+__device__ __forceinline__ int kv_sequence(const KvCache &c, int r) {
+    if (c.starts == nullptr) return r;
+    const int b = kv_last_not_above(c.B, r, [&](int i) { return (int64_t)c.starts[i]; });
+    if (b < 0) return -1;
+    const KvRows k = kv_rows(c, b);
+    return r >= k.first && r < k.first + k.count ? b : -1;
+}
+
+// the page that holds position pos of sequence b, or -1
+__device__ __forceinline__ int kv_page(const KvCache &c, int b, int pos) {
+    const int p = c.table[(int64_t)b * c.width + (pos >> c.page_log2)];
+    return p >= 0 && p < c.pages ? p : -1;
+}
+
+// ---- codes.  Eight codes of a word as fp16 integers -8 .. 7, in the order 0 4 1 5 2 6 3 7:
+// 0x6400 | u is 1024 + u in fp16.
+__device__ __forceinline__ h2 kv_pair(uint32_t x) {
+    return as_h2((x & 0x000f000fu) | 0x64006400u) - h2{(_Float16)1032.0f, (_Float16)1032.0f};
+}
+
+// ---- element types: eight consecutive elements at a 16-byte aligned address
+template <int TYPE>  // qmm_float_type
+__device__ __forceinline__ void kv_load8(const void *base, int64_t at, float *v) {
+    if constexpr (TYPE == 0) {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 u = ld16(static_cast<const uint16_t *>(base) + at);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (TYPE == 1) {
+                v[2 * i] = f16_bits_to_f32(w[i] & 0xffffu);
+                v[2 * i + 1] = f16_bits_to_f32(w[i] >> 16);
+            } else {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+}
+__device__ __forceinline__ void kv_load8(int type, const void *base, int64_t at, float *v) {
+    if (type == 0) kv_load8<0>(base, at, v);
+    else if (type == 1) kv_load8<1>(base, at, v);
+    else kv_load8<2>(base, at, v);
+}
+
+// fp32 to bf16, to nearest even; NaN stays one
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+    const __bf16 b = (__bf16)f;
+    return __builtin_bit_cast(uint16_t, b);
+}
+template <int TYPE>
+__device__ __forceinline__ void kv_store8(void *base, int64_t at, const float *v) {
+    if constexpr (TYPE == 0) {
+        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = TYPE == 1 ? f32_to_f16_bits(v[2 * i]) | (f32_to_f16_bits(v[2 * i + 1]) << 16)
+                             : bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void kv_store8(int type, void *base, int64_t at, const float *v) {
+    if (type == 0) kv_store8<0>(base, at, v);
+    else if (type == 1) kv_store8<1>(base, at, v);
+    else kv_store8<2>(base, at, v);
+}
+
+}  // namespace qmm

@@ -245,4 +245,62 @@ int64_t logprobs_max_rows();  // rows of one launch
 int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t k);  // 0: not used
 hipError_t launch_logprobs(int type, LogprobArgs a, void *ws, hipStream_t s);
 
+// ---- rotary positions (rope.hip); type is a qmm_float_type (of x and out).
+struct RopeArgs {
+    const void *x;
+    void *out;               // may be x
+    const int32_t *positions;
+    const float *factors;    // [rot / 2] or null
+    int64_t ld_x, ld_out;    // elements from a token to the next
+    int64_t head_x, head_out;  // elements from a head to the next
+    int T, H, D, rot;
+    double log2_base, freq_scale, low, high, magnitude;  // high <= low: no ramp
+};
+int64_t rope_max_dim();
+hipError_t launch_rope(int type, bool interleaved, const RopeArgs &a, hipStream_t s);
+
+// ---- the paged cache of 4-bit keys and values (kv_cache.hip, attention.hip, evict.hip)
+struct KvCache {
+    uint8_t *data;           // [pages][2][heads][page * D * 9 / 16]
+    const int32_t *table;    // [B][width]
+    const int32_t *lens;     // [B]
+    const int32_t *starts;   // [B + 1] or null: one row each
+    int pages, page_log2, heads, D, B, width, T;
+};
+hipError_t launch_cache_write(int type, const KvCache &c, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                              hipStream_t s);
+hipError_t launch_cache_read(int type, const KvCache &c, void *k, void *v, hipStream_t s);
+
+// attention of T rows of `group` query heads per cache head
+struct AttendArgs {
+    KvCache c;
+    const void *q;           // [T][heads * group][D], ld_q elements from a row to the next
+    void *out;               // likewise, ld_out
+    float *lse;              // [T][heads * group] or null
+    float *mass;             // [B][heads][ld_mass] or null
+    float *ws;
+    int64_t ld_q, ld_out, ld_mass;
+    float scale;             // of the scores, times log2 e
+    int group, window;       // window 0: none
+    bool causal;
+};
+int64_t attend_workspace_bytes(int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
+                               bool ragged, bool mass);
+void attend_shape(const AttendArgs &a, int *splits);  // of a launch
+bool attend_grid_ok(const AttendArgs &a);  // every launch fits a grid
+hipError_t launch_attend(int type, const AttendArgs &a, hipStream_t s);
+
+// eviction: the entries that stay move from c.table's pages to those of `to`
+struct EvictArgs {
+    KvCache c;               // starts and T are not used
+    const float *mass;       // [B][heads][ld_mass]
+    const int32_t *to;       // [B][to_width]
+    int32_t *lens_out;       // [B]
+    float *mass_out;         // [B][heads][ld_out]
+    int32_t *ids;            // [B][heads][budget]
+    int64_t ld_mass, ld_out;
+    int to_width, budget, recent;
+};
+hipError_t launch_cache_evict(const EvictArgs &a, hipStream_t s);
+
 }  // namespace qmm

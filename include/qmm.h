@@ -55,7 +55,10 @@
  * Around the product: qmm_embed_rows (rows of a packed table by id, decoded),
  * qmm_lora_add (low-rank adapters by id per row, on top of a product's output),
  * qmm_logprobs and qmm_mul_mat_logprobs (log probabilities, entropy and the most
- * likely tokens of rows of logits).
+ * likely tokens of rows of logits).  Between the projections: qmm_rope (rotary
+ * positions), qmm_cache_write and qmm_cache_read (keys and values in pages of 4-bit
+ * blocks), qmm_cache_attention (attention over them) and qmm_cache_evict (the
+ * entries that matter most stay).
  *
  * Conventions for every entry point:
  *   - All array pointers are DEVICE pointers (hipMalloc / torch CUDA tensors)
@@ -468,6 +471,110 @@ qmm_status qmm_mul_mat_logprobs(qmm_weight_type t, const void *w, size_t w_bytes
                                 const int32_t *tokens, int64_t G, float *token_logprobs, float *entropy,
                                 int64_t k, int32_t *top_ids, float *top_logprobs,
                                 void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- Between the projections: rotary positions, the cache of keys and values in 4 bits, attention over it, and
+ * what of it stays.  The pages do not cover them; the formulas below define them. */
+
+/* Rotary positions of T tokens of H heads of D elements (format t):
+ *     (a, b) -> (a * m cos theta - b * m sin theta, a * m sin theta + b * m cos theta),   m = magnitude,
+ *     theta = positions[t] * base^(-2i/rot) / factors[i] * (1 - r_i * (1 - freq_scale)),
+ * for the pairs i < rot/2: elements i and i + rot/2 of a head (interleaved = 0) or 2i and 2i + 1 (1).  Elements from
+ * rot on stay as they are.  r_i = 1 where ramp_high <= ramp_low (freq_scale = 1: no scaling, 1/s: positions s times as
+ * dense), else clamp((i - ramp_low) / (ramp_high - ramp_low), 0, 1): the slow pairs are scaled and the fast ones are
+ * not.  factors: device fp32 [rot/2], or NULL (1).  positions: device int32 [T], any sign (-p undoes p, up to m).
+ * Angles are formed in 64 bits; products and sums are fp32, rounded once to t.
+ * x, out: element e of head h of token i at i*ld + h*head + e; out may be x itself (same pointer and strides) or a
+ * column range of the same matrix that shares no element with it, else they must not overlap.  out's heads (and
+ * tokens) must not overlap one another.  x_bytes and out_bytes count from the given pointers.
+ * Requires 1 <= H <= 65536, D <= 1024, rot even in [2, D], base > 0, T <= 2^22. */
+qmm_status qmm_rope(qmm_float_type t, const void *x, size_t x_bytes, int64_t ld_x, int64_t head_x,
+                    const int32_t *positions, const float *factors, void *out, size_t out_bytes, int64_t ld_out,
+                    int64_t head_out, int64_t T, int64_t H, int64_t D, int64_t rot, int interleaved, double base,
+                    double freq_scale, double ramp_low, double ramp_high, double magnitude, void *stream);
+
+/* A cache of keys and values in blocks of 32 elements with an fp16 scale d and 4-bit codes, value d * (q - 8) (the
+ * numbers of Q4_0), in pages, and the batch that a call is about.  All arrays are device arrays.
+ *   data, bytes    [pages][2][heads][page * dim * 9/16 bytes]: of each page the keys (0) and values (1) of each head:
+ *                  the codes of `page` entries, dim/2 bytes each, then their scales, fp16 [dim/32][page].  The code of
+ *                  element 8w + i sits in bits 4i .. 4i + 3 of a 32-bit word; entry t's word w is, for keys, word
+ *                  t * dim/8 + (w % 4) * dim/32 + w/4, and for values word ((t/4) * dim/8 + w) * 4 + t % 4.
+ *   page           entries of a page: 16, 32, .. 1024 (a power of two)
+ *   dim            elements of a head: 64, 96, 128, 192 or 256
+ *   table          int32 [seqs][width]: position p of sequence b is entry p % page of page table[b][p / page]
+ *   lens           int32 [seqs]: entries of each sequence, the rows of this call among them (below 0: 0; above
+ *                  width * page: that)
+ *   starts         int32 [seqs + 1], ascending: the rows of sequence b are starts[b] .. starts[b+1] - 1 of the call's;
+ *                  or NULL: row b is sequence b's (then rows = seqs).  Row i of a sequence's n stands at position
+ *                  lens[b] - n + i.  What is no sequence's row is neither read nor written.
+ *   rows           rows of the call
+ * Arrays on the device cannot be checked on the host: values outside what they index read and write nothing outside
+ * the arrays; each call says what comes of them.  Requires rows <= 2^22, seqs <= 65536, heads <= 1024,
+ * width * page <= 2^30, pages < 2^31. */
+typedef struct {
+    void *data;
+    size_t bytes;
+    int64_t pages, page, heads, dim;
+    const int32_t *table;
+    int64_t seqs, width;
+    const int32_t *lens, *starts;
+    int64_t rows;
+} qmm_cache;
+
+/* Bytes of a cache; 0 for sizes that are not supported. */
+size_t qmm_cache_bytes(int64_t pages, int64_t page, int64_t heads, int64_t dim);
+
+/* Writes the call's rows of keys and values (format t, [rows][heads][dim], ld_k and ld_v elements from a row to the
+ * next, heads side by side) at their positions.  A block of 32 elements x: d = -x_i/8 with x_i the element of largest
+ * magnitude (the first of equals), q = clamp(rint(x * (1/d)) + 8, 0, 15), d stored as fp16: the rule of
+ * qmm_quantize_weights for Q4_0.  A block with an infinity or NaN, or whose d passes fp16's range, gets d = NaN; where
+ * d is 0 in fp16 all codes are 8.  A row whose position is below 0 or whose page is not in [0, pages) is not written.
+ * Sequences that share a page must not write it in one call.  Rows start on 16 bytes (QMM_EALIGN). */
+qmm_status qmm_cache_write(const qmm_cache *c, qmm_float_type t, const void *k, size_t k_bytes, int64_t ld_k,
+                           const void *v, size_t v_bytes, int64_t ld_v, void *stream);
+
+/* The call's entries as numbers of format t: k, v [rows][heads][dim], contiguous.  An entry whose position is below 0
+ * or whose page is not in [0, pages) is NaN. */
+qmm_status qmm_cache_read(const qmm_cache *c, qmm_float_type t, void *k, size_t k_bytes, void *v, size_t v_bytes,
+                          void *stream);
+
+/* Bytes of the workspace qmm_cache_attention needs (0: none).  q_heads query heads; ragged: starts is given; mass:
+ * mass is. */
+size_t qmm_cache_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t dim, int64_t seqs,
+                                           int64_t width, int64_t page, int ragged, int mass);
+
+/* Attention of the call's rows over the entries of their sequences: query head h of a row at position p, with the
+ * keys k_j and values v_j of cache head h / (q_heads / heads),
+ *     out = sum_j e^(s_j - lse) v_j,   s_j = scale * q . k_j,   lse = log sum_j e^(s_j)
+ * over the entries j < lens[b] that it sees: j <= p where causal is set, and j > p - window where window > 0 (then
+ * causal must be set).  A row that sees none: out 0, lse -inf.  q, out (format t): [rows][q_heads][dim], ld_q and
+ * ld_out elements from a row to the next; rows start on 16 bytes.  lse: fp32 [rows][q_heads], or NULL.
+ * mass: fp32 [seqs][heads][ld_mass], ld_mass >= width * page, or NULL: mass[b][h][j] += the sum over the call's rows
+ * and the query heads of cache head h of e^(s_j - lse).
+ * fp32 queries are multiplied exactly to 22 bits of their row's largest element, and sums are fp32; with 16-bit
+ * queries the weights e^(..) and the values are rounded to fp16 before their product.  Results do not depend on
+ * timing.  What stands behind lens[b], or in pages that no row sees, may hold anything.  An entry that a row sees and
+ * that has a NaN scale, or whose page is not in [0, pages), makes the row NaN; so does an infinity or NaN in its query.
+ * workspace: qmm_cache_attention_workspace_bytes, overwritten; calls that may overlap need one each.  out must not
+ * overlap anything else of the call but a matrix whose columns it shares with q, element by element apart. */
+qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void *q, size_t q_bytes, int64_t ld_q,
+                               int64_t q_heads, void *out, size_t out_bytes, int64_t ld_out, float scale, int causal,
+                               int64_t window, float *lse, float *mass, int64_t ld_mass, void *workspace,
+                               size_t ws_bytes, void *stream);
+
+/* At most `budget` entries of every sequence and head stay, in their order: the newest `recent`, and of the others
+ * those of the largest mass (fp32 [seqs][heads][ld_mass], ld_mass >= width * page; ties to the lower position; NaN
+ * counts as the largest).  With n = min(lens[b], budget):
+ *   ids      int32 [seqs][heads][budget]: the positions that stay, ascending; -1 from n on
+ *   mass_out fp32 [seqs][heads][ld_out], ld_out >= budget: their mass; 0 from n on
+ *   lens_out int32 [seqs]: n
+ * and entry i of the pages of `to` (int32 [seqs][to_width], to_width * page >= budget) becomes entry ids[i].  `to` may
+ * be c->table, or hold the same pages in the same places: the entries move within their pages.  Else its pages must
+ * be none that the tables name elsewhere.  An entry whose page is not in [0, pages) becomes NaN; one that would move
+ * to such a page is not written.  Keys keep the rotation of the positions they were written with.  c->starts and
+ * c->rows are not used. */
+qmm_status qmm_cache_evict(const qmm_cache *c, const float *mass, int64_t ld_mass, int64_t budget, int64_t recent,
+                           const int32_t *to, int64_t to_width, int32_t *lens_out, float *mass_out, int64_t ld_out,
+                           int32_t *ids, void *stream);
 
 /* Static description of a status code. */
 const char *qmm_status_string(qmm_status s);
