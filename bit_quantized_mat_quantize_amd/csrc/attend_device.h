@@ -38,20 +38,43 @@ __device__ __forceinline__ int query_shift(uint32_t top) {
     return e < -114 ? 126 : 12 - e;
 }
 
-// elements of a word as the cache's pairs hold them: 0 4 1 5 2 6 3 7
+// elements of a word as key_codes holds them: 0 4 1 5 2 6 3 7, the odd ones over 16, which
+// the codes' places take back
 template <int PIECES>
 __device__ __forceinline__ void query_pieces(const float *x, float by, h8 &hi, h8 &lo) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float v = x[(i >> 1) + 4 * (i & 1)] * by;
+        const float v = x[(i >> 1) + 4 * (i & 1)] * ((i >> 1) & 1 ? by * 0.0625f : by);
         hi[i] = (_Float16)v;
         if constexpr (PIECES == 2) lo[i] = (_Float16)(v - (float)hi[i]);
     }
 }
 
-// eight codes of a word, exact
-__device__ __forceinline__ h8 key_codes(uint32_t w) {
-    const h2 a = kv_pair(w), b = kv_pair(w >> 4), c = kv_pair(w >> 8), d = kv_pair(w >> 12);
+// Constants of the decode in registers: an instruction of this family takes no
+// literals, and one scalar register at most.
+struct Decode {
+    uint32_t low, high;  // 0x000f000f, 0x00f000f0 (scalar)
+    uint32_t magic;      // 1024 in both halves (vector)
+    __device__ __forceinline__ void set() {
+        asm("s_mov_b32 %0, 0x000f000f" : "=s"(low));
+        asm("s_mov_b32 %0, 0x00f000f0" : "=s"(high));
+        asm("v_mov_b32 %0, 0x64006400" : "=v"(magic));
+    }
+    // 1024 + u of the codes in bits 0..3 of both halves; 1024 + 16 u of those in bits 4..7
+    __device__ __forceinline__ h2 even(uint32_t x) const { return as_h2((x & low) | magic); }
+    __device__ __forceinline__ h2 odd(uint32_t x) const { return as_h2((x & high) | magic); }
+};
+// u - 8 and 16 (u - 8), exact
+__device__ __forceinline__ h2 centred_even(h2 x) { return x - h2{(_Float16)1032.0f, (_Float16)1032.0f}; }
+__device__ __forceinline__ h2 centred_odd(h2 x) { return x - h2{(_Float16)1152.0f, (_Float16)1152.0f}; }
+
+// Eight codes of a word against query_pieces.  CENTRED: u - 8, exact; else 1024 + u (16 times
+// that for the odd ones), whose product with the query is that much too large by
+// 1032 (1152) times the sum of its even (odd) elements.
+template <bool CENTRED>
+__device__ __forceinline__ h8 key_codes(const Decode &k, uint32_t w) {
+    h2 a = k.even(w), b = k.odd(w), c = k.even(w >> 8), d = k.odd(w >> 8);
+    if constexpr (CENTRED) a = centred_even(a), b = centred_odd(b), c = centred_even(c), d = centred_odd(d);
     return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
@@ -71,11 +94,11 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 }
 
 // The power of two that value scales are multiplied by, from the largest scale's bits:
-// its exponent becomes 11 (products with codes stay within fp16, two pieces of them keep
-// everything down to 2^-40 of the largest); at most 2^15.
+// its exponent becomes 7 (products with codes, 16-fold ones too, stay within fp16, and two
+// pieces of them keep everything down to 2^-36 of the largest); at most 2^15.
 __device__ __forceinline__ int value_shift(uint32_t top) {
     const int e = (int)(top >> 10);
-    return e < 11 ? 15 : 26 - e;
+    return e < 7 ? 15 : 22 - e;
 }
 
 // ---- partial results of a split: [split][row][D] sums, [split][row] (reference, sum)

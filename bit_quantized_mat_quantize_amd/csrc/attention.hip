@@ -30,6 +30,8 @@ constexpr int kThreads = 256, kWaves = 4;
 constexpr int kRows = 16;  // query rows of a tile
 constexpr int kKeys = 32;  // entries of a wavefront's step
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 __device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
 // What a lane reads of 32 entries.  Lane (n, g), n = lane & 15, g = lane >> 4:
@@ -89,18 +91,44 @@ __device__ __forceinline__ void read_step(const KvCache &c, int b, int head, int
     }
 }
 
-// scores of 32 entries: x[4 s + r] is entry 16 s + 4 g + r against row n
+// A lane's share of 16 query rows: row n, elements 8 g .. 8 g + 7 of each block
 template <int PIECES, int D>
-__device__ __forceinline__ void scores(const Step<D> &t, const h8 (&qh)[D / 32], const h8 (&ql)[D / 32], float factor,
-                                       float *x) {
+struct Query {
+    static constexpr bool CENTRED = PIECES == 2;
+    h8 hi[D / 32], lo[CENTRED ? D / 32 : 1];
+    f4 less[CENTRED ? 1 : D / 32];  // what the products are too large by (key_codes), block by block, negative
+
+    __device__ __forceinline__ void set(const float (&x)[D / 32][8], float by) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            if constexpr (CENTRED) query_pieces<2>(x[i], by, hi[i], lo[i]);
+            else {
+                query_pieces<1>(x[i], by, hi[i], lo[0]);
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fmaf((j >> 1) & 1 ? 1152.0f : 1032.0f, (float)hi[i][j], sum);
+                sum += __shfl_xor(sum, 16, 64);
+                sum += __shfl_xor(sum, 32, 64);
+                less[i] = f4{-sum, -sum, -sum, -sum};
+            }
+        }
+    }
+};
+
+// Products of 32 entries with the queries: x[4 s + r] is entry 16 s + 4 g + r against row n.
+// For 16-bit queries the codes go in as 1024 + u, which saves half of their decode: the sums of
+// 32 products then reach 1032 times a query's sum, and their rounding 3e-5 of a score.
+template <int PIECES, int D>
+__device__ __forceinline__ void products(const Decode &k, const Step<D> &t, const Query<PIECES, D> &q, float *x) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         f4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
-            const h8 codes = key_codes(t.k[s][b]);
-            f4 dot = mfma16(codes, qh[b], f4{0, 0, 0, 0});
-            if constexpr (PIECES == 2) dot = mfma16(codes, ql[b], dot);
+            const h8 codes = key_codes<PIECES == 2>(k, t.k[s][b]);
+            f4 dot;
+            if constexpr (PIECES == 2) dot = mfma16(codes, q.lo[b], mfma16(codes, q.hi[b], f4{0, 0, 0, 0}));
+            else dot = mfma16(codes, q.hi[b], q.less[b]);
             const h2 d0 = as_h2(t.ks[s][b].x), d1 = as_h2(t.ks[s][b].y);
             acc[0] = fmaf((float)d0.x, dot[0], acc[0]);
             acc[1] = fmaf((float)d0.y, dot[1], acc[1]);
@@ -108,8 +136,116 @@ __device__ __forceinline__ void scores(const Step<D> &t, const h8 (&qh)[D / 32],
             acc[3] = fmaf((float)d1.y, dot[3], acc[3]);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[4 * s + r] = (t.bad >> s) & 1 ? __builtin_nanf("") : acc[r] * factor;
+        for (int r = 0; r < 4; ++r) x[4 * s + r] = acc[r];
     }
+    if (t.bad) {  // the same for the whole wavefront
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (t.bad >> (i >> 2)) & 1 ? __builtin_nanf("") : x[i];
+    }
+}
+
+// ---- a wavefront's ring of steps in LDS, filled by direct loads.  16 entries of a head are
+// one run of D/2 * 16 bytes of codes, for keys and for values alike, so a lane's place
+// in a load is fixed and only its page's base and the entry's offset, both scalar, change.
+// A group's image: keys' codes, values' codes, filler to 1 KiB; scales as [keys or
+// values][block][16 entries], filler to 256 bytes.
+template <int D>
+struct Ring {
+    static constexpr int CODES = (16 * D + 1023) / 1024, SCALES = (2 * D + 255) / 256;  // load instructions
+    static constexpr int SCALE_AT = 1024 * CODES, GROUP = SCALE_AT + 256 * SCALES, BYTES = 2 * GROUP;
+    static constexpr int LOADS = 2 * (CODES + SCALES);
+    // steps in LDS: two workgroups of four wavefronts per CU
+    static constexpr int SLOTS = D <= 128 ? 4 : 2;
+    static constexpr int WAVE = SLOTS * BYTES;
+    uint32_t code_at[CODES], scale_at[SCALES];  // this lane's place in a chunk pair, per instruction
+    uint32_t records;                           // bytes from a page's keys to the end of its values, of one head
+    uint32_t lds;                               // this wavefront's ring
+    const uint8_t *ring;
+
+    __device__ __forceinline__ void set(const KvCache &c, const uint8_t *mine) {
+        const int lane = threadIdx.x & 63;
+        const uint32_t chunk = (uint32_t)kv_chunk_bytes(c), values = chunk * (uint32_t)c.heads;
+#pragma unroll
+        for (int i = 0; i < CODES; ++i) {
+            int p = 64 * i + lane;  // 16-byte piece of keys, then of values
+            p = p < D ? p : D - 1;
+            code_at[i] = p < D / 2 ? p * 16 : values + (p - D / 2) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < SCALES; ++i) {
+            int p = 64 * i + lane;  // 4-byte piece
+            p = p < D / 2 ? p : D / 2 - 1;
+            const int part = p / (D / 4), b = p % (D / 4) / 8, e = p % 8;
+            scale_at[i] = part * values + (((D / 2) << c.page_log2) + 2 * (b << c.page_log2)) + 4 * e;
+        }
+        records = values + chunk;
+        ring = mine;
+        lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)mine);
+    }
+    // 16 entries from entry e0 of a page on (base: its keys) into half s of a slot
+    __device__ __forceinline__ void load(int slot, int s, const uint8_t *base, int e0) const {
+        const uint64_t at = (uint64_t)(uintptr_t)base;
+        const u32x4 r = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, records, 0x00020000u};
+        const uint32_t to = lds + slot * BYTES + s * GROUP;
+#pragma unroll
+        for (int i = 0; i < CODES; ++i)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + 1024 * i),
+                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "memory", "m0");
+#pragma unroll
+        for (int i = 0; i < SCALES; ++i)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to + SCALE_AT + 256 * i),
+                         "v"(scale_at[i]), "s"(r), "s"(e0 * 2) : "memory", "m0");
+    }
+    __device__ __forceinline__ void read(int slot, Step<D> &t) const {
+        constexpr int NB = D / 32, ROUNDS = Step<D>::ROUNDS, WORDS = D / 8;
+        const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint8_t *from = ring + slot * BYTES + s * GROUP;
+            const uint32_t *kw = reinterpret_cast<const uint32_t *>(from) + n * WORDS + g * NB;
+            if constexpr (NB % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < NB / 4; ++i) {
+                    const uint4 u = ld16(kw + 4 * i);
+                    t.k[s][4 * i] = u.x, t.k[s][4 * i + 1] = u.y, t.k[s][4 * i + 2] = u.z, t.k[s][4 * i + 3] = u.w;
+                }
+            } else if constexpr (NB % 2 == 0) {
+#pragma unroll
+                for (int i = 0; i < NB / 2; ++i) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(kw + 2 * i);
+                    t.k[s][2 * i] = u.x, t.k[s][2 * i + 1] = u.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) t.k[s][i] = kw[i];
+            }
+            const uint8_t *sc = from + SCALE_AT + 8 * g;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) t.ks[s][i] = *reinterpret_cast<const uint2 *>(sc + 32 * i);
+#pragma unroll
+            for (int r = 0; r < ROUNDS; ++r) {
+                const int w = (16 * r + n) % WORDS;
+                t.v[s][r] = ld16(from + 8 * D + (g * WORDS + w) * 16);
+                t.vs[s][r] = *reinterpret_cast<const uint2 *>(sc + 32 * (NB + (w >> 2)));
+            }
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// until at most n steps' loads are on their way (0 <= n < SLOTS, the same for the wavefront)
+template <int LOADS, int MOST>
+__device__ __forceinline__ void wait_steps(int n) {
+    if constexpr (MOST > 0) {
+        if (n >= MOST) {
+            wait_loads<MOST * LOADS>();
+            return;
+        }
+        wait_steps<LOADS, MOST - 1>(n);
+    } else wait_loads<0>();
 }
 
 // A tile's rows and the queries of this lane's row
@@ -123,7 +259,7 @@ struct Tile {
     int all_lo, all_hi;  // entries that every row sees
     float factor;      // of the dot products of codes, to log2 units
     int64_t out_row;   // row * heads of the batch
-    h8 qh[D / 32], ql[D / 32];
+    Query<PIECES, D> q;
 
     __device__ __forceinline__ bool open(const AttendArgs &a, int seq, int tile, int head) {
         b = seq;
@@ -157,8 +293,7 @@ struct Tile {
             top = u > top ? u : top;
         }
         const int shift = query_shift(top);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) query_pieces<PIECES>(x[i], pow2i(shift), qh[i], ql[i]);
+        q.set(x, pow2i(shift));
         factor = (top >> 23) == 255 ? __builtin_nanf("") : a.scale * pow2i(-shift);
         return true;
     }
@@ -192,13 +327,13 @@ struct Running {
     }
 };
 
-// MASKED: some row does not see some entry of the step
+// masked: some row does not see some entry of the step
 template <int PIECES, int D>
-__device__ __forceinline__ void step(Step<D> &t, const Tile<PIECES, D> &q, int k0, bool masked, Running<D> &run) {
+__device__ __forceinline__ void step(const Decode &k, Step<D> &t, const Tile<PIECES, D> &q, int k0, bool masked, Running<D> &run) {
     constexpr int ROUNDS = Step<D>::ROUNDS;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     float x[8];
-    scores<PIECES, D>(t, q.qh, q.ql, q.factor, x);
+    products<PIECES, D>(k, t, q.q, x);
     if (masked) {  // entries that no row sees hold anything
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -256,10 +391,16 @@ __device__ __forceinline__ void step(Step<D> &t, const Tile<PIECES, D> &q, int k
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int at = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
+            x[i] *= q.factor;
             if (at < q.lo || at >= q.hi) x[i] = -INFINITY;
         }
     }
+    const float factor = masked ? 1.0f : q.factor;  // x[i] * factor: scores
+    // the largest score: of the largest product, or of the smallest for a negative scale
     float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    if (factor < 0.0f)
+        most = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+    most *= factor;
     if (__any(most > run.ref + kSlack)) {
         for (int o = 16; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
         const float ref = fmaxf(run.ref, most), by = ref == -INFINITY ? 1.0f : exp2_fast(run.ref - ref);
@@ -271,7 +412,7 @@ __device__ __forceinline__ void step(Step<D> &t, const Tile<PIECES, D> &q, int k
     h8 ph, pl;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float p = exp2_fast(x[i] - from);
+        const float p = exp2_fast(fmaf(x[i], factor, -from));
         run.sum += p;
         ph[i] = (_Float16)p;
         if constexpr (PIECES == 2) pl[i] = (_Float16)(p - (float)ph[i]);
@@ -287,22 +428,22 @@ __device__ __forceinline__ void step(Step<D> &t, const Tile<PIECES, D> &q, int k
         for (int i = 0; i < 4; ++i) d[i] = as_h2(su[i]) * h2{unit, unit};
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            h2 even[4], odd[4];  // elements 2y and 2y + 1 of the word, entries in pairs
+            h2 code[2][4];  // elements 2y and 2y + 1 of the word (these 16-fold), entries in pairs
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t both = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x0c040c00u + 0x00010001u * y);
-                even[i] = kv_pair(both);
-                odd[i] = kv_pair(both >> 4);
+                code[0][i] = centred_even(k.even(both));
+                code[1][i] = centred_odd(k.odd(both));
             }
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
                 h8 vh, vl;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const h2 code = o ? odd[i] : even[i], h = code * d[i];
+                    const h2 h = code[o][i] * d[i];
                     vh[2 * i] = h.x, vh[2 * i + 1] = h.y;
                     if constexpr (PIECES == 2) {
-                        const h2 l = __builtin_elementwise_fma(code, d[i], -h);
+                        const h2 l = __builtin_elementwise_fma(code[o][i], d[i], -h);
                         vl[2 * i] = l.x, vl[2 * i + 1] = l.y;
                     }
                 }
@@ -346,9 +487,12 @@ struct Splits {
 };
 
 template <int PIECES, int D>
-__global__ __launch_bounds__(kThreads) void k_attend(AttendArgs a, Splits sp, int type) {
+__global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp, int type) {
     constexpr int ROUNDS = Step<D>::ROUNDS, PITCH = D + 4;
-    __shared__ float buf[2][kRows][PITCH];
+    using R = Ring<D>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    static_assert(kWaves * R::WAVE >= 2 * kRows * PITCH * 4, "the joint of the wavefronts takes the rings' place");
+    float(*buf)[kRows][PITCH] = reinterpret_cast<float(*)[kRows][PITCH]>(lds);
     __shared__ float2 stats[kWaves][kRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, split = x % sp.n;
@@ -366,17 +510,49 @@ __global__ __launch_bounds__(kThreads) void k_attend(AttendArgs a, Splits sp, in
     const int rounds = s1 > s0 ? (s1 - s0 + kWaves - 1) / kWaves : 0;
     const int from = s0 + (int)((int64_t)rounds * split / sp.n) * kWaves, to0 = s0 + (int)((int64_t)rounds * (split + 1) / sp.n) * kWaves;
     const int to = to0 < s1 ? to0 : s1, last16 = q.last > 0 ? (q.last - 1) & ~15 : 0;
-    int at = from + wave;
-    if (at < to) {
-        Step<D> cur, next;
-        read_step<D>(a.c, b, head, at * kKeys, last16, cur);
-        for (; at < to; at += kWaves) {
-            if (at + kWaves < to) read_step<D>(a.c, b, head, (at + kWaves) * kKeys, last16, next);
-            const int k0 = at * kKeys;
-            step<PIECES, D>(cur, q, k0, k0 < q.all_lo || k0 + kKeys > q.all_hi, run);
-            cur = next;
+    const int at0 = __builtin_amdgcn_readfirstlane(from + wave), steps = __builtin_amdgcn_readfirstlane(at0 < to ? (to - at0 + kWaves - 1) / kWaves : 0);
+    if (steps > 0) {
+        R ring;
+        ring.set(a.c, lds + wave * R::WAVE);
+        Decode decode;
+        decode.set();
+        typedef const __attribute__((address_space(4))) int32_t *scalar_ints;
+        const scalar_ints table = (scalar_ints)(uintptr_t)(a.c.table + (int64_t)b * a.c.width);
+        uint32_t bad = 0;  // of the steps on their way, two bits each, the next one lowest
+        auto issue = [&](int i) {
+            const int k0 = (at0 + i * kWaves) * kKeys, slot = i % R::SLOTS;
+            uint32_t none = 0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int at = k0 + 16 * s < last16 ? k0 + 16 * s : last16;  // the last 16 entries that hold anything
+                int page = table[at >> a.c.page_log2];
+                if (page < 0 || page >= a.c.pages) {
+                    none |= 1u << s;
+                    page = 0;
+                }
+                ring.load(slot, s, kv_chunk(a.c, page, 0, head), at & ((1 << a.c.page_log2) - 1));
+            }
+            bad |= none << (2 * ((R::SLOTS - 1)));
+        };
+        constexpr int AHEAD = R::SLOTS - 1;
+        for (int i = 0; i < AHEAD; ++i) {
+            bad >>= 2;
+            if (i < steps) issue(i);
+        }
+        for (int i = 0; i < steps; ++i) {
+            bad >>= 2;
+            if (i + AHEAD < steps) issue(i + AHEAD);
+            const int later = steps - 1 - i < AHEAD ? steps - 1 - i : AHEAD;
+            wait_steps<R::LOADS, AHEAD>(later);
+            Step<D> t;
+            ring.read(i % R::SLOTS, t);
+            t.bad = bad & 3;
+            const int k0 = (at0 + i * kWaves) * kKeys;
+            step<PIECES, D>(decode, t, q, k0, k0 < q.all_lo || k0 + kKeys > q.all_hi, run);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this slot's reads are done
         }
     }
+    __syncthreads();  // the rings' place is the joint's now
     for (int o = 16; o < 64; o <<= 1) run.sum += __shfl_xor(run.sum, o, 64);
     // the wavefronts' parts, to the largest reference
     if (g == 0) stats[wave][n] = make_float2(run.ref, run.sum);
@@ -390,6 +566,10 @@ __global__ __launch_bounds__(kThreads) void k_attend(AttendArgs a, Splits sp, in
         sum += s.x == -INFINITY ? s.y : s.y * exp2_fast(s.x - ref);  // a NaN stands in sums without a reference too
     }
     const float by = (run.ref == -INFINITY ? 1.0f : exp2_fast(run.ref - ref)) * pow2i(-run.shift);
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r)
+#pragma unroll
+        for (int j = 1; j < 8; j += 2) run.o[r][j] *= 0.0625f;  // the odd elements' codes were 16-fold
     for (int half = 2; half >= 1; half >>= 1) {  // wavefronts half .. 2 half - 1 into 0 .. half - 1
         if (wave >= half && wave < 2 * half) {
 #pragma unroll
@@ -512,6 +692,8 @@ __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits s
     if (k0 >= rows.len || rows.count == 0) return;
     Step<D> t;
     read_step<D>(a.c, b, head, k0, (rows.len - 1) & ~15, t);
+    Decode decode;
+    decode.set();
     // rows that see any of these entries
     const int shift = rows.len - rows.count;
     int i0 = a.causal ? k0 - shift : 0, i1 = a.window > 0 ? k0 + kKeys - 1 + a.window - shift : rows.count;
@@ -523,12 +705,12 @@ __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits s
         q.type = type;
         if (!q.open(a, b, tile, head)) break;
         float p[8];
-        scores<PIECES, D>(t, q.qh, q.ql, q.factor, p);
+        products<PIECES, D>(decode, t, q.q, p);
         const float lse = sp.lse2[q.out_row];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int at = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
-            if (q.live && lse != -INFINITY && at >= q.lo && at < q.hi) got[i] += exp2_fast(p[i] - lse);
+            if (q.live && lse != -INFINITY && at >= q.lo && at < q.hi) got[i] += exp2_fast(fmaf(p[i], q.factor, -lse));
         }
     }
 #pragma unroll
@@ -559,8 +741,12 @@ int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 template <int PIECES, int D>
 hipError_t launch(int type, const AttendArgs &a, const Splits &sp, hipStream_t s) {
     const int64_t tiles = tiles_of(a.c.T, a.c.B, a.group, a.c.starts != nullptr);
-    hipLaunchKernelGGL((k_attend<PIECES, D>), dim3((unsigned)(tiles * sp.n * a.c.heads)), dim3(kThreads), 0, s, a, sp, type);
-    hipError_t e = hipGetLastError();
+    constexpr int bytes = kWaves * Ring<D>::WAVE;
+    static std::atomic<uint64_t> lds_set{0};
+    hipError_t e = ensure_lds_bytes((const void *)k_attend<PIECES, D>, bytes, lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_attend<PIECES, D>), dim3((unsigned)(tiles * sp.n * a.c.heads)), dim3(kThreads), bytes, s, a, sp, type);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (sp.n > 1) {
         hipLaunchKernelGGL(k_attend_join, dim3((unsigned)((sp.rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, s, a, sp, type);
