@@ -92,7 +92,7 @@ def load() -> ctypes.CDLL:
         "qmm_cache_bytes": (SZ, [I64, I64, I64, I64]),
         "qmm_cache_write": (I, [C, I, P, SZ, I64, P, SZ, I64, P]),
         "qmm_cache_read": (I, [C, I, P, SZ, P, SZ, P]),
-        "qmm_cache_attention_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I64, I64, I, I]),
+        "qmm_cache_attention_workspace_bytes": (SZ, [I, I64, I64, I64, I64, I64, I64, I64, I, I]),
         "qmm_cache_attention": (I, [C, I, P, SZ, I64, I64, P, SZ, I64, ctypes.c_float, I, I64, P, P, I64, P, SZ, P]),
         "qmm_cache_evict": (I, [C, P, I64, I64, I64, P, I64, P, P, I64, P, P]),
         "qmm_debug_block_sums": (I, [I, P, SZ, I, P, SZ, P, SZ, I64, I64, I64, P]),
@@ -783,9 +783,11 @@ def cache_read(cache, rows: int, table, lens, starts=None, dtype=None, stream=No
     return k, v
 
 
-def cache_attention_workspace_bytes(rows: int, q_heads: int, heads: int, dim: int, seqs: int, width: int, page: int,
-                                    ragged: bool, mass: bool = False) -> int:
-    return int(load().qmm_cache_attention_workspace_bytes(rows, q_heads, heads, dim, seqs, width, page, ragged, mass))
+def cache_attention_workspace_bytes(q, heads: int, seqs: int, width: int, page: int, ragged: bool,
+                                    mass: bool = False) -> int:
+    """For q [T, q_heads, dim] over a cache of `heads` heads, with `seqs` tables of `width` pages; ragged: with starts."""
+    rows, q_heads, dim = q.shape
+    return int(load().qmm_cache_attention_workspace_bytes(_float_type(q, "q"), rows, q_heads, heads, dim, seqs, width, page, ragged, mass))
 
 
 def cache_attention(q, cache, table, lens, starts=None, scale=None, causal: bool = True, window: int = 0, mass=None,
@@ -832,7 +834,7 @@ def cache_attention(q, cache, table, lens, starts=None, scale=None, causal: bool
     stats = _new(torch, T, HQ, torch.float32, device) if lse else None
     lib = load()
     workspace, nw = _workspace(torch, workspace, lib.qmm_cache_attention_workspace_bytes(
-        T, HQ, heads, dim, B, W, page, starts is not None, mass is not None), device)
+        _float_type(q, "q"), T, HQ, heads, dim, B, W, page, starts is not None, mass is not None), device)
     _check(lib.qmm_cache_attention(c, _float_type(q, "q"), q.data_ptr(), nq, ldq, HQ, out.data_ptr(), no, ldo,
                                    dim ** -0.5 if scale is None else scale, causal, window, _ptr(stats), _ptr(mass),
                                    ld_mass, _ptr(workspace), nw, torch._C._cuda_getCurrentRawStream(index)),

@@ -1271,13 +1271,13 @@ qmm_status qmm_cache_read(const qmm_cache *c, qmm_float_type t, void *k, size_t 
     return device_status(qmm::launch_cache_read((int)t, view, k, v, static_cast<hipStream_t>(stream)), "cache_read launch");
 }
 
-size_t qmm_cache_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t dim, int64_t seqs,
+size_t qmm_cache_attention_workspace_bytes(qmm_float_type t, int64_t rows, int64_t q_heads, int64_t heads, int64_t dim, int64_t seqs,
                                            int64_t width, int64_t page, int ragged, int mass) {
-    if (rows < 1 || rows > kMaxTokens || heads < 1 || heads > kMaxHeads || q_heads < heads || q_heads > kMaxHeads ||
+    if (!float_size(t) || rows < 1 || rows > kMaxTokens || heads < 1 || heads > kMaxHeads || q_heads < heads || q_heads > kMaxHeads ||
         q_heads % heads || !cache_dim_ok(dim) || !cache_page_ok(page) || seqs < 1 || seqs > kMaxSeqs || width < 1 ||
         width > kMaxPositions / page)
         return 0;
-    return (size_t)qmm::attend_workspace_bytes(rows, seqs, width * page, heads, q_heads / heads, dim, ragged != 0, mass != 0);
+    return (size_t)qmm::attend_workspace_bytes((int)t, rows, seqs, width * page, heads, q_heads / heads, dim, ragged != 0, mass != 0);
 }
 
 qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void *q, size_t q_bytes, int64_t ld_q,
@@ -1303,7 +1303,7 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
         QMM_TRY(check_ptr("mass", mass));
         QMM_TRY(check_ld("ld_mass", ld_mass, capacity));
     }
-    const size_t ws_need = qmm_cache_attention_workspace_bytes(c->rows, q_heads, c->heads, c->dim, c->seqs, c->width,
+    const size_t ws_need = qmm_cache_attention_workspace_bytes(t, c->rows, q_heads, c->heads, c->dim, c->seqs, c->width,
                                                                c->page, c->starts != nullptr, mass != nullptr);
     if (ws_need != 0) {
         QMM_TRY(check_ptr("workspace", workspace));
@@ -1335,15 +1335,15 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
     a.group = (int)(q_heads / c->heads);
     a.window = (int)(window > kMaxPositions ? 0 : window);
     a.causal = causal != 0;
-    if (!qmm::attend_grid_ok(a))
+    if (!qmm::attend_grid_ok((int)t, a))
         return fail(QMM_EUNSUPPORTED, "rows = %lld, seqs = %lld, heads = %lld need more than %lld workgroups",
                     (long long)c->rows, (long long)c->seqs, (long long)c->heads, (long long)kMaxBlocks);
     if (log_enabled()) {
-        int splits;
-        qmm::attend_shape(a, &splits);
-        fprintf(stderr, "qmm: cache_attention %s rows=%lld seqs=%lld heads=%lld/%lld dim=%lld page=%lld -> %d split(s)%s\n",
+        int few, many;
+        qmm::attend_shape((int)t, a, &few, &many);
+        fprintf(stderr, "qmm: cache_attention %s rows=%lld seqs=%lld heads=%lld/%lld dim=%lld page=%lld -> %d split(s), %d of long runs of rows%s\n",
                 float_name(t), (long long)c->rows, (long long)c->seqs, (long long)q_heads, (long long)c->heads,
-                (long long)c->dim, (long long)c->page, splits, mass != nullptr ? ", mass" : "");
+                (long long)c->dim, (long long)c->page, few, many, mass != nullptr ? ", mass" : "");
     }
     return device_status(qmm::launch_attend((int)t, a, static_cast<hipStream_t>(stream)), "cache_attention launch");
 }

@@ -101,10 +101,43 @@ __device__ __forceinline__ int value_shift(uint32_t top) {
     return e < 7 ? 15 : 22 - e;
 }
 
-// ---- partial results of a split: [split][row][D] sums, [split][row] (reference, sum)
-struct AttendPartial {
-    float *sums;
-    float2 *stats;
+typedef float f16v __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f16v mfma32(h8 a, h8 b, f16v c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+
+// ---- who takes a sequence, and where its splits' parts go.  Query rows of a sequence
+// and cache head: token * group + head of the group.  Up to kFewRows of them (all, where
+// every sequence has one token) go to attention.hip's kernel, more to attend_rows.hip's.
+constexpr int kFewRows = 32;
+
+struct Splits {
+    int few, many;        // splits of the two kernels' tiles
+    int few_room;         // rows that a sequence and head has among the parts of the first
+    float *few_sums;      // [few][seqs * heads * few_room][D]
+    float2 *few_stats;    // [few][seqs * heads * few_room]: (reference - bias, sum)
+    float *many_sums;     // [many][T * query heads][D]
+    float2 *many_stats;   // [many][T * query heads]
+    float *lse2;          // [T * query heads] in log2 units, or null
 };
+
+// the row of the batch's output, token * query heads + head, of a sequence's query row
+__device__ __forceinline__ int64_t attend_out_row(const AttendArgs &a, const KvRows &rows, int head, int row) {
+    const int token = row / a.group, h = row - token * a.group;
+    return (int64_t)(rows.first + token) * (a.c.heads * a.group) + head * a.group + h;
+}
+// where an output row starts in q or out
+__device__ __forceinline__ int64_t attend_at(const AttendArgs &a, int64_t out_row, int64_t ld) {
+    const int heads = a.c.heads * a.group;
+    const int64_t token = out_row / heads;
+    return token * ld + (out_row - token * heads) * a.c.D;
+}
+__device__ __forceinline__ void attend_lse(const AttendArgs &a, float *lse2, int64_t out_row, float l2) {
+    if (a.lse != nullptr) a.lse[out_row] = l2 * kLn2;
+    if (lse2 != nullptr) lse2[out_row] = l2;
+}
+
+// attend_rows.hip: sequences of more than kFewRows rows
+int64_t attend_rows_tile(int type, int64_t D);  // rows of a tile
+hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s);
 
 }  // namespace qmm

@@ -1,0 +1,438 @@
+// attend_rows.hip -- attention over the paged 4-bit cache, many rows per sequence
+// (gfx950): prompts, and parts of them.
+//
+// A workgroup takes a tile of query rows (row = token * group + head of the group: 32 per
+// wavefront) and one cache head, and goes over the entries that any of them sees, KT at a
+// time.  The entries are decoded once per workgroup, to fp16 in LDS, keys as [entry][element]
+// and values as [element][entry], a tile ahead of the one that is multiplied; its codes
+// come from memory while that one is.  Then, per wavefront and 32 entries,
+//
+//   S^T = K Q^T    (32 entries x 32 rows, on 32x32x16 matrix instructions)
+//   O^T += V^T P^T
+//
+// with the entries along the registers and the rows along the lanes in both, so that P
+// needs no exchange between lanes: the order in which a lane's registers hold the
+// entries is the order of the values in LDS.
+//
+// Scale * code is rounded to fp16 for 16-bit queries.  fp32 queries, and with them the decoded
+// entries and P, are two fp16 pieces each (22 bits), of whose four products the three
+// large ones are taken.  All scales of a workgroup are multiplied by one power of two for
+// the keys and one for the values, which move when a larger scale turns up (then the
+// tile is decoded again; after the first tile that is seldom).
+#include "attend_device.h"
+
+namespace qmm {
+namespace {
+
+// Rows of a tile, entries of a step.  Two pieces of long heads need the registers of
+// one wavefront per SIMD, and LDS for half as many entries.
+template <int PIECES, int D>
+struct Shape {
+    static constexpr int WAVES = PIECES == 2 && D > 128 ? 4 : 8;
+    static constexpr int KT = PIECES == 2 && D > 128 ? 32 : 64;
+    static constexpr int ROWS = 32 * WAVES, THREADS = 64 * WAVES;
+    static constexpr int NB = D / 32, WORDS = D / 8, ROUNDS = D > 128 ? 2 : 1;
+    static constexpr int KEY_ROW = D == 96 ? 128 : D;              // elements of a key's row in LDS
+    static constexpr int KEYS = KT * KEY_ROW * 2, VALUES = D * KT * 2;  // bytes of one piece
+    static constexpr int STAGE = PIECES * (KEYS + VALUES), BYTES = 2 * STAGE;
+    static constexpr int GROUPS = 2 * KT / 16, MINE = GROUPS / WAVES;  // groups of 16 entries' keys or values; per wavefront
+    static_assert(MINE == 1, "one group per wavefront");
+};
+
+// 16-byte pieces of LDS rows are placed so that eight lanes of one access meet eight of them
+template <int PIECES, int D>
+__device__ __forceinline__ int key_piece(int entry, int w) {
+    return entry * Shape<PIECES, D>::KEY_ROW * 2 + ((w ^ (entry & 7)) * 16);
+}
+template <int PIECES, int D>
+__device__ __forceinline__ int value_piece(int element, int c) {  // c: eight entries
+    constexpr int KT = Shape<PIECES, D>::KT;
+    const int by = KT == 64 ? (element ^ (element >> 3)) & 7 : ((element >> 1) ^ (element >> 3)) & 3;
+    return element * KT * 2 + ((c ^ by) * 16);
+}
+
+// what a lane holds of its group on the way from memory to LDS
+template <int D>
+struct Raw {
+    static constexpr int NB = D / 32, ROUNDS = D > 128 ? 2 : 1;
+    uint32_t w[ROUNDS * 4];              // keys: the words of all blocks; values: a word of four entries
+    uint32_t s[NB > 2 * ROUNDS ? NB : 2 * ROUNDS];  // keys: scales of all blocks; values: of four entries
+};
+
+template <int PIECES, int D>
+__global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(AttendArgs a, Splits sp, int type, int tiles) {
+    using S = Shape<PIECES, D>;
+    constexpr int NB = S::NB, KT = S::KT, WORDS = S::WORDS, ROUNDS = S::ROUNDS;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ uint32_t flags[10];
+    uint32_t(*largest)[2] = reinterpret_cast<uint32_t(*)[2]>(flags);    // [stage][keys, values]: the bits of scales beyond the bound
+    uint32_t(*unfit)[2] = reinterpret_cast<uint32_t(*)[2]>(flags + 4);  // [step % 3]: entries that make NaN, a bit each
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, hf = lane >> 5;
+    const int head = blockIdx.x % a.c.heads, x0 = blockIdx.x / a.c.heads, split = x0 % sp.many;
+    const int x = tiles - 1 - x0 / sp.many;  // later rows see more entries: first
+    // sequence b's tiles start at slot floor(starts[b] * group / ROWS) + b
+    auto slot = [&](int i) {
+        const int t = a.c.starts[i];
+        return (int64_t)(t < 0 ? 0 : (t > a.c.T ? a.c.T : t)) * a.group / S::ROWS + i;
+    };
+    const int b = __builtin_amdgcn_readfirstlane(kv_last_not_above(a.c.B, x, slot));
+    if (b < 0) return;
+    const KvRows rows = kv_rows(a.c, b);
+    const int total = rows.count * a.group;
+    const int64_t r0_ = (x - slot(b)) * S::ROWS;
+    if (total <= sp.few_room || r0_ >= total) return;
+    const int r0 = __builtin_amdgcn_readfirstlane((int)r0_), r1 = r0 + S::ROWS - 1 < total ? r0 + S::ROWS - 1 : total - 1;
+
+    // ---- this lane's row
+    const int wr0 = r0 + 32 * wave, wr1 = wr0 + 31 < total ? wr0 + 31 : total - 1;  // the wavefront's
+    const bool busy = wr0 < total, live = wr0 + n < total;
+    const int use = live ? wr0 + n : r1;
+    int lo, hi, first, last, seen0, seen1, all0, all1, unused;
+    attend_span(a, rows, use / a.group, lo, hi);
+    attend_span(a, rows, r0 / a.group, first, unused);   // entries that the tile sees: [first, last)
+    attend_span(a, rows, r1 / a.group, unused, last);
+    attend_span(a, rows, (busy ? wr0 : r1) / a.group, seen0, all1);  // that the wavefront sees: [seen0, seen1)
+    attend_span(a, rows, (busy ? wr1 : r1) / a.group, all0, seen1);  // that all its rows see: [all0, all1)
+    const int64_t out_row = attend_out_row(a, rows, head, use);
+    h8 qh[2 * NB], ql[PIECES == 2 ? 2 * NB : 1];  // elements 16 i + 8 hf ..
+    float factor;
+    {
+        const int64_t at = attend_at(a, out_row, a.ld_q) + 8 * hf;
+        uint32_t top = 0;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) {
+            kv_load8(type, a.q, at + 16 * i, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t u = __float_as_uint(f[j]) & 0x7fffffffu;
+                top = u > top ? u : top;
+            }
+        }
+        const uint32_t other = __shfl_xor(top, 32, 64);
+        top = other > top ? other : top;
+        const int shift = query_shift(top);
+        const float by = a.scale < 0.0f ? -pow2i(shift) : pow2i(shift);
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) {
+            kv_load8(type, a.q, at + 16 * i, f);
+            query_pieces<PIECES>(f, by, qh[i], ql[PIECES == 2 ? i : 0]);
+        }
+        factor = (top >> 23) == 255 ? __builtin_nanf("") : fabsf(a.scale) * pow2i(-shift);
+    }
+
+    // ---- this split's steps
+    const int s0 = (first < 0 ? 0 : first) / KT, s1 = last > 0 ? (last + KT - 1) / KT : 0, all = s1 > s0 ? s1 - s0 : 0;
+    const int from = s0 + (int)((int64_t)all * split / sp.many), to = s0 + (int)((int64_t)all * (split + 1) / sp.many);
+    const int last16 = last > 0 ? (last - 1) & ~15 : 0;
+
+    // ---- staging.  Group g < KT / 16: keys of its 16 entries, else values.  Lane of a key group: entry
+    // lane / 4, word lane % 4 of every block.  Lane of a value group: word w (and w + 16) of
+    // entries 4 e .. 4 e + 3.
+    const bool keys = wave < KT / 16;
+    const int group = keys ? wave : wave - KT / 16;
+    const int ke = lane >> 2, kg = lane & 3;
+    const int vw = (lane & 7) | ((lane >> 4) & 1) << 3, ve = ((lane >> 3) & 1) << 1 | lane >> 5;
+    Decode decode;
+    decode.set();
+    typedef const __attribute__((address_space(4))) int32_t *scalar_ints;
+    const scalar_ints table = (scalar_ints)(uintptr_t)(a.c.table + (int64_t)b * a.c.width);
+    bool nowhere = false;  // the group's page is not in the pool
+    auto load = [&](int step, Raw<D> &raw) {
+        int at = step * KT + 16 * group;
+        at = at < last16 ? at : last16;
+        int page = table[at >> a.c.page_log2];
+        nowhere = page < 0 || page >= a.c.pages;
+        if (nowhere) page = 0;
+        const uint8_t *chunk = kv_chunk(a.c, page, keys ? 0 : 1, head);
+        const int e0 = at & ((1 << a.c.page_log2) - 1);
+        if (keys) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(chunk) + (e0 + ke) * WORDS + kg * NB;
+            if constexpr (NB % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < NB / 4; ++i) {
+                    const uint4 u = ld16(p + 4 * i);
+                    raw.w[4 * i] = u.x, raw.w[4 * i + 1] = u.y, raw.w[4 * i + 2] = u.z, raw.w[4 * i + 3] = u.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) raw.w[i] = p[i];
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                raw.s[i] = reinterpret_cast<const uint16_t *>(chunk)[kv_scale_at(a.c, e0 + ke, i)];
+        } else {
+#pragma unroll
+            for (int r = 0; r < ROUNDS; ++r) {
+                const int w = (16 * r + vw) % WORDS;
+                const uint4 u = ld16(reinterpret_cast<const uint32_t *>(chunk) + kv_value_word(D, e0 + 4 * ve, w));
+                raw.w[4 * r] = u.x, raw.w[4 * r + 1] = u.y, raw.w[4 * r + 2] = u.z, raw.w[4 * r + 3] = u.w;
+                const uint2 d = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(chunk) +
+                                                                 kv_scale_at(a.c, e0 + 4 * ve, w >> 2));
+                raw.s[2 * r] = d.x, raw.s[2 * r + 1] = d.y;
+            }
+        }
+    };
+    uint32_t bound = 0;        // of this wavefront's side's scales
+    int key_shift = 15, value_shift_ = 15;
+    uint32_t key_bound = 0, value_bound = 0;
+    auto put = [&](int step, const Raw<D> &raw) {
+        uint8_t *stage = lds + (step & 1) * S::STAGE;
+        const int e = 16 * group, k0 = step * KT + e;  // in LDS; in the sequence
+        const bool edge = k0 < first || k0 + 16 > last;
+        uint32_t top = 0, bad = 0;  // bits of this group's 16 entries
+        if (keys) {
+            const _Float16 unit = (_Float16)pow2i(key_shift);
+            const bool out = edge && (k0 + ke < first || k0 + ke >= last);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const uint32_t s = out ? 0 : raw.s[i], m = s & 0x7fffu;
+                top = m > top && m < 0x7c00u ? m : top;
+                const uint32_t ss = s | s << 16;
+                const h2 d = as_h2(ss) * h2{unit, unit};
+                const uint32_t w = raw.w[i];
+                const h2 c[4] = {centred_even(decode.even(w)), centred_odd(decode.odd(w)), centred_even(decode.even(w >> 8)),
+                                 centred_odd(decode.odd(w >> 8))};
+                h2 h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = c[j] * d;
+                uint8_t *to = stage + key_piece<PIECES, D>(e + ke, 4 * i + kg);
+                *reinterpret_cast<uint4 *>(to) = make_uint4(as_u32(h[0]), as_u32(h[1]), as_u32(h[2]), as_u32(h[3]));
+                if constexpr (PIECES == 2) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[j] = __builtin_elementwise_fma(c[j], d, -h[j]);
+                    *reinterpret_cast<uint4 *>(to + S::KEYS) =
+                        make_uint4(as_u32(h[0]), as_u32(h[1]), as_u32(h[2]), as_u32(h[3]));
+                }
+            }
+            bound = key_bound;
+        } else {
+            stage += PIECES * S::KEYS;
+            const _Float16 unit = (_Float16)pow2i(value_shift_);
+#pragma unroll
+            for (int r = 0; r < ROUNDS; ++r) {
+                const int w = 16 * r + vw;
+                uint32_t s[2] = {raw.s[2 * r], raw.s[2 * r + 1]};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t m = (s[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
+                    const int at = k0 + 4 * ve + i;
+                    const bool out = edge && (at < first || at >= last);
+                    if (out || m >= 0x7c00u) s[i >> 1] &= i & 1 ? 0xffffu : 0xffff0000u;
+                    if (!out && m >= 0x7c00u) bad |= 1u << (4 * ve + i);
+                    top = m > top && !out && m < 0x7c00u ? m : top;
+                }
+                const h2 d[2] = {as_h2(s[0]) * h2{unit, unit}, as_h2(s[1]) * h2{unit, unit}};
+                if (w < WORDS) {
+                    // entries 4 ve .. within the eight that a lane of the product holds: 0 and 2, or 1 and 3
+                    const int c = 2 * group + (ve & 1), half = (ve >> 1) * 8;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t both[2] = {__builtin_amdgcn_perm(raw.w[4 * r + 1], raw.w[4 * r], 0x0c040c00u + 0x00010001u * y),
+                                                  __builtin_amdgcn_perm(raw.w[4 * r + 3], raw.w[4 * r + 2], 0x0c040c00u + 0x00010001u * y)};
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            const h2 c0 = o ? centred_odd(decode.odd(both[0])) : centred_even(decode.even(both[0]));
+                            const h2 c1 = o ? centred_odd(decode.odd(both[1])) : centred_even(decode.even(both[1]));
+                            const h2 h0 = c0 * d[0], h1 = c1 * d[1];
+                            uint8_t *to = stage + value_piece<PIECES, D>(8 * w + 2 * y + o, c) + half;
+                            *reinterpret_cast<uint2 *>(to) = make_uint2(as_u32(h0), as_u32(h1));
+                            if constexpr (PIECES == 2)
+                                *reinterpret_cast<uint2 *>(to + S::VALUES) =
+                                    make_uint2(as_u32(__builtin_elementwise_fma(c0, d[0], -h0)),
+                                               as_u32(__builtin_elementwise_fma(c1, d[1], -h1)));
+                        }
+                    }
+                }
+            }
+            bound = value_bound;
+        }
+        if (nowhere) bad = edge ? 0xffffu & (last > k0 ? (last - k0 >= 16 ? 0xffffu : (1u << (last - k0)) - 1) : 0u) : 0xffffu;
+        if (__any(top >= bound)) atomicMax(&largest[step & 1][keys ? 0 : 1], top);
+        if (__any(bad != 0) && bad) atomicOr(&unfit[step % 3][e >> 5], bad << (e & 31));
+    };
+
+    // ---- the rows' running results
+    f16v o[NB];   // o[block][4 i + r]: element 32 block + 8 i + 4 hf + r of row n, times 2^value_shift (16-fold for odd r)
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+    float ref = -INFINITY, sum = 0.0f;
+    auto scale = [&](float by) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[i][r] *= by;
+    };
+
+    if (threadIdx.x < 10) flags[threadIdx.x] = 0;
+    __syncthreads();
+    Raw<D> raw;
+    if (from < to) {
+        load(from, raw);
+        put(from, raw);
+    }
+    for (int step = from; step < to; ++step) {
+        __syncthreads();  // the step's entries are in LDS, and nobody reads the step's before
+        const uint8_t *stage = lds + (step & 1) * S::STAGE;
+        const uint32_t top[2] = {largest[step & 1][0], largest[step & 1][1]};
+        if (top[0] >= key_bound || top[1] >= value_bound) {
+            // the same for the whole workgroup: a larger scale than all before
+            if (top[0] >= key_bound) {
+                key_shift = value_shift(top[0]);
+                key_bound = ((top[0] >> 10) + 1) << 10;
+            }
+            if (top[1] >= value_bound) {
+                const int shift = value_shift(top[1]);
+                scale(pow2i(shift - value_shift_));
+                value_shift_ = shift;
+                value_bound = ((top[1] >> 10) + 1) << 10;
+            }
+            __syncthreads();
+            put(step, raw);
+            __syncthreads();
+        }
+        if (threadIdx.x < 2) unfit[(step + 2) % 3][threadIdx.x] = 0;
+        if (step + 1 < to) load(step + 1, raw);
+        if (busy) {
+            const float by = factor * pow2i(-key_shift);
+#pragma unroll
+            for (int sub = 0; sub < KT / 32; ++sub) {
+                const int k0 = step * KT + 32 * sub;
+                if (k0 >= seen1 || k0 + 32 <= seen0) continue;  // the same for the wavefront
+                f16v x;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2 * NB; ++i) {
+                    const uint8_t *p = stage + key_piece<PIECES, D>(32 * sub + n, 2 * i + hf);
+                    const h8 kh = *reinterpret_cast<const h8 *>(p);
+                    x = mfma32(kh, qh[i], x);
+                    if constexpr (PIECES == 2) {
+                        const h8 kl = *reinterpret_cast<const h8 *>(p + S::KEYS);
+                        x = mfma32(kh, ql[i], x);
+                        x = mfma32(kl, qh[i], x);
+                    }
+                }
+                const uint32_t bad = __builtin_amdgcn_readfirstlane(unfit[step % 3][sub]);
+                if (bad) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if ((bad >> (8 * (r >> 2) + 4 * hf + (r & 3))) & 1) x[r] = __builtin_nanf("");
+                }
+                float f = by;
+                if (k0 < all0 || k0 + 32 > all1) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int at = k0 + 8 * (r >> 2) + 4 * hf + (r & 3);
+                        x[r] = at < lo || at >= hi ? -INFINITY : x[r] * by;
+                    }
+                    f = 1.0f;
+                }
+                float most = x[0];
+#pragma unroll
+                for (int r = 1; r < 16; ++r) most = fmaxf(most, x[r]);
+                most *= f;
+                if (__any(most > ref + kSlack)) {
+                    most = fmaxf(most, __shfl_xor(most, 32, 64));
+                    const float next = fmaxf(ref, most), down = next == -INFINITY ? 1.0f : exp2_fast(ref - next);
+                    scale(down);
+                    sum *= down;
+                    ref = next;
+                }
+                const float less = ref == -INFINITY ? 0.0f : kBias - ref;
+                h8 ph[2], pl[2];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float p = exp2_fast(fmaf(x[r], f, less));
+                    sum += p;
+                    ph[r >> 3][r & 7] = (_Float16)p;
+                    if constexpr (PIECES == 2) pl[r >> 3][r & 7] = (_Float16)(p - (float)ph[r >> 3][r & 7]);
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint8_t *p = stage + PIECES * S::KEYS + value_piece<PIECES, D>(32 * i + n, 2 * (2 * sub + t) + hf);
+                        const h8 vh = *reinterpret_cast<const h8 *>(p);
+                        o[i] = mfma32(vh, ph[t], o[i]);
+                        if constexpr (PIECES == 2) {
+                            const h8 vl = *reinterpret_cast<const h8 *>(p + S::VALUES);
+                            o[i] = mfma32(vh, pl[t], o[i]);
+                            o[i] = mfma32(vl, ph[t], o[i]);
+                        }
+                    }
+            }
+        }
+        if (step + 1 < to) put(step + 1, raw);
+    }
+    if (!busy) return;
+    sum += __shfl_xor(sum, 32, 64);
+    if (!live) return;
+    const bool none = !(sum != 0.0f);  // NaN is a sum
+    const float down = pow2i(-value_shift_);
+    if (sp.many == 1) {
+        const float inv = none ? 0.0f : down / sum;
+        const int64_t to_row = attend_at(a, out_row, a.ld_out);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = o[i][4 * c + r] * (r & 1 ? inv * 0.0625f : inv);
+                const int64_t at = to_row + 32 * i + 8 * c + 4 * hf;
+                if (type == 0) *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+                else {
+                    const uint2 u = type == 1 ? make_uint2(f32_to_f16_bits(v[0]) | f32_to_f16_bits(v[1]) << 16,
+                                                           f32_to_f16_bits(v[2]) | f32_to_f16_bits(v[3]) << 16)
+                                              : make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = u;
+                }
+            }
+        if (hf == 0) attend_lse(a, sp.lse2, out_row, none ? -INFINITY : ref - kBias + log2_fast(sum));
+    } else {
+        const int64_t row = (int64_t)split * a.c.T * (a.c.heads * a.group) + out_row;
+        if (hf == 0) sp.many_stats[row] = make_float2(ref == -INFINITY ? ref : ref - kBias, sum);
+        if (none) return;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<float4 *>(sp.many_sums + row * D + 32 * i + 8 * c + 4 * hf) =
+                    make_float4(o[i][4 * c] * down, o[i][4 * c + 1] * (down * 0.0625f), o[i][4 * c + 2] * down,
+                                o[i][4 * c + 3] * (down * 0.0625f));
+    }
+}
+
+template <int PIECES, int D>
+hipError_t launch(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s) {
+    using S = Shape<PIECES, D>;
+    static std::atomic<uint64_t> lds_set{0};
+    const hipError_t e = ensure_lds_bytes((const void *)k_attend_rows<PIECES, D>, S::BYTES, lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_attend_rows<PIECES, D>), dim3((unsigned)(tiles * sp.many * a.c.heads)), dim3(S::THREADS), S::BYTES, s,
+                       a, sp, type, (int)tiles);
+    return hipGetLastError();
+}
+template <int PIECES>
+hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s) {
+    switch (a.c.D) {
+        case 64: return launch<PIECES, 64>(type, a, sp, tiles, s);
+        case 96: return launch<PIECES, 96>(type, a, sp, tiles, s);
+        case 128: return launch<PIECES, 128>(type, a, sp, tiles, s);
+        case 192: return launch<PIECES, 192>(type, a, sp, tiles, s);
+        default: return launch<PIECES, 256>(type, a, sp, tiles, s);
+    }
+}
+
+}  // namespace
+
+int64_t attend_rows_tile(int type, int64_t D) { return type == 0 && D > 128 ? 128 : 256; }
+
+hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s) {
+    return type == 0 ? launch_for<2>(type, a, sp, tiles, s) : launch_for<1>(type, a, sp, tiles, s);
+}
+
+}  // namespace qmm

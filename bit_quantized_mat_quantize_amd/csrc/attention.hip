@@ -32,8 +32,6 @@ constexpr int kKeys = 32;  // entries of a wavefront's step
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-
 // What a lane reads of 32 entries.  Lane (n, g), n = lane & 15, g = lane >> 4:
 //   k[s]  words (b, g) of all blocks b of entry 16 s + n
 //   v[s]  words n (and 16 + n for D > 128) of the entries 16 s + 4 g .. + 3
@@ -270,13 +268,12 @@ struct Tile {
         const int r1 = r0 + kRows - 1 < total ? r0 + kRows - 1 : total - 1;
         row = r0 + n;
         live = row < total;
-        const int use = live ? row : r1, token = use / a.group, h = use - token * a.group;
+        const int use = live ? row : r1, token = use / a.group;
         attend_span(a, rows, token, lo, hi);
         attend_span(a, rows, r0 / a.group, first, all_hi);
         attend_span(a, rows, r1 / a.group, all_lo, last);
-        const int qh_head = head * a.group + h;
-        out_row = (int64_t)(rows.first + token) * (a.c.heads * a.group) + qh_head;
-        const int64_t at = (int64_t)(rows.first + token) * a.ld_q + (int64_t)qh_head * D + 8 * g;
+        out_row = attend_out_row(a, rows, head, use);
+        const int64_t at = attend_at(a, out_row, a.ld_q) + 8 * g;
         float x[D / 32][8];
         uint32_t top = 0;
 #pragma unroll
@@ -293,8 +290,8 @@ struct Tile {
             top = u > top ? u : top;
         }
         const int shift = query_shift(top);
-        q.set(x, pow2i(shift));
-        factor = (top >> 23) == 255 ? __builtin_nanf("") : a.scale * pow2i(-shift);
+        q.set(x, a.scale < 0.0f ? -pow2i(shift) : pow2i(shift));
+        factor = (top >> 23) == 255 ? __builtin_nanf("") : fabsf(a.scale) * pow2i(-shift);
         return true;
     }
     int type;
@@ -396,11 +393,7 @@ __device__ __forceinline__ void step(const Decode &k, Step<D> &t, const Tile<PIE
         }
     }
     const float factor = masked ? 1.0f : q.factor;  // x[i] * factor: scores
-    // the largest score: of the largest product, or of the smallest for a negative scale
-    float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    if (factor < 0.0f)
-        most = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
-    most *= factor;
+    float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * factor;
     if (__any(most > run.ref + kSlack)) {
         for (int o = 16; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
         const float ref = fmaxf(run.ref, most), by = ref == -INFINITY ? 1.0f : exp2_fast(run.ref - ref);
@@ -458,34 +451,6 @@ __device__ __forceinline__ void step(const Decode &k, Step<D> &t, const Tile<PIE
     }
 }
 
-// ---- which tile.  DIRECT: sequence x / per_seq, tile x % per_seq; else tiles of all
-// sequences in turn, sequence b's from floor(starts[b] * group / kRows) + b on (one slot a
-// sequence is at most unused).
-__device__ __forceinline__ bool find_tile(const AttendArgs &a, int x, int &b, int &tile) {
-    if (a.c.starts == nullptr) {
-        const int per = (a.group + kRows - 1) / kRows;
-        b = x / per;
-        tile = x - b * per;
-        return true;
-    }
-    auto slot = [&](int i) {
-        const int t = a.c.starts[i];
-        return (int64_t)(t < 0 ? 0 : (t > a.c.T ? a.c.T : t)) * a.group / kRows + i;
-    };
-    b = kv_last_not_above(a.c.B, x, slot);
-    if (b < 0) return false;
-    tile = x - (int)slot(b);
-    return true;
-}
-
-struct Splits {
-    int n;            // per tile
-    float *sums;      // [n][T * heads][D]
-    float2 *stats;    // [n][T * heads]: (reference - bias, sum)
-    float *lse2;      // [T * heads] in log2 units, or null
-    int64_t rows;     // T * heads
-};
-
 template <int PIECES, int D>
 __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp, int type) {
     constexpr int ROUNDS = Step<D>::ROUNDS, PITCH = D + 4;
@@ -495,11 +460,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp,
     float(*buf)[kRows][PITCH] = reinterpret_cast<float(*)[kRows][PITCH]>(lds);
     __shared__ float2 stats[kWaves][kRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-    const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, split = x % sp.n;
-    int b, tile;
-    if (!find_tile(a, x / sp.n, b, tile)) return;
-    b = __builtin_amdgcn_readfirstlane(b);
-    tile = __builtin_amdgcn_readfirstlane(tile);
+    const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, split = x % sp.few;
+    const int per = sp.few_room / kRows, b = x / sp.few / per, tile = x / sp.few - b * per;
+    if (kv_rows(a.c, b).count * a.group > sp.few_room) return;  // the other kernel's
     Tile<PIECES, D> q;
     q.type = type;
     if (!q.open(a, b, tile, head)) return;
@@ -508,7 +471,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp,
     // this split's steps of 32 entries: whole rounds of the four wavefronts
     const int s0 = (q.first < 0 ? 0 : q.first) / kKeys, s1 = q.last > 0 ? (q.last + kKeys - 1) / kKeys : 0;
     const int rounds = s1 > s0 ? (s1 - s0 + kWaves - 1) / kWaves : 0;
-    const int from = s0 + (int)((int64_t)rounds * split / sp.n) * kWaves, to0 = s0 + (int)((int64_t)rounds * (split + 1) / sp.n) * kWaves;
+    const int from = s0 + (int)((int64_t)rounds * split / sp.few) * kWaves;
+    const int to0 = s0 + (int)((int64_t)rounds * (split + 1) / sp.few) * kWaves;
     const int to = to0 < s1 ? to0 : s1, last16 = q.last > 0 ? (q.last - 1) & ~15 : 0;
     const int at0 = __builtin_amdgcn_readfirstlane(from + wave), steps = __builtin_amdgcn_readfirstlane(at0 < to ? (to - at0 + kWaves - 1) / kWaves : 0);
     if (steps > 0) {
@@ -603,10 +567,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp,
     }
     if (wave != 0 || !q.live) return;
     const bool none = !(sum != 0.0f);  // NaN is a sum
-    if (sp.n == 1) {
+    if (sp.few == 1) {
         const float inv = none ? 0.0f : 1.0f / sum, l2 = none ? -INFINITY : ref - kBias + log2_fast(sum);
-        const int64_t token = q.out_row / (a.c.heads * a.group);
-        const int64_t to_row = token * a.ld_out + (q.out_row - token * a.c.heads * a.group) * D;
+        const int64_t to_row = attend_at(a, q.out_row, a.ld_out);
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r)
 #pragma unroll
@@ -619,13 +582,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp,
                     kv_store8(type, a.out, to_row + 8 * w, v);
                 }
             }
-        if (g == 0) {
-            if (a.lse != nullptr) a.lse[q.out_row] = l2 * kLn2;
-            if (sp.lse2 != nullptr) sp.lse2[q.out_row] = l2;
-        }
+        if (g == 0) attend_lse(a, sp.lse2, q.out_row, l2);
     } else {
-        const int64_t row = split * sp.rows + q.out_row;
-        if (g == 0) sp.stats[row] = make_float2(ref == -INFINITY ? ref : ref - kBias, sum);
+        const int64_t row = ((int64_t)split * a.c.B + b) * a.c.heads * sp.few_room + head * sp.few_room + q.row;
+        if (g == 0) sp.few_stats[row] = make_float2(ref == -INFINITY ? ref : ref - kBias, sum);
         if (none) return;
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r)
@@ -636,48 +596,80 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp,
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = run.o[r][j][i];
-                    kv_store8<0>(sp.sums, row * D + 8 * w, v);
+                    kv_store8<0>(sp.few_sums, row * D + 8 * w, v);
                 }
             }
     }
 }
 
-// the splits of a row joined: one wavefront per row, eight elements per lane
-__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits sp, int type) {
-    const int lane = threadIdx.x & 63, D = a.c.D;
-    const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    if (row >= sp.rows) return;
-    const int heads = a.c.heads * a.group;
-    const int64_t token = row / heads;
-    const int b = kv_sequence(a.c, (int)token);
-    if (b < 0) return;  // a row of no sequence
-    float ref = -INFINITY, sum = 0.0f;
-    for (int s = lane; s < sp.n; s += 64) ref = fmaxf(ref, sp.stats[s * sp.rows + row].x);
-    for (int o = 32; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor(ref, o, 64));
-    float v[8] = {};
-    for (int s = 0; s < sp.n; ++s) {
-        const float2 st = sp.stats[s * sp.rows + row];
-        if (st.y == 0.0f) continue;  // nothing seen
-        const float by = st.x == -INFINITY ? 1.0f : exp2_fast(st.x - ref);
-        sum += st.y * by;
-        if (8 * lane < D) {
+// The splits of a row joined: one workgroup per row.  Lane group s of kThreads / (D/8) takes
+// the splits s, s + groups, ..; the groups are added in their order.  Workgroups below
+// few_blocks take the rows of sequences with few, by (sequence, head, row), the others
+// those of the rest, by output row.
+__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits sp, int type, int few_blocks) {
+    __shared__ float part[kThreads * 8];
+    __shared__ float weight[kThreads];
+    const int D = a.c.D, lanes = D / 8, groups = kThreads / lanes, tid = threadIdx.x;
+    int64_t out_row, row, rows;
+    const float *sums;
+    const float2 *stats;
+    int n;
+    if ((int)blockIdx.x < few_blocks) {
+        const int r = blockIdx.x % sp.few_room, bh = blockIdx.x / sp.few_room, b = bh / a.c.heads, head = bh - b * a.c.heads;
+        const KvRows k = kv_rows(a.c, b);
+        if (r >= k.count * a.group || k.count * a.group > sp.few_room) return;
+        out_row = attend_out_row(a, k, head, r);
+        row = blockIdx.x;
+        rows = (int64_t)a.c.B * a.c.heads * sp.few_room;
+        sums = sp.few_sums;
+        stats = sp.few_stats;
+        n = sp.few;
+    } else {
+        row = out_row = blockIdx.x - few_blocks;
+        rows = (int64_t)a.c.T * a.c.heads * a.group;
+        const int b = kv_sequence(a.c, (int)(out_row / (a.c.heads * a.group)));
+        if (b < 0 || kv_rows(a.c, b).count * a.group <= sp.few_room) return;
+        sums = sp.many_sums;
+        stats = sp.many_stats;
+        n = sp.many;
+    }
+    const int s0 = tid / lanes, e = tid - s0 * lanes;
+    float ref = -INFINITY;
+    for (int s = 0; s < n; ++s) ref = fmaxf(ref, stats[s * rows + row].x);
+    float v[8] = {}, sum = 0.0f;
+    if (s0 < groups) {
+#pragma unroll 4
+        for (int s = s0; s < n; s += groups) {
+            const float2 st = stats[s * rows + row];
             float u[8];
-            kv_load8<0>(sp.sums, (s * sp.rows + row) * D + 8 * lane, u);
+            kv_load8<0>(sums, (s * rows + row) * D + 8 * e, u);
+            const bool some = st.y != 0.0f;  // else nothing was seen, and nothing written
+            const float by = !some ? 0.0f : (st.x == -INFINITY ? 1.0f : exp2_fast(st.x - ref));
+            sum += st.y * by;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = fmaf(u[j], by, v[j]);
+            for (int j = 0; j < 8; ++j) v[j] = fmaf(some ? u[j] : 0.0f, by, v[j]);
         }
     }
+    if (groups > 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[j * kThreads + tid] = v[j];
+        weight[tid] = sum;
+        __syncthreads();
+        if (tid < lanes) {
+            for (int s = 1; s < groups && s < n; ++s) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += part[j * kThreads + s * lanes + tid];
+                sum += weight[s * lanes + tid];
+            }
+        }
+    }
+    if (tid >= lanes) return;
     const bool none = !(sum != 0.0f);
     const float inv = none ? 0.0f : 1.0f / sum, l2 = none ? -INFINITY : ref + log2_fast(sum);
-    if (8 * lane < D) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= inv;
-        kv_store8(type, a.out, token * a.ld_out + (row - token * heads) * D + 8 * lane, v);
-    }
-    if (lane == 0) {
-        if (a.lse != nullptr) a.lse[row] = l2 * kLn2;
-        if (sp.lse2 != nullptr) sp.lse2[row] = l2;
-    }
+    for (int j = 0; j < 8; ++j) v[j] *= inv;
+    kv_store8(type, a.out, attend_at(a, out_row, a.ld_out) + 8 * tid, v);
+    if (tid == 0) attend_lse(a, sp.lse2, out_row, l2);
 }
 
 // The weight that each entry got: mass[j] += sum over rows and heads of the group of
@@ -722,84 +714,108 @@ __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits s
     }
 }
 
-int64_t tiles_of(int64_t T, int64_t B, int64_t group, bool ragged) {
-    return ragged ? T * group / kRows + B : B * ((group + kRows - 1) / kRows);
+// ---- the shape of a call, from what the host knows
+struct Shape {
+    Splits sp;
+    int64_t few_tiles, many_tiles;  // times heads and splits: workgroups; many_tiles 0: no sequence has so many rows
+    int64_t few_rows, many_rows;    // rows that have parts
+    int64_t bytes;                  // of the workspace
+};
+Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D, bool ragged, bool mass) {
+    Shape p{};
+    p.sp.few_room = (int)(ragged ? kFewRows : (group + kRows - 1) / kRows * kRows);
+    p.few_tiles = B * (p.sp.few_room / kRows);
+    // slots of the other kernel's tiles: each sequence's first one starts at the slot of its first row + its number
+    p.many_tiles = ragged && T * group > kFewRows ? T * group / attend_rows_tile(type, D) + B : 0;
+    // Workgroups: four for each CU, but no split below one step of each of its wavefronts
+    auto splits = [&](int64_t tiles, int64_t want, int64_t step) {
+        const int64_t rounds = (capacity + step - 1) / step;
+        int64_t n = (want + tiles * heads - 1) / (tiles * heads);
+        n = n > rounds ? rounds : n;
+        return (int)(n > 256 ? 256 : (n < 1 ? 1 : n));
+    };
+    p.sp.few = splits(p.few_tiles, 1024, kKeys * kWaves);
+    p.sp.many = p.many_tiles ? splits(p.many_tiles, 512, 512) : 1;
+    p.few_rows = p.sp.few > 1 ? B * heads * p.sp.few_room : 0;
+    p.many_rows = p.sp.many > 1 ? T * heads * group : 0;
+    p.bytes = (p.sp.few * p.few_rows + p.sp.many * p.many_rows) * (D * 4 + 8) + (mass ? (T * heads * group * 4 + 15) / 16 * 16 : 0);
+    return p;
 }
-
-// Workgroups per tile: two for each CU, but no split below two steps of its wavefronts
-int64_t splits_of(int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, bool ragged) {
-    const int64_t tiles = tiles_of(T, B, group, ragged) * heads;
-    const int64_t rounds = (capacity + kKeys * kWaves - 1) / (kKeys * kWaves);
-    int64_t n = (1024 + tiles - 1) / tiles;
-    n = n > rounds ? rounds : n;
-    n = n > 256 ? 256 : n;
-    return n < 1 ? 1 : n;
+Shape shape_of(int type, const AttendArgs &a) {
+    Shape p = shape_of(type, a.c.T, a.c.B, (int64_t)a.c.width << a.c.page_log2, a.c.heads, a.group, a.c.D, a.c.starts != nullptr,
+                       a.mass != nullptr);
+    float *at = a.ws;
+    p.sp.few_sums = at;
+    at += p.sp.few * p.few_rows * a.c.D;
+    p.sp.many_sums = at;
+    at += p.sp.many * p.many_rows * a.c.D;
+    p.sp.few_stats = reinterpret_cast<float2 *>(at);
+    at += p.sp.few * p.few_rows * 2;
+    p.sp.many_stats = reinterpret_cast<float2 *>(at);
+    at += p.sp.many * p.many_rows * 2;
+    p.sp.lse2 = a.mass != nullptr ? at : nullptr;
+    return p;
 }
-
-int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+int64_t mass_tiles(const AttendArgs &a) {
+    return (((int64_t)a.c.width << a.c.page_log2) + kKeys * kWaves - 1) / (kKeys * kWaves);
+}
 
 template <int PIECES, int D>
-hipError_t launch(int type, const AttendArgs &a, const Splits &sp, hipStream_t s) {
-    const int64_t tiles = tiles_of(a.c.T, a.c.B, a.group, a.c.starts != nullptr);
+hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) {
     constexpr int bytes = kWaves * Ring<D>::WAVE;
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = ensure_lds_bytes((const void *)k_attend<PIECES, D>, bytes, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attend<PIECES, D>), dim3((unsigned)(tiles * sp.n * a.c.heads)), dim3(kThreads), bytes, s, a, sp, type);
+    hipLaunchKernelGGL((k_attend<PIECES, D>), dim3((unsigned)(p.few_tiles * p.sp.few * a.c.heads)), dim3(kThreads), bytes, s,
+                       a, p.sp, type);
     e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (sp.n > 1) {
-        hipLaunchKernelGGL(k_attend_join, dim3((unsigned)((sp.rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, s, a, sp, type);
+    if (e == hipSuccess && p.many_tiles) e = launch_attend_rows(type, a, p.sp, p.many_tiles, s);
+    if (e == hipSuccess && p.few_rows + p.many_rows) {
+        hipLaunchKernelGGL(k_attend_join, dim3((unsigned)(p.few_rows + p.many_rows)), dim3(kThreads), 0, s, a, p.sp, type,
+                           (int)p.few_rows);
         e = hipGetLastError();
-        if (e != hipSuccess) return e;
     }
-    if (a.mass == nullptr) return e;
-    const int per = ((a.c.width << a.c.page_log2) + kKeys * kWaves - 1) / (kKeys * kWaves);
-    hipLaunchKernelGGL((k_attend_mass<PIECES, D>), dim3((unsigned)((int64_t)a.c.B * per * a.c.heads)), dim3(kThreads), 0, s, a,
-                       sp, type, per);
+    if (e != hipSuccess || a.mass == nullptr) return e;
+    const int64_t per = mass_tiles(a);
+    hipLaunchKernelGGL((k_attend_mass<PIECES, D>), dim3((unsigned)(a.c.B * per * a.c.heads)), dim3(kThreads), 0, s, a, p.sp,
+                       type, (int)per);
     return hipGetLastError();
 }
 
 template <int PIECES>
-hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, hipStream_t s) {
+hipError_t launch_for(int type, const AttendArgs &a, const Shape &p, hipStream_t s) {
     switch (a.c.D) {
-        case 64: return launch<PIECES, 64>(type, a, sp, s);
-        case 96: return launch<PIECES, 96>(type, a, sp, s);
-        case 128: return launch<PIECES, 128>(type, a, sp, s);
-        case 192: return launch<PIECES, 192>(type, a, sp, s);
-        default: return launch<PIECES, 256>(type, a, sp, s);
+        case 64: return launch<PIECES, 64>(type, a, p, s);
+        case 96: return launch<PIECES, 96>(type, a, p, s);
+        case 128: return launch<PIECES, 128>(type, a, p, s);
+        case 192: return launch<PIECES, 192>(type, a, p, s);
+        default: return launch<PIECES, 256>(type, a, p, s);
     }
 }
 
 }  // namespace
 
-int64_t attend_workspace_bytes(int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
+int64_t attend_workspace_bytes(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
                                bool ragged, bool mass) {
-    const int64_t n = splits_of(T, B, capacity, heads, group, ragged), rows = T * heads * group;
-    return (n > 1 ? n * rows * (D * 4 + 8) : 0) + (mass ? up16(rows * 4) : 0);
+    return shape_of(type, T, B, capacity, heads, group, D, ragged, mass).bytes;
 }
 
-void attend_shape(const AttendArgs &a, int *splits) {
-    *splits = (int)splits_of(a.c.T, a.c.B, (int64_t)a.c.width << a.c.page_log2, a.c.heads, a.group, a.c.starts != nullptr);
+void attend_shape(int type, const AttendArgs &a, int *few, int *many) {
+    const Shape p = shape_of(type, a);
+    *few = p.sp.few;
+    *many = p.many_tiles ? p.sp.many : 0;
 }
 
-bool attend_grid_ok(const AttendArgs &a) {
-    constexpr int64_t most = (int64_t(1) << 24) - 1;  // workgroups of 256 threads
-    const int64_t capacity = (int64_t)a.c.width << a.c.page_log2, rows = (int64_t)a.c.T * a.c.heads * a.group;
-    const bool ragged = a.c.starts != nullptr;
-    const int64_t n = splits_of(a.c.T, a.c.B, capacity, a.c.heads, a.group, ragged);
-    return tiles_of(a.c.T, a.c.B, a.group, ragged) * n * a.c.heads <= most && (rows + kWaves - 1) / kWaves <= most &&
-           (a.mass == nullptr || a.c.B * ((capacity + kKeys * kWaves - 1) / (kKeys * kWaves)) * a.c.heads <= most);
+bool attend_grid_ok(int type, const AttendArgs &a) {
+    constexpr int64_t most = (int64_t(1) << 24) - 1;  // workgroups of 256 threads; half as many of 512
+    const Shape p = shape_of(type, a);
+    return p.few_tiles * p.sp.few * a.c.heads <= most && p.many_tiles * p.sp.many * a.c.heads <= most / 2 &&
+           p.few_rows + p.many_rows <= most && (a.mass == nullptr || a.c.B * mass_tiles(a) * a.c.heads <= most);
 }
 
 hipError_t launch_attend(int type, const AttendArgs &a, hipStream_t s) {
-    Splits sp{};
-    sp.n = (int)splits_of(a.c.T, a.c.B, (int64_t)a.c.width << a.c.page_log2, a.c.heads, a.group, a.c.starts != nullptr);
-    sp.rows = (int64_t)a.c.T * a.c.heads * a.group;
-    sp.sums = a.ws;
-    sp.stats = reinterpret_cast<float2 *>(a.ws + (sp.n > 1 ? sp.n * sp.rows * a.c.D : 0));
-    sp.lse2 = a.mass != nullptr ? a.ws + (sp.n > 1 ? sp.n * sp.rows * (a.c.D + 2) : 0) : nullptr;
-    return type == 0 ? launch_for<2>(type, a, sp, s) : launch_for<1>(type, a, sp, s);
+    const Shape p = shape_of(type, a);
+    return type == 0 ? launch_for<2>(type, a, p, s) : launch_for<1>(type, a, p, s);
 }
 
 }  // namespace qmm

@@ -284,10 +284,11 @@ struct AttendArgs {
     int group, window;       // window 0: none
     bool causal;
 };
-int64_t attend_workspace_bytes(int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
+int64_t attend_workspace_bytes(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
                                bool ragged, bool mass);
-void attend_shape(const AttendArgs &a, int *splits);  // of a launch
-bool attend_grid_ok(const AttendArgs &a);  // every launch fits a grid
+// splits of sequences with few rows, and with many (0: there can be none)
+void attend_shape(int type, const AttendArgs &a, int *few, int *many);
+bool attend_grid_ok(int type, const AttendArgs &a);  // every launch fits a grid
 hipError_t launch_attend(int type, const AttendArgs &a, hipStream_t s);
 
 // eviction: the entries that stay move from c.table's pages to those of `to`

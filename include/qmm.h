@@ -537,10 +537,10 @@ qmm_status qmm_cache_write(const qmm_cache *c, qmm_float_type t, const void *k, 
 qmm_status qmm_cache_read(const qmm_cache *c, qmm_float_type t, void *k, size_t k_bytes, void *v, size_t v_bytes,
                           void *stream);
 
-/* Bytes of the workspace qmm_cache_attention needs (0: none).  q_heads query heads; ragged: starts is given; mass:
+/* Bytes of the workspace qmm_cache_attention needs (0: none).  q_heads query heads of format t; ragged: starts is given; mass:
  * mass is. */
-size_t qmm_cache_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t dim, int64_t seqs,
-                                           int64_t width, int64_t page, int ragged, int mass);
+size_t qmm_cache_attention_workspace_bytes(qmm_float_type t, int64_t rows, int64_t q_heads, int64_t heads, int64_t dim,
+                                           int64_t seqs, int64_t width, int64_t page, int ragged, int mass);
 
 /* Attention of the call's rows over the entries of their sequences: query head h of a row at position p, with the
  * keys k_j and values v_j of cache head h / (q_heads / heads),

@@ -149,7 +149,7 @@ def test_cache_attention_refusals(lib):  # noqa: F811
     assert call(qb=7 * 768 * 4 - 1) == EINVAL and call(ob=7 * 768 * 4 - 1) == EINVAL
     assert call(ldm=127) == EINVAL and "ld_mass" in _last(lib)
     size = lib.qmm_cache_attention_workspace_bytes
-    need = size(7, 6, 2, 128, 3, 4, 32, 1, 1)
+    need = size(0, 7, 6, 2, 128, 3, 4, 32, 1, 1)
     assert need > 0 and call(wsb=need - 1) == EINVAL and "workspace" in _last(lib)
     for o in ("o", "lse", "mass", "ws"):
         for i in ("data", "table", "lens", "starts"):
@@ -166,7 +166,8 @@ def test_cache_attention_refusals(lib):  # noqa: F811
     assert call(**many) == EUNSUP and "workgroups" in _last(lib)
     for bad in ((0, 6, 2, 128, 3, 4, 32), (7, 5, 2, 128, 3, 4, 32), (7, 6, 2, 100, 3, 4, 32), (7, 6, 2, 128, 0, 4, 32),
                 (7, 6, 2, 128, 3, 0, 32), (7, 6, 2, 128, 3, 4, 40), (2**22 + 1, 6, 2, 128, 3, 4, 32)):
-        assert size(*bad, 1, 1) == 0, bad
+        assert size(0, *bad, 1, 1) == 0, bad
+    assert size(3, 7, 6, 2, 128, 3, 4, 32, 1, 1) == 0
 
 
 def lambda_with(call, **more):
