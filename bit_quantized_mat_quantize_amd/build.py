@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(ROOT, "_build_asan" if os.environ.get("QMM_ASAN") else 
 SOURCES = ["api.hip", "quantize.hip", "repack.hip", "gemv.hip", "skinny.hip", "skinny16.hip", "skinny16r.hip", "skinny32r.hip", "q6k.hip", "q6k_gemm.hip", "q6k_skinny.hip",
            "q2k.hip", "q2k_gemm.hip", "q2k_skinny.hip", "q40_gemm.hip", "q40_skinny.hip", "moe.hip", "gemm.hip",
            "embed.hip", "lora.hip", "logprobs.hip", "rope.hip", "kv_cache.hip", "attention.hip",
-           "attend_rows.hip", "evict.hip"]
+           "attend_rows.hip", "attend_mass.hip", "evict.hip"]
 PROBE_SOURCES = ["probe.hip"]
 PROBE_OUT = os.path.join(PKG, "libqmm_probe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -68,13 +68,10 @@ struct Decode {
 __device__ __forceinline__ h2 centred_even(h2 x) { return x - h2{(_Float16)1032.0f, (_Float16)1032.0f}; }
 __device__ __forceinline__ h2 centred_odd(h2 x) { return x - h2{(_Float16)1152.0f, (_Float16)1152.0f}; }
 
-// Eight codes of a word against query_pieces.  CENTRED: u - 8, exact; else 1024 + u (16 times
-// that for the odd ones), whose product with the query is that much too large by
-// 1032 (1152) times the sum of its even (odd) elements.
-template <bool CENTRED>
+// eight codes of a word against query_pieces
 __device__ __forceinline__ h8 key_codes(const Decode &k, uint32_t w) {
-    h2 a = k.even(w), b = k.odd(w), c = k.even(w >> 8), d = k.odd(w >> 8);
-    if constexpr (CENTRED) a = centred_even(a), b = centred_odd(b), c = centred_even(c), d = centred_odd(d);
+    const h2 a = centred_even(k.even(w)), b = centred_odd(k.odd(w)), c = centred_even(k.even(w >> 8)),
+             d = centred_odd(k.odd(w >> 8));
     return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
@@ -139,5 +136,9 @@ __device__ __forceinline__ void attend_lse(const AttendArgs &a, float *lse2, int
 // attend_rows.hip: sequences of more than kFewRows rows
 int64_t attend_rows_tile(int type, int64_t D);  // rows of a tile
 hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s);
+
+// attend_mass.hip: the weights of their entries; workgroups per sequence and head
+int64_t attend_mass_tiles(const AttendArgs &a);
+hipError_t launch_attend_mass_rows(int type, const AttendArgs &a, const Splits &sp, hipStream_t s);
 
 }  // namespace qmm

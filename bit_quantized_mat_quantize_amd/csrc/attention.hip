@@ -92,30 +92,15 @@ __device__ __forceinline__ void read_step(const KvCache &c, int b, int head, int
 // A lane's share of 16 query rows: row n, elements 8 g .. 8 g + 7 of each block
 template <int PIECES, int D>
 struct Query {
-    static constexpr bool CENTRED = PIECES == 2;
-    h8 hi[D / 32], lo[CENTRED ? D / 32 : 1];
-    f4 less[CENTRED ? 1 : D / 32];  // what the products are too large by (key_codes), block by block, negative
+    h8 hi[D / 32], lo[PIECES == 2 ? D / 32 : 1];
 
     __device__ __forceinline__ void set(const float (&x)[D / 32][8], float by) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            if constexpr (CENTRED) query_pieces<2>(x[i], by, hi[i], lo[i]);
-            else {
-                query_pieces<1>(x[i], by, hi[i], lo[0]);
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum = fmaf((j >> 1) & 1 ? 1152.0f : 1032.0f, (float)hi[i][j], sum);
-                sum += __shfl_xor(sum, 16, 64);
-                sum += __shfl_xor(sum, 32, 64);
-                less[i] = f4{-sum, -sum, -sum, -sum};
-            }
-        }
+        for (int i = 0; i < D / 32; ++i) query_pieces<PIECES>(x[i], by, hi[i], lo[PIECES == 2 ? i : 0]);
     }
 };
 
 // Products of 32 entries with the queries: x[4 s + r] is entry 16 s + 4 g + r against row n.
-// For 16-bit queries the codes go in as 1024 + u, which saves half of their decode: the sums of
-// 32 products then reach 1032 times a query's sum, and their rounding 3e-5 of a score.
 template <int PIECES, int D>
 __device__ __forceinline__ void products(const Decode &k, const Step<D> &t, const Query<PIECES, D> &q, float *x) {
 #pragma unroll
@@ -123,10 +108,9 @@ __device__ __forceinline__ void products(const Decode &k, const Step<D> &t, cons
         f4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
-            const h8 codes = key_codes<PIECES == 2>(k, t.k[s][b]);
-            f4 dot;
-            if constexpr (PIECES == 2) dot = mfma16(codes, q.lo[b], mfma16(codes, q.hi[b], f4{0, 0, 0, 0}));
-            else dot = mfma16(codes, q.hi[b], q.less[b]);
+            const h8 codes = key_codes(k, t.k[s][b]);
+            f4 dot = mfma16(codes, q.hi[b], f4{0, 0, 0, 0});
+            if constexpr (PIECES == 2) dot = mfma16(codes, q.lo[b], dot);
             const h2 d0 = as_h2(t.ks[s][b].x), d1 = as_h2(t.ks[s][b].y);
             acc[0] = fmaf((float)d0.x, dot[0], acc[0]);
             acc[1] = fmaf((float)d0.y, dot[1], acc[1]);
@@ -136,7 +120,8 @@ __device__ __forceinline__ void products(const Decode &k, const Step<D> &t, cons
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[4 * s + r] = acc[r];
     }
-    if (t.bad) {  // the same for the whole wavefront
+    if (__builtin_expect(t.bad != 0, 0)) {  // the same for the whole wavefront
+        asm volatile("");                      // not worth eight selects in every step
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = (t.bad >> (i >> 2)) & 1 ? __builtin_nanf("") : x[i];
     }
@@ -152,8 +137,7 @@ struct Ring {
     static constexpr int CODES = (16 * D + 1023) / 1024, SCALES = (2 * D + 255) / 256;  // load instructions
     static constexpr int SCALE_AT = 1024 * CODES, GROUP = SCALE_AT + 256 * SCALES, BYTES = 2 * GROUP;
     static constexpr int LOADS = 2 * (CODES + SCALES);
-    // steps in LDS: two workgroups of four wavefronts per CU
-    static constexpr int SLOTS = D <= 128 ? 4 : 2;
+    static constexpr int SLOTS = 2;  // steps in LDS
     static constexpr int WAVE = SLOTS * BYTES;
     uint32_t code_at[CODES], scale_at[SCALES];  // this lane's place in a chunk pair, per instruction
     uint32_t records;                           // bytes from a page's keys to the end of its values, of one head
@@ -188,11 +172,11 @@ struct Ring {
 #pragma unroll
         for (int i = 0; i < CODES; ++i)
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + 1024 * i),
-                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "memory", "m0");
+                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "memory");
 #pragma unroll
         for (int i = 0; i < SCALES; ++i)
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to + SCALE_AT + 256 * i),
-                         "v"(scale_at[i]), "s"(r), "s"(e0 * 2) : "memory", "m0");
+                         "v"(scale_at[i]), "s"(r), "s"(e0 * 2) : "memory");
     }
     __device__ __forceinline__ void read(int slot, Step<D> &t) const {
         constexpr int NB = D / 32, ROUNDS = Step<D>::ROUNDS, WORDS = D / 8;
@@ -452,7 +436,7 @@ __device__ __forceinline__ void step(const Decode &k, Step<D> &t, const Tile<PIE
 }
 
 template <int PIECES, int D>
-__global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp, int type) {
+__global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attend(AttendArgs a, Splits sp, int type) {
     constexpr int ROUNDS = Step<D>::ROUNDS, PITCH = D + 4;
     using R = Ring<D>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -461,7 +445,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp,
     __shared__ float2 stats[kWaves][kRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, split = x % sp.few;
-    const int per = sp.few_room / kRows, b = x / sp.few / per, tile = x / sp.few - b * per;
+    const int per = (sp.few_room + kRows - 1) / kRows, b = x / sp.few / per, tile = x / sp.few - b * per;
     if (kv_rows(a.c, b).count * a.group > sp.few_room) return;  // the other kernel's
     Tile<PIECES, D> q;
     q.type = type;
@@ -602,68 +586,76 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a, Splits sp,
     }
 }
 
-// The splits of a row joined: one workgroup per row.  Lane group s of kThreads / (D/8) takes
-// the splits s, s + groups, ..; the groups are added in their order.  Workgroups below
-// few_blocks take the rows of sequences with few, by (sequence, head, row), the others
-// those of the rest, by output row.
-__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits sp, int type, int few_blocks) {
+// The splits of a row joined.  A row's part of a workgroup is `lanes` threads (64, or 256
+// for rows of many splits): thread t of them has elements 8 (t % (D/8)) .. of the splits
+// t / (D/8), + groups, ..; the groups' sums are added in their order.  Rows below few_rows
+// are those of sequences with few, by (sequence, head, row), the others by output row.
+template <int LANES>
+__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits sp, int type, int few_rows, int all_rows) {
     __shared__ float part[kThreads * 8];
-    __shared__ float weight[kThreads];
-    const int D = a.c.D, lanes = D / 8, groups = kThreads / lanes, tid = threadIdx.x;
-    int64_t out_row, row, rows;
-    const float *sums;
-    const float2 *stats;
-    int n;
-    if ((int)blockIdx.x < few_blocks) {
-        const int r = blockIdx.x % sp.few_room, bh = blockIdx.x / sp.few_room, b = bh / a.c.heads, head = bh - b * a.c.heads;
+    __shared__ float weight[kThreads], by[kThreads];
+    const int D = a.c.D, each = D / 8, groups = LANES / each;
+    const int tid = threadIdx.x % LANES, base = threadIdx.x - tid;
+    const int at = blockIdx.x * (kThreads / LANES) + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
+    int64_t out_row = 0, row = 0, rows = 0;
+    const float *sums = nullptr;
+    const float2 *stats = nullptr;
+    int n = 0;
+    if (at < few_rows) {
+        const int r = at % sp.few_room, bh = at / sp.few_room, b = bh / a.c.heads, head = bh - b * a.c.heads;
         const KvRows k = kv_rows(a.c, b);
-        if (r >= k.count * a.group || k.count * a.group > sp.few_room) return;
-        out_row = attend_out_row(a, k, head, r);
-        row = blockIdx.x;
-        rows = (int64_t)a.c.B * a.c.heads * sp.few_room;
-        sums = sp.few_sums;
-        stats = sp.few_stats;
-        n = sp.few;
-    } else {
-        row = out_row = blockIdx.x - few_blocks;
+        if (r < k.count * a.group && k.count * a.group <= sp.few_room) {
+            out_row = attend_out_row(a, k, head, r);
+            row = at;
+            rows = (int64_t)a.c.B * a.c.heads * sp.few_room;
+            sums = sp.few_sums;
+            stats = sp.few_stats;
+            n = sp.few;
+        }
+    } else if (at < all_rows) {
+        row = out_row = at - few_rows;
         rows = (int64_t)a.c.T * a.c.heads * a.group;
         const int b = kv_sequence(a.c, (int)(out_row / (a.c.heads * a.group)));
-        if (b < 0 || kv_rows(a.c, b).count * a.group <= sp.few_room) return;
-        sums = sp.many_sums;
-        stats = sp.many_stats;
-        n = sp.many;
+        if (b >= 0 && kv_rows(a.c, b).count * a.group > sp.few_room) {
+            sums = sp.many_sums;
+            stats = sp.many_stats;
+            n = sp.many;
+        }
     }
-    const int s0 = tid / lanes, e = tid - s0 * lanes;
-    float ref = -INFINITY;
-    for (int s = 0; s < n; ++s) ref = fmaxf(ref, stats[s * rows + row].x);
-    float v[8] = {}, sum = 0.0f;
+    // n <= LANES splits: a thread has one's reference and sum
+    float2 st = make_float2(-INFINITY, 0.0f);
+    if (tid < n) st = stats[tid * rows + row];
+    float ref = st.x, sum = 0.0f, v[8] = {};
+    for (int o = 1; o < 64; o <<= 1) ref = fmaxf(ref, __shfl_xor(ref, o, 64));
+    if (LANES > 64) {
+        if ((tid & 63) == 0) weight[threadIdx.x] = ref;
+        __syncthreads();
+        for (int w = 0; w < LANES / 64; ++w) ref = fmaxf(ref, weight[base + 64 * w]);
+        __syncthreads();
+    }
+    const bool some = st.y != 0.0f;  // else nothing was seen, and nothing written
+    by[threadIdx.x] = !some ? 0.0f : (st.x == -INFINITY ? 1.0f : exp2_fast(st.x - ref));
+    weight[threadIdx.x] = some ? st.y * by[threadIdx.x] : 0.0f;
+    __syncthreads();
+    const int s0 = tid / each, e = tid - s0 * each;
     if (s0 < groups) {
 #pragma unroll 4
         for (int s = s0; s < n; s += groups) {
-            const float2 st = stats[s * rows + row];
             float u[8];
             kv_load8<0>(sums, (s * rows + row) * D + 8 * e, u);
-            const bool some = st.y != 0.0f;  // else nothing was seen, and nothing written
-            const float by = !some ? 0.0f : (st.x == -INFINITY ? 1.0f : exp2_fast(st.x - ref));
-            sum += st.y * by;
+            const float f = by[base + s];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = fmaf(some ? u[j] : 0.0f, by, v[j]);
+            for (int j = 0; j < 8; ++j) v[j] = f != 0.0f ? fmaf(u[j], f, v[j]) : v[j];
         }
     }
-    if (groups > 1) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) part[j * kThreads + tid] = v[j];
-        weight[tid] = sum;
-        __syncthreads();
-        if (tid < lanes) {
-            for (int s = 1; s < groups && s < n; ++s) {
+    for (int j = 0; j < 8; ++j) part[j * kThreads + threadIdx.x] = v[j];
+    __syncthreads();
+    if (n == 0 || tid >= each) return;
+    for (int s = 1; s < groups && s < n; ++s)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += part[j * kThreads + s * lanes + tid];
-                sum += weight[s * lanes + tid];
-            }
-        }
-    }
-    if (tid >= lanes) return;
+        for (int j = 0; j < 8; ++j) v[j] += part[j * kThreads + base + s * each + tid];
+    for (int s = 0; s < n; ++s) sum += weight[base + s];
     const bool none = !(sum != 0.0f);
     const float inv = none ? 0.0f : 1.0f / sum, l2 = none ? -INFINITY : ref + log2_fast(sum);
 #pragma unroll
@@ -672,16 +664,16 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits s
     if (tid == 0) attend_lse(a, sp.lse2, out_row, l2);
 }
 
-// The weight that each entry got: mass[j] += sum over rows and heads of the group of
-// 2^(x - lse2).  A wavefront owns 32 entries of a head and goes over all rows that can
-// see them, 16 at a time, so every place is added to by one lane, in a fixed order.
+// The weight that each entry got, for sequences of few rows: mass[j] += sum over rows and
+// heads of the group of 2^(x - lse2).  A wavefront owns 32 entries of a head and goes
+// over the rows, 16 at a time, so every place is added to by one lane, in a fixed order.
 template <int PIECES, int D>
 __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits sp, int type, int tiles) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, b = x / tiles;
     const int k0 = ((x - b * tiles) * kWaves + wave) * kKeys;
     const KvRows rows = kv_rows(a.c, b);
-    if (k0 >= rows.len || rows.count == 0) return;
+    if (k0 >= rows.len || rows.count == 0 || rows.count * a.group > sp.few_room) return;
     Step<D> t;
     read_step<D>(a.c, b, head, k0, (rows.len - 1) & ~15, t);
     Decode decode;
@@ -723,19 +715,19 @@ struct Shape {
 };
 Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D, bool ragged, bool mass) {
     Shape p{};
-    p.sp.few_room = (int)(ragged ? kFewRows : (group + kRows - 1) / kRows * kRows);
-    p.few_tiles = B * (p.sp.few_room / kRows);
+    p.sp.few_room = (int)(ragged ? kFewRows : group);
+    p.few_tiles = B * ((p.sp.few_room + kRows - 1) / kRows);
     // slots of the other kernel's tiles: each sequence's first one starts at the slot of its first row + its number
     p.many_tiles = ragged && T * group > kFewRows ? T * group / attend_rows_tile(type, D) + B : 0;
     // Workgroups: four for each CU, but no split below one step of each of its wavefronts
     auto splits = [&](int64_t tiles, int64_t want, int64_t step) {
         const int64_t rounds = (capacity + step - 1) / step;
-        int64_t n = (want + tiles * heads - 1) / (tiles * heads);
+        int64_t n = want / (tiles * heads);
         n = n > rounds ? rounds : n;
         return (int)(n > 256 ? 256 : (n < 1 ? 1 : n));
     };
     p.sp.few = splits(p.few_tiles, 1024, kKeys * kWaves);
-    p.sp.many = p.many_tiles ? splits(p.many_tiles, 512, 512) : 1;
+    p.sp.many = p.many_tiles ? splits(p.many_tiles, 256, 512) : 1;
     p.few_rows = p.sp.few > 1 ? B * heads * p.sp.few_room : 0;
     p.many_rows = p.sp.many > 1 ? T * heads * group : 0;
     p.bytes = (p.sp.few * p.few_rows + p.sp.many * p.many_rows) * (D * 4 + 8) + (mass ? (T * heads * group * 4 + 15) / 16 * 16 : 0);
@@ -756,9 +748,7 @@ Shape shape_of(int type, const AttendArgs &a) {
     p.sp.lse2 = a.mass != nullptr ? at : nullptr;
     return p;
 }
-int64_t mass_tiles(const AttendArgs &a) {
-    return (((int64_t)a.c.width << a.c.page_log2) + kKeys * kWaves - 1) / (kKeys * kWaves);
-}
+static_assert(kKeys * kWaves == 128, "both kernels of the weights take 128 entries a workgroup");
 
 template <int PIECES, int D>
 hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) {
@@ -771,12 +761,20 @@ hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) 
     e = hipGetLastError();
     if (e == hipSuccess && p.many_tiles) e = launch_attend_rows(type, a, p.sp, p.many_tiles, s);
     if (e == hipSuccess && p.few_rows + p.many_rows) {
-        hipLaunchKernelGGL(k_attend_join, dim3((unsigned)(p.few_rows + p.many_rows)), dim3(kThreads), 0, s, a, p.sp, type,
-                           (int)p.few_rows);
+        const int64_t rows = p.few_rows + p.many_rows;
+        // few rows of many splits: a workgroup each
+        if ((p.few_rows && p.sp.few > 64) || (p.many_rows && p.sp.many > 64) || rows <= 512)
+            hipLaunchKernelGGL(k_attend_join<kThreads>, dim3((unsigned)rows), dim3(kThreads), 0, s, a, p.sp, type,
+                               (int)p.few_rows, (int)rows);
+        else
+            hipLaunchKernelGGL(k_attend_join<64>, dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s, a, p.sp, type,
+                               (int)p.few_rows, (int)rows);
         e = hipGetLastError();
     }
     if (e != hipSuccess || a.mass == nullptr) return e;
-    const int64_t per = mass_tiles(a);
+    if (p.many_tiles) e = launch_attend_mass_rows(type, a, p.sp, s);
+    if (e != hipSuccess) return e;
+    const int64_t per = attend_mass_tiles(a);
     hipLaunchKernelGGL((k_attend_mass<PIECES, D>), dim3((unsigned)(a.c.B * per * a.c.heads)), dim3(kThreads), 0, s, a, p.sp,
                        type, (int)per);
     return hipGetLastError();
@@ -810,7 +808,7 @@ bool attend_grid_ok(int type, const AttendArgs &a) {
     constexpr int64_t most = (int64_t(1) << 24) - 1;  // workgroups of 256 threads; half as many of 512
     const Shape p = shape_of(type, a);
     return p.few_tiles * p.sp.few * a.c.heads <= most && p.many_tiles * p.sp.many * a.c.heads <= most / 2 &&
-           p.few_rows + p.many_rows <= most && (a.mass == nullptr || a.c.B * mass_tiles(a) * a.c.heads <= most);
+           p.few_rows + p.many_rows <= most && (a.mass == nullptr || a.c.B * attend_mass_tiles(a) * a.c.heads <= most / 2);
 }
 
 hipError_t launch_attend(int type, const AttendArgs &a, hipStream_t s) {
