@@ -173,22 +173,45 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
             }
         }
     };
-    uint32_t bound = 0;        // of this wavefront's side's scales
     int key_shift = 15, value_shift_ = 15;
     uint32_t key_bound = 0, value_bound = 0;
-    auto put = [&](int step, const Raw<D> &raw) {
+    auto put = [&](int step, Raw<D> &raw) {
         uint8_t *stage = lds + (step & 1) * S::STAGE;
         const int e = 16 * group, k0 = step * KT + e;  // in LDS; in the sequence
-        const bool edge = k0 < first || k0 + 16 > last;
-        uint32_t top = 0, bad = 0;  // bits of this group's 16 entries
+        constexpr int SCALES = NB > 2 * ROUNDS ? NB : 2 * ROUNDS;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < SCALES; ++i)
+            if (i < (keys ? NB : 2 * ROUNDS)) top = max_u16x2(top, raw.s[i] & 0x7fff7fffu);
+        top = (top & 0xffffu) > (top >> 16) ? top & 0xffffu : top >> 16;
+        if (k0 < first || k0 + 16 > last || nowhere || __any(top >= (keys ? key_bound : value_bound))) {
+            // entries that no row sees are zero, values that are not finite too (their entries' scores are
+            // made NaN), and a scale beyond all so far is told to the workgroup
+            uint32_t bad = 0;  // bits of the group's 16 entries
+            auto keep = [&](uint32_t &s, int i, int at) {  // 16-bit scale i of s, of entry `at` of the group
+                const uint32_t m = (s >> (16 * i)) & 0x7fffu;
+                const bool out = k0 + at < first || k0 + at >= last;
+                if (out || (m >= 0x7c00u && !keys)) s &= i ? 0xffffu : 0xffff0000u;
+                if (!out && (nowhere || (m >= 0x7c00u && !keys))) bad |= 1u << at;
+                return out || m >= 0x7c00u ? 0u : m;
+            };
+            top = 0;
+#pragma unroll
+            for (int i = 0; i < SCALES; ++i)
+                if (i < (keys ? NB : 2 * ROUNDS)) {
+                    const uint32_t m0 = keys ? keep(raw.s[i], 0, ke) : keep(raw.s[i], 0, 4 * ve + 2 * (i & 1));
+                    const uint32_t m1 = keys ? 0u : keep(raw.s[i], 1, 4 * ve + 2 * (i & 1) + 1);
+                    top = m0 > top ? m0 : top;
+                    top = m1 > top ? m1 : top;
+                }
+            if (top >= (keys ? key_bound : value_bound)) atomicMax(&largest[step & 1][keys ? 0 : 1], top);
+            if (bad) atomicOr(&unfit[step % 3][e >> 5], bad << (e & 31));
+        }
         if (keys) {
             const _Float16 unit = (_Float16)pow2i(key_shift);
-            const bool out = edge && (k0 + ke < first || k0 + ke >= last);
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                const uint32_t s = out ? 0 : raw.s[i], m = s & 0x7fffu;
-                top = m > top && m < 0x7c00u ? m : top;
-                const uint32_t ss = s | s << 16;
+                const uint32_t ss = raw.s[i] | raw.s[i] << 16;
                 const h2 d = as_h2(ss) * h2{unit, unit};
                 const uint32_t w = raw.w[i];
                 const h2 c[4] = {centred_even(decode.even(w)), centred_odd(decode.odd(w)), centred_even(decode.even(w >> 8)),
@@ -205,24 +228,13 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                         make_uint4(as_u32(h[0]), as_u32(h[1]), as_u32(h[2]), as_u32(h[3]));
                 }
             }
-            bound = key_bound;
         } else {
             stage += PIECES * S::KEYS;
             const _Float16 unit = (_Float16)pow2i(value_shift_);
 #pragma unroll
             for (int r = 0; r < ROUNDS; ++r) {
                 const int w = 16 * r + vw;
-                uint32_t s[2] = {raw.s[2 * r], raw.s[2 * r + 1]};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t m = (s[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
-                    const int at = k0 + 4 * ve + i;
-                    const bool out = edge && (at < first || at >= last);
-                    if (out || m >= 0x7c00u) s[i >> 1] &= i & 1 ? 0xffffu : 0xffff0000u;
-                    if (!out && m >= 0x7c00u) bad |= 1u << (4 * ve + i);
-                    top = m > top && !out && m < 0x7c00u ? m : top;
-                }
-                const h2 d[2] = {as_h2(s[0]) * h2{unit, unit}, as_h2(s[1]) * h2{unit, unit}};
+                const h2 d[2] = {as_h2(raw.s[2 * r]) * h2{unit, unit}, as_h2(raw.s[2 * r + 1]) * h2{unit, unit}};
                 if (w < WORDS) {
                     // entries 4 ve .. within the eight that a lane of the product holds: 0 and 2, or 1 and 3
                     const int c = 2 * group + (ve & 1), half = (ve >> 1) * 8;
@@ -245,11 +257,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                     }
                 }
             }
-            bound = value_bound;
         }
-        if (nowhere) bad = edge ? 0xffffu & (last > k0 ? (last - k0 >= 16 ? 0xffffu : (1u << (last - k0)) - 1) : 0u) : 0xffffu;
-        if (__any(top >= bound)) atomicMax(&largest[step & 1][keys ? 0 : 1], top);
-        if (__any(bad != 0) && bad) atomicOr(&unfit[step % 3][e >> 5], bad << (e & 31));
     };
 
     // ---- the rows' running results
@@ -268,6 +276,9 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
 
     if (threadIdx.x < 10) flags[threadIdx.x] = 0;
     __syncthreads();
+    // The two wavefronts of a SIMD would all multiply, or all form weights, at the same time; with
+    // one ahead of the other, its weights are formed while the other multiplies.
+    if (wave < S::WAVES / 2) __builtin_amdgcn_s_setprio(1);
     Raw<D> raw;
     if (from < to) {
         load(from, raw);
@@ -316,7 +327,8 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                     }
                 }
                 const uint32_t bad = __builtin_amdgcn_readfirstlane(unfit[step % 3][sub]);
-                if (bad) {
+                if (__builtin_expect(bad != 0, 0)) {
+                    asm volatile("");  // not worth a select per score
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         if ((bad >> (8 * (r >> 2) + 4 * hf + (r & 3))) & 1) x[r] = __builtin_nanf("");
