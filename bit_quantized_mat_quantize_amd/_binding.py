@@ -850,8 +850,8 @@ def cache_evict(cache, table, lens, mass, budget: int, recent: int = 0, to=None,
     """(lens, mass, ids) after at most `budget` entries of each sequence and head stay: the newest `recent` and, of the
     others, those of the largest mass (fp32 [B, heads, n] as in cache_attention), ties to the lower position.
 
-    They move in their order into the pages of `to` (int32 [B, pages]), which are the sequences' own (None, or a table
-    with the same pages in the same places) or others that no sequence uses.  ids: int32 [B, heads, budget], where they
+    They move in their order within the sequences' own pages (to: None; no two sequences may share one then), or into
+    those of `to` (int32 [B, pages]), which must be none of the table's.  ids: int32 [B, heads, budget], where they
     were, -1 behind; mass: fp32 [B, heads, pages of `to` * page], 0 behind; lens: int32 [B]."""
     import torch
     if mass.requires_grad and torch.is_grad_enabled():

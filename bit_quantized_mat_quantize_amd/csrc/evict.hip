@@ -5,20 +5,22 @@
 // k_evict_select, one workgroup per (sequence, head): the weights' bits, mapped to
 // unsigned keys of the same order, by radix select in digits of 11, 11 and 10 bits (a
 // histogram in LDS each: integer counts, so their order does not matter), which gives the
-// key of the last entry that stays and how many of its equals do; then each
-// wavefront counts and writes its own range's places by ballots.
+// key of the last entry that stays and how many of its equals do; then the places
+// of what stays by ballots and a sum over wavefronts, in the entries' order.  The keys
+// stay in registers up to 16384 entries.
 //
-// k_evict_move, one workgroup per (sequence, head, keys or values): entries in
-// ascending order, a chunk at a time, where all of a chunk is in registers before
-// any of it is stored.  An entry only ever moves down, so chunks yet to be read lie
-// above everything stored before: the pages may be the sequence's own.
+// k_evict_move: entries in ascending order.  Into other pages every chunk has a workgroup
+// of its own.  Within the same pages one workgroup per (sequence, head, keys or
+// values) goes through them, all of a chunk in registers before any of it is
+// stored: an entry only ever moves down, so chunks yet to be read lie above everything
+// stored before.
 #include "kv_device.h"
 
 namespace qmm {
 namespace {
 
-constexpr int kSelect = 1024, kBins = 2048;
-constexpr int kMove = 1024;
+constexpr int kSelect = 1024, kWaves = kSelect / 64, kBins = 2048;
+constexpr int kMove = 256;
 
 // larger keys for larger weights, -0 as 0, NaN above all
 __device__ __forceinline__ uint32_t order_key(float m) {
@@ -27,9 +29,11 @@ __device__ __forceinline__ uint32_t order_key(float m) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// KEYS: entries per thread that stay in registers (0: none do, they are read anew)
+template <int KEYS>
 __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
     __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t wave_above[kSelect / 64], wave_equal[kSelect / 64];
+    __shared__ uint32_t sums[2][KEYS > 1 ? KEYS : 1][kWaves];
     __shared__ uint32_t found[2];  // the digit, and what is left to take within it
     const int h = blockIdx.x % a.c.heads, b = blockIdx.x / a.c.heads, tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
@@ -49,85 +53,154 @@ __global__ __launch_bounds__(kSelect) void k_evict_select(EvictArgs a) {
         return;
     }
     const int old = L - a.recent, need = a.budget - a.recent;  // recent <= budget < L
+    float m[KEYS > 0 ? KEYS : 1];
+    if constexpr (KEYS > 0) {
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j) m[j] = j * kSelect + tid < old ? mass[j * kSelect + tid] : 0.0f;
+    }
     for (int i = tid; i < a.recent; i += kSelect) {
         ids[need + i] = old + i;
         mass_out[need + i] = mass[old + i];
     }
     if (need == 0) return;
+    // f(position, weight) for this thread's entries among the old ones
+    auto each = [&](auto f) {
+        if constexpr (KEYS > 0) {
+#pragma unroll
+            for (int j = 0; j < KEYS; ++j)
+                if (j * kSelect + tid < old) f(j * kSelect + tid, m[j]);
+        } else
+            for (int i = tid; i < old; i += kSelect) f(i, mass[i]);
+    };
     uint32_t prefix = 0, left = need;  // the key's digits found so far; entries to take among those that share them
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-        for (int i = tid; i < kBins; i += kSelect) hist[i] = 0;
+        reinterpret_cast<uint2 *>(hist)[tid] = make_uint2(0, 0);
         __syncthreads();
-        for (int i = tid; i < old; i += kSelect) {
-            const uint32_t key = order_key(mass[i]);
+        each([&](int, float w) {
+            const uint32_t key = order_key(w);
             if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1u);
-        }
+        });
         __syncthreads();
-        if (wave == 0) {  // from the largest digit down: lane i has the bins behind i * kBins / 64 of them
-            constexpr int per = kBins / 64;
-            uint32_t sum = 0;
-            for (int i = 0; i < per; ++i) sum += hist[kBins - 1 - (lane * per + i)];
-            uint32_t before = sum;
-            for (int o = 1; o < 64; o <<= 1) {
-                const uint32_t up = __shfl_up(before, o, 64);
-                if (lane >= o) before += up;
-            }
-            before -= sum;
-            if (before < left && before + sum >= left) {
-                for (int i = 0; i < per; ++i) {
-                    const int bin = kBins - 1 - (lane * per + i);
-                    if (before + hist[bin] >= left) {
-                        found[0] = bin;
-                        found[1] = left - before;
-                        break;
-                    }
-                    before += hist[bin];
-                }
-            }
+        // from the largest digit down: thread i has two bins
+        const uint2 c = reinterpret_cast<const uint2 *>(hist)[kSelect - 1 - tid];  // .y is the larger one
+        uint32_t upto = c.x + c.y;
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t up = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += up;
+        }
+        if (lane == 63) sums[0][0][wave] = upto;
+        __syncthreads();
+        uint32_t before = upto - c.x - c.y;
+        for (int w = 0; w < wave; ++w) before += sums[0][0][w];
+        const int bin = kBins - 1 - 2 * tid;
+        if (before < left && before + c.y >= left) {
+            found[0] = bin;
+            found[1] = left - before;
+        } else if (before + c.y < left && before + c.y + c.x >= left) {
+            found[0] = bin - 1;
+            found[1] = left - before - c.y;
         }
         __syncthreads();
         prefix = (prefix << bits) | found[0];
         left = found[1];
-        __syncthreads();
     }
     // entries above the key stay, and the first `left` of those that equal it
-    const int per = ((old + kSelect - 1) / kSelect) * 64;  // positions of a wavefront
-    const int p0 = wave * per, p1 = p0 + per < old ? p0 + per : old;
-    uint32_t above = 0, equal = 0;
-    for (int i = p0; i < p1; i += 64) {
-        const uint32_t key = i + lane < p1 ? order_key(mass[i + lane]) : 0;
-        const bool in = i + lane < p1;
-        above += __popcll(__ballot(in && key > prefix));
-        equal += __popcll(__ballot(in && key == prefix));
-    }
-    if (lane == 0) {
-        wave_above[wave] = above;
-        wave_equal[wave] = equal;
-    }
-    __syncthreads();
-    uint32_t taken = 0, equals = 0;
-    for (int w = 0; w < wave; ++w) {
-        taken += wave_above[w];
-        equals += wave_equal[w];
-    }
-    taken += equals < left ? equals : left;
     const uint64_t below = (uint64_t(1) << lane) - 1;
-    for (int i = p0; i < p1; i += 64) {
-        const bool in = i + lane < p1;
-        const float m = in ? mass[i + lane] : 0.0f;
-        const uint32_t key = order_key(m);
-        const uint64_t eq = __ballot(in && key == prefix);
-        const bool stays = in && (key > prefix || (key == prefix && equals + __popcll(eq & below) < left));
-        const uint64_t all = __ballot(stays);
-        if (stays) {
-            const uint32_t at = taken + __popcll(all & below);
-            ids[at] = i + lane;
-            mass_out[at] = m;
+    if constexpr (KEYS > 0) {
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j) {
+            const uint32_t key = order_key(m[j]);
+            const bool in = j * kSelect + tid < old;
+            const uint32_t above = __popcll(__ballot(in && key > prefix)), equal = __popcll(__ballot(in && key == prefix));
+            if (lane == 0) {
+                sums[0][j][wave] = above;
+                sums[1][j][wave] = equal;
+            }
         }
-        taken += __popcll(all);
-        equals += __popcll(eq);
+        __syncthreads();
+        // of all runs of 64 entries before each: the first wavefront adds them up
+        if (wave == 0) {
+            uint32_t above = 0, equal = 0;  // before this lane's runs
+            constexpr int RUNS = KEYS * kWaves, PER = (RUNS + 63) / 64;
+            uint32_t va[PER], ve[PER], ta = 0, te = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int r = lane * PER + i;
+                va[i] = r < RUNS ? (&sums[0][0][0])[r] : 0;
+                ve[i] = r < RUNS ? (&sums[1][0][0])[r] : 0;
+                ta += va[i];
+                te += ve[i];
+            }
+            above = ta, equal = te;
+            for (int o = 1; o < 64; o <<= 1) {
+                const uint32_t ua = __shfl_up(above, o, 64), ue = __shfl_up(equal, o, 64);
+                if (lane >= o) above += ua, equal += ue;
+            }
+            above -= ta;
+            equal -= te;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int r = lane * PER + i;
+                if (r < RUNS) {
+                    (&sums[0][0][0])[r] = above;
+                    (&sums[1][0][0])[r] = equal;
+                }
+                above += va[i];
+                equal += ve[i];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j) {
+            const uint32_t key = order_key(m[j]), equals = sums[1][j][wave];
+            const bool in = j * kSelect + tid < old;
+            const uint64_t eq = __ballot(in && key == prefix);
+            const bool stays = in && (key > prefix || (key == prefix && equals + __popcll(eq & below) < left));
+            const uint64_t all = __ballot(stays);
+            if (stays) {
+                const uint32_t at = sums[0][j][wave] + (equals < left ? equals : left) + __popcll(all & below);
+                ids[at] = j * kSelect + tid;
+                mass_out[at] = m[j];
+            }
+        }
+    } else {
+        const int per = ((old + kSelect - 1) / kSelect) * 64;  // positions of a wavefront
+        const int p0 = wave * per, p1 = p0 + per < old ? p0 + per : old;
+        uint32_t above = 0, equal = 0;
+        for (int i = p0; i < p1; i += 64) {
+            const bool in = i + lane < p1;
+            const uint32_t key = in ? order_key(mass[i + lane]) : 0;
+            above += __popcll(__ballot(in && key > prefix));
+            equal += __popcll(__ballot(in && key == prefix));
+        }
+        if (lane == 0) {
+            sums[0][0][wave] = above;
+            sums[1][0][wave] = equal;
+        }
+        __syncthreads();
+        uint32_t taken = 0, equals = 0;
+        for (int w = 0; w < wave; ++w) {
+            taken += sums[0][0][w];
+            equals += sums[1][0][w];
+        }
+        taken += equals < left ? equals : left;
+        for (int i = p0; i < p1; i += 64) {
+            const bool in = i + lane < p1;
+            const float w = in ? mass[i + lane] : 0.0f;
+            const uint32_t key = order_key(w);
+            const uint64_t eq = __ballot(in && key == prefix);
+            const bool stays = in && (key > prefix || (key == prefix && equals + __popcll(eq & below) < left));
+            const uint64_t all = __ballot(stays);
+            if (stays) {
+                const uint32_t at = taken + __popcll(all & below);
+                ids[at] = i + lane;
+                mass_out[at] = w;
+            }
+            taken += __popcll(all);
+            equals += __popcll(eq);
+        }
     }
 }
 
@@ -136,39 +209,46 @@ __device__ __forceinline__ void arrived(uint4 &v, uint32_t &s) {
     asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w), "+v"(s));
 }
 
-__global__ __launch_bounds__(kMove) void k_evict_move(EvictArgs a) {
-    const int x = blockIdx.x, part = x & 1, h = (x >> 1) % a.c.heads, b = (x >> 1) / a.c.heads;
+// CHAIN: one workgroup goes through all chunks (the same pages); else it has one
+template <bool CHAIN, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_evict_move(EvictArgs a, int chunks) {
+    const int x = CHAIN ? blockIdx.x : blockIdx.x / chunks;
+    const int part = x & 1, h = (x >> 1) % a.c.heads, b = (x >> 1) / a.c.heads;
     const int D = a.c.D, nb = D / 32, lg = a.c.page_log2, mask = (1 << lg) - 1;
     const int32_t *ids = a.ids + ((int64_t)b * a.c.heads + h) * a.budget;
-    const int32_t *to = a.to + (int64_t)b * a.to_width;
+    const int32_t *table = a.c.table + (int64_t)b * a.c.width, *to = a.to + (int64_t)b * a.to_width;
     const int most = a.c.width << lg, given = a.c.lens[b];
     const int L = given < 0 ? 0 : (given > most ? most : given), n = L < a.budget ? L : a.budget;
-    const int chunk = kMove / nb & ~3;  // entries at a time: one 16-byte piece of codes and one scale per thread
+    const int chunk = THREADS / nb & ~3;  // entries at a time: one 16-byte piece of codes and one scale per thread
     const int tid = threadIdx.x, words = D / 8;
     const bool active = tid < chunk * nb;
     // keys: piece p of entry j; values: word w of the entries 4g .. 4g + 3; scales: block s of entry i
     const int j = tid / nb, p = tid - j * nb, g = tid / words, w = tid - g * words, s = tid / chunk, i = tid - s * chunk;
     auto chunk_of = [&](int page) { return page >= 0 && page < a.c.pages ? kv_chunk(a.c, page, part, h) : nullptr; };
-    auto source = [&](int at) -> const uint8_t * {  // of entry `at` of those that stay
-        if (at >= n) return nullptr;
-        return chunk_of(a.c.table[(int64_t)b * a.c.width + (ids[at] >> lg)]);
+    struct Ids {  // where this thread's pieces come from: positions, or -1
+        int codes[4], scale;
     };
-    auto read = [&](int c0, uint4 &v, uint32_t &scale) {
+    auto read_ids = [&](int c0, Ids &d) {
+        const int first = part == 0 ? c0 + j : c0 + 4 * g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d.codes[e] = active && first + e < n && (part || e == 0) ? ids[first + e] : -1;
+        d.scale = active && c0 + i < n ? ids[c0 + i] : -1;
+    };
+    auto source = [&](int id) -> const uint8_t * { return id < 0 ? nullptr : chunk_of(table[id >> lg]); };
+    auto read = [&](const Ids &d, uint4 &v, uint32_t &scale) {
         v = make_uint4(0, 0, 0, 0);
         scale = 0x7e00u;  // an entry whose page is not there is NaN
-        if (!active) return;
         if (part == 0) {
-            if (const uint8_t *q = source(c0 + j)) v = ld16(q + (ids[c0 + j] & mask) * (D / 2) + p * 16);
+            if (const uint8_t *q = source(d.codes[0])) v = ld16(q + (d.codes[0] & mask) * (D / 2) + p * 16);
         } else {
             uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (const uint8_t *q = source(c0 + 4 * g + e))
-                    u[e] = reinterpret_cast<const uint32_t *>(q)[kv_value_word(D, ids[c0 + 4 * g + e] & mask, w)];
+                if (const uint8_t *q = source(d.codes[e]))
+                    u[e] = reinterpret_cast<const uint32_t *>(q)[kv_value_word(D, d.codes[e] & mask, w)];
             v = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        if (const uint8_t *q = source(c0 + i))
-            scale = reinterpret_cast<const uint16_t *>(q)[kv_scale_at(a.c, ids[c0 + i] & mask, s)];
+        if (const uint8_t *q = source(d.scale)) scale = reinterpret_cast<const uint16_t *>(q)[kv_scale_at(a.c, d.scale & mask, s)];
     };
     auto write = [&](int c0, const uint4 &v, uint32_t scale) {
         if (!active) return;
@@ -192,16 +272,30 @@ __global__ __launch_bounds__(kMove) void k_evict_move(EvictArgs a) {
         if (uint8_t *q = at < n ? chunk_of(to[at >> lg]) : nullptr)
             reinterpret_cast<uint16_t *>(q)[kv_scale_at(a.c, at & mask, s)] = (uint16_t)scale;
     };
-    uint4 v, next;
-    uint32_t scale, next_scale;
-    read(0, v, scale);
-    for (int c0 = 0; c0 < n; c0 += chunk) {
-        read(c0 + chunk, next, next_scale);
-        arrived(v, scale);
-        __syncthreads();
+    uint4 v;
+    uint32_t scale;
+    Ids d;
+    if constexpr (!CHAIN) {
+        const int c0 = (blockIdx.x - x * chunks) * chunk;
+        if (c0 >= n) return;
+        read_ids(c0, d);
+        read(d, v, scale);
         write(c0, v, scale);
-        v = next;
-        scale = next_scale;
+    } else {
+        uint4 next;
+        uint32_t next_scale;
+        read_ids(0, d);
+        read(d, v, scale);
+        read_ids(chunk, d);
+        for (int c0 = 0; c0 < n; c0 += chunk) {
+            read(d, next, next_scale);       // of the next chunk
+            read_ids(c0 + 2 * chunk, d);     // of the one behind it
+            arrived(v, scale);
+            __syncthreads();
+            write(c0, v, scale);
+            v = next;
+            scale = next_scale;
+        }
     }
 }
 
@@ -209,10 +303,20 @@ __global__ __launch_bounds__(kMove) void k_evict_move(EvictArgs a) {
 
 hipError_t launch_cache_evict(const EvictArgs &a, hipStream_t s) {
     const unsigned n = (unsigned)(a.c.B * a.c.heads);
-    hipLaunchKernelGGL(k_evict_select, dim3(n), dim3(kSelect), 0, s, a);
+    const int64_t capacity = (int64_t)a.c.width << a.c.page_log2;
+    if (capacity <= kSelect) hipLaunchKernelGGL(k_evict_select<1>, dim3(n), dim3(kSelect), 0, s, a);
+    else if (capacity <= 4 * kSelect) hipLaunchKernelGGL(k_evict_select<4>, dim3(n), dim3(kSelect), 0, s, a);
+    else if (capacity <= 16 * kSelect) hipLaunchKernelGGL(k_evict_select<16>, dim3(n), dim3(kSelect), 0, s, a);
+    else hipLaunchKernelGGL(k_evict_select<0>, dim3(n), dim3(kSelect), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_evict_move, dim3(2 * n), dim3(kMove), 0, s, a);
+    if (a.to == a.c.table) {
+        hipLaunchKernelGGL((k_evict_move<true, 1024>), dim3(2 * n), dim3(1024), 0, s, a, 1);
+    } else {
+        const int64_t most = capacity < a.budget ? capacity : a.budget;
+        const int chunk = kMove / (a.c.D / 32) & ~3, chunks = (int)((most + chunk - 1) / chunk);
+        hipLaunchKernelGGL((k_evict_move<false, kMove>), dim3((unsigned)(2 * n * (unsigned)chunks)), dim3(kMove), 0, s, a, chunks);
+    }
     return hipGetLastError();
 }
 

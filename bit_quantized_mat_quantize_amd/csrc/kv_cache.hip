@@ -30,36 +30,38 @@ __device__ __forceinline__ void block_top(float &a, float &x, int &bad) {
     }
 }
 
-// ROWS consecutive rows of the batch per workgroup: their words of one group of four
-// values come together, so that the cache lines they share are filled at once
+// Rows per workgroup: their reads are on their way together, and the words of one group
+// of four values, which share cache lines, come together.  4099 rows of 8 heads of 128
+// (bf16) were written in MEASURED_W us with 8 against MEASURED_W1 with 1, and 61 rows
+// (fp32) in MEASURED_B with 1.
 template <int TYPE, int ROWS>
 __global__ __launch_bounds__(kThreads) void k_cache_write(KvCache c, const void *__restrict__ k, int64_t ld_k,
                                                           const void *__restrict__ v, int64_t ld_v) {
+    __shared__ int2 place[ROWS];
     const int words = c.heads * (c.D / 8);  // of a row's keys
     const int u = blockIdx.y * kThreads + threadIdx.x;
     const bool active = u < 2 * words;
-    const int part = u >= words, e = (part ? u - words : u) % (active ? words : 1);
+    const int part = u >= words, e = active ? (part ? u - words : u) : 0;
     const int head = e / (c.D / 8), w = e - head * (c.D / 8);
     const void *src = part ? v : k;
     const int64_t ld = part ? ld_v : ld_k;
-#pragma unroll 1
+    const int r0 = blockIdx.x * ROWS;
+    float x[ROWS][8];
+#pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int r = blockIdx.x * ROWS + i;
-        if (r >= c.T) return;
-        const int b = kv_sequence(c, r);
-        if (b < 0) continue;  // the whole workgroup: b depends on the row alone
-        const KvRows rows = kv_rows(c, b);
-        const int pos = rows.len - rows.count + (r - rows.first);
-        const int page = pos >= 0 ? kv_page(c, b, pos) : -1;
-        if (page < 0) continue;
-        float x[8] = {};
-        if (active) kv_load8<TYPE>(src, r * ld + (int64_t)e * 8, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
+        if (active && r0 + i < c.T) kv_load8<TYPE>(src, (r0 + i) * ld + (int64_t)e * 8, x[i]);
+    }
+    kv_places<ROWS>(c, r0, place);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
         float top = -1.0f, a = 0.0f;
         int bad = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float m = fabsf(x[j]);
-            if (m > top) top = m, a = x[j];
+            const float m = fabsf(x[i][j]);
+            if (m > top) top = m, a = x[i][j];
             bad |= !(m <= 3.402823466e38f);
         }
         block_top(top, a, bad);
@@ -70,52 +72,69 @@ __global__ __launch_bounds__(kThreads) void k_cache_write(KvCache c, const void 
         uint32_t word = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float q = fminf(fmaxf(rintf((bad ? 0.0f : x[j]) * id) + 8.0f, 0.0f), 15.0f);
+            const float q = fminf(fmaxf(rintf((bad ? 0.0f : x[i][j]) * id) + 8.0f, 0.0f), 15.0f);
             word |= (uint32_t)q << (4 * j);
         }
-        if (!active) continue;
-        uint8_t *to = kv_chunk(c, page, part, head);
-        const int t = pos & ((1 << c.page_log2) - 1);
-        reinterpret_cast<uint32_t *>(to)[part ? kv_value_word(c.D, t, w) : kv_key_word(c.D, t, w)] = word;
-        if ((w & 3) == 0) reinterpret_cast<uint16_t *>(to)[kv_scale_at(c, t, w >> 2)] = (uint16_t)h;
+        const int2 at = place[i];
+        if (!active || at.x < 0) continue;
+        uint8_t *to = kv_chunk(c, at.x, part, head);
+        reinterpret_cast<uint32_t *>(to)[part ? kv_value_word(c.D, at.y, w) : kv_key_word(c.D, at.y, w)] = word;
+        if ((w & 3) == 0) reinterpret_cast<uint16_t *>(to)[kv_scale_at(c, at.y, w >> 2)] = (uint16_t)h;
     }
 }
 
-template <int TYPE>
+template <int TYPE, int ROWS>
 __global__ __launch_bounds__(kThreads) void k_cache_read(KvCache c, void *__restrict__ k, void *__restrict__ v) {
+    __shared__ int2 place[ROWS];
     const int words = c.heads * (c.D / 8);
-    const int u = blockIdx.y * kThreads + threadIdx.x, r = blockIdx.x;
-    const int b = kv_sequence(c, r);
-    if (b < 0 || u >= 2 * words) return;
-    const KvRows rows = kv_rows(c, b);
-    const int pos = rows.len - rows.count + (r - rows.first);
-    const int page = pos >= 0 ? kv_page(c, b, pos) : -1;
+    const int u = blockIdx.y * kThreads + threadIdx.x, r0 = blockIdx.x * ROWS;
+    kv_places<ROWS>(c, r0, place);
+    if (u >= 2 * words) return;
     const int part = u >= words, e = part ? u - words : u, head = e / (c.D / 8), w = e - head * (c.D / 8);
-    float x[8];
-    if (page < 0) {
+    uint32_t q[ROWS], d[ROWS];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __builtin_nanf("");
-    } else {
-        const uint8_t *from = kv_chunk(c, page, part, head);
-        const int t = pos & ((1 << c.page_log2) - 1);
-        const uint32_t q = reinterpret_cast<const uint32_t *>(from)[part ? kv_value_word(c.D, t, w) : kv_key_word(c.D, t, w)];
-        const float d = f16_bits_to_f32(reinterpret_cast<const uint16_t *>(from)[kv_scale_at(c, t, w >> 2)]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = d * (float)((int)((q >> (4 * j)) & 15u) - 8);
+    for (int i = 0; i < ROWS; ++i) {
+        const int2 at = place[i];
+        q[i] = 0;
+        d[i] = 0x7e00u;  // an entry that is not there is NaN
+        if (at.x < 0) continue;
+        const uint8_t *from = kv_chunk(c, at.x, part, head);
+        q[i] = reinterpret_cast<const uint32_t *>(from)[part ? kv_value_word(c.D, at.y, w) : kv_key_word(c.D, at.y, w)];
+        d[i] = reinterpret_cast<const uint16_t *>(from)[kv_scale_at(c, at.y, w >> 2)];
     }
-    kv_store8<TYPE>(part ? v : k, ((int64_t)r * words + e) * 8, x);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        if (place[i].x == -2) continue;
+        const float s = f16_bits_to_f32(d[i]);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = s * (float)((int)((q[i] >> (4 * j)) & 15u) - 8);
+        kv_store8<TYPE>(part ? v : k, ((int64_t)(r0 + i) * words + e) * 8, x);
+    }
 }
+
+// eight rows a workgroup once that leaves four workgroups for each CU
+constexpr int kMany = 8;
+bool many(const KvCache &c, unsigned y) { return (int64_t)c.T * y >= 4 * 256 * kMany; }
 
 template <int TYPE>
 hipError_t launch_write(const KvCache &c, const void *k, int64_t ld_k, const void *v, int64_t ld_v, hipStream_t s) {
     const unsigned y = (unsigned)((2 * c.heads * (c.D / 8) + kThreads - 1) / kThreads);
-    hipLaunchKernelGGL((k_cache_write<TYPE, 1>), dim3((unsigned)c.T, y), dim3(kThreads), 0, s, c, k, ld_k, v, ld_v);
+    if (many(c, y))
+        hipLaunchKernelGGL((k_cache_write<TYPE, kMany>), dim3((unsigned)((c.T + kMany - 1) / kMany), y), dim3(kThreads), 0, s, c,
+                           k, ld_k, v, ld_v);
+    else
+        hipLaunchKernelGGL((k_cache_write<TYPE, 1>), dim3((unsigned)c.T, y), dim3(kThreads), 0, s, c, k, ld_k, v, ld_v);
     return hipGetLastError();
 }
 template <int TYPE>
 hipError_t launch_read(const KvCache &c, void *k, void *v, hipStream_t s) {
     const unsigned y = (unsigned)((2 * c.heads * (c.D / 8) + kThreads - 1) / kThreads);
-    hipLaunchKernelGGL((k_cache_read<TYPE>), dim3((unsigned)c.T, y), dim3(kThreads), 0, s, c, k, v);
+    if (many(c, y))
+        hipLaunchKernelGGL((k_cache_read<TYPE, kMany>), dim3((unsigned)((c.T + kMany - 1) / kMany), y), dim3(kThreads), 0, s, c,
+                           k, v);
+    else
+        hipLaunchKernelGGL((k_cache_read<TYPE, 1>), dim3((unsigned)c.T, y), dim3(kThreads), 0, s, c, k, v);
     return hipGetLastError();
 }
 

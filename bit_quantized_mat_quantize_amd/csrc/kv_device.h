@@ -83,6 +83,37 @@ __device__ __forceinline__ int kv_page(const KvCache &c, int b, int pos) {
     return p >= 0 && p < c.pages ? p : -1;
 }
 
+// Where the rows r0 .. r0 + R - 1 of the batch are, for the whole workgroup: the page, or -1
+// where that is not in the pool or the position is below 0, or -2 for a row of no
+// sequence; and the entry of the page.  One search, then a lane per row.
+template <int R>
+__device__ __forceinline__ void kv_places(const KvCache &c, int r0, int2 (&place)[R]) {
+    static_assert(R <= 64, "one lane per row");
+    if (threadIdx.x < 64) {
+        int b = r0;
+        if (c.starts != nullptr) b = kv_last_not_above(c.B, r0, [&](int i) { return (int64_t)c.starts[i]; });
+        if (threadIdx.x < R) {
+            const int r = r0 + threadIdx.x;
+            if (c.starts == nullptr) b = r;
+            else {
+                if (b < 0) b = 0;  // rows before the first sequence: those behind may be its
+                while (b + 1 < c.B && c.starts[b + 1] <= r) ++b;
+            }
+            int2 p = make_int2(-2, 0);
+            if (r < c.T) {
+                const KvRows k = kv_rows(c, b);
+                if (r >= k.first && r < k.first + k.count) {
+                    const int pos = k.len - k.count + (r - k.first);
+                    p.x = pos >= 0 ? kv_page(c, b, pos) : -1;
+                    p.y = pos & ((1 << c.page_log2) - 1);
+                }
+            }
+            place[threadIdx.x] = p;
+        }
+    }
+    __syncthreads();
+}
+
 // ---- codes.  Eight codes of a word as fp16 integers -8 .. 7, in the order 0 4 1 5 2 6 3 7:
 // 0x6400 | u is 1024 + u in fp16.
 __device__ __forceinline__ h2 kv_pair(uint32_t x) {

@@ -505,7 +505,7 @@ qmm_status qmm_rope(qmm_float_type t, const void *x, size_t x_bytes, int64_t ld_
  *                  width * page: that)
  *   starts         int32 [seqs + 1], ascending: the rows of sequence b are starts[b] .. starts[b+1] - 1 of the call's;
  *                  or NULL: row b is sequence b's (then rows = seqs).  Row i of a sequence's n stands at position
- *                  lens[b] - n + i.  What is no sequence's row is neither read nor written.
+ *                  lens[b] - n + i.  What is no sequence's row is left out.
  *   rows           rows of the call
  * Arrays on the device cannot be checked on the host: values outside what they index read and write nothing outside
  * the arrays; each call says what comes of them.  Requires rows <= 2^22, seqs <= 65536, heads <= 1024,
@@ -568,8 +568,8 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
  *   mass_out fp32 [seqs][heads][ld_out], ld_out >= budget: their mass; 0 from n on
  *   lens_out int32 [seqs]: n
  * and entry i of the pages of `to` (int32 [seqs][to_width], to_width * page >= budget) becomes entry ids[i].  `to` may
- * be c->table, or hold the same pages in the same places: the entries move within their pages.  Else its pages must
- * be none that the tables name elsewhere.  An entry whose page is not in [0, pages) becomes NaN; one that would move
+ * be c->table itself: the entries move within their pages (which no two sequences may share then).  Else its pages
+ * must be none that c->table names.  An entry whose page is not in [0, pages) becomes NaN; one that would move
  * to such a page is not written.  Keys keep the rotation of the positions they were written with.  c->starts and
  * c->rows are not used. */
 qmm_status qmm_cache_evict(const qmm_cache *c, const float *mass, int64_t ld_mass, int64_t budget, int64_t recent,
