@@ -30,8 +30,6 @@ constexpr int kThreads = 256, kWaves = 4;
 constexpr int kRows = 16;  // query rows of a tile
 constexpr int kKeys = 32;  // entries of a wavefront's step
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 // What a lane reads of 32 entries.  Lane (n, g), n = lane & 15, g = lane >> 4:
 //   k[s]  words (b, g) of all blocks b of entry 16 s + n
 //   v[s]  words n (and 16 + n for D > 128) of the entries 16 s + 4 g .. + 3

@@ -209,10 +209,13 @@ __device__ __forceinline__ void arrived(uint4 &v, uint32_t &s) {
     asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w), "+v"(s));
 }
 
-// CHAIN: one workgroup goes through all chunks (the same pages); else it has one
-template <bool CHAIN, int THREADS>
-__global__ __launch_bounds__(THREADS) void k_evict_move(EvictArgs a, int chunks) {
-    const int x = CHAIN ? blockIdx.x : blockIdx.x / chunks;
+// CHAIN: one workgroup goes through all chunks (the same pages), the places of the one after
+// the next, the codes of the next and the stores of this one at a time; else it has BATCH
+// of them, each of these steps for all at once.
+template <bool CHAIN, int THREADS, int BATCH>
+__global__ __launch_bounds__(THREADS) void k_evict_move(EvictArgs a, int parts) {
+    __shared__ int2 from[CHAIN ? 3 : BATCH][THREADS / 2];  // page (-1: none) and entry that a chunk's entries come from
+    const int x = CHAIN ? blockIdx.x : blockIdx.x / parts;
     const int part = x & 1, h = (x >> 1) % a.c.heads, b = (x >> 1) / a.c.heads;
     const int D = a.c.D, nb = D / 32, lg = a.c.page_log2, mask = (1 << lg) - 1;
     const int32_t *ids = a.ids + ((int64_t)b * a.c.heads + h) * a.budget;
@@ -223,42 +226,49 @@ __global__ __launch_bounds__(THREADS) void k_evict_move(EvictArgs a, int chunks)
     const int tid = threadIdx.x, words = D / 8;
     const bool active = tid < chunk * nb;
     // keys: piece p of entry j; values: word w of the entries 4g .. 4g + 3; scales: block s of entry i
-    const int j = tid / nb, p = tid - j * nb, g = tid / words, w = tid - g * words, s = tid / chunk, i = tid - s * chunk;
-    auto chunk_of = [&](int page) { return page >= 0 && page < a.c.pages ? kv_chunk(a.c, page, part, h) : nullptr; };
-    struct Ids {  // where this thread's pieces come from: positions, or -1
-        int codes[4], scale;
+    const int j = active ? tid / nb : 0, p = tid - j * nb, g = active ? tid / words : 0, w = tid - g * words;
+    const int s = active ? tid / chunk : 0, i = tid - s * chunk;
+    auto places = [&](int c0, int slot) {
+        if (tid >= chunk) return;
+        int2 f = make_int2(-1, 0);
+        if (c0 + tid < n) {
+            const int id = ids[c0 + tid], page = table[id >> lg];
+            f = make_int2(page >= 0 && page < a.c.pages ? page : -1, id & mask);
+        }
+        from[slot][tid] = f;
     };
-    auto read_ids = [&](int c0, Ids &d) {
-        const int first = part == 0 ? c0 + j : c0 + 4 * g;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d.codes[e] = active && first + e < n && (part || e == 0) ? ids[first + e] : -1;
-        d.scale = active && c0 + i < n ? ids[c0 + i] : -1;
-    };
-    auto source = [&](int id) -> const uint8_t * { return id < 0 ? nullptr : chunk_of(table[id >> lg]); };
-    auto read = [&](const Ids &d, uint4 &v, uint32_t &scale) {
+    auto read = [&](int slot, uint4 &v, uint32_t &scale) {
         v = make_uint4(0, 0, 0, 0);
         scale = 0x7e00u;  // an entry whose page is not there is NaN
+        if (!active) return;
         if (part == 0) {
-            if (const uint8_t *q = source(d.codes[0])) v = ld16(q + (d.codes[0] & mask) * (D / 2) + p * 16);
+            const int2 f = from[slot][j];
+            if (f.x >= 0) v = ld16(kv_chunk(a.c, f.x, 0, h) + f.y * (D / 2) + p * 16);
         } else {
-            uint32_t u[4] = {0, 0, 0, 0};
+            uint32_t u[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (const uint8_t *q = source(d.codes[e]))
-                    u[e] = reinterpret_cast<const uint32_t *>(q)[kv_value_word(D, d.codes[e] & mask, w)];
+            for (int e = 0; e < 4; ++e) {
+                const int2 f = from[slot][4 * g + e];
+                u[e] = f.x >= 0 ? reinterpret_cast<const uint32_t *>(kv_chunk(a.c, f.x, 1, h))[kv_value_word(D, f.y, w)] : 0;
+            }
             v = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        if (const uint8_t *q = source(d.scale)) scale = reinterpret_cast<const uint16_t *>(q)[kv_scale_at(a.c, d.scale & mask, s)];
+        const int2 f = from[slot][i];
+        if (f.x >= 0) scale = reinterpret_cast<const uint16_t *>(kv_chunk(a.c, f.x, part, h))[kv_scale_at(a.c, f.y, s)];
+    };
+    auto target = [&](int at) -> uint8_t * {
+        if (at >= n) return nullptr;
+        const int page = to[at >> lg];
+        return page >= 0 && page < a.c.pages ? kv_chunk(a.c, page, part, h) : nullptr;
     };
     auto write = [&](int c0, const uint4 &v, uint32_t scale) {
         if (!active) return;
         if (part == 0) {
             const int at = c0 + j;
-            if (uint8_t *q = at < n ? chunk_of(to[at >> lg]) : nullptr)
-                *reinterpret_cast<uint4 *>(q + (at & mask) * (D / 2) + p * 16) = v;
+            if (uint8_t *q = target(at)) *reinterpret_cast<uint4 *>(q + (at & mask) * (D / 2) + p * 16) = v;
         } else {
             const int at = c0 + 4 * g;
-            if (uint8_t *q = at < n ? chunk_of(to[at >> lg]) : nullptr) {
+            if (uint8_t *q = target(at)) {
                 uint32_t *o = reinterpret_cast<uint32_t *>(q) + kv_value_word(D, at & mask, w);
                 const uint32_t u[4] = {v.x, v.y, v.z, v.w};
                 if (at + 4 <= n) *reinterpret_cast<uint4 *>(o) = v;
@@ -269,27 +279,30 @@ __global__ __launch_bounds__(THREADS) void k_evict_move(EvictArgs a, int chunks)
             }
         }
         const int at = c0 + i;
-        if (uint8_t *q = at < n ? chunk_of(to[at >> lg]) : nullptr)
-            reinterpret_cast<uint16_t *>(q)[kv_scale_at(a.c, at & mask, s)] = (uint16_t)scale;
+        if (uint8_t *q = target(at)) reinterpret_cast<uint16_t *>(q)[kv_scale_at(a.c, at & mask, s)] = (uint16_t)scale;
     };
-    uint4 v;
-    uint32_t scale;
-    Ids d;
     if constexpr (!CHAIN) {
-        const int c0 = (blockIdx.x - x * chunks) * chunk;
+        const int c0 = (blockIdx.x - x * parts) * BATCH * chunk;
         if (c0 >= n) return;
-        read_ids(c0, d);
-        read(d, v, scale);
-        write(c0, v, scale);
+        uint4 v[BATCH];
+        uint32_t scale[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) places(c0 + u * chunk, u);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) read(u, v[u], scale[u]);
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) write(c0 + u * chunk, v[u], scale[u]);
     } else {
-        uint4 next;
-        uint32_t next_scale;
-        read_ids(0, d);
-        read(d, v, scale);
-        read_ids(chunk, d);
-        for (int c0 = 0; c0 < n; c0 += chunk) {
-            read(d, next, next_scale);       // of the next chunk
-            read_ids(c0 + 2 * chunk, d);     // of the one behind it
+        uint4 v, next;
+        uint32_t scale, next_scale;
+        places(0, 0);
+        places(chunk, 1);
+        __syncthreads();
+        read(0, v, scale);
+        for (int c0 = 0, k = 0; c0 < n; c0 += chunk, ++k) {
+            read((k + 1) % 3, next, next_scale);
+            places(c0 + 2 * chunk, (k + 2) % 3);
             arrived(v, scale);
             __syncthreads();
             write(c0, v, scale);
@@ -297,6 +310,14 @@ __global__ __launch_bounds__(THREADS) void k_evict_move(EvictArgs a, int chunks)
             scale = next_scale;
         }
     }
+}
+
+template <int BATCH>
+hipError_t launch_move(const EvictArgs &a, int64_t most, hipStream_t s) {
+    const int per = BATCH * (kMove / (a.c.D / 32) & ~3), parts = (int)((most + per - 1) / per);
+    hipLaunchKernelGGL((k_evict_move<false, kMove, BATCH>), dim3((unsigned)(2 * a.c.B * a.c.heads) * (unsigned)parts), dim3(kMove),
+                       0, s, a, parts);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -311,13 +332,13 @@ hipError_t launch_cache_evict(const EvictArgs &a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.to == a.c.table) {
-        hipLaunchKernelGGL((k_evict_move<true, 1024>), dim3(2 * n), dim3(1024), 0, s, a, 1);
-    } else {
-        const int64_t most = capacity < a.budget ? capacity : a.budget;
-        const int chunk = kMove / (a.c.D / 32) & ~3, chunks = (int)((most + chunk - 1) / chunk);
-        hipLaunchKernelGGL((k_evict_move<false, kMove>), dim3((unsigned)(2 * n * (unsigned)chunks)), dim3(kMove), 0, s, a, chunks);
+        hipLaunchKernelGGL((k_evict_move<true, 1024, 1>), dim3(2 * n), dim3(1024), 0, s, a, 1);
+        return hipGetLastError();
     }
-    return hipGetLastError();
+    // four chunks a workgroup once that leaves four workgroups for each CU
+    const int64_t most = capacity < a.budget ? capacity : a.budget;
+    const int64_t chunks = 2 * (int64_t)n * (most / (kMove / (a.c.D / 32) & ~3));
+    return chunks >= 4 * 4 * 256 ? launch_move<4>(a, most, s) : launch_move<1>(a, most, s);
 }
 
 }  // namespace qmm

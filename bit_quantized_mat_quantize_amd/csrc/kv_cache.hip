@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kThreads) void k_cache_write(KvCache c, const void 
     }
 }
 
-template <int TYPE, int ROWS>
+template <int TYPE, int ROWS, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_cache_read(KvCache c, void *__restrict__ k, void *__restrict__ v) {
     __shared__ int2 place[ROWS];
     const int words = c.heads * (c.D / 8);
@@ -109,33 +109,40 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(KvCache c, void *__rest
         float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = s * (float)((int)((q[i] >> (4 * j)) & 15u) - 8);
-        kv_store8<TYPE>(part ? v : k, ((int64_t)(r0 + i) * words + e) * 8, x);
+        kv_store8<TYPE, PAST>(part ? v : k, ((int64_t)(r0 + i) * words + e) * 8, x);
     }
 }
 
-// eight rows a workgroup once that leaves four workgroups for each CU
-constexpr int kMany = 8;
-bool many(const KvCache &c, unsigned y) { return (int64_t)c.T * y >= 4 * 256 * kMany; }
+// Eight rows a workgroup once that leaves four workgroups for each CU; below, four were no faster than one (2561 rows of
+// 8 heads of 128: 9.4 us both to write and to read).
+bool eight_rows(const KvCache &c, unsigned y) { return (int64_t)c.T * y >= 8 * 4 * 256; }
+constexpr int64_t kLongBytes = 32 << 20;  // the L2 caches: 4 MiB for each of 8 XCDs
 
+template <int TYPE, int ROWS>
+hipError_t launch_write_rows(const KvCache &c, const void *k, int64_t ld_k, const void *v, int64_t ld_v, unsigned y,
+                             hipStream_t s) {
+    hipLaunchKernelGGL((k_cache_write<TYPE, ROWS>), dim3((unsigned)((c.T + ROWS - 1) / ROWS), y), dim3(kThreads), 0, s, c, k,
+                       ld_k, v, ld_v);
+    return hipGetLastError();
+}
 template <int TYPE>
 hipError_t launch_write(const KvCache &c, const void *k, int64_t ld_k, const void *v, int64_t ld_v, hipStream_t s) {
     const unsigned y = (unsigned)((2 * c.heads * (c.D / 8) + kThreads - 1) / kThreads);
-    if (many(c, y))
-        hipLaunchKernelGGL((k_cache_write<TYPE, kMany>), dim3((unsigned)((c.T + kMany - 1) / kMany), y), dim3(kThreads), 0, s, c,
-                           k, ld_k, v, ld_v);
-    else
-        hipLaunchKernelGGL((k_cache_write<TYPE, 1>), dim3((unsigned)c.T, y), dim3(kThreads), 0, s, c, k, ld_k, v, ld_v);
+    return eight_rows(c, y) ? launch_write_rows<TYPE, 8>(c, k, ld_k, v, ld_v, y, s)
+                            : launch_write_rows<TYPE, 1>(c, k, ld_k, v, ld_v, y, s);
+}
+template <int TYPE, int ROWS, bool PAST>
+hipError_t launch_read_rows(const KvCache &c, void *k, void *v, unsigned y, hipStream_t s) {
+    hipLaunchKernelGGL((k_cache_read<TYPE, ROWS, PAST>), dim3((unsigned)((c.T + ROWS - 1) / ROWS), y), dim3(kThreads), 0, s, c,
+                       k, v);
     return hipGetLastError();
 }
 template <int TYPE>
 hipError_t launch_read(const KvCache &c, void *k, void *v, hipStream_t s) {
     const unsigned y = (unsigned)((2 * c.heads * (c.D / 8) + kThreads - 1) / kThreads);
-    if (many(c, y))
-        hipLaunchKernelGGL((k_cache_read<TYPE, kMany>), dim3((unsigned)((c.T + kMany - 1) / kMany), y), dim3(kThreads), 0, s, c,
-                           k, v);
-    else
-        hipLaunchKernelGGL((k_cache_read<TYPE, 1>), dim3((unsigned)c.T, y), dim3(kThreads), 0, s, c, k, v);
-    return hipGetLastError();
+    const bool past = (int64_t)c.T * c.heads * c.D * 2 * (TYPE == 0 ? 4 : 2) >= kLongBytes;
+    if (!eight_rows(c, y)) return launch_read_rows<TYPE, 1, false>(c, k, v, y, s);
+    return past ? launch_read_rows<TYPE, 8, true>(c, k, v, y, s) : launch_read_rows<TYPE, 8, false>(c, k, v, y, s);
 }
 
 }  // namespace

@@ -10,6 +10,7 @@ namespace qmm {
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ h2 as_h2(uint32_t u) { return __builtin_bit_cast(h2, u); }
 __device__ __forceinline__ uint32_t as_u32(h2 h) { return __builtin_bit_cast(uint32_t, h); }
@@ -153,19 +154,26 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) {
     const __bf16 b = (__bf16)f;
     return __builtin_bit_cast(uint16_t, b);
 }
-template <int TYPE>
+// PAST: past the caches, for outputs that they cannot hold
+template <int TYPE, bool PAST = false>
 __device__ __forceinline__ void kv_store8(void *base, int64_t at, const float *v) {
     if constexpr (TYPE == 0) {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        f4 *p = reinterpret_cast<f4 *>(static_cast<float *>(base) + at);
+        const f4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        if constexpr (PAST) {
+            __builtin_nontemporal_store(a, p);
+            __builtin_nontemporal_store(b, p + 1);
+        } else p[0] = a, p[1] = b;
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             w[i] = TYPE == 1 ? f32_to_f16_bits(v[2 * i]) | (f32_to_f16_bits(v[2 * i + 1]) << 16)
                              : bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        u32x4 *p = reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(base) + at);
+        const u32x4 u = {w[0], w[1], w[2], w[3]};
+        if constexpr (PAST) __builtin_nontemporal_store(u, p);
+        else *p = u;
     }
 }
 __device__ __forceinline__ void kv_store8(int type, void *base, int64_t at, const float *v) {
