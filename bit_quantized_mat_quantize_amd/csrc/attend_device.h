@@ -115,6 +115,10 @@ struct Splits {
     float *many_sums;     // [many][T * query heads][D]
     float2 *many_stats;   // [many][T * query heads]
     float *lse2;          // [T * query heads] in log2 units, or null
+    // what attend_rows.hip leaves for attend_mass.hip, by (cache head, token, head of the group), or null:
+    _Float16 *queries;    // [pieces][heads * T * group][D], as query_pieces has them
+    int64_t query_piece;  // elements of a piece
+    float *factors;       // [heads * T * group], of the rows' products
 };
 
 // the row of the batch's output, token * query heads + head, of a sequence's query row

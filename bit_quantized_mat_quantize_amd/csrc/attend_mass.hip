@@ -5,9 +5,12 @@
 // A workgroup owns 128 entries of a sequence and cache head and goes over all rows that
 // see any of them, 64 at a time: wavefronts 0 .. 3 take 32 entries each against the first
 // 32 rows, 4 .. 7 the same entries against the others.  The entries stay in registers,
-// decoded to fp16 (two pieces for fp32 queries, as in attend_rows.hip); the rows come through
-// LDS, converted once for the workgroup.  Every entry's sum is formed in a fixed order
-// by its owner: per lane over the rows, over the lanes, over the two halves.
+// decoded to fp16 (two pieces for fp32 queries, as in attend_rows.hip).  The rows' queries
+// come by direct loads into LDS, two steps ahead, as attend_rows.hip left them, fp16 and
+// scaled: converting them anew in every workgroup took most of its time (three prompts
+// of 700 rows, 28 heads of 128, fp32: 180 against 128 us).  Every entry's sum is
+// formed in a fixed order by its owner: per lane over the rows, over the lanes, over the
+// two halves.
 #include "attend_device.h"
 
 namespace qmm {
@@ -18,20 +21,48 @@ constexpr int kThreads = 512, kRows = 64, kEntries = 128;
 template <int PIECES, int D>
 struct Shape {
     static constexpr int NB = D / 32, WORDS = D / 8;
-    static constexpr int ROW = D == 96 ? 128 : D;  // elements of a row in LDS
-    static constexpr int PIECE = kRows * ROW * 2, STAGE = PIECES * PIECE, BYTES = 2 * STAGE;
+    // load instructions of a wavefront; bytes, with room for what the last instructions load beyond row 63
+    static constexpr int PER_PIECE = (kRows * D * 2 + 8191) / 8192, LOADS = PIECES * PER_PIECE;
+    static constexpr int PIECE = PER_PIECE * 8192, STAGE = PIECES * PIECE;
+    static constexpr int SLOTS = STAGE * 3 <= 150 * 1024 ? 3 : 2, BYTES = SLOTS * STAGE;
+    static_assert(PIECE <= 65536 && BYTES <= 160 * 1024 - 1024, "LDS of a compute unit");
 };
+// The place of 16-byte piece w of a row: eight lanes of one access meet eight of them, for rows of
+// 128 bytes or multiples; rows of 192 bytes start 64 bytes apart already, four pieces are moved.
 template <int D>
 __device__ __forceinline__ int row_piece(int row, int w) {
-    return row * (D == 96 ? 128 : D) * 2 + ((w ^ (row & 7)) * 16);
+    return row * D * 2 + ((D == 96 ? w ^ ((row >> 1) & 3) : w ^ (row & 7)) * 16);
 }
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Query row r of a sequence as (token, head of the group), and steps of up to 64 rows without a
+// division by the group g: x * ceil(2^21 / g) >> 21 is x / g for x < 1088 and g <= 1024, because the
+// quotient is too large by less than x / 2^21 < 1 / g.
+struct Row {
+    int token, head;
+};
+struct Steps {
+    int group, magic;
+    __device__ __forceinline__ explicit Steps(int g) : group(g), magic(((1 << 21) + g - 1) / g) {}
+    __device__ __forceinline__ Row at(int r) const {
+        const int t = r / group;
+        return Row{t, r - t * group};
+    }
+    __device__ __forceinline__ Row on(const Row &r, int by) const {
+        const int x = r.head + by, t = (int)(((uint32_t)x * (uint32_t)magic) >> 21);
+        return Row{r.token + t, x - t * group};
+    }
+};
 
 template <int PIECES, int D>
 __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, Splits sp, int type, int tiles) {
     using S = Shape<PIECES, D>;
     constexpr int NB = S::NB, WORDS = S::WORDS;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ float2 rows_at[2][kRows];  // factor of a row's products, -lse2
+    __shared__ float2 rows_at[2][kRows];  // of a row's products: factor; -lse2
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, hf = lane >> 5;
     const int head = blockIdx.x % a.c.heads, x0 = blockIdx.x / a.c.heads, b = x0 / tiles;
     const int e0 = (x0 - b * tiles) * kEntries, k0 = e0 + 32 * (wave & 3), stream = wave >> 2;
@@ -89,68 +120,67 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
     }
     const float down = pow2i(-shift);
 
-    // ---- rows into LDS: eight threads a row, words tid % 8, + 8, ..
-    constexpr int EACH = (WORDS + 7) / 8;
-    const int sr = threadIdx.x >> 3, sw = threadIdx.x & 7;
-    float f[EACH][8];
-    float row_lse = 0.0f;
-    auto load = [&](int r0) {
-        int r = r0 + sr;
-        const bool live = r < total;
-        r = live ? r : total - 1;
-        const int64_t out_row = attend_out_row(a, rows, head, r), at = attend_at(a, out_row, a.ld_q);
+    // ---- rows into LDS: a wavefront loads eighths of each piece, a lane the 16 bytes that belong to its place
+    const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds);
+    uint32_t place[S::PER_PIECE];
 #pragma unroll
-        for (int j = 0; j < EACH; ++j)
-            if (sw + 8 * j < WORDS) kv_load8(type, a.q, at + 8 * (sw + 8 * j), f[j]);
-        row_lse = live ? sp.lse2[out_row] : -INFINITY;
-    };
-    auto put = [&](int stage) {
-        uint32_t top = 0;
+    for (int i = 0; i < S::PER_PIECE; ++i) {
+        const int at = 1024 * (wave * S::PER_PIECE + i) + 16 * lane, row = at / (D * 2), w = at % (D * 2) / 16;
+        place[i] = row * D * 2 + ((D == 96 ? w ^ ((row >> 1) & 3) : w ^ (row & 7)) * 16);
+    }
+    const int64_t row0 = ((int64_t)head * a.c.T + rows.first) * a.group;  // of the sequence, among the queries
+    const Steps by_group(a.group);
+    auto load = [&](int r0, int slot) {  // rows r0 .. r0 + 63: what lies behind the last of all is not read
 #pragma unroll
-        for (int j = 0; j < EACH; ++j)
-            if (sw + 8 * j < WORDS)
+        for (int k = 0; k < PIECES; ++k) {
+            const uint64_t base = (uint64_t)(uintptr_t)(sp.queries + k * sp.query_piece + (row0 + r0) * D);
+            const u32x4 r = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, (uint32_t)((total - r0 < kRows ? total - r0 : kRows) * D * 2),
+                             0x00020000u};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t u = __float_as_uint(f[j][e]) & 0x7fffffffu;
-                    top = u > top ? u : top;
-                }
-        for (int o = 1; o < 8; o <<= 1) {
-            const uint32_t u = __shfl_xor(top, o, 64);
-            top = u > top ? u : top;
+            for (int i = 0; i < S::PER_PIECE; ++i)
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+                                 lds_at + slot * S::STAGE + k * S::PIECE + 1024 * (wave * S::PER_PIECE + i)),
+                             "v"(place[i]), "s"(r) : "memory");
         }
-        const int qs = query_shift(top);
-        const float by = a.scale < 0.0f ? -pow2i(qs) : pow2i(qs);
-        uint8_t *to = lds + stage * S::STAGE;
-#pragma unroll
-        for (int j = 0; j < EACH; ++j)
-            if (sw + 8 * j < WORDS) {
-                h8 hi, lo;
-                query_pieces<PIECES>(f[j], by, hi, lo);
-                *reinterpret_cast<h8 *>(to + row_piece<D>(sr, sw + 8 * j)) = hi;
-                if constexpr (PIECES == 2) *reinterpret_cast<h8 *>(to + S::PIECE + row_piece<D>(sr, sw + 8 * j)) = lo;
-            }
-        // a row that has nothing (or is none) weighs nothing
-        if (sw == 0)
-            rows_at[stage][sr] = row_lse == -INFINITY ? make_float2(0.0f, -INFINITY)
-                                                      : make_float2((top >> 23) == 255 ? __builtin_nanf("") : fabsf(a.scale) * pow2i(-qs), -row_lse);
+    };
+    // factor and lse2 of a step's rows, by the first 64 threads
+    auto weights = [&](const Row &first, int stage) {
+        if (threadIdx.x >= kRows) return;
+        const Row at = by_group.on(first, threadIdx.x);
+        float2 v = make_float2(0.0f, -INFINITY);  // a row that has nothing (or is none) weighs nothing
+        if (at.token < rows.count) {
+            const float lse = sp.lse2[(int64_t)(rows.first + at.token) * (a.c.heads * a.group) + head * a.group + at.head];
+            if (lse != -INFINITY) v = make_float2(sp.factors[row0 + at.token * a.group + at.head], -lse);
+        }
+        rows_at[stage][threadIdx.x] = v;
     };
 
     float got[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) got[r] = 0.0f;
-    const int first = i0 * a.group / kRows * kRows, end = i1 * a.group;
-    load(first);
-    put(0);
-    for (int r0 = first, stage = 0; r0 < end; r0 += kRows, stage ^= 1) {
+    const int begin = i0 * a.group, end = i1 * a.group;
+    Row next = by_group.at(begin), mine = by_group.on(next, 32 * stream);  // of the weights; of this wavefront's products
+    constexpr int AHEAD = S::SLOTS - 1;
+    for (int i = 0; i < AHEAD; ++i)
+        if (begin + i * kRows < end) load(begin + i * kRows, i);
+    weights(next, 0);
+    int slot = 0;
+    for (int r0 = begin, stage = 0; r0 < end; r0 += kRows, stage ^= 1, slot = slot + 1 == S::SLOTS ? 0 : slot + 1) {
+        // this wavefront's part of the step's rows is there, then everybody's; nobody reads the slot that is filled next
+        if (AHEAD > 1 && r0 + kRows < end) wait_loads<(AHEAD > 1 ? S::LOADS : 0)>();
+        else wait_loads<0>();
         __syncthreads();
-        if (r0 + kRows < end) load(r0 + kRows);
+        if (r0 + AHEAD * kRows < end) load(r0 + AHEAD * kRows, slot == 0 ? S::SLOTS - 1 : slot - 1);
+        next = by_group.on(next, kRows);
+        if (r0 + kRows < end) weights(next, stage ^ 1);
         const int wr0 = r0 + 32 * stream, wr1 = wr0 + 31;
         if (wr0 < end && k0 < rows.len) {
             int lo0, hi0, lo1, hi1;  // what the first and the last of the wavefront's rows see
-            attend_span(a, rows, wr0 / a.group, lo0, hi0);
-            attend_span(a, rows, (wr1 < total ? wr1 : total - 1) / a.group, lo1, hi1);
+            const int last = by_group.on(mine, 31).token;
+            attend_span(a, rows, mine.token, lo0, hi0);
+            attend_span(a, rows, last < rows.count ? last : rows.count - 1, lo1, hi1);
             if (k0 < hi1 && k0 + 32 > lo0) {
-                const uint8_t *from = lds + stage * S::STAGE;
+                const uint8_t *from = lds + slot * S::STAGE;
                 f16v x;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[r] = 0.0f;
@@ -169,7 +199,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
                 const float by = row.x * down;
                 if (k0 < lo1 || k0 + 32 > hi0 || wr1 >= total) {
                     int lo = 1, hi = 0;
-                    if (wr0 + n < total) attend_span(a, rows, (wr0 + n) / a.group, lo, hi);
+                    const int token = by_group.on(mine, n).token;
+                    if (token < rows.count) attend_span(a, rows, token, lo, hi);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int at = k0 + 8 * (r >> 2) + 4 * hf + (r & 3);
@@ -181,7 +212,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
                 }
             }
         }
-        if (r0 + kRows < end) put(stage ^ 1);
+        mine = by_group.on(mine, kRows);
     }
     // over the 32 rows that lie along the lanes, then over the two halves
 #pragma unroll

@@ -37,6 +37,13 @@ struct Shape {
     static constexpr int STAGE = PIECES * (KEYS + VALUES), BYTES = 2 * STAGE;
     static constexpr int GROUPS = 2 * KT / 16, MINE = GROUPS / WAVES;  // groups of 16 entries' keys or values; per wavefront
     static_assert(MINE == 1, "one group per wavefront");
+    // a group on its way: 16 * D/2 bytes of codes, filler to 1 KiB, D/32 * 32 of scales, filler to 256
+    static constexpr int CODE_LOADS = (8 * D + 1023) / 1024, LOADS = CODE_LOADS + 1;
+    static constexpr int RAW = 1024 * CODE_LOADS + 256;
+    static constexpr int ROOM = 160 * 1024 - 512 - BYTES;  // of LDS
+    static constexpr int SLOTS = ROOM >= 3 * WAVES * RAW ? 3 : (ROOM >= 2 * WAVES * RAW ? 2 : 1);
+    static constexpr int ALL = BYTES + SLOTS * WAVES * RAW;
+    static_assert(ALL + 512 <= 160 * 1024, "LDS");
 };
 
 // 16-byte pieces of LDS rows are placed so that eight lanes of one access meet eight of them
@@ -51,13 +58,18 @@ __device__ __forceinline__ int value_piece(int element, int c) {  // c: eight en
     return element * KT * 2 + ((c ^ by) * 16);
 }
 
-// what a lane holds of its group on the way from memory to LDS
+// what a lane decodes of its group
 template <int D>
 struct Raw {
     static constexpr int NB = D / 32, ROUNDS = D > 128 ? 2 : 1;
     uint32_t w[ROUNDS * 4];              // keys: the words of all blocks; values: a word of four entries
     uint32_t s[NB > 2 * ROUNDS ? NB : 2 * ROUNDS];  // keys: scales of all blocks; values: of four entries
 };
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 template <int PIECES, int D>
 __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(AttendArgs a, Splits sp, int type, int tiles) {
@@ -93,34 +105,9 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     attend_span(a, rows, r1 / a.group, unused, last);
     attend_span(a, rows, (busy ? wr0 : r1) / a.group, seen0, all1);  // that the wavefront sees: [seen0, seen1)
     attend_span(a, rows, (busy ? wr1 : r1) / a.group, all0, seen1);  // that all its rows see: [all0, all1)
-    const int64_t out_row = attend_out_row(a, rows, head, use);
-    h8 qh[2 * NB], ql[PIECES == 2 ? 2 * NB : 1];  // elements 16 i + 8 hf ..
-    float factor;
-    {
-        const int64_t at = attend_at(a, out_row, a.ld_q) + 8 * hf;
-        uint32_t top = 0;
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) {
-            kv_load8(type, a.q, at + 16 * i, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t u = __float_as_uint(f[j]) & 0x7fffffffu;
-                top = u > top ? u : top;
-            }
-        }
-        const uint32_t other = __shfl_xor(top, 32, 64);
-        top = other > top ? other : top;
-        const int shift = query_shift(top);
-        const float by = a.scale < 0.0f ? -pow2i(shift) : pow2i(shift);
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) {
-            kv_load8(type, a.q, at + 16 * i, f);
-            query_pieces<PIECES>(f, by, qh[i], ql[PIECES == 2 ? i : 0]);
-        }
-        factor = (top >> 23) == 255 ? __builtin_nanf("") : fabsf(a.scale) * pow2i(-shift);
-    }
-
+    const int token = use / a.group, q_head = head * a.group + use - token * a.group;
+    const int64_t out_row = (int64_t)(rows.first + token) * (a.c.heads * a.group) + q_head;
+    const int64_t q_at = (int64_t)(rows.first + token) * a.ld_q + (int64_t)q_head * D;
     // ---- this split's steps
     const int s0 = (first < 0 ? 0 : first) / KT, s1 = last > 0 ? (last + KT - 1) / KT : 0, all = s1 > s0 ? s1 - s0 : 0;
     const int from = s0 + (int)((int64_t)all * split / sp.many), to = s0 + (int)((int64_t)all * (split + 1) / sp.many);
@@ -137,17 +124,44 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     decode.set();
     typedef const __attribute__((address_space(4))) int32_t *scalar_ints;
     const scalar_ints table = (scalar_ints)(uintptr_t)(a.c.table + (int64_t)b * a.c.width);
-    bool nowhere = false;  // the group's page is not in the pool
-    auto load = [&](int step, Raw<D> &raw) {
+    // Direct loads into this wavefront's slots, SLOTS steps ahead: the codes of a group are one run of
+    // memory, and a lane's place in it is fixed.
+    constexpr int SLOTS = S::SLOTS;
+    uint8_t *const ring = lds + S::BYTES + wave * (SLOTS * S::RAW);
+    const uint32_t ring_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring);
+    uint32_t code_at[S::CODE_LOADS];
+#pragma unroll
+    for (int i = 0; i < S::CODE_LOADS; ++i) code_at[i] = 16 * (64 * i + lane < D / 2 ? 64 * i + lane : D / 2 - 1);
+    const int piece = lane < D / 4 ? lane : D / 4 - 1;  // 4 bytes of a block's scales
+    const uint32_t scale_at = ((D / 2) << a.c.page_log2) + 2 * ((piece >> 3) << a.c.page_log2) + 4 * (piece & 7);
+    const uint32_t records = (uint32_t)kv_chunk_bytes(a.c);
+    uint32_t missing = 0;  // steps whose page is not in the pool, the next one lowest
+    auto load = [&](int step, int ahead) {  // ahead: of the step that is multiplied
         int at = step * KT + 16 * group;
         at = at < last16 ? at : last16;
         int page = table[at >> a.c.page_log2];
-        nowhere = page < 0 || page >= a.c.pages;
-        if (nowhere) page = 0;
-        const uint8_t *chunk = kv_chunk(a.c, page, keys ? 0 : 1, head);
+        const bool none = page < 0 || page >= a.c.pages;
+        if (none) page = 0;
+        missing |= (none ? 1u : 0u) << ahead;
+        const uint64_t base = (uint64_t)(uintptr_t)kv_chunk(a.c, page, keys ? 0 : 1, head);
+        const u32x4 r = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, records, 0x00020000u};
         const int e0 = at & ((1 << a.c.page_log2) - 1);
+        const uint32_t to = ring_at + ((step - from) % SLOTS) * S::RAW;
+#pragma unroll
+        for (int i = 0; i < S::CODE_LOADS; ++i)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + 1024 * i),
+                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "memory");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to + 1024 * S::CODE_LOADS),
+                     "v"(scale_at), "s"(r), "s"(e0 * 2) : "memory");
+    };
+    // the step's group out of its slot, once at most `later` steps' loads behind it are on their way
+    auto take = [&](int step, int later, Raw<D> &raw) {
+        if (SLOTS > 2 && later >= 2) wait_loads<2 * S::LOADS>();
+        else if (SLOTS > 1 && later >= 1) wait_loads<S::LOADS>();
+        else wait_loads<0>();
+        const uint8_t *slot = ring + ((step - from) % SLOTS) * S::RAW, *scales = slot + 1024 * S::CODE_LOADS;
         if (keys) {
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(chunk) + (e0 + ke) * WORDS + kg * NB;
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(slot) + ke * WORDS + kg * NB;
             if constexpr (NB % 4 == 0) {
 #pragma unroll
                 for (int i = 0; i < NB / 4; ++i) {
@@ -159,23 +173,21 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                 for (int i = 0; i < NB; ++i) raw.w[i] = p[i];
             }
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
-                raw.s[i] = reinterpret_cast<const uint16_t *>(chunk)[kv_scale_at(a.c, e0 + ke, i)];
+            for (int i = 0; i < NB; ++i) raw.s[i] = reinterpret_cast<const uint16_t *>(scales)[16 * i + ke];
         } else {
 #pragma unroll
             for (int r = 0; r < ROUNDS; ++r) {
                 const int w = (16 * r + vw) % WORDS;
-                const uint4 u = ld16(reinterpret_cast<const uint32_t *>(chunk) + kv_value_word(D, e0 + 4 * ve, w));
+                const uint4 u = ld16(slot + (ve * WORDS + w) * 16);
                 raw.w[4 * r] = u.x, raw.w[4 * r + 1] = u.y, raw.w[4 * r + 2] = u.z, raw.w[4 * r + 3] = u.w;
-                const uint2 d = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(chunk) +
-                                                                 kv_scale_at(a.c, e0 + 4 * ve, w >> 2));
+                const uint2 d = *reinterpret_cast<const uint2 *>(scales + 32 * (w >> 2) + 8 * ve);
                 raw.s[2 * r] = d.x, raw.s[2 * r + 1] = d.y;
             }
         }
     };
     int key_shift = 15, value_shift_ = 15;
     uint32_t key_bound = 0, value_bound = 0;
-    auto put = [&](int step, Raw<D> &raw) {
+    auto put = [&](int step, Raw<D> &raw, bool nowhere) {
         uint8_t *stage = lds + (step & 1) * S::STAGE;
         const int e = 16 * group, k0 = step * KT + e;  // in LDS; in the sequence
         constexpr int SCALES = NB > 2 * ROUNDS ? NB : 2 * ROUNDS;
@@ -280,9 +292,50 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     // one ahead of the other, its weights are formed while the other multiplies.
     if (wave < S::WAVES / 2) __builtin_amdgcn_s_setprio(1);
     Raw<D> raw;
+    for (int i = 0; i < SLOTS; ++i)
+        if (from + i < to) load(from + i, i);
+    // ---- the rows' queries, while the first entries are on their way
+    h8 qh[2 * NB], ql[PIECES == 2 ? 2 * NB : 1];  // elements 16 i + 8 hf ..
+    float factor;
+    {
+        const int64_t at = q_at + 8 * hf;
+        uint32_t top = 0;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) {
+            kv_load8(type, a.q, at + 16 * i, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t u = __float_as_uint(f[j]) & 0x7fffffffu;
+                top = u > top ? u : top;
+            }
+        }
+        const uint32_t other = __shfl_xor(top, 32, 64);
+        top = other > top ? other : top;
+        const int shift = query_shift(top);
+        const float by = a.scale < 0.0f ? -pow2i(shift) : pow2i(shift);
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) {
+            kv_load8(type, a.q, at + 16 * i, f);
+            query_pieces<PIECES>(f, by, qh[i], ql[PIECES == 2 ? i : 0]);
+        }
+        factor = (top >> 23) == 255 ? __builtin_nanf("") : fabsf(a.scale) * pow2i(-shift);
+        if (sp.queries != nullptr && split == 0 && live) {  // for the weights of the entries
+            const int64_t row = ((int64_t)head * a.c.T + rows.first) * a.group + use;
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) {
+                _Float16 *p = sp.queries + row * D + 16 * i + 8 * hf;
+                *reinterpret_cast<h8 *>(p) = qh[i];
+                if constexpr (PIECES == 2) *reinterpret_cast<h8 *>(p + sp.query_piece) = ql[i];
+            }
+            if (hf == 0) sp.factors[row] = factor;
+        }
+    }
+
+    auto behind = [&](int step) { return to - 1 - step < SLOTS - 1 ? to - 1 - step : SLOTS - 1; };
     if (from < to) {
-        load(from, raw);
-        put(from, raw);
+        take(from, behind(from), raw);
+        put(from, raw, missing & 1);
     }
     for (int step = from; step < to; ++step) {
         __syncthreads();  // the step's entries are in LDS, and nobody reads the step's before
@@ -301,11 +354,14 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                 value_bound = ((top[1] >> 10) + 1) << 10;
             }
             __syncthreads();
-            put(step, raw);
+            take(step, behind(step), raw);
+            put(step, raw, missing & 1);
             __syncthreads();
         }
         if (threadIdx.x < 2) unfit[(step + 2) % 3][threadIdx.x] = 0;
-        if (step + 1 < to) load(step + 1, raw);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot's reads are done
+        if (step + SLOTS < to) load(step + SLOTS, SLOTS);
+        missing >>= 1;
         if (busy) {
             const float by = factor * pow2i(-key_shift);
 #pragma unroll
@@ -377,7 +433,10 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                     }
             }
         }
-        if (step + 1 < to) put(step + 1, raw);
+        if (step + 1 < to) {
+            take(step + 1, behind(step + 1), raw);
+            put(step + 1, raw, missing & 1);
+        }
     }
     if (!busy) return;
     sum += __shfl_xor(sum, 32, 64);
@@ -386,7 +445,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     const float down = pow2i(-value_shift_);
     if (sp.many == 1) {
         const float inv = none ? 0.0f : down / sum;
-        const int64_t to_row = attend_at(a, out_row, a.ld_out);
+        const int64_t to_row = (int64_t)(rows.first + token) * a.ld_out + (int64_t)q_head * D;
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -422,9 +481,9 @@ template <int PIECES, int D>
 hipError_t launch(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s) {
     using S = Shape<PIECES, D>;
     static std::atomic<uint64_t> lds_set{0};
-    const hipError_t e = ensure_lds_bytes((const void *)k_attend_rows<PIECES, D>, S::BYTES, lds_set);
+    const hipError_t e = ensure_lds_bytes((const void *)k_attend_rows<PIECES, D>, S::ALL, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attend_rows<PIECES, D>), dim3((unsigned)(tiles * sp.many * a.c.heads)), dim3(S::THREADS), S::BYTES, s,
+    hipLaunchKernelGGL((k_attend_rows<PIECES, D>), dim3((unsigned)(tiles * sp.many * a.c.heads)), dim3(S::THREADS), S::ALL, s,
                        a, sp, type, (int)tiles);
     return hipGetLastError();
 }

@@ -125,6 +125,10 @@ __device__ __forceinline__ void products(const Decode &k, const Step<D> &t, cons
     }
 }
 
+// workgroups that a CU holds, by their registers
+template <int PIECES, int D>
+constexpr int at_once = D > 128 ? 2 : (PIECES == 2 && D == 128 ? 3 : 4);
+
 // ---- a wavefront's ring of steps in LDS, filled by direct loads.  16 entries of a head are
 // one run of D/2 * 16 bytes of codes, for keys and for values alike, so a lane's place
 // in a load is fixed and only its page's base and the entry's offset, both scalar, change.
@@ -238,13 +242,14 @@ struct Tile {
     int first, last;   // entries that any row of the tile sees: [first, last)
     int all_lo, all_hi;  // entries that every row sees
     float factor;      // of the dot products of codes, to log2 units
-    int64_t out_row;   // row * heads of the batch
+    int batch_row, q_head;
     Query<PIECES, D> q;
 
-    __device__ __forceinline__ bool open(const AttendArgs &a, int seq, int tile, int head) {
+    // what the rows see; their queries come later, so that entries can be on their way first
+    __device__ __forceinline__ bool open(const AttendArgs &a, int seq, const KvRows &its, int tile, int head) {
         b = seq;
-        rows = kv_rows(a.c, b);
-        const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, total = rows.count * a.group;
+        rows = its;
+        const int lane = threadIdx.x & 63, n = lane & 15, total = rows.count * a.group;
         const int r0 = tile * kRows;
         if (r0 >= total) return false;
         const int r1 = r0 + kRows - 1 < total ? r0 + kRows - 1 : total - 1;
@@ -254,8 +259,17 @@ struct Tile {
         attend_span(a, rows, token, lo, hi);
         attend_span(a, rows, r0 / a.group, first, all_hi);
         attend_span(a, rows, r1 / a.group, all_lo, last);
-        out_row = attend_out_row(a, rows, head, use);
-        const int64_t at = attend_at(a, out_row, a.ld_q) + 8 * g;
+        batch_row = rows.first + token;
+        q_head = head * a.group + use - token * a.group;
+        return true;
+    }
+    // the row in lse, and where it starts in q or out
+    __device__ __forceinline__ int64_t out_row(const AttendArgs &a) const {
+        return (int64_t)batch_row * (a.c.heads * a.group) + q_head;
+    }
+    __device__ __forceinline__ int64_t at_row(int64_t ld) const { return batch_row * ld + (int64_t)q_head * D; }
+    __device__ __forceinline__ void queries(const AttendArgs &a) {
+        const int64_t at = at_row(a.ld_q) + 8 * ((threadIdx.x & 63) >> 4);
         float x[D / 32][8];
         uint32_t top = 0;
 #pragma unroll
@@ -274,7 +288,6 @@ struct Tile {
         const int shift = query_shift(top);
         q.set(x, a.scale < 0.0f ? -pow2i(shift) : pow2i(shift));
         factor = (top >> 23) == 255 ? __builtin_nanf("") : fabsf(a.scale) * pow2i(-shift);
-        return true;
     }
     int type;
 };
@@ -434,7 +447,7 @@ __device__ __forceinline__ void step(const Decode &k, Step<D> &t, const Tile<PIE
 }
 
 template <int PIECES, int D>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attend(AttendArgs a, Splits sp, int type) {
+__global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(AttendArgs a, Splits sp, int type) {
     constexpr int ROUNDS = Step<D>::ROUNDS, PITCH = D + 4;
     using R = Ring<D>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -444,10 +457,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attend(AttendArg
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, split = x % sp.few;
     const int per = (sp.few_room + kRows - 1) / kRows, b = x / sp.few / per, tile = x / sp.few - b * per;
-    if (kv_rows(a.c, b).count * a.group > sp.few_room) return;  // the other kernel's
+    const KvRows rows = kv_rows(a.c, b);
+    if (rows.count * a.group > sp.few_room) return;  // the other kernel's
     Tile<PIECES, D> q;
     q.type = type;
-    if (!q.open(a, b, tile, head)) return;
+    if (!q.open(a, b, rows, tile, head)) return;
+    q.queries(a);
     Running<D> run;
     run.clear();
     // this split's steps of 32 entries: whole rounds of the four wavefronts
@@ -551,7 +566,6 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attend(AttendArg
     const bool none = !(sum != 0.0f);  // NaN is a sum
     if (sp.few == 1) {
         const float inv = none ? 0.0f : 1.0f / sum, l2 = none ? -INFINITY : ref - kBias + log2_fast(sum);
-        const int64_t to_row = attend_at(a, q.out_row, a.ld_out);
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r)
 #pragma unroll
@@ -561,10 +575,10 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attend(AttendArg
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = run.o[r][j][i] * inv;
-                    kv_store8(type, a.out, to_row + 8 * w, v);
+                    kv_store8(type, a.out, q.at_row(a.ld_out) + 8 * w, v);
                 }
             }
-        if (g == 0) attend_lse(a, sp.lse2, q.out_row, l2);
+        if (g == 0) attend_lse(a, sp.lse2, q.out_row(a), l2);
     } else {
         const int64_t row = ((int64_t)split * a.c.B + b) * a.c.heads * sp.few_room + head * sp.few_room + q.row;
         if (g == 0) sp.few_stats[row] = make_float2(ref == -INFINITY ? ref : ref - kBias, sum);
@@ -685,10 +699,11 @@ __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits s
     for (int tile = i0 * a.group / kRows; tile * kRows < i1 * a.group; ++tile) {
         Tile<PIECES, D> q;
         q.type = type;
-        if (!q.open(a, b, tile, head)) break;
+        if (!q.open(a, b, rows, tile, head)) break;
+        q.queries(a);
         float p[8];
         products<PIECES, D>(decode, t, q.q, p);
-        const float lse = sp.lse2[q.out_row];
+        const float lse = sp.lse2[q.out_row(a)];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int at = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
@@ -711,24 +726,32 @@ struct Shape {
     int64_t few_rows, many_rows;    // rows that have parts
     int64_t bytes;                  // of the workspace
 };
+constexpr int64_t quads(int64_t floats) { return (floats + 3) / 4 * 4; }  // whole 16 bytes of a workspace
+
 Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D, bool ragged, bool mass) {
     Shape p{};
     p.sp.few_room = (int)(ragged ? kFewRows : group);
     p.few_tiles = B * ((p.sp.few_room + kRows - 1) / kRows);
     // slots of the other kernel's tiles: each sequence's first one starts at the slot of its first row + its number
     p.many_tiles = ragged && T * group > kFewRows ? T * group / attend_rows_tile(type, D) + B : 0;
-    // Workgroups: four for each CU, but no split below one step of each of its wavefronts
+    // as many workgroups as the GPU holds at once, but no split below one step of each of their wavefronts
     auto splits = [&](int64_t tiles, int64_t want, int64_t step) {
         const int64_t rounds = (capacity + step - 1) / step;
         int64_t n = want / (tiles * heads);
         n = n > rounds ? rounds : n;
         return (int)(n > 256 ? 256 : (n < 1 ? 1 : n));
     };
-    p.sp.few = splits(p.few_tiles, 1024, kKeys * kWaves);
+    const int64_t each = D > 128 ? at_once<1, 256> : (type == 0 && D == 128 ? at_once<2, 128> : at_once<1, 128>);
+    p.sp.few = splits(p.few_tiles, 256 * each, kKeys * kWaves);
     p.sp.many = p.many_tiles ? splits(p.many_tiles, 256, 512) : 1;
     p.few_rows = p.sp.few > 1 ? B * heads * p.sp.few_room : 0;
     p.many_rows = p.sp.many > 1 ? T * heads * group : 0;
-    p.bytes = (p.sp.few * p.few_rows + p.sp.many * p.many_rows) * (D * 4 + 8) + (mass ? (T * heads * group * 4 + 15) / 16 * 16 : 0);
+    const int64_t parts = p.sp.few * p.few_rows + p.sp.many * p.many_rows, all = quads(T * heads * group);
+    p.bytes = parts * D * 4 + quads(parts * 2) * 4 + (mass ? all * 4 : 0);
+    if (mass && p.many_tiles) {
+        p.sp.query_piece = all * D;
+        p.bytes += all * D * 2 * (type == 0 ? 2 : 1) + all * 4;
+    }
     return p;
 }
 Shape shape_of(int type, const AttendArgs &a) {
@@ -740,10 +763,16 @@ Shape shape_of(int type, const AttendArgs &a) {
     p.sp.many_sums = at;
     at += p.sp.many * p.many_rows * a.c.D;
     p.sp.few_stats = reinterpret_cast<float2 *>(at);
-    at += p.sp.few * p.few_rows * 2;
-    p.sp.many_stats = reinterpret_cast<float2 *>(at);
-    at += p.sp.many * p.many_rows * 2;
-    p.sp.lse2 = a.mass != nullptr ? at : nullptr;
+    p.sp.many_stats = p.sp.few_stats + p.sp.few * p.few_rows;
+    if (a.mass == nullptr) return p;
+    at += quads((p.sp.few * p.few_rows + p.sp.many * p.many_rows) * 2);
+    const int64_t all = quads((int64_t)a.c.T * a.c.heads * a.group);
+    p.sp.lse2 = at;
+    at += all;
+    if (p.many_tiles) {
+        p.sp.factors = at;
+        p.sp.queries = reinterpret_cast<_Float16 *>(at + all);
+    }
     return p;
 }
 static_assert(kKeys * kWaves == 128, "both kernels of the weights take 128 entries a workgroup");
