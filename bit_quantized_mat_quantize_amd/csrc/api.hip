@@ -874,7 +874,8 @@ size_t head_row_bytes(int64_t N, int64_t k) {
 }
 
 // ---- between the projections
-constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxSeqs = 65536, kMaxHeads = 1024, kMaxPositions = int64_t(1) << 30;
+constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxSeqs = 65536, kMaxHeads = 1024, kMaxPositions = int64_t(1) << 30,
+                  kMaxQueryRows = int64_t(1) << 30;  // rows times query heads
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // workgroups of 256 threads of one launch
 
 // Two sets of rows of n elements, `ld` elements apart, that share no element although their ranges overlap: column
@@ -1274,7 +1275,7 @@ qmm_status qmm_cache_read(const qmm_cache *c, qmm_float_type t, void *k, size_t 
 size_t qmm_cache_attention_workspace_bytes(qmm_float_type t, int64_t rows, int64_t q_heads, int64_t heads, int64_t dim, int64_t seqs,
                                            int64_t width, int64_t page, int ragged, int mass) {
     if (!float_size(t) || rows < 1 || rows > kMaxTokens || heads < 1 || heads > kMaxHeads || q_heads < heads || q_heads > kMaxHeads ||
-        q_heads % heads || !cache_dim_ok(dim) || !cache_page_ok(page) || seqs < 1 || seqs > kMaxSeqs || width < 1 ||
+        q_heads % heads || rows > kMaxQueryRows / q_heads || !cache_dim_ok(dim) || !cache_page_ok(page) || seqs < 1 || seqs > kMaxSeqs || width < 1 ||
         width > kMaxPositions / page)
         return 0;
     return (size_t)qmm::attend_workspace_bytes((int)t, rows, seqs, width * page, heads, q_heads / heads, dim, ragged != 0, mass != 0);
@@ -1291,6 +1292,8 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
     if (q_heads < c->heads || q_heads > kMaxHeads || q_heads % c->heads)
         return fail(QMM_EUNSUPPORTED, "%lld query heads over %lld cache heads: a multiple of these, at most %lld",
                     (long long)q_heads, (long long)c->heads, (long long)kMaxHeads);
+    if (c->rows > kMaxQueryRows / q_heads)
+        return fail(QMM_EUNSUPPORTED, "%lld rows of %lld query heads exceed the limit of 2^30", (long long)c->rows, (long long)q_heads);
     if (!(scale >= -1e30f && scale <= 1e30f)) return fail(QMM_EINVAL, "scale = %g", (double)scale);
     if (window < 0) return fail(QMM_EINVAL, "window = %lld is negative", (long long)window);
     if (window > 0 && !causal) return fail(QMM_EUNSUPPORTED, "a window of what is not causal");
@@ -1333,7 +1336,7 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
     a.ld_mass = ld_mass;
     a.scale = (float)((double)scale * 1.4426950408889634074);  // log2 e
     a.group = (int)(q_heads / c->heads);
-    a.window = (int)(window > kMaxPositions ? 0 : window);
+    a.window = (int)(window >= capacity ? 0 : window);  // as good as none
     a.causal = causal != 0;
     if (!qmm::attend_grid_ok((int)t, a))
         return fail(QMM_EUNSUPPORTED, "rows = %lld, seqs = %lld, heads = %lld need more than %lld workgroups",

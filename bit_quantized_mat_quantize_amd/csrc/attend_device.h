@@ -114,8 +114,9 @@ struct Splits {
     float2 *few_stats;    // [few][seqs * heads * few_room]: (reference - bias, sum)
     float *many_sums;     // [many][T * query heads][D]
     float2 *many_stats;   // [many][T * query heads]
-    float *lse2;          // [T * query heads] in log2 units, or null
-    // what attend_rows.hip leaves for attend_mass.hip, by (cache head, token, head of the group), or null:
+    // for the weights of the entries, by (cache head, token, head of the group): attend_group_row
+    float *lse2;          // [heads * T * group] in log2 units, or null
+    // and what attend_rows.hip leaves for attend_mass.hip, or null:
     _Float16 *queries;    // [pieces][heads * T * group][D], as query_pieces has them
     int64_t query_piece;  // elements of a piece
     float *factors;       // [heads * T * group], of the rows' products
@@ -132,9 +133,16 @@ __device__ __forceinline__ int64_t attend_at(const AttendArgs &a, int64_t out_ro
     const int64_t token = out_row / heads;
     return token * ld + (out_row - token * heads) * a.c.D;
 }
+// the place of a token's query head among the rows of its cache head
+__device__ __forceinline__ int64_t attend_group_row(const AttendArgs &a, int token, int head, int of_group) {
+    return ((int64_t)head * a.c.T + token) * a.group + of_group;
+}
 __device__ __forceinline__ void attend_lse(const AttendArgs &a, float *lse2, int64_t out_row, float l2) {
     if (a.lse != nullptr) a.lse[out_row] = l2 * kLn2;
-    if (lse2 != nullptr) lse2[out_row] = l2;
+    if (lse2 == nullptr) return;
+    const int row = (int)out_row, token = row / (a.c.heads * a.group), q_head = row - token * (a.c.heads * a.group);
+    const int head = q_head / a.group;
+    lse2[attend_group_row(a, token, head, q_head - head * a.group)] = l2;
 }
 
 // attend_rows.hip: sequences of more than kFewRows rows

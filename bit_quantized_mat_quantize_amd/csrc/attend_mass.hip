@@ -22,7 +22,7 @@ template <int PIECES, int D>
 struct Shape {
     static constexpr int NB = D / 32, WORDS = D / 8;
     // load instructions of a wavefront; bytes, with room for what the last instructions load beyond row 63
-    static constexpr int PER_PIECE = (kRows * D * 2 + 8191) / 8192, LOADS = PIECES * PER_PIECE;
+    static constexpr int PER_PIECE = (kRows * D * 2 + 8191) / 8192, LOADS = PIECES * PER_PIECE + 1;
     static constexpr int PIECE = PER_PIECE * 8192, STAGE = PIECES * PIECE;
     static constexpr int SLOTS = STAGE * 3 <= 150 * 1024 ? 3 : 2, BYTES = SLOTS * STAGE;
     static_assert(PIECE <= 65536 && BYTES <= 160 * 1024 - 1024, "LDS of a compute unit");
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
     using S = Shape<PIECES, D>;
     constexpr int NB = S::NB, WORDS = S::WORDS;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ float2 rows_at[2][kRows];  // of a row's products: factor; -lse2
+    __shared__ __attribute__((aligned(16))) float rows_at[S::SLOTS][2][kRows];  // lse2 of a row; factor of its products
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, hf = lane >> 5;
     const int head = blockIdx.x % a.c.heads, x0 = blockIdx.x / a.c.heads, b = x0 / tiles;
     const int e0 = (x0 - b * tiles) * kEntries, k0 = e0 + 32 * (wave & 3), stream = wave >> 2;
@@ -128,7 +128,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
         const int at = 1024 * (wave * S::PER_PIECE + i) + 16 * lane, row = at / (D * 2), w = at % (D * 2) / 16;
         place[i] = row * D * 2 + ((D == 96 ? w ^ ((row >> 1) & 3) : w ^ (row & 7)) * 16);
     }
-    const int64_t row0 = ((int64_t)head * a.c.T + rows.first) * a.group;  // of the sequence, among the queries
+    const int64_t row0 = attend_group_row(a, rows.first, head, 0);
+    const uint32_t rows_lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) float *)&rows_at[0][0][0]);
     const Steps by_group(a.group);
     auto load = [&](int r0, int slot) {  // rows r0 .. r0 + 63: what lies behind the last of all is not read
 #pragma unroll
@@ -142,37 +143,29 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
                                  lds_at + slot * S::STAGE + k * S::PIECE + 1024 * (wave * S::PER_PIECE + i)),
                              "v"(place[i]), "s"(r) : "memory");
         }
+        // four wavefronts each load the same: a wavefront's number of loads is then known
+        const uint64_t base = (uint64_t)(uintptr_t)((wave & 1 ? sp.factors : sp.lse2) + row0 + r0);
+        const u32x4 r = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, (uint32_t)((total - r0 < kRows ? total - r0 : kRows) * 4),
+                         0x00020000u};
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
+                         rows_lds + slot * (8 * kRows) + (wave & 1) * (4 * kRows)),
+                     "v"(4 * lane), "s"(r) : "memory");
     };
-    // factor and lse2 of a step's rows, by the first 64 threads
-    auto weights = [&](const Row &first, int stage) {
-        if (threadIdx.x >= kRows) return;
-        const Row at = by_group.on(first, threadIdx.x);
-        float2 v = make_float2(0.0f, -INFINITY);  // a row that has nothing (or is none) weighs nothing
-        if (at.token < rows.count) {
-            const float lse = sp.lse2[(int64_t)(rows.first + at.token) * (a.c.heads * a.group) + head * a.group + at.head];
-            if (lse != -INFINITY) v = make_float2(sp.factors[row0 + at.token * a.group + at.head], -lse);
-        }
-        rows_at[stage][threadIdx.x] = v;
-    };
-
     float got[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) got[r] = 0.0f;
     const int begin = i0 * a.group, end = i1 * a.group;
-    Row next = by_group.at(begin), mine = by_group.on(next, 32 * stream);  // of the weights; of this wavefront's products
+    Row mine = by_group.on(by_group.at(begin), 32 * stream);
     constexpr int AHEAD = S::SLOTS - 1;
     for (int i = 0; i < AHEAD; ++i)
         if (begin + i * kRows < end) load(begin + i * kRows, i);
-    weights(next, 0);
     int slot = 0;
-    for (int r0 = begin, stage = 0; r0 < end; r0 += kRows, stage ^= 1, slot = slot + 1 == S::SLOTS ? 0 : slot + 1) {
+    for (int r0 = begin; r0 < end; r0 += kRows, slot = slot + 1 == S::SLOTS ? 0 : slot + 1) {
         // this wavefront's part of the step's rows is there, then everybody's; nobody reads the slot that is filled next
         if (AHEAD > 1 && r0 + kRows < end) wait_loads<(AHEAD > 1 ? S::LOADS : 0)>();
         else wait_loads<0>();
         __syncthreads();
         if (r0 + AHEAD * kRows < end) load(r0 + AHEAD * kRows, slot == 0 ? S::SLOTS - 1 : slot - 1);
-        next = by_group.on(next, kRows);
-        if (r0 + kRows < end) weights(next, stage ^ 1);
         const int wr0 = r0 + 32 * stream, wr1 = wr0 + 31;
         if (wr0 < end && k0 < rows.len) {
             int lo0, hi0, lo1, hi1;  // what the first and the last of the wavefront's rows see
@@ -195,8 +188,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
                         x = mfma32(kl[i], qh, x);
                     }
                 }
-                const float2 row = rows_at[stage][32 * stream + n];
-                const float by = row.x * down;
+                // a row that has nothing weighs nothing
+                const float lse = rows_at[slot][0][32 * stream + n], up = lse == -INFINITY ? lse : -lse;
+                const float by = lse == -INFINITY ? 0.0f : rows_at[slot][1][32 * stream + n] * down;
                 if (k0 < lo1 || k0 + 32 > hi0 || wr1 >= total) {
                     int lo = 1, hi = 0;
                     const int token = by_group.on(mine, n).token;
@@ -204,11 +198,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int at = k0 + 8 * (r >> 2) + 4 * hf + (r & 3);
-                        got[r] += at >= lo && at < hi ? exp2_fast(fmaf(x[r], by, row.y)) : 0.0f;
+                        got[r] += at >= lo && at < hi ? exp2_fast(fmaf(x[r], by, up)) : 0.0f;
                     }
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) got[r] += exp2_fast(fmaf(x[r], by, row.y));
+                    for (int r = 0; r < 16; ++r) got[r] += exp2_fast(fmaf(x[r], by, up));
                 }
             }
         }

@@ -321,7 +321,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
         }
         factor = (top >> 23) == 255 ? __builtin_nanf("") : fabsf(a.scale) * pow2i(-shift);
         if (sp.queries != nullptr && split == 0 && live) {  // for the weights of the entries
-            const int64_t row = ((int64_t)head * a.c.T + rows.first) * a.group + use;
+            const int64_t row = attend_group_row(a, rows.first, head, use);
 #pragma unroll
             for (int i = 0; i < 2 * NB; ++i) {
                 _Float16 *p = sp.queries + row * D + 16 * i + 8 * hf;

@@ -703,7 +703,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits s
         q.queries(a);
         float p[8];
         products<PIECES, D>(decode, t, q.q, p);
-        const float lse = sp.lse2[q.out_row(a)];
+        const float lse = sp.lse2[attend_group_row(a, q.batch_row, head, q.q_head - head * a.group)];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int at = k0 + 16 * (i >> 2) + 4 * g + (i & 3);
