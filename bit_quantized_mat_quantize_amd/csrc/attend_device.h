@@ -149,8 +149,7 @@ __device__ __forceinline__ void attend_lse(const AttendArgs &a, float *lse2, int
 int64_t attend_rows_tile(int type, int64_t D);  // rows of a tile
 hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s);
 
-// attend_mass.hip: the weights of their entries; workgroups per sequence and head
-int64_t attend_mass_tiles(const AttendArgs &a);
+// attend_mass.hip: the weights of their entries
 hipError_t launch_attend_mass_rows(int type, const AttendArgs &a, const Splits &sp, hipStream_t s);
 
 }  // namespace qmm

@@ -2,30 +2,34 @@
 // query rows (gfx950): mass[j] += sum over rows and heads of the group of 2^(x - lse2),
 // with the rows' lse2 from attend_rows.hip.
 //
-// A workgroup owns 128 entries of a sequence and cache head and goes over all rows that
-// see any of them, 64 at a time: wavefronts 0 .. 3 take 32 entries each against the first
-// 32 rows, 4 .. 7 the same entries against the others.  The entries stay in registers,
-// decoded to fp16 (two pieces for fp32 queries, as in attend_rows.hip).  The rows' queries
-// come by direct loads into LDS, two steps ahead, as attend_rows.hip left them, fp16 and
-// scaled: converting them anew in every workgroup took most of its time (three prompts
-// of 700 rows, 28 heads of 128, fp32: 180 against 128 us).  Every entry's sum is
-// formed in a fixed order by its owner: per lane over the rows, over the lanes, over the
-// two halves.
+// A workgroup of four wavefronts owns 64 entries of a sequence and cache head and goes over
+// all rows that see any of them, 64 at a time: two wavefronts take 32 entries each against
+// the first 32 rows, the others the same entries against the others.  Two such workgroups
+// share a compute unit, and one's products run beside the other's exponentials: 111 us at
+// the size below; one workgroup of eight wavefronts took 121 with 128 entries and 126 with
+// 128 rows.  The entries stay in registers, decoded to fp16 (two pieces for fp32 queries, as
+// in attend_rows.hip).  The rows' queries come by direct loads into LDS, a step or two
+// ahead, as attend_rows.hip left them, fp16 and scaled: converting them anew in every
+// workgroup took 180 us where loading them took 128 (three prompts of 700 rows, 28 heads of
+// 128, fp32), and 121 with the rows' factors and lse loaded that way too.  Every entry's sum
+// is formed in a fixed order: per lane over the rows, over the lanes, over the two
+// wavefronts that share the entries.
 #include "attend_device.h"
 
 namespace qmm {
 namespace {
 
-constexpr int kThreads = 512, kRows = 64, kEntries = 128;
+constexpr int kThreads = 256;
 
 template <int PIECES, int D>
 struct Shape {
     static constexpr int NB = D / 32, WORDS = D / 8;
-    // load instructions of a wavefront; bytes, with room for what the last instructions load beyond row 63
-    static constexpr int PER_PIECE = (kRows * D * 2 + 8191) / 8192, LOADS = PIECES * PER_PIECE + 1;
-    static constexpr int PIECE = PER_PIECE * 8192, STAGE = PIECES * PIECE;
-    static constexpr int SLOTS = STAGE * 3 <= 150 * 1024 ? 3 : 2, BYTES = SLOTS * STAGE;
-    static_assert(PIECE <= 65536 && BYTES <= 160 * 1024 - 1024, "LDS of a compute unit");
+    // wavefronts that share entries, each with 32 rows of a step; wavefronts with entries of their own
+    static constexpr int STREAMS = 2, OWNERS = 2, ROWS = 32 * STREAMS, ENTRIES = 32 * OWNERS;
+    static constexpr int PIECE = ROWS * D * 2, STAGE = PIECES * PIECE;  // bytes
+    static constexpr int PER_PIECE = PIECE / 4096, LOADS = PIECES * PER_PIECE + 1;  // load instructions of a wavefront
+    static constexpr int SLOTS = STAGE * 3 <= 75 * 1024 ? 3 : 2, BYTES = SLOTS * STAGE;
+    static_assert(ROWS == 64 && BYTES <= 160 * 1024 - 8 * SLOTS * ROWS, "a lane loads a row's numbers; LDS of a compute unit");
 };
 // The place of 16-byte piece w of a row: eight lanes of one access meet eight of them, for rows of
 // 128 bytes or multiples; rows of 192 bytes start 64 bytes apart already, four pieces are moved.
@@ -39,8 +43,8 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 // Query row r of a sequence as (token, head of the group), and steps of up to 64 rows without a
-// division by the group g: x * ceil(2^21 / g) >> 21 is x / g for x < 1088 and g <= 1024, because the
-// quotient is too large by less than x / 2^21 < 1 / g.
+// division by the group g: x * ceil(2^21 / g) >> 21 is x / g for x < g + 64 and g <= 1024, because
+// the quotient is too large by less than x / 2^21 < 1 / g.
 struct Row {
     int token, head;
 };
@@ -58,20 +62,22 @@ struct Steps {
 };
 
 template <int PIECES, int D>
-__global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, Splits sp, int type, int tiles) {
+__global__ __launch_bounds__(kThreads, 2) void k_attend_mass_rows(AttendArgs a, Splits sp) {
     using S = Shape<PIECES, D>;
     constexpr int NB = S::NB, WORDS = S::WORDS;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ __attribute__((aligned(16))) float rows_at[S::SLOTS][2][kRows];  // lse2 of a row; factor of its products
+    __shared__ __attribute__((aligned(16))) float rows_at[S::SLOTS][2][S::ROWS];  // lse2 of a row; factor of its products
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, hf = lane >> 5;
-    const int head = blockIdx.x % a.c.heads, x0 = blockIdx.x / a.c.heads, b = x0 / tiles;
-    const int e0 = (x0 - b * tiles) * kEntries, k0 = e0 + 32 * (wave & 3), stream = wave >> 2;
+    const int head = blockIdx.x % a.c.heads, x0 = blockIdx.x / a.c.heads;
+    constexpr int ROWS = S::ROWS, OWNERS = S::OWNERS;
+    const int tile = x0 / a.c.B, b = x0 - tile * a.c.B;  // more rows see earlier entries: first
+    const int e0 = tile * S::ENTRIES, k0 = e0 + 32 * (wave % OWNERS), stream = wave / OWNERS;
     const KvRows rows = kv_rows(a.c, b);
     const int total = rows.count * a.group;
     if (total <= sp.few_room || e0 >= rows.len) return;
     // tokens that see any of the 128 entries
     const int before = rows.len - rows.count;
-    int i0 = a.causal ? e0 - before : 0, i1 = a.window > 0 ? e0 + kEntries - 1 + a.window - before : rows.count;
+    int i0 = a.causal ? e0 - before : 0, i1 = a.window > 0 ? e0 + S::ENTRIES - 1 + a.window - before : rows.count;
     i0 = i0 < 0 ? 0 : i0;
     i1 = i1 > rows.count ? rows.count : i1;
     if (i0 >= i1) return;
@@ -120,7 +126,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
     }
     const float down = pow2i(-shift);
 
-    // ---- rows into LDS: a wavefront loads eighths of each piece, a lane the 16 bytes that belong to its place
+    // ---- rows into LDS: a wavefront loads a fourth of each piece, a lane the 16 bytes that belong to its place
     const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds);
     uint32_t place[S::PER_PIECE];
 #pragma unroll
@@ -131,11 +137,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
     const int64_t row0 = attend_group_row(a, rows.first, head, 0);
     const uint32_t rows_lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) float *)&rows_at[0][0][0]);
     const Steps by_group(a.group);
-    auto load = [&](int r0, int slot) {  // rows r0 .. r0 + 63: what lies behind the last of all is not read
+    auto load = [&](int r0, int slot) {  // rows from r0 on: what lies behind the last of all is not read
 #pragma unroll
         for (int k = 0; k < PIECES; ++k) {
             const uint64_t base = (uint64_t)(uintptr_t)(sp.queries + k * sp.query_piece + (row0 + r0) * D);
-            const u32x4 r = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, (uint32_t)((total - r0 < kRows ? total - r0 : kRows) * D * 2),
+            const u32x4 r = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, (uint32_t)((total - r0 < ROWS ? total - r0 : ROWS) * D * 2),
                              0x00020000u};
 #pragma unroll
             for (int i = 0; i < S::PER_PIECE; ++i)
@@ -143,12 +149,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
                                  lds_at + slot * S::STAGE + k * S::PIECE + 1024 * (wave * S::PER_PIECE + i)),
                              "v"(place[i]), "s"(r) : "memory");
         }
-        // four wavefronts each load the same: a wavefront's number of loads is then known
+        // the wavefronts load the same by twos, so that all have as many loads
         const uint64_t base = (uint64_t)(uintptr_t)((wave & 1 ? sp.factors : sp.lse2) + row0 + r0);
-        const u32x4 r = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, (uint32_t)((total - r0 < kRows ? total - r0 : kRows) * 4),
+        const u32x4 r = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, (uint32_t)((total - r0 < ROWS ? total - r0 : ROWS) * 4),
                          0x00020000u};
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
-                         rows_lds + slot * (8 * kRows) + (wave & 1) * (4 * kRows)),
+                         rows_lds + slot * (8 * ROWS) + (wave & 1) * (4 * ROWS)),
                      "v"(4 * lane), "s"(r) : "memory");
     };
     float got[16];
@@ -158,14 +164,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
     Row mine = by_group.on(by_group.at(begin), 32 * stream);
     constexpr int AHEAD = S::SLOTS - 1;
     for (int i = 0; i < AHEAD; ++i)
-        if (begin + i * kRows < end) load(begin + i * kRows, i);
+        if (begin + i * ROWS < end) load(begin + i * ROWS, i);
     int slot = 0;
-    for (int r0 = begin; r0 < end; r0 += kRows, slot = slot + 1 == S::SLOTS ? 0 : slot + 1) {
+    for (int r0 = begin; r0 < end; r0 += ROWS, slot = slot + 1 == S::SLOTS ? 0 : slot + 1) {
         // this wavefront's part of the step's rows is there, then everybody's; nobody reads the slot that is filled next
-        if (AHEAD > 1 && r0 + kRows < end) wait_loads<(AHEAD > 1 ? S::LOADS : 0)>();
+        if (AHEAD > 1 && r0 + ROWS < end) wait_loads<(AHEAD > 1 ? S::LOADS : 0)>();
         else wait_loads<0>();
         __syncthreads();
-        if (r0 + AHEAD * kRows < end) load(r0 + AHEAD * kRows, slot == 0 ? S::SLOTS - 1 : slot - 1);
+        if (r0 + AHEAD * ROWS < end) load(r0 + AHEAD * ROWS, slot == 0 ? S::SLOTS - 1 : slot - 1);
         const int wr0 = r0 + 32 * stream, wr1 = wr0 + 31;
         if (wr0 < end && k0 < rows.len) {
             int lo0, hi0, lo1, hi1;  // what the first and the last of the wavefront's rows see
@@ -206,26 +212,24 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_mass_rows(AttendArgs a, 
                 }
             }
         }
-        mine = by_group.on(mine, kRows);
+        mine = by_group.on(mine, ROWS);
     }
-    // over the 32 rows that lie along the lanes, then over the two halves
+    // over the 32 rows that lie along the lanes, then over the wavefronts that share the entries
 #pragma unroll
     for (int r = 0; r < 16; ++r)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) got[r] += __shfl_xor(got[r], o, 64);
     __syncthreads();
     float *other = reinterpret_cast<float *>(lds);
-    if (stream == 1 && n == 0)
+    if (n == 0)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) other[32 * (wave & 3) + 8 * (r >> 2) + 4 * hf + (r & 3)] = got[r];
+        for (int r = 0; r < 16; ++r) other[32 * wave + 8 * (r >> 2) + 4 * hf + (r & 3)] = got[r];
     __syncthreads();
-    if (stream == 0 && n == 0) {
-        float *mass = a.mass + ((int64_t)b * a.c.heads + head) * a.ld_mass;
+    if (threadIdx.x < S::ENTRIES && e0 + (int)threadIdx.x < rows.len) {
+        float sum = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int e = 8 * (r >> 2) + 4 * hf + (r & 3);
-            if (k0 + e < rows.len) mass[k0 + e] += got[r] + other[32 * wave + e];
-        }
+        for (int i = 0; i < S::STREAMS; ++i) sum += other[S::ENTRIES * i + threadIdx.x];
+        a.mass[((int64_t)b * a.c.heads + head) * a.ld_mass + e0 + threadIdx.x] += sum;
     }
 }
 
@@ -235,9 +239,8 @@ hipError_t launch(int type, const AttendArgs &a, const Splits &sp, hipStream_t s
     static std::atomic<uint64_t> lds_set{0};
     const hipError_t e = ensure_lds_bytes((const void *)k_attend_mass_rows<PIECES, D>, S::BYTES, lds_set);
     if (e != hipSuccess) return e;
-    const int64_t tiles = attend_mass_tiles(a);
-    hipLaunchKernelGGL((k_attend_mass_rows<PIECES, D>), dim3((unsigned)(a.c.B * tiles * a.c.heads)), dim3(kThreads), S::BYTES, s,
-                       a, sp, type, (int)tiles);
+    const int64_t tiles = (((int64_t)a.c.width << a.c.page_log2) + S::ENTRIES - 1) / S::ENTRIES;
+    hipLaunchKernelGGL((k_attend_mass_rows<PIECES, D>), dim3((unsigned)(a.c.B * tiles * a.c.heads)), dim3(kThreads), S::BYTES, s, a, sp);
     return hipGetLastError();
 }
 template <int PIECES>
@@ -252,10 +255,6 @@ hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, hipStream
 }
 
 }  // namespace
-
-int64_t attend_mass_tiles(const AttendArgs &a) {
-    return (((int64_t)a.c.width << a.c.page_log2) + kEntries - 1) / kEntries;
-}
 
 hipError_t launch_attend_mass_rows(int type, const AttendArgs &a, const Splits &sp, hipStream_t s) {
     return type == 0 ? launch_for<2>(type, a, sp, s) : launch_for<1>(type, a, sp, s);

@@ -775,7 +775,10 @@ Shape shape_of(int type, const AttendArgs &a) {
     }
     return p;
 }
-static_assert(kKeys * kWaves == 128, "both kernels of the weights take 128 entries a workgroup");
+// workgroups of k_attend_mass per sequence and head; attend_mass.hip's take half as many entries
+int64_t mass_tiles(const AttendArgs &a) {
+    return (((int64_t)a.c.width << a.c.page_log2) + kKeys * kWaves - 1) / (kKeys * kWaves);
+}
 
 template <int PIECES, int D>
 hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) {
@@ -801,7 +804,7 @@ hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) 
     if (e != hipSuccess || a.mass == nullptr) return e;
     if (p.many_tiles) e = launch_attend_mass_rows(type, a, p.sp, s);
     if (e != hipSuccess) return e;
-    const int64_t per = attend_mass_tiles(a);
+    const int64_t per = mass_tiles(a);
     hipLaunchKernelGGL((k_attend_mass<PIECES, D>), dim3((unsigned)(a.c.B * per * a.c.heads)), dim3(kThreads), 0, s, a, p.sp,
                        type, (int)per);
     return hipGetLastError();
@@ -835,7 +838,7 @@ bool attend_grid_ok(int type, const AttendArgs &a) {
     constexpr int64_t most = (int64_t(1) << 24) - 1;  // workgroups of 256 threads; half as many of 512
     const Shape p = shape_of(type, a);
     return p.few_tiles * p.sp.few * a.c.heads <= most && p.many_tiles * p.sp.many * a.c.heads <= most / 2 &&
-           p.few_rows + p.many_rows <= most && (a.mass == nullptr || a.c.B * attend_mass_tiles(a) * a.c.heads <= most / 2);
+           p.few_rows + p.many_rows <= most && (a.mass == nullptr || a.c.B * mass_tiles(a) * a.c.heads <= most / 2);
 }
 
 hipError_t launch_attend(int type, const AttendArgs &a, hipStream_t s) {
