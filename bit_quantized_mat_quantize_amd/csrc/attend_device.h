@@ -103,23 +103,115 @@ __device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) { return __builtin_amdgcn
 __device__ __forceinline__ f16v mfma32(h8 a, h8 b, f16v c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 
 // ---- who takes a sequence, and where its splits' parts go.  Query rows of a sequence
-// and cache head: token * group + head of the group.  Up to kFewRows of them (all, where
-// every sequence has one token) go to attention.hip's kernel, more to attend_rows.hip's.
-constexpr int kFewRows = 32;
+// and cache head: token * group + head of the group.  Up to few_room of them (all, where
+// every sequence has one token) go to attention.hip's kernel in tiles of kFewTile, more to
+// attend_rows.hip's in tiles of kManyTile.
+constexpr int kFewTile = 16, kManyTile = 256;
 
 struct Splits {
-    int few, many;        // splits of the two kernels' tiles
-    int few_room;         // rows that a sequence and head has among the parts of the first
-    float *few_sums;      // [few][seqs * heads * few_room][D]
-    float2 *few_stats;    // [few][seqs * heads * few_room]: (reference - bias, sum)
-    float *many_sums;     // [many][T * query heads][D]
-    float2 *many_stats;   // [many][T * query heads]
+    int few_room;
+    int few_tiles, many_tiles;  // tiles at most (starts that do not ascend could say more)
+    int few_want, many_want;    // workgroups of a cache head that fill the GPU
+    int few_most, many_most;    // splits at most
+    int few_rows;             // rows of a tile that can have any (many: kManyTile)
+    float *few_sums;          // [split][tile][head][few_rows][D]
+    float2 *few_stats;        // [split][tile][head][few_rows]: (reference - bias, sum)
+    float *many_sums;         // the same, of kManyTile rows
+    float2 *many_stats;
     // for the weights of the entries, by (cache head, token, head of the group): attend_group_row
-    float *lse2;          // [heads * T * group] in log2 units, or null
+    float *lse2;              // [heads * T * group] in log2 units, or null
     // and what attend_rows.hip leaves for attend_mass.hip, or null:
-    _Float16 *queries;    // [pieces][heads * T * group][D], as query_pieces has them
-    int64_t query_piece;  // elements of a piece
-    float *factors;       // [heads * T * group], of the rows' products
+    _Float16 *queries;        // [pieces][heads * T * group][D], as query_pieces has them
+    int64_t query_piece;      // elements of a piece
+    float *factors;           // [heads * T * group], of the rows' products
+};
+
+// The tiles of a call that have rows of one of the two kernels, in the sequences' order, and into how many splits
+// of the entries each goes: the GPU's workgroups over the tiles.  Only the device knows how many rows a sequence has,
+// so each wavefront counts them: sequence 64 k + lane's tiles end at upto[k].  Beyond kCounted sequences that
+// takes too long; there sequence b's tiles start at slot floor(starts[b] * group / ROWS) + b, not all slots have
+// rows, and nothing is split: so many sequences fill the GPU.
+constexpr int kCounted = 256;
+// sum over the lanes up to this one
+__device__ __forceinline__ int wave_upto(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // the lane 1, 2, 4, 8 below, in rows of 16
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row 0's last lane to row 1, 2's to 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row 1's last lane to rows 2 and 3
+    return v;
+}
+template <int ROWS>
+struct Tiles {
+    int upto[kCounted / 64], own[kCounted / 64];
+    KvRows rows[kCounted / 64];
+    int live, splits;
+
+    __device__ __forceinline__ void open(const AttendArgs &a, const Splits &sp) {
+        constexpr bool many = ROWS == kManyTile;
+        const int room = sp.few_room, want = many ? sp.many_want : sp.few_want, most = many ? sp.many_most : sp.few_most;
+        const int lane = threadIdx.x & 63;
+        splits = 1;
+        if (a.c.starts == nullptr) live = a.c.B * ((a.group + ROWS - 1) / ROWS);
+        else if (a.c.B > kCounted) {
+            live = a.c.T * a.group / ROWS + a.c.B;
+            return;
+        } else {
+            live = 0;
+#pragma unroll
+            for (int k = 0; k < kCounted / 64; ++k) {
+                if (64 * k >= a.c.B) break;
+                const int b = 64 * k + lane;
+                rows[k] = kv_rows(a.c, b < a.c.B ? b : a.c.B - 1);
+                const int n = b < a.c.B ? rows[k].count * a.group : 0;
+                own[k] = (n > room) == many ? (n + ROWS - 1) / ROWS : 0;
+                upto[k] = live + wave_upto(own[k]);
+                live = __builtin_amdgcn_readlane(upto[k], 63);
+            }
+            const int tiles = many ? sp.many_tiles : sp.few_tiles;
+            live = live < tiles ? live : tiles;
+        }
+        if (live > 0) {
+            const int n = want / live;
+            splits = n > most ? most : (n < 1 ? 1 : n);
+        }
+    }
+    // the sequence, its rows and tile, or false (a slot without rows)
+    __device__ __forceinline__ bool place(const AttendArgs &a, int at, int &b, int &tile, KvRows &its) const {
+        if (a.c.starts == nullptr) {
+            const int per = (a.group + ROWS - 1) / ROWS;
+            b = at / per;
+            tile = at - b * per;
+            its = kv_rows(a.c, b);
+            return true;
+        }
+        if (a.c.B > kCounted) {
+            auto slot = [&](int i) {
+                const int t = a.c.starts[i];
+                return (int64_t)(t < 0 ? 0 : (t > a.c.T ? a.c.T : t)) * a.group / ROWS + i;
+            };
+            b = __builtin_amdgcn_readfirstlane(kv_last_not_above(a.c.B, at, slot));
+            if (b < 0) return false;
+            tile = __builtin_amdgcn_readfirstlane((int)(at - slot(b)));
+            its = kv_rows(a.c, b);
+            return tile >= 0;  // below 0: starts that do not ascend
+        }
+#pragma unroll
+        for (int k = 0; k < kCounted / 64; ++k) {
+            if (64 * k >= a.c.B) break;
+            const uint64_t past = __ballot(upto[k] > at);
+            if (past == 0) continue;
+            const int l = __builtin_ctzll(past);
+            b = 64 * k + l;
+            tile = at - __builtin_amdgcn_readlane(upto[k] - own[k], l);
+            its.first = __builtin_amdgcn_readlane(rows[k].first, l);
+            its.count = __builtin_amdgcn_readlane(rows[k].count, l);
+            its.len = __builtin_amdgcn_readlane(rows[k].len, l);
+            return true;
+        }
+        return false;
+    }
 };
 
 // the row of the batch's output, token * query heads + head, of a sequence's query row
@@ -145,9 +237,9 @@ __device__ __forceinline__ void attend_lse(const AttendArgs &a, float *lse2, int
     lse2[attend_group_row(a, token, head, q_head - head * a.group)] = l2;
 }
 
-// attend_rows.hip: sequences of more than kFewRows rows
-int64_t attend_rows_tile(int type, int64_t D);  // rows of a tile
-hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s);
+// attend_rows.hip: sequences of more than few_room rows; whether it has a kernel for such rows
+constexpr bool attend_rows_has(int type, int64_t D) { return D <= (type == 0 ? 128 : 192); }
+hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t workgroups, hipStream_t s);
 
 // attend_mass.hip: the weights of their entries
 hipError_t launch_attend_mass_rows(int type, const AttendArgs &a, const Splits &sp, hipStream_t s);

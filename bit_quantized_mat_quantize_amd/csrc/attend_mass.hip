@@ -249,9 +249,9 @@ hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, hipStream
         case 64: return launch<PIECES, 64>(type, a, sp, s);
         case 96: return launch<PIECES, 96>(type, a, sp, s);
         case 128: return launch<PIECES, 128>(type, a, sp, s);
-        case 192: return launch<PIECES, 192>(type, a, sp, s);
-        default: return launch<PIECES, 256>(type, a, sp, s);
     }
+    if constexpr (PIECES == 1) return launch<1, 192>(type, a, sp, s);
+    return hipErrorInvalidValue;  // attend_rows_has
 }
 
 }  // namespace

@@ -24,13 +24,11 @@
 namespace qmm {
 namespace {
 
-// Rows of a tile, entries of a step.  Two pieces of long heads need the registers of
-// one wavefront per SIMD, and LDS for half as many entries.
+// Rows of a tile, entries of a step.
 template <int PIECES, int D>
 struct Shape {
-    static constexpr int WAVES = PIECES == 2 && D > 128 ? 4 : 8;
-    static constexpr int KT = PIECES == 2 && D > 128 ? 32 : 64;
-    static constexpr int ROWS = 32 * WAVES, THREADS = 64 * WAVES;
+    static constexpr int WAVES = 8, KT = 64, ROWS = kManyTile, THREADS = 64 * WAVES;
+    static_assert(ROWS == 32 * WAVES, "32 rows a wavefront");
     static constexpr int NB = D / 32, WORDS = D / 8, ROUNDS = D > 128 ? 2 : 1;
     static constexpr int KEY_ROW = D == 96 ? 128 : D;              // elements of a key's row in LDS
     static constexpr int KEYS = KT * KEY_ROW * 2, VALUES = D * KT * 2;  // bytes of one piece
@@ -54,7 +52,7 @@ __device__ __forceinline__ int key_piece(int entry, int w) {
 template <int PIECES, int D>
 __device__ __forceinline__ int value_piece(int element, int c) {  // c: eight entries
     constexpr int KT = Shape<PIECES, D>::KT;
-    const int by = KT == 64 ? (element ^ (element >> 3)) & 7 : ((element >> 1) ^ (element >> 3)) & 3;
+    const int by = (element ^ (element >> 3)) & 7;
     return element * KT * 2 + ((c ^ by) * 16);
 }
 
@@ -72,7 +70,7 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 template <int PIECES, int D>
-__global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(AttendArgs a, Splits sp, int type, int tiles) {
+__global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(AttendArgs a, Splits sp, int type) {
     using S = Shape<PIECES, D>;
     constexpr int NB = S::NB, KT = S::KT, WORDS = S::WORDS, ROUNDS = S::ROUNDS;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -80,20 +78,16 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     uint32_t(*largest)[2] = reinterpret_cast<uint32_t(*)[2]>(flags);    // [stage][keys, values]: the bits of scales beyond the bound
     uint32_t(*unfit)[2] = reinterpret_cast<uint32_t(*)[2]>(flags + 4);  // [step % 3]: entries that make NaN, a bit each
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, hf = lane >> 5;
-    const int head = blockIdx.x % a.c.heads, x0 = blockIdx.x / a.c.heads, split = x0 % sp.many;
-    const int x = tiles - 1 - x0 / sp.many;  // later rows see more entries: first
-    // sequence b's tiles start at slot floor(starts[b] * group / ROWS) + b
-    auto slot = [&](int i) {
-        const int t = a.c.starts[i];
-        return (int64_t)(t < 0 ? 0 : (t > a.c.T ? a.c.T : t)) * a.group / S::ROWS + i;
-    };
-    const int b = __builtin_amdgcn_readfirstlane(kv_last_not_above(a.c.B, x, slot));
-    if (b < 0) return;
-    const KvRows rows = kv_rows(a.c, b);
+    const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads;
+    Tiles<S::ROWS> tiles;
+    tiles.open(a, sp);
+    const int splits = tiles.splits, place = tiles.live - 1 - x / splits, split = x % splits;  // later rows see more: first
+    int b, tile;
+    KvRows rows;
+    if (place < 0 || !tiles.place(a, place, b, tile, rows)) return;
     const int total = rows.count * a.group;
-    const int64_t r0_ = (x - slot(b)) * S::ROWS;
-    if (total <= sp.few_room || r0_ >= total) return;
-    const int r0 = __builtin_amdgcn_readfirstlane((int)r0_), r1 = r0 + S::ROWS - 1 < total ? r0 + S::ROWS - 1 : total - 1;
+    if (total <= sp.few_room || tile * S::ROWS >= total) return;
+    const int r0 = tile * S::ROWS, r1 = r0 + S::ROWS - 1 < total ? r0 + S::ROWS - 1 : total - 1;
 
     // ---- this lane's row
     const int wr0 = r0 + 32 * wave, wr1 = wr0 + 31 < total ? wr0 + 31 : total - 1;  // the wavefront's
@@ -110,7 +104,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     const int64_t q_at = (int64_t)(rows.first + token) * a.ld_q + (int64_t)q_head * D;
     // ---- this split's steps
     const int s0 = (first < 0 ? 0 : first) / KT, s1 = last > 0 ? (last + KT - 1) / KT : 0, all = s1 > s0 ? s1 - s0 : 0;
-    const int from = s0 + (int)((int64_t)all * split / sp.many), to = s0 + (int)((int64_t)all * (split + 1) / sp.many);
+    const int from = s0 + (int)((int64_t)all * split / splits), to = s0 + (int)((int64_t)all * (split + 1) / splits);
     const int last16 = last > 0 ? (last - 1) & ~15 : 0;
 
     // ---- staging.  Group g < KT / 16: keys of its 16 entries, else values.  Lane of a key group: entry
@@ -443,7 +437,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     if (!live) return;
     const bool none = !(sum != 0.0f);  // NaN is a sum
     const float down = pow2i(-value_shift_);
-    if (sp.many == 1) {
+    if (splits == 1) {
         const float inv = none ? 0.0f : down / sum;
         const int64_t to_row = (int64_t)(rows.first + token) * a.ld_out + (int64_t)q_head * D;
 #pragma unroll
@@ -464,7 +458,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
             }
         if (hf == 0) attend_lse(a, sp.lse2, out_row, none ? -INFINITY : ref - kBias + log2_fast(sum));
     } else {
-        const int64_t row = (int64_t)split * a.c.T * (a.c.heads * a.group) + out_row;
+        const int64_t row = (((int64_t)split * tiles.live + place) * a.c.heads + head) * S::ROWS + (use - r0);
         if (hf == 0) sp.many_stats[row] = make_float2(ref == -INFINITY ? ref : ref - kBias, sum);
         if (none) return;
 #pragma unroll
@@ -478,32 +472,29 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
 }
 
 template <int PIECES, int D>
-hipError_t launch(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s) {
+hipError_t launch(int type, const AttendArgs &a, const Splits &sp, int64_t workgroups, hipStream_t s) {
     using S = Shape<PIECES, D>;
     static std::atomic<uint64_t> lds_set{0};
     const hipError_t e = ensure_lds_bytes((const void *)k_attend_rows<PIECES, D>, S::ALL, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attend_rows<PIECES, D>), dim3((unsigned)(tiles * sp.many * a.c.heads)), dim3(S::THREADS), S::ALL, s,
-                       a, sp, type, (int)tiles);
+    hipLaunchKernelGGL((k_attend_rows<PIECES, D>), dim3((unsigned)workgroups), dim3(S::THREADS), S::ALL, s, a, sp, type);
     return hipGetLastError();
 }
 template <int PIECES>
-hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s) {
+hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, int64_t workgroups, hipStream_t s) {
     switch (a.c.D) {
-        case 64: return launch<PIECES, 64>(type, a, sp, tiles, s);
-        case 96: return launch<PIECES, 96>(type, a, sp, tiles, s);
-        case 128: return launch<PIECES, 128>(type, a, sp, tiles, s);
-        case 192: return launch<PIECES, 192>(type, a, sp, tiles, s);
-        default: return launch<PIECES, 256>(type, a, sp, tiles, s);
+        case 64: return launch<PIECES, 64>(type, a, sp, workgroups, s);
+        case 96: return launch<PIECES, 96>(type, a, sp, workgroups, s);
+        case 128: return launch<PIECES, 128>(type, a, sp, workgroups, s);
     }
+    if constexpr (PIECES == 1) return launch<1, 192>(type, a, sp, workgroups, s);
+    return hipErrorInvalidValue;  // attend_rows_has
 }
 
 }  // namespace
 
-int64_t attend_rows_tile(int type, int64_t D) { return type == 0 && D > 128 ? 128 : 256; }
-
-hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t tiles, hipStream_t s) {
-    return type == 0 ? launch_for<2>(type, a, sp, tiles, s) : launch_for<1>(type, a, sp, tiles, s);
+hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t workgroups, hipStream_t s) {
+    return type == 0 ? launch_for<2>(type, a, sp, workgroups, s) : launch_for<1>(type, a, sp, workgroups, s);
 }
 
 }  // namespace qmm

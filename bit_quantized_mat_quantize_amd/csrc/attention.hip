@@ -27,7 +27,7 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256, kWaves = 4;
-constexpr int kRows = 16;  // query rows of a tile
+constexpr int kRows = kFewTile;  // query rows of a tile
 constexpr int kKeys = 32;  // entries of a wavefront's step
 
 // What a lane reads of 32 entries.  Lane (n, g), n = lane & 15, g = lane >> 4:
@@ -455,9 +455,13 @@ __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(Atten
     float(*buf)[kRows][PITCH] = reinterpret_cast<float(*)[kRows][PITCH]>(lds);
     __shared__ float2 stats[kWaves][kRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-    const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, split = x % sp.few;
-    const int per = (sp.few_room + kRows - 1) / kRows, b = x / sp.few / per, tile = x / sp.few - b * per;
-    const KvRows rows = kv_rows(a.c, b);
+    const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads;
+    Tiles<kRows> tiles;
+    tiles.open(a, sp);
+    const int splits = tiles.splits, place = x / splits, split = x - place * splits;
+    int b, tile;
+    KvRows rows;
+    if (place >= tiles.live || !tiles.place(a, place, b, tile, rows)) return;
     if (rows.count * a.group > sp.few_room) return;  // the other kernel's
     Tile<PIECES, D> q;
     q.type = type;
@@ -468,8 +472,8 @@ __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(Atten
     // this split's steps of 32 entries: whole rounds of the four wavefronts
     const int s0 = (q.first < 0 ? 0 : q.first) / kKeys, s1 = q.last > 0 ? (q.last + kKeys - 1) / kKeys : 0;
     const int rounds = s1 > s0 ? (s1 - s0 + kWaves - 1) / kWaves : 0;
-    const int from = s0 + (int)((int64_t)rounds * split / sp.few) * kWaves;
-    const int to0 = s0 + (int)((int64_t)rounds * (split + 1) / sp.few) * kWaves;
+    const int from = s0 + (int)((int64_t)rounds * split / splits) * kWaves;
+    const int to0 = s0 + (int)((int64_t)rounds * (split + 1) / splits) * kWaves;
     const int to = to0 < s1 ? to0 : s1, last16 = q.last > 0 ? (q.last - 1) & ~15 : 0;
     const int at0 = __builtin_amdgcn_readfirstlane(from + wave), steps = __builtin_amdgcn_readfirstlane(at0 < to ? (to - at0 + kWaves - 1) / kWaves : 0);
     if (steps > 0) {
@@ -564,7 +568,7 @@ __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(Atten
     }
     if (wave != 0 || !q.live) return;
     const bool none = !(sum != 0.0f);  // NaN is a sum
-    if (sp.few == 1) {
+    if (splits == 1) {
         const float inv = none ? 0.0f : 1.0f / sum, l2 = none ? -INFINITY : ref - kBias + log2_fast(sum);
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r)
@@ -580,7 +584,7 @@ __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(Atten
             }
         if (g == 0) attend_lse(a, sp.lse2, q.out_row(a), l2);
     } else {
-        const int64_t row = ((int64_t)split * a.c.B + b) * a.c.heads * sp.few_room + head * sp.few_room + q.row;
+        const int64_t row = (((int64_t)split * tiles.live + place) * a.c.heads + head) * sp.few_rows + n;
         if (g == 0) sp.few_stats[row] = make_float2(ref == -INFINITY ? ref : ref - kBias, sum);
         if (none) return;
 #pragma unroll
@@ -601,7 +605,22 @@ __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(Atten
 // The splits of a row joined.  A row's part of a workgroup is `lanes` threads (64, or 256
 // for rows of many splits): thread t of them has elements 8 (t % (D/8)) .. of the splits
 // t / (D/8), + groups, ..; the groups' sums are added in their order.  Rows below few_rows
-// are those of sequences with few, by (sequence, head, row), the others by output row.
+// are those of the one kernel's tiles, by (tile, head, row), the others the other's.
+template <int ROWS>
+__device__ __forceinline__ int join_row(const AttendArgs &a, const Splits &sp, int at, int64_t &out_row, int64_t &rows) {
+    constexpr bool many = ROWS == kManyTile;
+    Tiles<ROWS> tiles;
+    tiles.open(a, sp);
+    const int per = many ? ROWS : sp.few_rows, x = at / per, place = x / a.c.heads, head = x - place * a.c.heads;
+    rows = (int64_t)tiles.live * a.c.heads * per;
+    int b, tile;
+    KvRows k;
+    if (tiles.splits == 1 || place >= tiles.live || !tiles.place(a, place, b, tile, k)) return 0;
+    const int row = tile * ROWS + at - x * per;
+    if (row >= k.count * a.group) return 0;
+    out_row = attend_out_row(a, k, head, row);
+    return tiles.splits;
+}
 template <int LANES>
 __global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits sp, int type, int few_rows, int all_rows) {
     __shared__ float part[kThreads * 8];
@@ -609,31 +628,14 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits s
     const int D = a.c.D, each = D / 8, groups = LANES / each;
     const int tid = threadIdx.x % LANES, base = threadIdx.x - tid;
     const int at = blockIdx.x * (kThreads / LANES) + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
-    int64_t out_row = 0, row = 0, rows = 0;
-    const float *sums = nullptr;
-    const float2 *stats = nullptr;
+    const bool few = at < few_rows;
+    const int row = few ? at : at - few_rows;
+    const float *sums = few ? sp.few_sums : sp.many_sums;
+    const float2 *stats = few ? sp.few_stats : sp.many_stats;
+    int64_t out_row = 0, rows = 0;
     int n = 0;
-    if (at < few_rows) {
-        const int r = at % sp.few_room, bh = at / sp.few_room, b = bh / a.c.heads, head = bh - b * a.c.heads;
-        const KvRows k = kv_rows(a.c, b);
-        if (r < k.count * a.group && k.count * a.group <= sp.few_room) {
-            out_row = attend_out_row(a, k, head, r);
-            row = at;
-            rows = (int64_t)a.c.B * a.c.heads * sp.few_room;
-            sums = sp.few_sums;
-            stats = sp.few_stats;
-            n = sp.few;
-        }
-    } else if (at < all_rows) {
-        row = out_row = at - few_rows;
-        rows = (int64_t)a.c.T * a.c.heads * a.group;
-        const int b = kv_sequence(a.c, (int)(out_row / (a.c.heads * a.group)));
-        if (b >= 0 && kv_rows(a.c, b).count * a.group > sp.few_room) {
-            sums = sp.many_sums;
-            stats = sp.many_stats;
-            n = sp.many;
-        }
-    }
+    if (few) n = join_row<kFewTile>(a, sp, row, out_row, rows);
+    else if (at < all_rows) n = join_row<kManyTile>(a, sp, row, out_row, rows);
     // n <= LANES splits: a thread has one's reference and sum
     float2 st = make_float2(-INFINITY, 0.0f);
     if (tid < n) st = stats[tid * rows + row];
@@ -722,33 +724,54 @@ __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits s
 // ---- the shape of a call, from what the host knows
 struct Shape {
     Splits sp;
-    int64_t few_tiles, many_tiles;  // times heads and splits: workgroups; many_tiles 0: no sequence has so many rows
-    int64_t few_rows, many_rows;    // rows that have parts
-    int64_t bytes;                  // of the workspace
+    int64_t few_groups, many_groups;  // workgroups; many_groups 0: no sequence has so many rows
+    int64_t few_parts, many_parts;    // rows that have parts, times splits
+    int64_t few_join, many_join;      // rows that are joined
+    int64_t bytes;                    // of the workspace
 };
 constexpr int64_t quads(int64_t floats) { return (floats + 3) / 4 * 4; }  // whole 16 bytes of a workspace
 
+// The most rows of a sequence and head that k_attend takes.  It decodes the entries anew for every 16 rows, and
+// k_attend_rows for every 256, which pays once enough of these have rows.  us with up to 32 rows here and with all:
+//                             192 rows     512 rows     2048 rows     8192 rows
+//   bf16, D = 128, 2 x 4096    43    41     61    67     168   167     274   501
+//                 16 x 4000   162   133    323   323     647  1177    2073  3744
+//   fp32, D = 128, 2 x 4096    62    41     92    76     314   215     543   665
+//                 16 x 4000   299   170    616   427    1312  1601    4337  5247
+//   bf16, D = 192, 2 x 4096    65    54     94    97     287   295     459   933
+//         D = 256             115    57    174   103     576   313    1141   989  (its tiles pass the registers)
+constexpr int64_t kAnyRows = 0x7fffffff;
+int64_t few_room(int type, int64_t D) { return attend_rows_has(type, D) ? (type == 0 ? 1024 : 256) : kAnyRows; }
+
 Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D, bool ragged, bool mass) {
     Shape p{};
-    p.sp.few_room = (int)(ragged ? kFewRows : group);
-    p.few_tiles = B * ((p.sp.few_room + kRows - 1) / kRows);
-    // slots of the other kernel's tiles: each sequence's first one starts at the slot of its first row + its number
-    p.many_tiles = ragged && T * group > kFewRows ? T * group / attend_rows_tile(type, D) + B : 0;
-    // as many workgroups as the GPU holds at once, but no split below one step of each of their wavefronts
-    auto splits = [&](int64_t tiles, int64_t want, int64_t step) {
-        const int64_t rounds = (capacity + step - 1) / step;
-        int64_t n = want / (tiles * heads);
-        n = n > rounds ? rounds : n;
-        return (int)(n > 256 ? 256 : (n < 1 ? 1 : n));
+    const int64_t rows = T * group, room = ragged ? few_room(type, D) : kAnyRows;
+    p.sp.few_room = (int)room;
+    p.sp.few_rows = (int)(!ragged && group < kFewTile ? group : kFewTile);
+    auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+    // Tiles that can have rows.  As many workgroups as the GPU holds at once, but no split below one step of each of
+    // their wavefronts, and splits that a joining wavefront has a lane for, unless there are few rows.
+    auto share = [&](int64_t tiles, int64_t at_once, int64_t step, int per, int &most_tiles, int &want, int &most, int64_t &groups, int64_t &parts,
+                     int64_t &join) {
+        const int64_t fit = at_once / heads > 1 ? at_once / heads : 1, steps = (capacity + step - 1) / step;
+        most_tiles = (int)tiles;
+        want = (int)fit;
+        most = (int)least(least(steps, fit), tiles * heads <= at_once / 64 ? 256 : 64);
+        if (ragged && B > kCounted) most = 1;
+        groups = least(fit > tiles ? fit : tiles, tiles * most) * heads;
+        parts = most > 1 ? least(fit, tiles * most) * heads * per : 0;
+        join = most > 1 ? least(tiles, fit / 2) * heads * per : 0;
     };
     const int64_t each = D > 128 ? at_once<1, 256> : (type == 0 && D == 128 ? at_once<2, 128> : at_once<1, 128>);
-    p.sp.few = splits(p.few_tiles, 256 * each, kKeys * kWaves);
-    p.sp.many = p.many_tiles ? splits(p.many_tiles, 256, 512) : 1;
-    p.few_rows = p.sp.few > 1 ? B * heads * p.sp.few_room : 0;
-    p.many_rows = p.sp.many > 1 ? T * heads * group : 0;
-    const int64_t parts = p.sp.few * p.few_rows + p.sp.many * p.many_rows, all = quads(T * heads * group);
+    const int64_t apart = B * ((least(room, rows) + kFewTile - 1) / kFewTile), packed = rows / kFewTile + B;
+    share(!ragged ? B * ((group + kFewTile - 1) / kFewTile) : (B > kCounted ? packed : least(apart, packed)), 256 * each,
+          kKeys * kWaves, p.sp.few_rows, p.sp.few_tiles, p.sp.few_want, p.sp.few_most, p.few_groups, p.few_parts, p.few_join);
+    if (ragged && rows > room)
+        share(rows / kManyTile + (B > kCounted ? B : least(B, rows / room)), 256, 512, kManyTile, p.sp.many_tiles, p.sp.many_want, p.sp.many_most,
+              p.many_groups, p.many_parts, p.many_join);
+    const int64_t parts = p.few_parts + p.many_parts, all = quads(rows * heads);
     p.bytes = parts * D * 4 + quads(parts * 2) * 4 + (mass ? all * 4 : 0);
-    if (mass && p.many_tiles) {
+    if (mass && p.many_groups) {
         p.sp.query_piece = all * D;
         p.bytes += all * D * 2 * (type == 0 ? 2 : 1) + all * 4;
     }
@@ -759,17 +782,17 @@ Shape shape_of(int type, const AttendArgs &a) {
                        a.mass != nullptr);
     float *at = a.ws;
     p.sp.few_sums = at;
-    at += p.sp.few * p.few_rows * a.c.D;
+    at += p.few_parts * a.c.D;
     p.sp.many_sums = at;
-    at += p.sp.many * p.many_rows * a.c.D;
+    at += p.many_parts * a.c.D;
     p.sp.few_stats = reinterpret_cast<float2 *>(at);
-    p.sp.many_stats = p.sp.few_stats + p.sp.few * p.few_rows;
+    p.sp.many_stats = p.sp.few_stats + p.few_parts;
     if (a.mass == nullptr) return p;
-    at += quads((p.sp.few * p.few_rows + p.sp.many * p.many_rows) * 2);
+    at += quads((p.few_parts + p.many_parts) * 2);
     const int64_t all = quads((int64_t)a.c.T * a.c.heads * a.group);
     p.sp.lse2 = at;
     at += all;
-    if (p.many_tiles) {
+    if (p.many_groups) {
         p.sp.factors = at;
         p.sp.queries = reinterpret_cast<_Float16 *>(at + all);
     }
@@ -786,23 +809,22 @@ hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) 
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = ensure_lds_bytes((const void *)k_attend<PIECES, D>, bytes, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attend<PIECES, D>), dim3((unsigned)(p.few_tiles * p.sp.few * a.c.heads)), dim3(kThreads), bytes, s,
-                       a, p.sp, type);
+    hipLaunchKernelGGL((k_attend<PIECES, D>), dim3((unsigned)p.few_groups), dim3(kThreads), bytes, s, a, p.sp, type);
     e = hipGetLastError();
-    if (e == hipSuccess && p.many_tiles) e = launch_attend_rows(type, a, p.sp, p.many_tiles, s);
-    if (e == hipSuccess && p.few_rows + p.many_rows) {
-        const int64_t rows = p.few_rows + p.many_rows;
+    if (e == hipSuccess && p.many_groups) e = launch_attend_rows(type, a, p.sp, p.many_groups, s);
+    if (e == hipSuccess && p.few_join + p.many_join) {
+        const int64_t rows = p.few_join + p.many_join;
         // few rows of many splits: a workgroup each
-        if ((p.few_rows && p.sp.few > 64) || (p.many_rows && p.sp.many > 64) || rows <= 512)
-            hipLaunchKernelGGL(k_attend_join<kThreads>, dim3((unsigned)rows), dim3(kThreads), 0, s, a, p.sp, type,
-                               (int)p.few_rows, (int)rows);
+        if (p.sp.few_most > 64 || p.sp.many_most > 64 || rows <= 512)
+            hipLaunchKernelGGL(k_attend_join<kThreads>, dim3((unsigned)rows), dim3(kThreads), 0, s, a, p.sp, type, (int)p.few_join,
+                               (int)rows);
         else
             hipLaunchKernelGGL(k_attend_join<64>, dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s, a, p.sp, type,
-                               (int)p.few_rows, (int)rows);
+                               (int)p.few_join, (int)rows);
         e = hipGetLastError();
     }
     if (e != hipSuccess || a.mass == nullptr) return e;
-    if (p.many_tiles) e = launch_attend_mass_rows(type, a, p.sp, s);
+    if (p.many_groups) e = launch_attend_mass_rows(type, a, p.sp, s);
     if (e != hipSuccess) return e;
     const int64_t per = mass_tiles(a);
     hipLaunchKernelGGL((k_attend_mass<PIECES, D>), dim3((unsigned)(a.c.B * per * a.c.heads)), dim3(kThreads), 0, s, a, p.sp,
@@ -830,15 +852,15 @@ int64_t attend_workspace_bytes(int type, int64_t T, int64_t B, int64_t capacity,
 
 void attend_shape(int type, const AttendArgs &a, int *few, int *many) {
     const Shape p = shape_of(type, a);
-    *few = p.sp.few;
-    *many = p.many_tiles ? p.sp.many : 0;
+    *few = p.sp.few_most;
+    *many = p.many_groups ? p.sp.many_most : 0;
 }
 
 bool attend_grid_ok(int type, const AttendArgs &a) {
     constexpr int64_t most = (int64_t(1) << 24) - 1;  // workgroups of 256 threads; half as many of 512
     const Shape p = shape_of(type, a);
-    return p.few_tiles * p.sp.few * a.c.heads <= most && p.many_tiles * p.sp.many * a.c.heads <= most / 2 &&
-           p.few_rows + p.many_rows <= most && (a.mass == nullptr || a.c.B * mass_tiles(a) * a.c.heads <= most / 2);
+    return p.few_groups <= most && p.many_groups <= most / 2 && p.few_join + p.many_join <= most &&
+           (a.mass == nullptr || a.c.B * mass_tiles(a) * a.c.heads <= most / 2);
 }
 
 hipError_t launch_attend(int type, const AttendArgs &a, hipStream_t s) {
