@@ -225,6 +225,14 @@ __device__ __forceinline__ int64_t attend_at(const AttendArgs &a, int64_t out_ro
     const int64_t token = out_row / heads;
     return token * ld + (out_row - token * heads) * a.c.D;
 }
+// four elements of an output row
+__device__ __forceinline__ void attend_store4(int type, void *out, int64_t at, float a, float b, float c, float d) {
+    if (type == 0) *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = make_float4(a, b, c, d);
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
+            type == 1 ? make_uint2(f32_to_f16_bits(a) | f32_to_f16_bits(b) << 16, f32_to_f16_bits(c) | f32_to_f16_bits(d) << 16)
+                      : make_uint2(bf16_bits(a) | bf16_bits(b) << 16, bf16_bits(c) | bf16_bits(d) << 16);
+}
 // the place of a token's query head among the rows of its cache head
 __device__ __forceinline__ int64_t attend_group_row(const AttendArgs &a, int token, int head, int of_group) {
     return ((int64_t)head * a.c.T + token) * a.group + of_group;

@@ -447,14 +447,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = o[i][4 * c + r] * (r & 1 ? inv * 0.0625f : inv);
-                const int64_t at = to_row + 32 * i + 8 * c + 4 * hf;
-                if (type == 0) *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-                else {
-                    const uint2 u = type == 1 ? make_uint2(f32_to_f16_bits(v[0]) | f32_to_f16_bits(v[1]) << 16,
-                                                           f32_to_f16_bits(v[2]) | f32_to_f16_bits(v[3]) << 16)
-                                              : make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = u;
-                }
+                attend_store4(type, a.out, to_row + 32 * i + 8 * c + 4 * hf, v[0], v[1], v[2], v[3]);
             }
         if (hf == 0) attend_lse(a, sp.lse2, out_row, none ? -INFINITY : ref - kBias + log2_fast(sum));
     } else {

@@ -602,16 +602,18 @@ __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(Atten
     }
 }
 
-// The splits of a row joined.  A row's part of a workgroup is `lanes` threads (64, or 256
-// for rows of many splits): thread t of them has elements 8 (t % (D/8)) .. of the splits
-// t / (D/8), + groups, ..; the groups' sums are added in their order.  Rows below few_rows
-// are those of the one kernel's tiles, by (tile, head, row), the others the other's.
+// The splits of a row joined.  Rows of k_attend have LANES threads (64, or 256 for rows of
+// many splits): thread t of them has elements 8 (t % (D/8)) .. of the splits t / (D/8), +
+// groups, ..; the groups' sums are added in their order.  The workgroups from few_blocks on
+// have rows of k_attend_rows, which are many and of few splits: a thread has four elements
+// of a row and adds up all splits (14000 rows of 64 elements in 4 splits: 17.2 us with a
+// wavefront a row, 9.5 that way).
 template <int ROWS>
-__device__ __forceinline__ int join_row(const AttendArgs &a, const Splits &sp, int at, int64_t &out_row, int64_t &rows) {
+__device__ __forceinline__ int join_row(const AttendArgs &a, const Splits &sp, int first, int at, int64_t &out_row, int64_t &rows) {
     constexpr bool many = ROWS == kManyTile;
     Tiles<ROWS> tiles;
     tiles.open(a, sp);
-    const int per = many ? ROWS : sp.few_rows, x = at / per, place = x / a.c.heads, head = x - place * a.c.heads;
+    const int per = many ? ROWS : sp.few_rows, x = first / per, place = x / a.c.heads, head = x - place * a.c.heads;
     rows = (int64_t)tiles.live * a.c.heads * per;
     int b, tile;
     KvRows k;
@@ -621,51 +623,98 @@ __device__ __forceinline__ int join_row(const AttendArgs &a, const Splits &sp, i
     out_row = attend_out_row(a, k, head, row);
     return tiles.splits;
 }
+__device__ __forceinline__ void join_many(const AttendArgs &a, const Splits &sp, int type, int block) {
+    const int D = a.c.D, lanes = D <= 64 ? 16 : (D <= 128 ? 32 : 64);  // a row's
+    const int first = block * (kThreads / lanes), row = first + threadIdx.x / lanes, e = threadIdx.x % lanes;  // of one tile
+    int64_t out_row, rows;
+    const int n = join_row<kManyTile>(a, sp, first, row, out_row, rows);
+    if (n == 0 || 4 * e >= D) return;
+    float ref = -INFINITY, sum = 0.0f;
+    f4 v = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) ref = fmaxf(ref, sp.many_stats[s * rows + row].x);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+        const float2 st = sp.many_stats[s * rows + row];
+        const f4 u = *reinterpret_cast<const f4 *>(sp.many_sums + (s * rows + row) * D + 4 * e);
+        // a sum of 0: nothing was seen, and nothing written
+        const float f = st.y == 0.0f ? 0.0f : (st.x == -INFINITY ? 1.0f : exp2_fast(st.x - ref));
+        if (f != 0.0f) {
+            sum = fmaf(st.y, f, sum);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = fmaf(u[j], f, v[j]);
+        }
+    }
+    const bool none = !(sum != 0.0f);
+    const float inv = none ? 0.0f : 1.0f / sum;
+    attend_store4(type, a.out, attend_at(a, out_row, a.ld_out) + 4 * e, v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    if (e == 0) attend_lse(a, sp.lse2, out_row, none ? -INFINITY : ref + log2_fast(sum));
+}
 template <int LANES>
-__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits sp, int type, int few_rows, int all_rows) {
+__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits sp, int type, int few_rows, int few_blocks) {
+    if ((int)blockIdx.x >= few_blocks) {
+        join_many(a, sp, type, blockIdx.x - few_blocks);
+        return;
+    }
     __shared__ float part[kThreads * 8];
     __shared__ float weight[kThreads], by[kThreads];
     const int D = a.c.D, each = D / 8, groups = LANES / each;
     const int tid = threadIdx.x % LANES, base = threadIdx.x - tid;
-    const int at = blockIdx.x * (kThreads / LANES) + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
-    const bool few = at < few_rows;
-    const int row = few ? at : at - few_rows;
-    const float *sums = few ? sp.few_sums : sp.many_sums;
-    const float2 *stats = few ? sp.few_stats : sp.many_stats;
-    int64_t out_row = 0, rows = 0;
-    int n = 0;
-    if (few) n = join_row<kFewTile>(a, sp, row, out_row, rows);
-    else if (at < all_rows) n = join_row<kManyTile>(a, sp, row, out_row, rows);
+    const int row = blockIdx.x * (kThreads / LANES) + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
+    const float *sums = sp.few_sums;
+    const float2 *stats = sp.few_stats;
+    int64_t out_row, rows;
+    const int n = row < few_rows ? join_row<kFewTile>(a, sp, row, row, out_row, rows) : 0;
+    // a row's threads are one wavefront or the workgroup
+    auto sync = [] {
+        if (LANES > 64) __syncthreads();
+        else {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    };
+    if (n == 0) return;
     // n <= LANES splits: a thread has one's reference and sum
     float2 st = make_float2(-INFINITY, 0.0f);
     if (tid < n) st = stats[tid * rows + row];
+    const int s0 = tid / each, e = tid - s0 * each;
+    constexpr int FIRST = 4;  // of the thread's splits, on their way meanwhile (what was not written is not used)
+    float first[FIRST][8];
+#pragma unroll
+    for (int i = 0; i < FIRST; ++i)
+        if (s0 < groups && s0 + i * groups < n) kv_load8<0>(sums, ((s0 + i * groups) * rows + row) * D + 8 * e, first[i]);
     float ref = st.x, sum = 0.0f, v[8] = {};
     for (int o = 1; o < 64; o <<= 1) ref = fmaxf(ref, __shfl_xor(ref, o, 64));
     if (LANES > 64) {
         if ((tid & 63) == 0) weight[threadIdx.x] = ref;
-        __syncthreads();
+        sync();
         for (int w = 0; w < LANES / 64; ++w) ref = fmaxf(ref, weight[base + 64 * w]);
-        __syncthreads();
+        sync();
     }
     const bool some = st.y != 0.0f;  // else nothing was seen, and nothing written
     by[threadIdx.x] = !some ? 0.0f : (st.x == -INFINITY ? 1.0f : exp2_fast(st.x - ref));
     weight[threadIdx.x] = some ? st.y * by[threadIdx.x] : 0.0f;
-    __syncthreads();
-    const int s0 = tid / each, e = tid - s0 * each;
+    sync();
+    auto add = [&](int s, const float (&u)[8]) {
+        const float f = by[base + s];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = f != 0.0f ? fmaf(u[j], f, v[j]) : v[j];
+    };
     if (s0 < groups) {
+#pragma unroll
+        for (int i = 0; i < FIRST; ++i)
+            if (s0 + i * groups < n) add(s0 + i * groups, first[i]);
 #pragma unroll 4
-        for (int s = s0; s < n; s += groups) {
+        for (int s = s0 + FIRST * groups; s < n; s += groups) {
             float u[8];
             kv_load8<0>(sums, (s * rows + row) * D + 8 * e, u);
-            const float f = by[base + s];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = f != 0.0f ? fmaf(u[j], f, v[j]) : v[j];
+            add(s, u);
         }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[j * kThreads + threadIdx.x] = v[j];
-    __syncthreads();
-    if (n == 0 || tid >= each) return;
+    sync();
+    if (tid >= each) return;
     for (int s = 1; s < groups && s < n; ++s)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += part[j * kThreads + base + s * each + tid];
@@ -750,25 +799,26 @@ Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, 
     p.sp.few_rows = (int)(!ragged && group < kFewTile ? group : kFewTile);
     auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
     // Tiles that can have rows.  As many workgroups as the GPU holds at once, but no split below one step of each of
-    // their wavefronts, and splits that a joining wavefront has a lane for, unless there are few rows.
-    auto share = [&](int64_t tiles, int64_t at_once, int64_t step, int per, int &most_tiles, int &want, int &most, int64_t &groups, int64_t &parts,
-                     int64_t &join) {
+    // their wavefronts, and splits that a joining wavefront has a lane for, unless there are few rows.  sure: tiles
+    // that have rows for certain.
+    auto share = [&](int64_t tiles, int64_t sure, int64_t at_once, int64_t step, int per, int &most_tiles, int &want, int &most,
+                     int64_t &groups, int64_t &parts, int64_t &join) {
         const int64_t fit = at_once / heads > 1 ? at_once / heads : 1, steps = (capacity + step - 1) / step;
         most_tiles = (int)tiles;
         want = (int)fit;
         most = (int)least(least(steps, fit), tiles * heads <= at_once / 64 ? 256 : 64);
-        if (ragged && B > kCounted) most = 1;
+        if ((ragged && B > kCounted) || fit < 2 * sure) most = 1;
         groups = least(fit > tiles ? fit : tiles, tiles * most) * heads;
         parts = most > 1 ? least(fit, tiles * most) * heads * per : 0;
         join = most > 1 ? least(tiles, fit / 2) * heads * per : 0;
     };
     const int64_t each = D > 128 ? at_once<1, 256> : (type == 0 && D == 128 ? at_once<2, 128> : at_once<1, 128>);
     const int64_t apart = B * ((least(room, rows) + kFewTile - 1) / kFewTile), packed = rows / kFewTile + B;
-    share(!ragged ? B * ((group + kFewTile - 1) / kFewTile) : (B > kCounted ? packed : least(apart, packed)), 256 * each,
+    share(!ragged ? B * ((group + kFewTile - 1) / kFewTile) : (B > kCounted ? packed : least(apart, packed)), 0, 256 * each,
           kKeys * kWaves, p.sp.few_rows, p.sp.few_tiles, p.sp.few_want, p.sp.few_most, p.few_groups, p.few_parts, p.few_join);
     if (ragged && rows > room)
-        share(rows / kManyTile + (B > kCounted ? B : least(B, rows / room)), 256, 512, kManyTile, p.sp.many_tiles, p.sp.many_want, p.sp.many_most,
-              p.many_groups, p.many_parts, p.many_join);
+        share(rows / kManyTile + (B > kCounted ? B : least(B, rows / room)), rows > B * room ? (rows - B * room) / kManyTile : 0,
+              256, 512, kManyTile, p.sp.many_tiles, p.sp.many_want, p.sp.many_most, p.many_groups, p.many_parts, p.many_join);
     const int64_t parts = p.few_parts + p.many_parts, all = quads(rows * heads);
     p.bytes = parts * D * 4 + quads(parts * 2) * 4 + (mass ? all * 4 : 0);
     if (mass && p.many_groups) {
@@ -813,14 +863,14 @@ hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) 
     e = hipGetLastError();
     if (e == hipSuccess && p.many_groups) e = launch_attend_rows(type, a, p.sp, p.many_groups, s);
     if (e == hipSuccess && p.few_join + p.many_join) {
-        const int64_t rows = p.few_join + p.many_join;
+        const int64_t lanes = D <= 64 ? 16 : (D <= 128 ? 32 : 64), many = p.many_join / (kThreads / lanes);
         // few rows of many splits: a workgroup each
-        if (p.sp.few_most > 64 || p.sp.many_most > 64 || rows <= 512)
-            hipLaunchKernelGGL(k_attend_join<kThreads>, dim3((unsigned)rows), dim3(kThreads), 0, s, a, p.sp, type, (int)p.few_join,
-                               (int)rows);
+        if (p.sp.few_most > 64 || p.few_join <= 512)
+            hipLaunchKernelGGL(k_attend_join<kThreads>, dim3((unsigned)(p.few_join + many)), dim3(kThreads), 0, s, a, p.sp, type,
+                               (int)p.few_join, (int)p.few_join);
         else
-            hipLaunchKernelGGL(k_attend_join<64>, dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s, a, p.sp, type,
-                               (int)p.few_join, (int)rows);
+            hipLaunchKernelGGL(k_attend_join<64>, dim3((unsigned)((p.few_join + 3) / 4 + many)), dim3(kThreads), 0, s, a, p.sp,
+                               type, (int)p.few_join, (int)((p.few_join + 3) / 4));
         e = hipGetLastError();
     }
     if (e != hipSuccess || a.mass == nullptr) return e;

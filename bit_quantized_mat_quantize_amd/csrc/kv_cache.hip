@@ -31,9 +31,7 @@ __device__ __forceinline__ void block_top(float &a, float &x, int &bad) {
 }
 
 // Rows per workgroup: their reads are on their way together, and the words of one group
-// of four values, which share cache lines, come together.  4099 rows of 8 heads of 128
-// (bf16) were written in MEASURED_W us with 8 against MEASURED_W1 with 1, and 61 rows
-// (fp32) in MEASURED_B with 1.
+// of four values, which share cache lines, come together.
 template <int TYPE, int ROWS>
 __global__ __launch_bounds__(kThreads) void k_cache_write(KvCache c, const void *__restrict__ k, int64_t ld_k,
                                                           const void *__restrict__ v, int64_t ld_v) {
@@ -113,8 +111,9 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(KvCache c, void *__rest
     }
 }
 
-// Eight rows a workgroup once that leaves four workgroups for each CU; below, four were no faster than one (2561 rows of
-// 8 heads of 128: 9.4 us both to write and to read).
+// Eight rows a workgroup once that leaves four workgroups for each CU.  8 heads of 128 in bf16, us with eight against one:
+// 2561 rows written in 10.2 and 8.8 (read in 10.0 and 10.5), 8192 in 16.7 and 19.9 (10.5 and 14.5), 60013 in 102 and 112, at
+// 3.1 TB/s (56 and 79).
 bool eight_rows(const KvCache &c, unsigned y) { return (int64_t)c.T * y >= 8 * 4 * 256; }
 constexpr int64_t kLongBytes = 32 << 20;  // the L2 caches: 4 MiB for each of 8 XCDs
 

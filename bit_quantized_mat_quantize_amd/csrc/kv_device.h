@@ -115,12 +115,6 @@ __device__ __forceinline__ void kv_places(const KvCache &c, int r0, int2 (&place
     __syncthreads();
 }
 
-// ---- codes.  Eight codes of a word as fp16 integers -8 .. 7, in the order 0 4 1 5 2 6 3 7:
-// 0x6400 | u is 1024 + u in fp16.
-__device__ __forceinline__ h2 kv_pair(uint32_t x) {
-    return as_h2((x & 0x000f000fu) | 0x64006400u) - h2{(_Float16)1032.0f, (_Float16)1032.0f};
-}
-
 // ---- element types: eight consecutive elements at a 16-byte aligned address
 template <int TYPE>  // qmm_float_type
 __device__ __forceinline__ void kv_load8(const void *base, int64_t at, float *v) {
