@@ -107,6 +107,11 @@ __device__ __forceinline__ f16v mfma32(h8 a, h8 b, f16v c) { return __builtin_am
 // every sequence has one token) go to attention.hip's kernel in tiles of kFewTile, more to
 // attend_rows.hip's in tiles of kManyTile.
 constexpr int kFewTile = 16, kManyTile = 256;
+// The most rows whose entries' weights k_attend_mass forms, which converts the queries anew for every 32 entries;
+// attend_mass.hip's kernel has the more, from queries that the attention left.  What the weights add to a call, us, here and
+// there, 16 sequences of 4000 entries, 8 heads of 128: bf16 of 32 rows 48 and 54, 64: 72 and 57, 256: 199 and 92;
+// fp32 64: 85 and 83, 512: 491 and 245.
+constexpr int kMassRoom = 32;
 
 struct Splits {
     int few_room;
@@ -120,7 +125,7 @@ struct Splits {
     float2 *many_stats;
     // for the weights of the entries, by (cache head, token, head of the group): attend_group_row
     float *lse2;              // [heads * T * group] in log2 units, or null
-    // and what attend_rows.hip leaves for attend_mass.hip, or null:
+    // and what sequences of more than kMassRoom rows leave for attend_mass.hip, or null:
     _Float16 *queries;        // [pieces][heads * T * group][D], as query_pieces has them
     int64_t query_piece;      // elements of a piece
     float *factors;           // [heads * T * group], of the rows' products

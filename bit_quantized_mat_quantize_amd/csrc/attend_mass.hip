@@ -1,6 +1,6 @@
 // attend_mass.hip -- the weight that each entry of the cache got, for sequences of many
 // query rows (gfx950): mass[j] += sum over rows and heads of the group of 2^(x - lse2),
-// with the rows' lse2 from attend_rows.hip.
+// with the rows' lse2 from attention.hip and attend_rows.hip.
 //
 // A workgroup of four wavefronts owns 64 entries of a sequence and cache head and goes over
 // all rows that see any of them, 64 at a time: two wavefronts take 32 entries each against
@@ -9,7 +9,7 @@
 // the size below; one workgroup of eight wavefronts took 121 with 128 entries and 126 with
 // 128 rows.  The entries stay in registers, decoded to fp16 (two pieces for fp32 queries, as
 // in attend_rows.hip).  The rows' queries come by direct loads into LDS, a step or two
-// ahead, as attend_rows.hip left them, fp16 and scaled: converting them anew in every
+// ahead, as the attention left them, fp16 and scaled: converting them anew in every
 // workgroup took 180 us where loading them took 128 (three prompts of 700 rows, 28 heads of
 // 128, fp32), and 121 with the rows' factors and lse loaded that way too.  Every entry's sum
 // is formed in a fixed order: per lane over the rows, over the lanes, over the two
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_mass_rows(AttendArgs a, 
     const int e0 = tile * S::ENTRIES, k0 = e0 + 32 * (wave % OWNERS), stream = wave / OWNERS;
     const KvRows rows = kv_rows(a.c, b);
     const int total = rows.count * a.group;
-    if (total <= sp.few_room || e0 >= rows.len) return;
+    if (total <= kMassRoom || e0 >= rows.len) return;
     // tokens that see any of the 128 entries
     const int before = rows.len - rows.count;
     int i0 = a.causal ? e0 - before : 0, i1 = a.window > 0 ? e0 + S::ENTRIES - 1 + a.window - before : rows.count;
@@ -249,9 +249,9 @@ hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, hipStream
         case 64: return launch<PIECES, 64>(type, a, sp, s);
         case 96: return launch<PIECES, 96>(type, a, sp, s);
         case 128: return launch<PIECES, 128>(type, a, sp, s);
+        case 192: return launch<PIECES, 192>(type, a, sp, s);
+        default: return launch<PIECES, 256>(type, a, sp, s);
     }
-    if constexpr (PIECES == 1) return launch<1, 192>(type, a, sp, s);
-    return hipErrorInvalidValue;  // attend_rows_has
 }
 
 }  // namespace

@@ -467,6 +467,16 @@ __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(Atten
     q.type = type;
     if (!q.open(a, b, rows, tile, head)) return;
     q.queries(a);
+    if (sp.queries != nullptr && split == 0 && wave == 0 && q.live && rows.count * a.group > kMassRoom) {
+        const int64_t row = attend_group_row(a, rows.first, head, q.row);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            _Float16 *p = sp.queries + row * D + 32 * i + 8 * g;
+            *reinterpret_cast<h8 *>(p) = q.q.hi[i];
+            if constexpr (PIECES == 2) *reinterpret_cast<h8 *>(p + sp.query_piece) = q.q.lo[i];
+        }
+        if (g == 0) sp.factors[row] = q.factor;
+    }
     Running<D> run;
     run.clear();
     // this split's steps of 32 entries: whole rounds of the four wavefronts
@@ -736,7 +746,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits s
     const int head = blockIdx.x % a.c.heads, x = blockIdx.x / a.c.heads, b = x / tiles;
     const int k0 = ((x - b * tiles) * kWaves + wave) * kKeys;
     const KvRows rows = kv_rows(a.c, b);
-    if (k0 >= rows.len || rows.count == 0 || rows.count * a.group > sp.few_room) return;
+    if (k0 >= rows.len || rows.count == 0 || rows.count * a.group > kMassRoom) return;
     Step<D> t;
     read_step<D>(a.c, b, head, k0, (rows.len - 1) & ~15, t);
     Decode decode;
@@ -776,6 +786,7 @@ struct Shape {
     int64_t few_groups, many_groups;  // workgroups; many_groups 0: no sequence has so many rows
     int64_t few_parts, many_parts;    // rows that have parts, times splits
     int64_t few_join, many_join;      // rows that are joined
+    bool mass_rows;                   // whether a sequence can have more than kMassRoom
     int64_t bytes;                    // of the workspace
 };
 constexpr int64_t quads(int64_t floats) { return (floats + 3) / 4 * 4; }  // whole 16 bytes of a workspace
@@ -821,7 +832,8 @@ Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, 
               256, 512, kManyTile, p.sp.many_tiles, p.sp.many_want, p.sp.many_most, p.many_groups, p.many_parts, p.many_join);
     const int64_t parts = p.few_parts + p.many_parts, all = quads(rows * heads);
     p.bytes = parts * D * 4 + quads(parts * 2) * 4 + (mass ? all * 4 : 0);
-    if (mass && p.many_groups) {
+    p.mass_rows = mass && (ragged ? rows : group) > kMassRoom;
+    if (p.mass_rows) {
         p.sp.query_piece = all * D;
         p.bytes += all * D * 2 * (type == 0 ? 2 : 1) + all * 4;
     }
@@ -842,7 +854,7 @@ Shape shape_of(int type, const AttendArgs &a) {
     const int64_t all = quads((int64_t)a.c.T * a.c.heads * a.group);
     p.sp.lse2 = at;
     at += all;
-    if (p.many_groups) {
+    if (p.mass_rows) {
         p.sp.factors = at;
         p.sp.queries = reinterpret_cast<_Float16 *>(at + all);
     }
@@ -874,7 +886,7 @@ hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) 
         e = hipGetLastError();
     }
     if (e != hipSuccess || a.mass == nullptr) return e;
-    if (p.many_groups) e = launch_attend_mass_rows(type, a, p.sp, s);
+    if (p.mass_rows) e = launch_attend_mass_rows(type, a, p.sp, s);
     if (e != hipSuccess) return e;
     const int64_t per = mass_tiles(a);
     hipLaunchKernelGGL((k_attend_mass<PIECES, D>), dim3((unsigned)(a.c.B * per * a.c.heads)), dim3(kThreads), 0, s, a, p.sp,
