@@ -1,10 +1,12 @@
 // attention.hip -- attention over the paged 4-bit cache, few rows per sequence
-// (gfx950): one token, or a few, of each sequence against all its entries.
+// (gfx950): one token, or some, of each sequence against all its entries; the joint of
+// splits; and the weights that entries get from few rows.
 //
 // A workgroup takes one tile of 16 query rows (row = token * group + head of the
 // group, so that one read of an entry serves the whole group), one cache head and
-// one split of the entries; its four wavefronts take 32 entries each in turn, straight
-// from memory into registers, and are joined at the end.  Per 32 entries:
+// one split of the entries; its four wavefronts take 32 entries each in turn, by direct
+// loads into rings of LDS of their own, a step ahead, and are joined at the end.  Per 32
+// entries:
 //
 //   S^T = K Q^T     16 entries x 16 rows per matrix instruction, one per block of 32
 //                   elements: the codes are exact in fp16, the block's scale multiplies
@@ -21,6 +23,12 @@
 // An entry whose page is not in the pool, or that has a NaN scale, makes the rows that
 // see it NaN: its score becomes NaN and its values 0, so that rows that do not see it
 // are not touched.
+//
+// Bounds: single tokens of long contexts, the issue of vector instructions beside the
+// bytes (345 of them for 32 entries of 128 elements, 60% of the issue slots; 32
+// sequences of up to 8192 entries, 8 cache heads of 128, fp32: 69 us, 3.7 TB/s of the
+// cache; 2 of 131072 in bf16: 62 us, 4.5 TB/s); many rows, the same once per 16 of them;
+// one short sequence, a chain of latencies (8 us for 1000 entries).
 #include "attend_device.h"
 
 namespace qmm {

@@ -10,8 +10,10 @@
 //
 // A workgroup forms one token's angles (one pair per thread, in LDS) and turns them
 // into that token's heads, so the 64-bit work is paid once per token and not per
-// head.  Everything else is 16-byte loads and stores: bound by HBM for prompts, by
-// the launch for single tokens, whose heads several workgroups share.
+// head.  Everything else is 16-byte loads and stores: bound by HBM for prompts (4099
+// tokens of 40 heads of 128 in bf16: 14.3 us, 5.9 TB/s, some of it from the caches), by
+// the launch for single tokens, whose heads several workgroups share (40 heads of 128
+// in fp32: 2.6 us).
 #include "kv_device.h"
 
 namespace qmm {
@@ -108,7 +110,8 @@ hipError_t launch(const RopeArgs &a, hipStream_t s) {
     const int64_t all = a.ld_x | a.ld_out | a.head_x | a.head_out | a.D | (INTER ? a.rot : a.rot / 2);
     const bool wide = all % V == 0;
     const int64_t units = (int64_t)a.H * (a.D / (wide ? V : 1));
-    // a token's heads on several workgroups while there are few tokens
+    // a token's heads on several workgroups while there are few tokens (in a graph: one of 40 heads of 128 2.97 us, on one
+    // workgroup 3.26; 64 3.18 and 3.50; 256 3.73 and 3.83)
     int64_t share = (units + kThreads - 1) / kThreads;
     const int64_t want = (2 * 256 + a.T - 1) / a.T;
     if (share > want) share = want;
