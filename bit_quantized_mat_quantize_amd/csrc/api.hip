@@ -1344,7 +1344,7 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
     if (log_enabled()) {
         int few, many;
         qmm::attend_shape((int)t, a, &few, &many);
-        fprintf(stderr, "qmm: cache_attention %s rows=%lld seqs=%lld heads=%lld/%lld dim=%lld page=%lld -> %d split(s), %d of long runs of rows%s\n",
+        fprintf(stderr, "qmm: cache_attention %s rows=%lld seqs=%lld heads=%lld/%lld dim=%lld page=%lld -> up to %d split(s), %d of long runs of rows%s\n",
                 float_name(t), (long long)c->rows, (long long)c->seqs, (long long)q_heads, (long long)c->heads,
                 (long long)c->dim, (long long)c->page, few, many, mass != nullptr ? ", mass" : "");
     }
@@ -1363,6 +1363,8 @@ qmm_status qmm_cache_evict(const qmm_cache *c, const float *mass, int64_t ld_mas
         return fail(QMM_EINVAL, "to has room for %lld pages; at least %lld entries are needed", (long long)to_width,
                     (long long)budget);
     if (c->seqs == 0) return QMM_OK;
+    if (to == c->table && to_width != c->width)
+        return fail(QMM_EINVAL, "to is the table, of %lld pages, and not of %lld", (long long)c->width, (long long)to_width);
     if (c->seqs * c->heads >= int64_t(1) << 21)
         return fail(QMM_EUNSUPPORTED, "seqs * heads = %lld; below 2^21", (long long)(c->seqs * c->heads));
     QMM_TRY(check_ld("ld_mass", ld_mass, c->width * c->page));

@@ -568,7 +568,8 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
  *   mass_out fp32 [seqs][heads][ld_out], ld_out >= budget: their mass; 0 from n on
  *   lens_out int32 [seqs]: n
  * and entry i of the pages of `to` (int32 [seqs][to_width], to_width * page >= budget) becomes entry ids[i].  `to` may
- * be c->table itself: the entries move within their pages (which no two sequences may share then).  Else its pages
+ * be c->table itself (then to_width = width): the entries move within their pages (which no two sequences may share
+ * then).  Else its pages
  * must be none that c->table names.  An entry whose page is not in [0, pages) becomes NaN; one that would move
  * to such a page is not written.  Keys keep the rotation of the positions they were written with.  c->starts and
  * c->rows are not used. */

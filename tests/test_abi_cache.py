@@ -205,6 +205,19 @@ def test_cache_evict_refusals(lib):  # noqa: F811
     assert call(seqs=0, data=None, mass=None) == OK
 
 
+def test_rows_times_heads_and_tables_of_another_width(lib):  # noqa: F811
+    """More query rows than 32-bit row numbers count are refused; so is the table itself read with another width."""
+    size = lib.qmm_cache_attention_workspace_bytes
+    assert size(1, 2**20, 1024, 1024, 64, 9, 4, 32, 1, 1) > 0
+    assert size(1, 2**20 + 1, 1024, 1024, 64, 9, 4, 32, 1, 1) == 0
+    c = _cache(heads=1024, rows=2**20 + 1, dim=64)
+    assert lib.qmm_cache_attention(c, 1, _far(4), 1 << 62, 65536, 1024, _far(5), 1 << 62, 65536, 0.1, 1, 0, None, None, 0,
+                                   _far(8), 1 << 62, None) == EUNSUP and "2^30" in _last(lib)
+    for width in (2, 5):
+        assert lib.qmm_cache_evict(_cache(), _far(4), 128, 50, 10, CACHE["table"], width, _far(6), _far(7), 64, _far(8),
+                                   None) == EINVAL and "to is the table" in _last(lib)
+
+
 def test_binding_refusals():
     """Shapes and types are checked before the library is called; CPU tensors are refused."""
     i32 = torch.int32
