@@ -21,9 +21,9 @@
 // tile is decoded again; after the first tile that is seldom).
 //
 // Bounds: matrix and vector instructions, which overlap in part only (of the cycles, 2 prompts
-// of 2048 rows on 8192 entries, 32 heads of 128 in bf16: 32% and 46%; 525 to 549 us a call
+// of 2048 rows on 8192 entries, 32 heads of 128 in bf16: 32% and 42%; 525 to 549 us a call
 // from card to card, 800 TFLOP/s; fp32, 3 of 700 rows on 2100 entries, 28 heads: 29% and
-// 24%, 200 us, waiting for one another's steps).  256 rows are what the registers of
+// 22%, 200 us, waiting for one another's steps).  256 rows are what the registers of
 // two wavefronts a SIMD hold; of half as many rows the decode would weigh twice as much.
 // The two halves of a workgroup taking turns, one multiplying while the other forms
 // weights, took 730 us.
