@@ -81,14 +81,21 @@ __global__ __launch_bounds__(kThreads) void k_cache_write(KvCache c, const void 
     }
 }
 
+// A thread stores 16 bytes, so that a wavefront stores whole lines: eight numbers of 16 bits, or four of a word's in fp32
+// (two stores each of eight: 8192 rows of 8 heads of 128 29 us against 14).
+template <int TYPE>
+constexpr int kRead = TYPE == 0 ? 4 : 8;
+
 template <int TYPE, int ROWS, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_cache_read(KvCache c, void *__restrict__ k, void *__restrict__ v) {
+    constexpr int E = kRead<TYPE>;
     __shared__ int2 place[ROWS];
-    const int words = c.heads * (c.D / 8);
+    const int units = c.heads * (c.D / E);
     const int u = blockIdx.y * kThreads + threadIdx.x, r0 = blockIdx.x * ROWS;
     kv_places<ROWS>(c, r0, place);
-    if (u >= 2 * words) return;
-    const int part = u >= words, e = part ? u - words : u, head = e / (c.D / 8), w = e - head * (c.D / 8);
+    if (u >= 2 * units) return;
+    const int part = u >= units, e = part ? u - units : u, head = e / (c.D / E), at_head = e - head * (c.D / E);
+    const int w = at_head * E / 8, first = at_head * E % 8;  // word; of its eight numbers
     uint32_t q[ROWS], d[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -104,19 +111,21 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(KvCache c, void *__rest
     for (int i = 0; i < ROWS; ++i) {
         if (place[i].x == -2) continue;
         const float s = f16_bits_to_f32(d[i]);
-        float x[8];
+        float x[E];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = s * (float)((int)((q[i] >> (4 * j)) & 15u) - 8);
-        kv_store8<TYPE, PAST>(part ? v : k, ((int64_t)(r0 + i) * words + e) * 8, x);
+        for (int j = 0; j < E; ++j) x[j] = s * (float)((int)((q[i] >> (4 * (first + j))) & 15u) - 8);
+        kv_store16<TYPE, PAST>(part ? v : k, ((int64_t)(r0 + i) * units + e) * E, x);
     }
 }
 
-// Eight rows a workgroup once that leaves four workgroups for each CU.  8 heads of 128 in bf16, us with eight against one:
-// 2561 rows written in 10.2 and 8.8 (read in 10.0 and 10.5), 8192 in 16.7 and 19.9 (10.5 and 14.5), 60013 in 102 and 112, at
-// 3.1 TB/s (56 and 79).
-bool eight_rows(const KvCache &c, unsigned y) { return (int64_t)c.T * y >= 8 * 4 * 256; }
-// The L2 caches, 4 MiB for each of 8 XCDs: longer outputs go past them (20011 rows of 8 heads of 128 in bf16 22.6 us, into
-// the caches 23.4; 60013 rows 56.8 and 92.8).
+// Eight rows a workgroup once that leaves enough workgroups for each CU: four to write, two to read.  8 heads of 128, us
+// with eight against one: bf16, 2561 rows written in 10.2 and 8.8, 8192 in 16.7 and 19.9, 60013 in 102 and 112 (3.1
+// TB/s); 4200 rows read in 9.0 and 8.9, 5000 in 9.3 and 9.8, 8000 in 11.7 and 14.3; fp32, 2100 rows read in 8.3 and
+// 7.9, 3775 in 10.4 and 12.1.
+bool eight_written(const KvCache &c, unsigned y) { return (int64_t)c.T * y >= 8 * 4 * 256; }
+bool eight_read(const KvCache &c, unsigned y) { return (int64_t)c.T * y >= 8 * 2 * 256; }
+// The L2 caches, 4 MiB for each of 8 XCDs: longer outputs go past them (us past and into them: bf16, 8192 rows 10.4 and
+// 12.2, 20011 20.9 and 21.7, 80000 66 and 93; fp32, 8192 rows 15.0 and 16.7, 40000 63.5 and 85.9, 5.8 TB/s).
 constexpr int64_t kLongBytes = 32 << 20;
 
 template <int TYPE, int ROWS>
@@ -129,7 +138,7 @@ hipError_t launch_write_rows(const KvCache &c, const void *k, int64_t ld_k, cons
 template <int TYPE>
 hipError_t launch_write(const KvCache &c, const void *k, int64_t ld_k, const void *v, int64_t ld_v, hipStream_t s) {
     const unsigned y = (unsigned)((2 * c.heads * (c.D / 8) + kThreads - 1) / kThreads);
-    return eight_rows(c, y) ? launch_write_rows<TYPE, 8>(c, k, ld_k, v, ld_v, y, s)
+    return eight_written(c, y) ? launch_write_rows<TYPE, 8>(c, k, ld_k, v, ld_v, y, s)
                             : launch_write_rows<TYPE, 1>(c, k, ld_k, v, ld_v, y, s);
 }
 template <int TYPE, int ROWS, bool PAST>
@@ -140,9 +149,9 @@ hipError_t launch_read_rows(const KvCache &c, void *k, void *v, unsigned y, hipS
 }
 template <int TYPE>
 hipError_t launch_read(const KvCache &c, void *k, void *v, hipStream_t s) {
-    const unsigned y = (unsigned)((2 * c.heads * (c.D / 8) + kThreads - 1) / kThreads);
+    const unsigned y = (unsigned)((2 * c.heads * (c.D / kRead<TYPE>) + kThreads - 1) / kThreads);
     const bool past = (int64_t)c.T * c.heads * c.D * 2 * (TYPE == 0 ? 4 : 2) >= kLongBytes;
-    if (!eight_rows(c, y)) return launch_read_rows<TYPE, 1, false>(c, k, v, y, s);
+    if (!eight_read(c, y)) return launch_read_rows<TYPE, 1, false>(c, k, v, y, s);
     return past ? launch_read_rows<TYPE, 8, true>(c, k, v, y, s) : launch_read_rows<TYPE, 8, false>(c, k, v, y, s);
 }
 

@@ -148,16 +148,14 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) {
     const __bf16 b = (__bf16)f;
     return __builtin_bit_cast(uint16_t, b);
 }
-// PAST: past the caches, for outputs that they cannot hold
-template <int TYPE, bool PAST = false>
-__device__ __forceinline__ void kv_store8(void *base, int64_t at, const float *v) {
+// Four fp32 or eight 16-bit elements.  PAST: past the caches, for outputs that they cannot hold.
+template <int TYPE, bool PAST>
+__device__ __forceinline__ void kv_store16(void *base, int64_t at, const float *v) {
     if constexpr (TYPE == 0) {
+        const f4 a = {v[0], v[1], v[2], v[3]};
         f4 *p = reinterpret_cast<f4 *>(static_cast<float *>(base) + at);
-        const f4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-        if constexpr (PAST) {
-            __builtin_nontemporal_store(a, p);
-            __builtin_nontemporal_store(b, p + 1);
-        } else p[0] = a, p[1] = b;
+        if constexpr (PAST) __builtin_nontemporal_store(a, p);
+        else *p = a;
     } else {
         uint32_t w[4];
 #pragma unroll
@@ -169,6 +167,11 @@ __device__ __forceinline__ void kv_store8(void *base, int64_t at, const float *v
         if constexpr (PAST) __builtin_nontemporal_store(u, p);
         else *p = u;
     }
+}
+template <int TYPE>
+__device__ __forceinline__ void kv_store8(void *base, int64_t at, const float *v) {
+    kv_store16<TYPE, false>(base, at, v);
+    if constexpr (TYPE == 0) kv_store16<TYPE, false>(base, at + 4, v + 4);
 }
 __device__ __forceinline__ void kv_store8(int type, void *base, int64_t at, const float *v) {
     if (type == 0) kv_store8<0>(base, at, v);
