@@ -69,15 +69,6 @@ __device__ __forceinline__ int kv_last_not_above(int B, int64_t x, Key key) {
     }
 }
 
-// the sequence of batch row r, or -1 (a row of none)
-__device__ __forceinline__ int kv_sequence(const KvCache &c, int r) {
-    if (c.starts == nullptr) return r;
-    const int b = kv_last_not_above(c.B, r, [&](int i) { return (int64_t)c.starts[i]; });
-    if (b < 0) return -1;
-    const KvRows k = kv_rows(c, b);
-    return r >= k.first && r < k.first + k.count ? b : -1;
-}
-
 // the page that holds position pos of sequence b, or -1
 __device__ __forceinline__ int kv_page(const KvCache &c, int b, int pos) {
     const int p = c.table[(int64_t)b * c.width + (pos >> c.page_log2)];
