@@ -7,8 +7,8 @@
 // the first 32 rows, the others the same entries against the others.  Two such workgroups
 // share a compute unit, and one's products run beside the other's exponentials: 111 us at
 // the size below; one workgroup of eight wavefronts took 121 with 128 entries and 126 with
-// 128 rows.  The entries stay in registers, decoded to fp16 (two pieces for fp32 queries, as
-// in attend_rows.hip).  The rows' queries come by direct loads into LDS, a step or two
+// 128 rows.  The entries stay in registers, decoded to two fp16 pieces, whatever the queries are:
+// weights are fp32 numbers.  The rows' queries come by direct loads into LDS, a step or two
 // ahead, as the attention left them, fp16 and scaled: converting them anew in every
 // workgroup took 180 us where loading them took 128 (three prompts of 700 rows, 28 heads of
 // 128, fp32), and 121 with the rows' factors and lse loaded that way too.  Every entry's sum
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_mass_rows(AttendArgs a, 
     if (i0 >= i1) return;
 
     // ---- the entries: lane (n, hf) has words 2 i + hf of entry k0 + n
-    h8 kh[2 * NB], kl[PIECES == 2 ? 2 * NB : 1];
+    h8 kh[2 * NB], kl[2 * NB];
     int shift;
     {
         Decode decode;
@@ -117,10 +117,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_mass_rows(AttendArgs a, 
             for (int j = 0; j < 4; ++j) {
                 const h2 h = c[j] * d;
                 kh[i][2 * j] = h.x, kh[i][2 * j + 1] = h.y;
-                if constexpr (PIECES == 2) {
-                    const h2 l = __builtin_elementwise_fma(c[j], d, -h);
-                    kl[i][2 * j] = l.x, kl[i][2 * j + 1] = l.y;
-                }
+                const h2 l = __builtin_elementwise_fma(c[j], d, -h);
+                kl[i][2 * j] = l.x, kl[i][2 * j + 1] = l.y;
             }
         }
     }
@@ -191,8 +189,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_mass_rows(AttendArgs a, 
                     if constexpr (PIECES == 2) {
                         const h8 ql = *reinterpret_cast<const h8 *>(p + S::PIECE);
                         x = mfma32(kh[i], ql, x);
-                        x = mfma32(kl[i], qh, x);
                     }
+                    x = mfma32(kl[i], qh, x);
                 }
                 // a row that has nothing weighs nothing
                 const float lse = rows_at[slot][0][32 * stream + n], up = lse == -INFINITY ? lse : -lse;

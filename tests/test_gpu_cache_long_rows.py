@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv_reference import DIMS, TYPES, Batch, qmm, to_host
+from kv_reference import DIMS, TYPES, Batch, attention, qmm, to_host, tolerance
 from test_gpu_cache_attention import check, queries
 
 pytestmark = pytest.mark.gpu
@@ -96,6 +96,8 @@ def test_nan_reaches_those_that_see_it(kind):
             mass = torch.zeros(1, 1, b.width * page, device="cuda")
             got, lse = qmm.cache_attention(qd.cuda(), *dev, window=w, lse=True, mass=mass)
             sees = torch.from_numpy((pos >= at) & ((pos - at < w) if w else True))
+            alone = qmm.cache_attention(qd.cuda(), *dev, window=w).cpu()
+            assert torch.equal(torch.isnan(alone), sees[:, None, None].expand_as(alone))
             got, lse = got.cpu(), lse.cpu()
             print(kind, at, part, w, flush=True)
             assert torch.equal(torch.isnan(got), sees[:, None, None].expand_as(got))
@@ -117,22 +119,48 @@ def test_pages_and_queries_that_are_not_there(kind):
     L = n + 30
     b = Batch(rng, [L, L], [n, n], 1, 96, 16)
     qd, q = queries(rng, b.T, GROUP, 96, kind)
-    want = check(kind, b, q, qd).cpu()
+    check(kind, b, q, qd)
     at = L // 32 * 16
     for bad in (-1, b.cache.pages, 2**31 - 1, -2**31):
         table = b.table.copy()
         table[1, at // 16] = bad
         cache, _, lens, st = b.dev()
         got = qmm.cache_attention(qd.cuda(), cache, torch.from_numpy(table).cuda(), lens, st).cpu()
+        want = qmm.cache_attention(qd.cuda(), *b.dev()).cpu()
         pos = np.arange(L - n, L)
         nan = torch.from_numpy(np.concatenate((np.zeros(n, bool), pos >= at)))
         assert torch.isnan(got[nan]).all() and torch.equal(got[~nan], want[~nan])
     y = qd.clone()
     y[0, 1, 7], y[-1, 2, 90], y[n, 3, 0] = float("inf"), float("nan"), -float("inf")
-    got = qmm.cache_attention(y.cuda(), *b.dev()).cpu()
+    got, want = qmm.cache_attention(y.cuda(), *b.dev()).cpu(), qmm.cache_attention(qd.cuda(), *b.dev()).cpu()
     bad = torch.zeros(b.T, GROUP, dtype=torch.bool)
     bad[0, 1] = bad[-1, 2] = bad[n, 3] = True
     assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("ask", ["lse", "mass", "both"])
+def test_sums_of_16_bit_calls(ask, D, kind):
+    """lse and mass are fp32 results: their scores come from keys that are not rounded (`rounded_keys` left out of the
+    tolerance; a weight is off by its score's and the lse's error, relative to itself)."""
+    rng = np.random.default_rng([51, D])
+    b = Batch(rng, [60, 45, 30], [40, 3, 1], 1, D, 16)
+    qd, q = queries(rng, b.T, GROUP, D, kind, 2.0)
+    out_ref, lse_ref, mass_ref, slack = attention(b, q, D ** -0.5)
+    ds = tolerance(kind, D, 60, slack, out_ref)[1]
+    print(ask, D, kind, flush=True)
+    cache, table, lens, st = b.dev()
+    mass = torch.zeros(mass_ref.shape, device="cuda") if ask != "lse" else None
+    got = qmm.cache_attention(qd.cuda(), cache, table, lens, st, lse=ask != "mass", mass=mass)
+    off = ds + 2.0 ** -22 * (2 + np.abs(lse_ref))
+    if ask != "mass":
+        assert (np.abs(to_host(got[1]) - lse_ref) <= off * 1.01).all()
+    if mass is not None:
+        # fp32 queries' pieces are not needed, the keys' two hold 22 bits: 2^-22 of the sum of magnitudes beside ds
+        per = 2 * (off + 2.0 ** -22 * slack[0]).max()
+        n = b.T * GROUP + 2
+        assert (np.abs(to_host(mass) - mass_ref) <= (per + n * 2.0 ** -24) * mass_ref + n * 2.0 ** -40).all()
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16"])
