@@ -145,7 +145,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_mass_rows(AttendArgs a, 
             for (int i = 0; i < S::PER_PIECE; ++i)
                 asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
                                  lds_at + slot * S::STAGE + k * S::PIECE + 1024 * (wave * S::PER_PIECE + i)),
-                             "v"(place[i]), "s"(r) : "memory");
+                             "v"(place[i]), "s"(r) : "m0", "memory");
         }
         // the wavefronts load the same by twos, so that all have as many loads
         const uint64_t base = (uint64_t)(uintptr_t)((wave & 1 ? sp.factors : sp.lse2) + row0 + r0);
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_mass_rows(AttendArgs a, 
                          0x00020000u};
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
                          rows_lds + slot * (8 * ROWS) + (wave & 1) * (4 * ROWS)),
-                     "v"(4 * lane), "s"(r) : "memory");
+                     "v"(4 * lane), "s"(r) : "m0", "memory");
     };
     float got[16];
 #pragma unroll

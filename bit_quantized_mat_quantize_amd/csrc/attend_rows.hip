@@ -152,9 +152,9 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
 #pragma unroll
         for (int i = 0; i < S::CODE_LOADS; ++i)
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + 1024 * i),
-                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "memory");
+                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "m0", "memory");
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to + 1024 * S::CODE_LOADS),
-                     "v"(scale_at), "s"(r), "s"(e0 * 2) : "memory");
+                     "v"(scale_at), "s"(r), "s"(e0 * 2) : "m0", "memory");
     };
     // the step's group out of its slot, once at most `later` steps' loads behind it are on their way
     auto take = [&](int step, int later, Raw<D> &raw) {

@@ -182,11 +182,11 @@ struct Ring {
 #pragma unroll
         for (int i = 0; i < CODES; ++i)
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + 1024 * i),
-                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "memory");
+                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "m0", "memory");
 #pragma unroll
         for (int i = 0; i < SCALES; ++i)
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to + SCALE_AT + 256 * i),
-                         "v"(scale_at[i]), "s"(r), "s"(e0 * 2) : "memory");
+                         "v"(scale_at[i]), "s"(r), "s"(e0 * 2) : "m0", "memory");
     }
     __device__ __forceinline__ void read(int slot, Step<D> &t) const {
         constexpr int NB = D / 32, ROUNDS = Step<D>::ROUNDS, WORDS = D / 8;
