@@ -1374,13 +1374,9 @@ qmm_status qmm_cache_evict(const qmm_cache *c, const float *mass, int64_t ld_mas
     QMM_TRY(check_ptr("lens_out", lens_out));
     QMM_TRY(check_ptr("mass_out", mass_out));
     QMM_TRY(check_ptr("ids", ids));
-    {
-        const int64_t capacity = c->width * c->page, most = capacity < budget ? capacity : budget;
-        const int64_t chunks = (most + 27) / 28;  // the smallest chunk of entries that a workgroup moves
-        if (to != c->table && 2 * c->seqs * c->heads * chunks > kMaxBlocks)
-            return fail(QMM_EUNSUPPORTED, "seqs = %lld, heads = %lld, budget = %lld need more than %lld workgroups",
-                        (long long)c->seqs, (long long)c->heads, (long long)budget, (long long)kMaxBlocks);
-    }
+    if (to != c->table && qmm::evict_workgroups(c->seqs, c->heads, c->dim, c->width * c->page, budget) > kMaxBlocks)
+        return fail(QMM_EUNSUPPORTED, "seqs = %lld, heads = %lld, budget = %lld need more than %lld workgroups",
+                    (long long)c->seqs, (long long)c->heads, (long long)budget, (long long)kMaxBlocks);
     const int64_t rows = c->seqs * c->heads;
     const Span in[] = {{mass, strided_bytes(rows, ld_mass, c->width * c->page, sizeof(float))},
                        {to, (size_t)(c->seqs * to_width) * sizeof(int32_t)}};

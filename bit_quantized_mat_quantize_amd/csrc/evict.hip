@@ -214,6 +214,14 @@ __device__ __forceinline__ void arrived(uint4 &v, uint32_t &s) {
     asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w), "+v"(s));
 }
 
+// entries at a time: one 16-byte piece of codes and one scale per thread, values in fours
+__host__ __device__ constexpr int move_chunk(int threads, int D) { return threads / (D / 32) & ~3; }
+// chunks of a sequence and head, of kMove threads each
+int64_t move_parts(int64_t D, int64_t capacity, int64_t budget) {
+    const int chunk = move_chunk(kMove, (int)D);
+    return ((capacity < budget ? capacity : budget) + chunk - 1) / chunk;
+}
+
 // CHAIN: one workgroup goes through all chunks (the same pages), the places of the one after
 // the next, the codes of the next and the stores of this one at a time; else it has one.
 template <bool CHAIN, int THREADS>
@@ -226,7 +234,7 @@ __global__ __launch_bounds__(THREADS) void k_evict_move(EvictArgs a, int parts) 
     const int32_t *table = a.c.table + (int64_t)b * a.c.width, *to = a.to + (int64_t)b * a.to_width;
     const int most = a.c.width << lg, given = a.c.lens[b];
     const int L = given < 0 ? 0 : (given > most ? most : given), n = L < a.budget ? L : a.budget;
-    const int chunk = THREADS / nb & ~3;  // entries at a time: one 16-byte piece of codes and one scale per thread
+    const int chunk = move_chunk(THREADS, D);
     const int tid = threadIdx.x, words = D / 8;
     const bool active = tid < chunk * nb;
     // keys: piece p of entry j; values: word w of the entries 4g .. 4g + 3; scales: block s of entry i
@@ -315,6 +323,10 @@ __global__ __launch_bounds__(THREADS) void k_evict_move(EvictArgs a, int parts) 
 
 }  // namespace
 
+int64_t evict_workgroups(int64_t B, int64_t heads, int64_t D, int64_t capacity, int64_t budget) {
+    return 2 * B * heads * move_parts(D, capacity, budget);
+}
+
 hipError_t launch_cache_evict(const EvictArgs &a, hipStream_t s) {
     const unsigned n = (unsigned)(a.c.B * a.c.heads);
     const int64_t capacity = (int64_t)a.c.width << a.c.page_log2;
@@ -329,8 +341,7 @@ hipError_t launch_cache_evict(const EvictArgs &a, hipStream_t s) {
         return hipGetLastError();
     }
     // (four chunks a workgroup: 54.5 us against 51.5 for 16 x 9000 -> 4096 entries, 69 against 73 for 8 x 16000 -> 12000)
-    const int64_t most = capacity < a.budget ? capacity : a.budget;
-    const int chunk = kMove / (a.c.D / 32) & ~3, parts = (int)((most + chunk - 1) / chunk);
+    const int parts = (int)move_parts(a.c.D, capacity, a.budget);
     hipLaunchKernelGGL((k_evict_move<false, kMove>), dim3(2 * n * (unsigned)parts), dim3(kMove), 0, s, a, parts);
     return hipGetLastError();
 }

@@ -302,6 +302,8 @@ struct EvictArgs {
     int64_t ld_mass, ld_out;
     int to_width, budget, recent;
 };
+// workgroups that move the entries into other pages
+int64_t evict_workgroups(int64_t B, int64_t heads, int64_t D, int64_t capacity, int64_t budget);
 hipError_t launch_cache_evict(const EvictArgs &a, hipStream_t s);
 
 }  // namespace qmm

@@ -1,0 +1,46 @@
+"""What cache_evict launches and refuses near the limit of a launch's workgroups.  As in test_dispatch_log.py: a valid call
+is logged after the argument checks and before the launch, which fails with QMM_EDEVICE where there is no GPU; the
+pointers are placeholders."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+pytestmark = pytest.mark.skipif(os.path.exists("/dev/kfd"),
+                                reason="placeholder pointers are only passed where no GPU exists")
+
+CHILD = r"""
+import ctypes, sys
+sys.path.insert(0, sys.argv[1])
+from bit_quantized_mat_quantize_amd import _binding
+lib = _binding.load()
+hip = ctypes.CDLL("libamdhip64.so")
+n = ctypes.c_int(0)
+if hip.hipGetDeviceCount(ctypes.byref(n)) == 0 and n.value > 0:
+    sys.exit(3)                      # a device exists: placeholder pointers must not be launched
+p = lambda i: 65536 + (i << 52)
+SEQS, HEADS = 4096, 64               # 2 * SEQS * HEADS = 2^19 workgroups for each chunk of entries: 31 chunks at most
+
+
+def evict(dim, budget, same=False):
+    c = _binding._Cache(p(0), 1 << 50, 8, 16, HEADS, dim, p(1), SEQS, 1024, p(2), None, 0)
+    return lib.qmm_cache_evict(ctypes.byref(c), p(3), 1024 * 16, budget, 5, p(1) if same else p(4), 1024, p(5), p(6),
+                               1024 * 16, p(7), None)
+
+
+# entries of a chunk: 256 threads over the blocks of an entry, in fours
+for dim, chunk in ((64, 128), (96, 84), (128, 64), (192, 40), (256, 32)):
+    print(dim, evict(dim, 31 * chunk), evict(dim, 31 * chunk + 1), evict(dim, 31 * chunk + 1, True))
+"""
+
+
+def test_evict_up_to_the_largest_launch():
+    r = subprocess.run([sys.executable, "-c", CHILD, ROOT], capture_output=True, text=True,
+                       env=dict(os.environ, QMM_LOG="1"), timeout=300)
+    if r.returncode == 3:
+        pytest.skip("a GPU is present")
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split("\n")[:5] == [f"{dim} 4 3 4" for dim in (64, 96, 128, 192, 256)]
