@@ -785,7 +785,8 @@ def cache_read(cache, rows: int, table, lens, starts=None, dtype=None, stream=No
 
 def cache_attention_workspace_bytes(q, heads: int, seqs: int, width: int, page: int, ragged: bool,
                                     mass: bool = False) -> int:
-    """For q [T, q_heads, dim] over a cache of `heads` heads, with `seqs` tables of `width` pages; ragged: with starts."""
+    """For q [T, q_heads, dim] over a cache of `heads` heads, with `seqs` tables of `width` pages; ragged: with starts.  That
+    of the largest call serves those with fewer rows, sequences or pages, without lse, without starts and without mass."""
     rows, q_heads, dim = q.shape
     return int(load().qmm_cache_attention_workspace_bytes(_float_type(q, "q"), rows, q_heads, heads, dim, seqs, width, page, ragged, mass))
 

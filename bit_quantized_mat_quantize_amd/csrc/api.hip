@@ -1306,8 +1306,10 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
         QMM_TRY(check_ptr("mass", mass));
         QMM_TRY(check_ld("ld_mass", ld_mass, capacity));
     }
-    const size_t ws_need = qmm_cache_attention_workspace_bytes(t, c->rows, q_heads, c->heads, c->dim, c->seqs, c->width,
-                                                               c->page, c->starts != nullptr, mass != nullptr);
+    a.lse = lse;
+    a.mass = mass;
+    a.group = (int)(q_heads / c->heads);
+    const size_t ws_need = (size_t)qmm::attend_workspace_used((int)t, a);
     if (ws_need != 0) {
         QMM_TRY(check_ptr("workspace", workspace));
         QMM_TRY(check_size("workspace", ws_bytes, ws_need));
@@ -1328,14 +1330,11 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
     }
     a.q = q;
     a.out = out;
-    a.lse = lse;
-    a.mass = mass;
     a.ws = static_cast<float *>(workspace);
     a.ld_q = ld_q;
     a.ld_out = ld_out;
     a.ld_mass = ld_mass;
     a.scale = (float)((double)scale * 1.4426950408889634074);  // log2 e
-    a.group = (int)(q_heads / c->heads);
     a.window = (int)(window >= capacity ? 0 : window);  // as good as none
     a.causal = causal != 0;
     if (!qmm::attend_grid_ok((int)t, a))

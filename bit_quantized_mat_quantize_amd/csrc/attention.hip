@@ -816,10 +816,15 @@ int64_t few_room(int type, int64_t D, bool sums) {
     return attend_rows_has(type, D) && !(type != 0 && sums) ? (type == 0 ? 1024 : 256) : kAnyRows;
 }
 
+// largest: no call's shape but one whose workspace is no smaller than that of any call of up to T rows and B sequences,
+// with lse or without: with parts in either kernel, for as many sequences as are split, however many tiles are sure to
+// have rows.
 Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D, bool ragged, bool mass,
-               bool lse) {
+               bool lse, bool largest = false) {
     Shape p{};
-    const int64_t rows = T * group, room = ragged ? few_room(type, D, mass || lse) : kAnyRows;
+    if (largest && ragged && B > kCounted) B = kCounted;
+    const int64_t rows = T * group, room = ragged ? few_room(type, D, !largest && (mass || lse)) : kAnyRows;
+    const int64_t few = largest ? kAnyRows : room;  // rows of a sequence that k_attend can have
     p.sp.few_room = (int)room;
     p.sp.few_rows = (int)(!ragged && group < kFewTile ? group : kFewTile);
     auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
@@ -832,13 +837,13 @@ Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, 
         most_tiles = (int)tiles;
         want = (int)fit;
         most = (int)least(least(steps, fit), tiles * heads <= at_once / 64 ? 256 : 64);
-        if ((ragged && B > kCounted) || fit < 2 * sure) most = 1;
+        if (!largest && ((ragged && B > kCounted) || fit < 2 * sure)) most = 1;
         groups = least(fit > tiles ? fit : tiles, tiles * most) * heads;
         parts = most > 1 ? least(fit, tiles * most) * heads * per : 0;
         join = most > 1 ? least(tiles, fit / 2) * heads * per : 0;
     };
     const int64_t each = D > 128 ? at_once<1, 256> : (type == 0 && D == 128 ? at_once<2, 128> : at_once<1, 128>);
-    const int64_t apart = B * ((least(room, rows) + kFewTile - 1) / kFewTile), packed = rows / kFewTile + B;
+    const int64_t apart = B * ((least(few, rows) + kFewTile - 1) / kFewTile), packed = rows / kFewTile + B;
     share(!ragged ? B * ((group + kFewTile - 1) / kFewTile) : (B > kCounted ? packed : least(apart, packed)), 0, 256 * each,
           kKeys * kWaves, p.sp.few_rows, p.sp.few_tiles, p.sp.few_want, p.sp.few_most, p.few_groups, p.few_parts, p.few_join);
     if (ragged && rows > room)
@@ -923,11 +928,10 @@ hipError_t launch_for(int type, const AttendArgs &a, const Shape &p, hipStream_t
 
 int64_t attend_workspace_bytes(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
                                bool ragged, bool mass) {
-    // with lse or without
-    const int64_t with = shape_of(type, T, B, capacity, heads, group, D, ragged, mass, true).bytes;
-    const int64_t without = shape_of(type, T, B, capacity, heads, group, D, ragged, mass, false).bytes;
-    return with > without ? with : without;
+    return shape_of(type, T, B, capacity, heads, group, D, ragged, mass, true, true).bytes;
 }
+
+int64_t attend_workspace_used(int type, const AttendArgs &a) { return shape_of(type, a).bytes; }
 
 void attend_shape(int type, const AttendArgs &a, int *few, int *many) {
     const Shape p = shape_of(type, a);

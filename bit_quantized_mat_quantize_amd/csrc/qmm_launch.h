@@ -284,8 +284,10 @@ struct AttendArgs {
     int group, window;       // window 0: none
     bool causal;
 };
+// of a call of up to T rows and B sequences; and what a call uses of it
 int64_t attend_workspace_bytes(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
                                bool ragged, bool mass);
+int64_t attend_workspace_used(int type, const AttendArgs &a);
 // splits of sequences with few rows, and with many (0: there can be none)
 void attend_shape(int type, const AttendArgs &a, int *few, int *many);
 bool attend_grid_ok(int type, const AttendArgs &a);  // every launch fits a grid

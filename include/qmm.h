@@ -538,7 +538,8 @@ qmm_status qmm_cache_read(const qmm_cache *c, qmm_float_type t, void *k, size_t 
                           void *stream);
 
 /* Bytes of the workspace qmm_cache_attention needs (0: none).  q_heads query heads of format t; ragged: starts is given; mass:
- * mass is. */
+ * mass is.  That of the largest call serves the smaller ones: with fewer rows, sequences or pages of a table, with lse or
+ * without, and, of a call with starts or mass, those without. */
 size_t qmm_cache_attention_workspace_bytes(qmm_float_type t, int64_t rows, int64_t q_heads, int64_t heads, int64_t dim,
                                            int64_t seqs, int64_t width, int64_t page, int ragged, int mass);
 
