@@ -14,11 +14,16 @@
 // needs no exchange between lanes: the order in which a lane's registers hold the
 // entries is the order of the values in LDS.
 //
-// Scale * code is rounded to fp16 for 16-bit queries.  fp32 queries, and with them the decoded
-// entries and P, are two fp16 pieces each (22 bits), of whose four products the three
-// large ones are taken.  All scales of a workgroup are multiplied by one power of two for
-// the keys and one for the values, which move when a larger scale turns up (then the
-// tile is decoded again; after the first tile that is seldom).
+// Of 16-bit queries, values and P are rounded to fp16.  Keys, scale * code of up to 14 bits, are two
+// fp16 pieces, exact, for fp16 queries: rounded to one they put outputs at 4.4e-4 of the norm from
+// the 64-bit result where fp16 itself costs 2.1e-4, and now 2.9e-4 (9 sequences, 555 rows,
+// window 1024), and with scores of hundreds moved weights by per cents.  For bf16 ones they are rounded: outputs are 1.7e-3 off either way, and two
+// pieces are half as many matrix instructions again (2 prompts of 2048 rows on 8192 entries each, 32 heads of 128:
+// 695 us and 847).  fp32 queries, and with them the decoded entries and P, are two fp16
+// pieces each (22 bits), of whose four products the three large ones are taken.  All scales
+// of a workgroup are multiplied by one power of two for the keys and one for the values,
+// which move when a larger scale turns up (then the tile is decoded again; after the first
+// tile that is seldom).
 //
 // Bounds: matrix and vector instructions, which overlap in part only (of the cycles, 2 prompts
 // of 2048 rows on 8192 entries, 32 heads of 128 in bf16: 32% and 42%; 525 to 549 us a call
@@ -33,19 +38,20 @@ namespace qmm {
 namespace {
 
 // Rows of a tile, entries of a step.
-template <int PIECES, int D>
+// KP: pieces of a key.  PIECES: of a query, a weight and a value.
+template <int KP, int PIECES, int D>
 struct Shape {
     static constexpr int WAVES = 8, KT = 64, ROWS = kManyTile, THREADS = 64 * WAVES;
     static_assert(ROWS == 32 * WAVES, "32 rows a wavefront");
     static constexpr int NB = D / 32, WORDS = D / 8, ROUNDS = D > 128 ? 2 : 1;
     static constexpr int KEY_ROW = D == 96 ? 128 : D;              // elements of a key's row in LDS
     static constexpr int KEYS = KT * KEY_ROW * 2, VALUES = D * KT * 2;  // bytes of one piece
-    static constexpr int STAGE = PIECES * (KEYS + VALUES), BYTES = 2 * STAGE;
+    static constexpr int STAGE = KP * KEYS + PIECES * VALUES, BYTES = 2 * STAGE;
     static constexpr int GROUPS = 2 * KT / 16, MINE = GROUPS / WAVES;  // groups of 16 entries' keys or values; per wavefront
     static_assert(MINE == 1, "one group per wavefront");
-    // a group on its way: 16 * D/2 bytes of codes, filler to 1 KiB, D/32 * 32 of scales, filler to 256
+    // a group on its way: 16 * D/2 bytes of codes, D/32 * 32 of scales
     static constexpr int CODE_LOADS = (8 * D + 1023) / 1024, LOADS = CODE_LOADS + 1;
-    static constexpr int RAW = 1024 * CODE_LOADS + 256;
+    static constexpr int RAW = 9 * D;
     static constexpr int ROOM = 160 * 1024 - 512 - BYTES;  // of LDS
     static constexpr int SLOTS = ROOM >= 3 * WAVES * RAW ? 3 : (ROOM >= 2 * WAVES * RAW ? 2 : 1);
     static constexpr int ALL = BYTES + SLOTS * WAVES * RAW;
@@ -53,13 +59,13 @@ struct Shape {
 };
 
 // 16-byte pieces of LDS rows are placed so that eight lanes of one access meet eight of them
-template <int PIECES, int D>
+template <int D>
 __device__ __forceinline__ int key_piece(int entry, int w) {
-    return entry * Shape<PIECES, D>::KEY_ROW * 2 + ((w ^ (entry & 7)) * 16);
+    return entry * Shape<1, 1, D>::KEY_ROW * 2 + ((w ^ (entry & 7)) * 16);
 }
-template <int PIECES, int D>
+template <int D>
 __device__ __forceinline__ int value_piece(int element, int c) {  // c: eight entries
-    constexpr int KT = Shape<PIECES, D>::KT;
+    constexpr int KT = Shape<1, 1, D>::KT;
     const int by = (element ^ (element >> 3)) & 7;
     return element * KT * 2 + ((c ^ by) * 16);
 }
@@ -77,9 +83,9 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <int PIECES, int D>
-__global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(AttendArgs a, Splits sp, int type) {
-    using S = Shape<PIECES, D>;
+template <int KP, int PIECES, int D>
+__global__ __launch_bounds__((Shape<KP, PIECES, D>::THREADS), 1) void k_attend_rows(AttendArgs a, Splits sp, int type) {
+    using S = Shape<KP, PIECES, D>;
     constexpr int NB = S::NB, KT = S::KT, WORDS = S::WORDS, ROUNDS = S::ROUNDS;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ uint32_t flags[10];
@@ -133,9 +139,8 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     const uint32_t ring_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring);
     uint32_t code_at[S::CODE_LOADS];
 #pragma unroll
-    for (int i = 0; i < S::CODE_LOADS; ++i) code_at[i] = 16 * (64 * i + lane < D / 2 ? 64 * i + lane : D / 2 - 1);
-    const int piece = lane < D / 4 ? lane : D / 4 - 1;  // 4 bytes of a block's scales
-    const uint32_t scale_at = ((D / 2) << a.c.page_log2) + 2 * ((piece >> 3) << a.c.page_log2) + 4 * (piece & 7);
+    for (int i = 0; i < S::CODE_LOADS; ++i) code_at[i] = 16 * (64 * i + lane);
+    const uint32_t scale_at = ((D / 2) << a.c.page_log2) + 2 * ((lane >> 3) << a.c.page_log2) + 4 * (lane & 7);  // 4 bytes
     const uint32_t records = (uint32_t)kv_chunk_bytes(a.c);
     uint32_t missing = 0;  // steps whose page is not in the pool, the next one lowest
     auto load = [&](int step, int ahead) {  // ahead: of the step that is multiplied
@@ -150,18 +155,20 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
         const int e0 = at & ((1 << a.c.page_log2) - 1);
         const uint32_t to = ring_at + ((step - from) % SLOTS) * S::RAW;
 #pragma unroll
-        for (int i = 0; i < S::CODE_LOADS; ++i)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + 1024 * i),
-                         "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "m0", "memory");
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to + 1024 * S::CODE_LOADS),
-                     "v"(scale_at), "s"(r), "s"(e0 * 2) : "m0", "memory");
+        for (int i = 0; i < S::CODE_LOADS; ++i)  // lanes behind the group's end are off: they would write to LDS too
+            if (64 * i + 64 <= D / 2 || lane < D / 2 - 64 * i)
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to + 1024 * i),
+                             "v"(code_at[i]), "s"(r), "s"(e0 * (D / 2)) : "m0", "memory");
+        if (lane < D / 4)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to + 8 * D),
+                         "v"(scale_at), "s"(r), "s"(e0 * 2) : "m0", "memory");
     };
     // the step's group out of its slot, once at most `later` steps' loads behind it are on their way
     auto take = [&](int step, int later, Raw<D> &raw) {
         if (SLOTS > 2 && later >= 2) wait_loads<2 * S::LOADS>();
         else if (SLOTS > 1 && later >= 1) wait_loads<S::LOADS>();
         else wait_loads<0>();
-        const uint8_t *slot = ring + ((step - from) % SLOTS) * S::RAW, *scales = slot + 1024 * S::CODE_LOADS;
+        const uint8_t *slot = ring + ((step - from) % SLOTS) * S::RAW, *scales = slot + 8 * D;
         if (keys) {
             const uint32_t *p = reinterpret_cast<const uint32_t *>(slot) + ke * WORDS + kg * NB;
             if constexpr (NB % 4 == 0) {
@@ -233,9 +240,9 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                 h2 h[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) h[j] = c[j] * d;
-                uint8_t *to = stage + key_piece<PIECES, D>(e + ke, 4 * i + kg);
+                uint8_t *to = stage + key_piece<D>(e + ke, 4 * i + kg);
                 *reinterpret_cast<uint4 *>(to) = make_uint4(as_u32(h[0]), as_u32(h[1]), as_u32(h[2]), as_u32(h[3]));
-                if constexpr (PIECES == 2) {
+                if constexpr (KP == 2) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) h[j] = __builtin_elementwise_fma(c[j], d, -h[j]);
                     *reinterpret_cast<uint4 *>(to + S::KEYS) =
@@ -243,7 +250,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                 }
             }
         } else {
-            stage += PIECES * S::KEYS;
+            stage += KP * S::KEYS;
             const _Float16 unit = (_Float16)pow2i(value_shift_);
 #pragma unroll
             for (int r = 0; r < ROUNDS; ++r) {
@@ -261,7 +268,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                             const h2 c0 = o ? centred_odd(decode.odd(both[0])) : centred_even(decode.even(both[0]));
                             const h2 c1 = o ? centred_odd(decode.odd(both[1])) : centred_even(decode.even(both[1]));
                             const h2 h0 = c0 * d[0], h1 = c1 * d[1];
-                            uint8_t *to = stage + value_piece<PIECES, D>(8 * w + 2 * y + o, c) + half;
+                            uint8_t *to = stage + value_piece<D>(8 * w + 2 * y + o, c) + half;
                             *reinterpret_cast<uint2 *>(to) = make_uint2(as_u32(h0), as_u32(h1));
                             if constexpr (PIECES == 2)
                                 *reinterpret_cast<uint2 *>(to + S::VALUES) =
@@ -375,12 +382,12 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                 for (int r = 0; r < 16; ++r) x[r] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2 * NB; ++i) {
-                    const uint8_t *p = stage + key_piece<PIECES, D>(32 * sub + n, 2 * i + hf);
+                    const uint8_t *p = stage + key_piece<D>(32 * sub + n, 2 * i + hf);
                     const h8 kh = *reinterpret_cast<const h8 *>(p);
                     x = mfma32(kh, qh[i], x);
-                    if constexpr (PIECES == 2) {
+                    if constexpr (PIECES == 2) x = mfma32(kh, ql[i], x);
+                    if constexpr (KP == 2) {
                         const h8 kl = *reinterpret_cast<const h8 *>(p + S::KEYS);
-                        x = mfma32(kh, ql[i], x);
                         x = mfma32(kl, qh[i], x);
                     }
                 }
@@ -424,7 +431,7 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const uint8_t *p = stage + PIECES * S::KEYS + value_piece<PIECES, D>(32 * i + n, 2 * (2 * sub + t) + hf);
+                        const uint8_t *p = stage + KP * S::KEYS + value_piece<D>(32 * i + n, 2 * (2 * sub + t) + hf);
                         const h8 vh = *reinterpret_cast<const h8 *>(p);
                         o[i] = mfma32(vh, ph[t], o[i]);
                         if constexpr (PIECES == 2) {
@@ -472,30 +479,31 @@ __global__ __launch_bounds__((Shape<PIECES, D>::THREADS), 1) void k_attend_rows(
     }
 }
 
-template <int PIECES, int D>
+template <int KP, int PIECES, int D>
 hipError_t launch(int type, const AttendArgs &a, const Splits &sp, int64_t workgroups, hipStream_t s) {
-    using S = Shape<PIECES, D>;
+    using S = Shape<KP, PIECES, D>;
     static std::atomic<uint64_t> lds_set{0};
-    const hipError_t e = ensure_lds_bytes((const void *)k_attend_rows<PIECES, D>, S::ALL, lds_set);
+    const hipError_t e = ensure_lds_bytes((const void *)k_attend_rows<KP, PIECES, D>, S::ALL, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attend_rows<PIECES, D>), dim3((unsigned)workgroups), dim3(S::THREADS), S::ALL, s, a, sp, type);
+    hipLaunchKernelGGL((k_attend_rows<KP, PIECES, D>), dim3((unsigned)workgroups), dim3(S::THREADS), S::ALL, s, a, sp, type);
     return hipGetLastError();
 }
-template <int PIECES>
+template <int KP, int PIECES>
 hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, int64_t workgroups, hipStream_t s) {
     switch (a.c.D) {
-        case 64: return launch<PIECES, 64>(type, a, sp, workgroups, s);
-        case 96: return launch<PIECES, 96>(type, a, sp, workgroups, s);
-        case 128: return launch<PIECES, 128>(type, a, sp, workgroups, s);
+        case 64: return launch<KP, PIECES, 64>(type, a, sp, workgroups, s);
+        case 96: return launch<KP, PIECES, 96>(type, a, sp, workgroups, s);
+        case 128: return launch<KP, PIECES, 128>(type, a, sp, workgroups, s);
     }
-    if constexpr (PIECES == 1) return launch<1, 192>(type, a, sp, workgroups, s);
+    if constexpr (PIECES == 1) return launch<KP, 1, 192>(type, a, sp, workgroups, s);
     return hipErrorInvalidValue;  // attend_rows_has
 }
 
 }  // namespace
 
 hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t workgroups, hipStream_t s) {
-    return type == 0 ? launch_for<2>(type, a, sp, workgroups, s) : launch_for<1>(type, a, sp, workgroups, s);
+    if (type == 0) return launch_for<2, 2>(type, a, sp, workgroups, s);
+    return type == 1 ? launch_for<2, 1>(type, a, sp, workgroups, s) : launch_for<1, 1>(type, a, sp, workgroups, s);
 }
 
 }  // namespace qmm

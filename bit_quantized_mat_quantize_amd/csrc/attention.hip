@@ -808,12 +808,11 @@ constexpr int64_t quads(int64_t floats) { return (floats + 3) / 4 * 4; }  // who
 //                 16 x 4000   299   170    616   427    1312  1601    4337  5247
 //   bf16, D = 192, 2 x 4096    65    54     94    97     287   295     459   933
 //         D = 256             115    57    174   103     576   313    1141   989  (its tiles pass the registers)
-//
-// k_attend_rows rounds keys to fp16 for 16-bit queries, which the sums would show: where lse or mass are asked for, k_attend
-// takes all rows of 16-bit calls.
+// k_attend_rows rounds keys to fp16 for bf16 queries, which the sums would show: where lse or mass are asked for, k_attend
+// takes all rows of such calls.
 constexpr int64_t kAnyRows = 0x7fffffff;
 int64_t few_room(int type, int64_t D, bool sums) {
-    return attend_rows_has(type, D) && !(type != 0 && sums) ? (type == 0 ? 1024 : 256) : kAnyRows;
+    return attend_rows_has(type, D) && !(type == 2 && sums) ? (type == 0 ? 1024 : 256) : kAnyRows;
 }
 
 // largest: no call's shape but one whose workspace is no smaller than that of any call of up to T rows and B sequences,

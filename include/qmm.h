@@ -552,7 +552,8 @@ size_t qmm_cache_attention_workspace_bytes(qmm_float_type t, int64_t rows, int64
  * mass: fp32 [seqs][heads][ld_mass], ld_mass >= width * page, or NULL: mass[b][h][j] += the sum over the call's rows
  * and the query heads of cache head h of e^(s_j - lse).
  * Sums are fp32.  fp32 queries are multiplied to 22 bits of their row's largest element; with 16-bit queries values and
- * the weights e^(..) may be rounded to fp16 before their product, and, where neither lse nor mass is asked for, keys.  Results do not depend on timing.
+ * the weights e^(..) may be rounded to fp16 before their product, and with bf16 ones, where neither lse nor mass is
+ * asked for, keys.  Results do not depend on timing.
  * Requires rows * q_heads <= 2^30.  What stands behind lens[b], or in pages that no row sees, may hold anything.  An entry that a row sees and
  * that has a NaN scale, or whose page is not in [0, pages), makes the row NaN; so does an infinity or NaN in its query.
  * workspace: qmm_cache_attention_workspace_bytes, overwritten; calls that may overlap need one each.  out must not
