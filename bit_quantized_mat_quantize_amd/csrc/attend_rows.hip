@@ -14,16 +14,17 @@
 // needs no exchange between lanes: the order in which a lane's registers hold the
 // entries is the order of the values in LDS.
 //
-// Of 16-bit queries, values and P are rounded to fp16.  Keys, scale * code of up to 14 bits, are two
-// fp16 pieces, exact, for fp16 queries: rounded to one they put outputs at 4.4e-4 of the norm from
-// the 64-bit result where fp16 itself costs 2.1e-4, and now 2.9e-4 (9 sequences, 555 rows,
-// window 1024), and with scores of hundreds moved weights by per cents.  For bf16 ones they are rounded: outputs are 1.7e-3 off either way, and two
-// pieces are half as many matrix instructions again (2 prompts of 2048 rows on 8192 entries each, 32 heads of 128:
-// 695 us and 847).  fp32 queries, and with them the decoded entries and P, are two fp16
-// pieces each (22 bits), of whose four products the three large ones are taken.  All scales
-// of a workgroup are multiplied by one power of two for the keys and one for the values,
-// which move when a larger scale turns up (then the tile is decoded again; after the first
-// tile that is seldom).
+// Of 16-bit queries, values and P are rounded to fp16.  Keys, scale * code of up to 14 bits, are
+// two fp16 pieces, exact, for fp16 queries and where lse or mass are asked for: rounded to one
+// they put fp16 outputs at 4.4e-4 of the norm from the 64-bit result where fp16 itself costs
+// 2.1e-4 (now 2.9e-4; 9 sequences, 555 rows, window 1024), moved weights by per cents with scores of
+// hundreds, and would show in lse and mass.  For bf16 outputs alone they are rounded: these are 1.7e-3 off either
+// way, and two pieces are half as many matrix instructions again (2 prompts of 2048 rows on
+// 8192 entries each, 32 heads of 128: 695 us and 847).  fp32 queries, and with them the
+// decoded entries and P, are two fp16 pieces each (22 bits), of whose four products the three
+// large ones are taken.  All scales of a workgroup are multiplied by one power of two for the
+// keys and one for the values, which move when a larger scale turns up (then the tile is
+// decoded again; after the first tile that is seldom).
 //
 // Bounds: matrix and vector instructions, which overlap in part only (of the cycles, 2 prompts
 // of 2048 rows on 8192 entries, 32 heads of 128 in bf16: 32% and 42%; 525 to 549 us a call
@@ -503,7 +504,8 @@ hipError_t launch_for(int type, const AttendArgs &a, const Splits &sp, int64_t w
 
 hipError_t launch_attend_rows(int type, const AttendArgs &a, const Splits &sp, int64_t workgroups, hipStream_t s) {
     if (type == 0) return launch_for<2, 2>(type, a, sp, workgroups, s);
-    return type == 1 ? launch_for<2, 1>(type, a, sp, workgroups, s) : launch_for<1, 1>(type, a, sp, workgroups, s);
+    const bool exact = type == 1 || a.lse != nullptr || a.mass != nullptr;
+    return exact ? launch_for<2, 1>(type, a, sp, workgroups, s) : launch_for<1, 1>(type, a, sp, workgroups, s);
 }
 
 }  // namespace qmm

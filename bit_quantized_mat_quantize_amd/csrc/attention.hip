@@ -808,22 +808,17 @@ constexpr int64_t quads(int64_t floats) { return (floats + 3) / 4 * 4; }  // who
 //                 16 x 4000   299   170    616   427    1312  1601    4337  5247
 //   bf16, D = 192, 2 x 4096    65    54     94    97     287   295     459   933
 //         D = 256             115    57    174   103     576   313    1141   989  (its tiles pass the registers)
-// k_attend_rows rounds keys to fp16 for bf16 queries, which the sums would show: where lse or mass are asked for, k_attend
-// takes all rows of such calls.
 constexpr int64_t kAnyRows = 0x7fffffff;
-int64_t few_room(int type, int64_t D, bool sums) {
-    return attend_rows_has(type, D) && !(type == 2 && sums) ? (type == 0 ? 1024 : 256) : kAnyRows;
-}
+int64_t few_room(int type, int64_t D) { return attend_rows_has(type, D) ? (type == 0 ? 1024 : 256) : kAnyRows; }
 
 // largest: no call's shape but one whose workspace is no smaller than that of any call of up to T rows and B sequences,
-// with lse or without: with parts in either kernel, for as many sequences as are split, however many tiles are sure to
-// have rows.
+// with starts or without: for as many sequences as are split, however many tiles are sure to have rows.
 Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D, bool ragged, bool mass,
-               bool lse, bool largest = false) {
+               bool largest = false) {
     Shape p{};
     if (largest && ragged && B > kCounted) B = kCounted;
-    const int64_t rows = T * group, room = ragged ? few_room(type, D, !largest && (mass || lse)) : kAnyRows;
-    const int64_t few = largest ? kAnyRows : room;  // rows of a sequence that k_attend can have
+    const int64_t rows = T * group, room = ragged ? few_room(type, D) : kAnyRows;
+    const int64_t few = largest ? kAnyRows : room;  // rows of a sequence that k_attend can have: without starts any
     p.sp.few_room = (int)room;
     p.sp.few_rows = (int)(!ragged && group < kFewTile ? group : kFewTile);
     auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
@@ -859,7 +854,7 @@ Shape shape_of(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, 
 }
 Shape shape_of(int type, const AttendArgs &a) {
     Shape p = shape_of(type, a.c.T, a.c.B, (int64_t)a.c.width << a.c.page_log2, a.c.heads, a.group, a.c.D, a.c.starts != nullptr,
-                       a.mass != nullptr, a.lse != nullptr);
+                       a.mass != nullptr);
     float *at = a.ws;
     p.sp.few_sums = at;
     at += p.few_parts * a.c.D;
@@ -927,7 +922,7 @@ hipError_t launch_for(int type, const AttendArgs &a, const Shape &p, hipStream_t
 
 int64_t attend_workspace_bytes(int type, int64_t T, int64_t B, int64_t capacity, int64_t heads, int64_t group, int64_t D,
                                bool ragged, bool mass) {
-    return shape_of(type, T, B, capacity, heads, group, D, ragged, mass, true, true).bytes;
+    return shape_of(type, T, B, capacity, heads, group, D, ragged, mass, true).bytes;
 }
 
 int64_t attend_workspace_used(int type, const AttendArgs &a) { return shape_of(type, a).bytes; }
