@@ -800,16 +800,21 @@ struct Shape {
 constexpr int64_t quads(int64_t floats) { return (floats + 3) / 4 * 4; }  // whole 16 bytes of a workspace
 
 // The most rows of a sequence and head that k_attend takes.  It decodes the entries anew for every 16 rows, and
-// k_attend_rows for every 256, which pays once enough of these have rows.  us with up to 32 rows here and with all:
-//                             192 rows     512 rows     2048 rows     8192 rows
-//   bf16, D = 128, 2 x 4096    43    41     61    67     168   167     274   501
-//                 16 x 4000   162   133    323   323     647  1177    2073  3744
-//   fp32, D = 128, 2 x 4096    62    41     92    76     314   215     543   665
-//                 16 x 4000   299   170    616   427    1312  1601    4337  5247
-//   bf16, D = 192, 2 x 4096    65    54     94    97     287   295     459   933
-//         D = 256             115    57    174   103     576   313    1141   989  (its tiles pass the registers)
+// k_attend_rows for every 256, which pays once enough of these have rows.  us with up to 32 rows here and with all (8 cache
+// heads, 4 query heads of each, out alone):
+//                             256 rows    512 rows    768 rows    1024 rows    2048 rows    8192 rows
+//   bf16, D =  64, 2 x 4096    44   39     50   59     57   73     62    88     94   149    226   427
+//         D = 128, 2 x 4096    57   44     61   69     71   85     80   102    120   175    283   511
+//                 16 x 4000   121  179    184  332    335  475    348   624    652  1175   2076  3714
+//         D = 192, 2 x 4096    77   60     88   95    107  134    121   167    195   304    464   935
+//                 16 x 4000   197  307    301  595    562  866    572  1141   1156  2200   3597  7093
+//   fp32, D =  64, 2 x 4096    56   49     61   76     74   96     84   115    134   195    347   575
+//         D = 128, 2 x 4096    76   51     83   78    106  100    126   127    210   223    562   676
+//                  4 x 4000    82   76    125  127    186  175    208   224    355   413   1068  1308
+//                 16 x 4000   208  228    361  432    638  626    699   829   1343  1593   4181  5048
+// Which is better turns on the tiles that fill the GPU too; rows alone are what the host knows.
 constexpr int64_t kAnyRows = 0x7fffffff;
-int64_t few_room(int type, int64_t D) { return attend_rows_has(type, D) ? (type == 0 ? 1024 : 256) : kAnyRows; }
+int64_t few_room(int type, int64_t D) { return attend_rows_has(type, D) ? (type == 0 ? 768 : 256) : kAnyRows; }
 
 // largest: no call's shape but one whose workspace is no smaller than that of any call of up to T rows and B sequences,
 // with starts or without: for as many sequences as are split, however many tiles are sure to have rows.

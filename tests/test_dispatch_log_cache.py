@@ -47,7 +47,7 @@ def test_evict_up_to_the_largest_launch():
     assert r.stdout.split("\n")[:5] == [f"{dim} 4 3 4" for dim in (64, 96, 128, 192, 256)]
 
 
-ATTEND = r"""
+ATTEND_HEAD = r"""
 import ctypes, sys
 sys.path.insert(0, sys.argv[1])
 from bit_quantized_mat_quantize_amd import _binding
@@ -57,6 +57,8 @@ n = ctypes.c_int(0)
 if hip.hipGetDeviceCount(ctypes.byref(n)) == 0 and n.value > 0:
     sys.exit(3)
 p = lambda i: 65536 + (i << 52)
+"""
+ATTEND = ATTEND_HEAD + r"""
 for t in (0, 1, 2):
     for dim in (64, 96, 128, 192, 256):
         for lse, mass in ((0, 0), (1, 0), (0, 1), (1, 1)):
@@ -77,3 +79,22 @@ def test_long_runs_have_their_kernel_whatever_is_asked_for():
     got = [(l.split()[2], int(l.split("dim=")[1].split()[0]), int(l.split(" of long runs")[0].split()[-1]) > 0) for l in lines]
     assert got == [(t, dim, dim <= (128 if t == "fp32" else 192)) for t in ("fp32", "fp16", "bf16")
                    for dim in (64, 96, 128, 192, 256) for _ in range(4)]
+
+
+BORDERS = ATTEND_HEAD + r"""
+for t, rows in ((0, 768), (0, 769), (1, 256), (1, 257), (2, 256), (2, 257)):
+    c = _binding._Cache(p(0), 1 << 50, 8, 64, 8, 128, p(1), 2, 128, p(2), p(3), rows)
+    assert lib.qmm_cache_attention(ctypes.byref(c), t, p(4), 1 << 50, 1024, 8, p(5), 1 << 50, 1024, 0.1, 1, 0, None, None, 0,
+                                   p(8), 1 << 50, None) == 4
+"""
+
+
+def test_from_how_many_rows_on():
+    """The kernel of long runs begins where it was measured to pay: above 256 rows in 16 bits, 768 in fp32."""
+    r = subprocess.run([sys.executable, "-c", BORDERS, ROOT], capture_output=True, text=True,
+                       env=dict(os.environ, QMM_LOG="1"), timeout=300)
+    if r.returncode == 3:
+        pytest.skip("a GPU is present")
+    assert r.returncode == 0, r.stderr[-2000:]
+    lines = [l for l in r.stderr.splitlines() if l.startswith("qmm: cache_attention")]
+    assert [int(l.split(" of long runs")[0].split()[-1]) > 0 for l in lines] == [False, True] * 3

@@ -10,7 +10,7 @@ from test_gpu_cache_attention import queries
 
 pytestmark = pytest.mark.gpu
 
-# Rows of a sequence and cache head that the kernel takes begin above 256 in 16 bits and 1024 in fp32; heads up to 192 and
+# Rows of a sequence and cache head that the kernel takes begin above 256 in 16 bits and 768 in fp32; heads up to 192 and
 # 128.  The splits are those that fill 256 workgroups over the tiles of 256 rows and the heads: none with these heads.
 RUN = {"f32": (1100, 64), "f16": (300, 128), "bf16": (300, 128)}
 
@@ -270,3 +270,19 @@ def test_starts_that_make_no_sense_in_16_bits(order, B, kind):
     qmm.cache_attention(q, cache, table, n, s, out=wide[4:T + 4], workspace=room[:need])
     torch.cuda.synchronize()
     assert (room[need:] == 0x5A).all() and (wide[:4] == 7).all() and (wide[T + 4:] == 7).all()
+
+
+@pytest.mark.parametrize("kind,rows", [("f32", 767), ("f32", 768), ("f32", 769), ("f32", 1024), ("f32", 1025), ("f16", 256),
+                                       ("f16", 257), ("bf16", 256), ("bf16", 257)])
+def test_borders_of_who_takes_the_rows(kind, rows):
+    rng = np.random.default_rng([68, rows])
+    b = batch_of(rng, [rows + 33, rows - 1], [rows, rows - 1], 2, 128, 32)
+    qd, q = queries(rng, b.T, 2, 128, kind)
+    print(kind, rows, flush=True)
+    ref = reference(b, q, 128 ** -0.5)
+    cache, table, lens, st = b.dev()
+    compare(kind, b, q, qmm.cache_attention(qd.cuda(), cache, table, lens, st), ref, kind == "bf16")
+    got, lse = qmm.cache_attention(qd.cuda(), cache, table, lens, st, lse=True)
+    compare(kind, b, q, got, ref, False)
+    ds = tolerance(kind, 128, max(b.lens), ref[3], ref[0])[1]
+    assert (np.abs(to_host(lse) - ref[1]) <= (ds + 2.0 ** -22 * (2 + np.abs(ref[1]))) * 1.01).all()
