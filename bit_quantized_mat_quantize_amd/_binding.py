@@ -621,8 +621,9 @@ def mul_mat_logprobs(wfmt: str, w, y, M: int, N: int, K: int, tokens=None, k: in
 # ---- between the projections: rotary positions, the 4-bit cache of keys and values, attention over it, eviction.
 
 def rope_ramp(rot: int, base: float, length: int, factor: float, fast: float = 32.0, slow: float = 1.0):
-    """rope's scaling arguments for a model trained on `length` positions and used on `factor` times as many: pairs that
-    turn more than `fast` times within `length` keep their angles, those of fewer than `slow` turns are slowed by
+    """rope's scaling arguments for a model trained on `length` positions and used on `factor` times as many, by the
+    published YaRN method (Peng et al., "YaRN: Efficient Context Window Extension", 2023, its ramp over dimensions and its
+    attention factor; the ends are whole pairs): pairs that turn more than `fast` times within `length` keep their angles, those of fewer than `slow` turns are slowed by
     `factor`, those between in part, and magnitude = 0.1 ln(factor) + 1."""
     import math
 
@@ -852,7 +853,9 @@ def cache_evict(cache, table, lens, mass, budget: int, recent: int = 0, to=None,
     others, those of the largest mass (fp32 [B, heads, n] as in cache_attention), ties to the lower position.
 
     They move in their order within the sequences' own pages (to: None; no two sequences may share one then), or into
-    those of `to` (int32 [B, pages]), which must be none of the table's.  ids: int32 [B, heads, budget], where they
+    those of `to` (int32 [B, pages]), which must be none of the table's: a copy of some of its columns is not refused, and
+    entries would be read after others were written over them.  To keep a sequence's first pages alone, let `to` be None and
+    cut the table after the call (its entries past lens are nobody's): table[:, :n].contiguous().  ids: int32 [B, heads, budget], where they
     were, -1 behind; mass: fp32 [B, heads, pages of `to` * page], 0 behind; lens: int32 [B]."""
     import torch
     if mass.requires_grad and torch.is_grad_enabled():

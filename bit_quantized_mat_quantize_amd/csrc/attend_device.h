@@ -91,8 +91,8 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 }
 
 // The power of two that value scales are multiplied by, from the largest scale's bits:
-// its exponent becomes 7 (products with codes, 16-fold ones too, stay within fp16, and two
-// pieces of them keep everything down to 2^-36 of the largest); at most 2^15.
+// its exponent becomes 7 (products with codes, 16-fold ones too, stay within fp16; a scale below
+// 2^-21 of the largest is rounded to a step of 2^-31 of it); at most 2^15.
 __device__ __forceinline__ int value_shift(uint32_t top) {
     const int e = (int)(top >> 10);
     return e < 7 ? 15 : 22 - e;
@@ -109,8 +109,9 @@ __device__ __forceinline__ f16v mfma32(h8 a, h8 b, f16v c) { return __builtin_am
 constexpr int kFewTile = 16, kManyTile = 256;
 // The most rows whose entries' weights k_attend_mass forms, which converts the queries anew for every 32 entries;
 // attend_mass.hip's kernel has the more, from queries that the attention left.  What the weights add to a call, us, here and
-// there, 16 sequences of 4000 entries, 8 heads of 128: bf16 of 32 rows 48 and 54, 64: 72 and 57, 256: 199 and 92;
-// fp32 64: 85 and 83, 512: 491 and 245.
+// there, 16 sequences of 4000 entries, 8 heads of 128: bf16 of 32 rows 50 and 59, 48: 60 and 61, 64: 72 and 60, 256: 201 and
+// 99; fp32 32: 57 and 82, 48: 73 and 86, 64: 87 and 85, 512: 487 and 248; heads of 64 in bf16 32: 27 and 45, 64: 38 and 47;
+// of 256, whose rows do not stay in registers here, 4: 110 and 95, 64: 262 and 99.
 constexpr int kMassRoom = 32;
 
 struct Splits {
@@ -133,9 +134,11 @@ struct Splits {
 
 // The tiles of a call that have rows of one of the two kernels, in the sequences' order, and into how many splits
 // of the entries each goes: the GPU's workgroups over the tiles.  Only the device knows how many rows a sequence has,
-// so each wavefront counts them: sequence 64 k + lane's tiles end at upto[k].  Beyond kCounted sequences that
-// takes too long; there sequence b's tiles start at slot floor(starts[b] * group / ROWS) + b, not all slots have
-// rows, and nothing is split: so many sequences fill the GPU.
+// so each wavefront counts them: sequence 64 k + lane's tiles end at upto[k].  All tiles of a call go into as many
+// splits, whatever their sequences' lengths: one of 131072 entries takes 51 us alone, and among 63 of 500, where the tiles
+// fill the GPU and nothing is split, 1308 (fp32, 8 heads of 128).  Beyond kCounted sequences counting takes too long;
+// there sequence b's tiles start at slot floor(starts[b] * group / ROWS) + b, not all slots have rows, and nothing is
+// split either.
 constexpr int kCounted = 256;
 // sum over the lanes up to this one
 __device__ __forceinline__ int wave_upto(int v) {

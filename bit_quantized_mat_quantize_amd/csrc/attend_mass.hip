@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_mass_rows(AttendArgs a, 
     const KvRows rows = kv_rows(a.c, b);
     const int total = rows.count * a.group;
     if (total <= kMassRoom || e0 >= rows.len) return;
-    // tokens that see any of the 128 entries
+    // tokens that see any of the workgroup's entries
     const int before = rows.len - rows.count;
     int i0 = a.causal ? e0 - before : 0, i1 = a.window > 0 ? e0 + S::ENTRIES - 1 + a.window - before : rows.count;
     i0 = i0 < 0 ? 0 : i0;

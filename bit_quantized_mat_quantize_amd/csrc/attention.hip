@@ -25,9 +25,9 @@
 // are not touched.
 //
 // Bounds: single tokens of long contexts, the issue of vector instructions beside the
-// bytes (345 of them for 32 entries of 128 elements, 60% of the issue slots; 32
-// sequences of up to 8192 entries, 8 cache heads of 128, fp32: 69 us, 3.7 TB/s of the
-// cache; 2 of 131072 in bf16: 62 us, 4.5 TB/s); many rows, the same once per 16 of them;
+// bytes (56% of the issue slots and matrix instructions 21% of the cycles for fp32 queries,
+// 51% and 10% for 16-bit ones; 32 sequences of up to 8192 entries, 8 cache heads of 128, fp32: 66 us,
+// 3.8 TB/s of the cache; 2 of 131072 in bf16: 61 us, 4.5 TB/s); many rows, the same once per 16 of them;
 // one short sequence, a chain of latencies (8 us for 1000 entries).
 #include "attend_device.h"
 
@@ -748,6 +748,8 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, Splits s
 // The weight that each entry got, for sequences of few rows: mass[j] += sum over rows and
 // heads of the group of 2^(x - lse2).  A wavefront owns 32 entries of a head and goes
 // over the rows, 16 at a time, so every place is added to by one lane, in a fixed order.
+// A chain of latencies (table, codes, queries, lse) that little overlaps, and the keys are read and decoded a second
+// time: 16 sequences of 4000 entries, 8 heads of 128, one token of 4 query heads each add 37 us to 30, their bytes 8.
 template <int PIECES, int D>
 __global__ __launch_bounds__(kThreads) void k_attend_mass(AttendArgs a, Splits sp, int type, int tiles) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;

@@ -553,9 +553,13 @@ size_t qmm_cache_attention_workspace_bytes(qmm_float_type t, int64_t rows, int64
  * and the query heads of cache head h of e^(s_j - lse).
  * Sums are fp32.  fp32 queries are multiplied to 22 bits of their row's largest element; with 16-bit queries values and
  * the weights e^(..) may be rounded to fp16 before their product, and with bf16 ones, where neither lse nor mass is
- * asked for, keys.  Results do not depend on timing.
- * Requires rows * q_heads <= 2^30.  What stands behind lens[b], or in pages that no row sees, may hold anything.  An entry that a row sees and
- * that has a NaN scale, or whose page is not in [0, pages), makes the row NaN; so does an infinity or NaN in its query.
+ * asked for, keys.  Numbers far below others of a call are held to a part of the largest: elements of a query to 2^-33
+ * of its row's, weights to 2^-33 of the row's sum, keys and values to 2^-31 of the largest that the call's rows of the
+ * sequence see (where an entry that some rows do not see is 2^20 times all that they do, these lose bits by it).
+ * Results do not depend on timing.
+ * Requires rows * q_heads <= 2^30.  What stands behind lens[b], or in pages that no row sees, may hold anything.  An
+ * entry that a row sees and that has a NaN scale, or whose page is not in [0, pages), makes the row NaN; so does an
+ * infinity or NaN in its query.
  * workspace: qmm_cache_attention_workspace_bytes, overwritten; calls that may overlap need one each.  out must not
  * overlap anything else of the call but a matrix whose columns it shares with q, element by element apart. */
 qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void *q, size_t q_bytes, int64_t ld_q,
@@ -571,10 +575,10 @@ qmm_status qmm_cache_attention(const qmm_cache *c, qmm_float_type t, const void 
  *   lens_out int32 [seqs]: n
  * and entry i of the pages of `to` (int32 [seqs][to_width], to_width * page >= budget) becomes entry ids[i].  `to` may
  * be c->table itself (then to_width = width): the entries move within their pages (which no two sequences may share
- * then).  Else its pages
- * must be none that c->table names.  An entry whose page is not in [0, pages) becomes NaN; one that would move
- * to such a page is not written.  Keys keep the rotation of the positions they were written with.  c->starts and
- * c->rows are not used. */
+ * then).  Else its pages must be none that c->table names, which is not checked (a copy of the table's first columns is
+ * such a mistake: entries would be read after others were written over them; pass c->table, and drop the pages behind
+ * lens_out afterwards).  An entry whose page is not in [0, pages) becomes NaN; one that would move to such a page is not
+ * written.  Keys keep the rotation of the positions they were written with.  c->starts and c->rows are not used. */
 qmm_status qmm_cache_evict(const qmm_cache *c, const float *mass, int64_t ld_mass, int64_t budget, int64_t recent,
                            const int32_t *to, int64_t to_width, int32_t *lens_out, float *mass_out, int64_t ld_out,
                            int32_t *ids, void *stream);
