@@ -14,7 +14,12 @@
 //   O^T += V^T P^T  a lane holds eight entries' words of the same eight elements, so the
 //                   codes are transposed by byte permutes within the lane; code * scale
 //                   is rounded to fp16 for 16-bit queries, and cut in two exact pieces for
-//                   fp32 ones, as p is.
+//                   fp32 ones.  p is rounded to fp16 for bf16 queries, and two pieces for fp16
+//                   and fp32 ones: rounded to one it put fp16 outputs on short contexts at up to
+//                   1.6 times the 64-bit error that fp16 itself costs (1.4 with two; of 40 random
+//                   calls), and two are a twentieth of the time (32 sequences of 8192
+//                   entries, 8 query heads of a cache head of 128: 70 us and 74; with 256
+//                   rows, 16 of 4000: 193 and 211).
 //
 // In both products the entries lie along the registers of a lane and the rows along
 // the lanes, so softmax needs no exchange between lanes, and P goes from one product
@@ -327,8 +332,8 @@ struct Running {
     }
 };
 
-// masked: some row does not see some entry of the step
-template <int PIECES, int D>
+// WP: pieces of a weight.  masked: some row does not see some entry of the step
+template <int PIECES, int WP, int D>
 __device__ __forceinline__ void step(const Decode &k, Step<D> &t, const Tile<PIECES, D> &q, int k0, bool masked, Running<D> &run) {
     constexpr int ROUNDS = Step<D>::ROUNDS;
     const int lane = threadIdx.x & 63, g = lane >> 4;
@@ -411,7 +416,7 @@ __device__ __forceinline__ void step(const Decode &k, Step<D> &t, const Tile<PIE
         const float p = exp2_fast(fmaf(x[i], factor, -from));
         run.sum += p;
         ph[i] = (_Float16)p;
-        if constexpr (PIECES == 2) pl[i] = (_Float16)(p - (float)ph[i]);
+        if constexpr (WP == 2) pl[i] = (_Float16)(p - (float)ph[i]);
     }
     const _Float16 unit = (_Float16)pow2i(run.shift);
 #pragma unroll
@@ -445,16 +450,14 @@ __device__ __forceinline__ void step(const Decode &k, Step<D> &t, const Tile<PIE
                 }
                 f4 &acc = run.o[r][2 * y + o];
                 acc = mfma16(vh, ph, acc);
-                if constexpr (PIECES == 2) {
-                    acc = mfma16(vh, pl, acc);
-                    acc = mfma16(vl, ph, acc);
-                }
+                if constexpr (WP == 2) acc = mfma16(vh, pl, acc);
+                if constexpr (PIECES == 2) acc = mfma16(vl, ph, acc);
             }
         }
     }
 }
 
-template <int PIECES, int D>
+template <int PIECES, int WP, int D>
 __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(AttendArgs a, Splits sp, int type) {
     constexpr int ROUNDS = Step<D>::ROUNDS, PITCH = D + 4;
     using R = Ring<D>;
@@ -531,7 +534,7 @@ __global__ __launch_bounds__(kThreads, (at_once<PIECES, D>)) void k_attend(Atten
             ring.read(i % R::SLOTS, t);
             t.bad = bad & 3;
             const int k0 = (at0 + i * kWaves) * kKeys;
-            step<PIECES, D>(decode, t, q, k0, k0 < q.all_lo || k0 + kKeys > q.all_hi, run);
+            step<PIECES, WP, D>(decode, t, q, k0, k0 < q.all_lo || k0 + kKeys > q.all_hi, run);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this slot's reads are done
         }
     }
@@ -885,13 +888,13 @@ int64_t mass_tiles(const AttendArgs &a) {
     return (((int64_t)a.c.width << a.c.page_log2) + kKeys * kWaves - 1) / (kKeys * kWaves);
 }
 
-template <int PIECES, int D>
+template <int PIECES, int WP, int D>
 hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) {
     constexpr int bytes = kWaves * Ring<D>::WAVE;
     static std::atomic<uint64_t> lds_set{0};
-    hipError_t e = ensure_lds_bytes((const void *)k_attend<PIECES, D>, bytes, lds_set);
+    hipError_t e = ensure_lds_bytes((const void *)k_attend<PIECES, WP, D>, bytes, lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attend<PIECES, D>), dim3((unsigned)p.few_groups), dim3(kThreads), bytes, s, a, p.sp, type);
+    hipLaunchKernelGGL((k_attend<PIECES, WP, D>), dim3((unsigned)p.few_groups), dim3(kThreads), bytes, s, a, p.sp, type);
     e = hipGetLastError();
     if (e == hipSuccess && p.many_groups) e = launch_attend_rows(type, a, p.sp, p.many_groups, s);
     if (e == hipSuccess && p.few_join + p.many_join) {
@@ -914,14 +917,14 @@ hipError_t launch(int type, const AttendArgs &a, const Shape &p, hipStream_t s) 
     return hipGetLastError();
 }
 
-template <int PIECES>
+template <int PIECES, int WP>
 hipError_t launch_for(int type, const AttendArgs &a, const Shape &p, hipStream_t s) {
     switch (a.c.D) {
-        case 64: return launch<PIECES, 64>(type, a, p, s);
-        case 96: return launch<PIECES, 96>(type, a, p, s);
-        case 128: return launch<PIECES, 128>(type, a, p, s);
-        case 192: return launch<PIECES, 192>(type, a, p, s);
-        default: return launch<PIECES, 256>(type, a, p, s);
+        case 64: return launch<PIECES, WP, 64>(type, a, p, s);
+        case 96: return launch<PIECES, WP, 96>(type, a, p, s);
+        case 128: return launch<PIECES, WP, 128>(type, a, p, s);
+        case 192: return launch<PIECES, WP, 192>(type, a, p, s);
+        default: return launch<PIECES, WP, 256>(type, a, p, s);
     }
 }
 
@@ -949,7 +952,8 @@ bool attend_grid_ok(int type, const AttendArgs &a) {
 
 hipError_t launch_attend(int type, const AttendArgs &a, hipStream_t s) {
     const Shape p = shape_of(type, a);
-    return type == 0 ? launch_for<2>(type, a, p, s) : launch_for<1>(type, a, p, s);
+    if (type == 0) return launch_for<2, 2>(type, a, p, s);
+    return type == 1 ? launch_for<1, 2>(type, a, p, s) : launch_for<1, 1>(type, a, p, s);
 }
 
 }  // namespace qmm

@@ -551,11 +551,11 @@ size_t qmm_cache_attention_workspace_bytes(qmm_float_type t, int64_t rows, int64
  * ld_out elements from a row to the next; rows start on 16 bytes.  lse: fp32 [rows][q_heads], or NULL.
  * mass: fp32 [seqs][heads][ld_mass], ld_mass >= width * page, or NULL: mass[b][h][j] += the sum over the call's rows
  * and the query heads of cache head h of e^(s_j - lse).
- * Sums are fp32.  fp32 queries are multiplied to 22 bits of their row's largest element; with 16-bit queries values and
- * the weights e^(..) may be rounded to fp16 before their product, and with bf16 ones, where neither lse nor mass is
- * asked for, keys.  Numbers far below others of a call are held to a part of the largest: elements of a query to 2^-33
- * of its row's, weights to 2^-33 of the row's sum, keys and values to 2^-31 of the largest that the call's rows of the
- * sequence see (where an entry that some rows do not see is 2^20 times all that they do, these lose bits by it).
+ * Sums are fp32.  fp32 queries are multiplied to 22 bits of their row's largest element; with 16-bit queries values may
+ * be rounded to fp16 before their product, and the weights e^(..), and with bf16 ones, where neither lse nor mass is asked
+ * for, keys.  Numbers far below others of a call are held to a part of the largest: elements of a query to 2^-33 of its
+ * row's, weights to 2^-33 of the row's sum, keys and values to 2^-31 of the largest that the call's rows of the sequence
+ * see (where an entry that some rows do not see is 2^20 times all that they do, these lose bits by it).
  * Results do not depend on timing.
  * Requires rows * q_heads <= 2^30.  What stands behind lens[b], or in pages that no row sees, may hold anything.  An
  * entry that a row sees and that has a NaN scale, or whose page is not in [0, pages), makes the row NaN; so does an
